@@ -255,6 +255,80 @@ pa_status pa_append_kv(void* k_cache, void* v_cache, const void* k_new, const vo
                        const int32_t* block_tables, const int32_t* positions,
                        const pa_shape* shape, void* stream);
 
+/* Rotary embedding of pa_rope_append_kv.  Strides are in elements between the
+ * tokens of the flattened [batch * q_len] order (a token's heads are
+ * contiguous), so that q, k_new and v_new may be views of one fused
+ * projection's output; each at least a token's row and a multiple of 8. */
+typedef struct pa_rope {
+    int32_t rotary_dim;   /* R: leading elements of a head that turn, a multiple of 16, <= head_dim */
+    int32_t num_axes;     /* position axes (1 for text; time, height, width for video), >= 1 */
+    int32_t interleaved;  /* 0: pair j is elements (j, j + R/2); 1: (2j, 2j + 1) */
+    int32_t reserved;     /* 0 */
+    int64_t q_stride, q_out_stride, k_stride, v_stride;
+} pa_rope;
+
+/*
+ * Rotary positions with one or several axes for the new tokens, and their
+ * append to the cache: the step between a layer's projections and
+ * pa_decode_splitkv / pa_decode_multi.  For token i of sequence b, pair j of
+ * every query and key head turns by the angle
+ *   a = rotary_positions[axes[j]][b][i] * f_j,
+ *   (x, y) -> (x cos a - y sin a, x sin a + y cos a);
+ * elements from rotary_dim on, and the values, pass through.  The turned
+ * query goes to q_out; the turned key and the value go to cache position
+ * context_lens[b] - q_len + i of sequence b (context_lens counts the q_len new
+ * tokens, as in pa_decode_multi).  Rotary positions and cache positions are
+ * apart: an image's patches share a time, and eviction moves tokens to lower
+ * slots.  A token at a negative position (padding) or past the table, or whose
+ * table entry is masked, is turned into q_out and writes nothing to the cache.
+ *   q, q_out          [batch, q_len, num_heads, head_dim]     kv_dtype (q_out may be q)
+ *   k_new, v_new      [batch, q_len, num_kv_heads, head_dim]  kv_dtype
+ *   rotary_positions  [num_axes, batch, q_len]  int32, any value
+ *   phases            [rotary_dim / 2]  int64: f_j / (2 pi) * 2^64, modulo 2^64
+ *   axes              [rotary_dim / 2]  int32; a pair whose axis is outside
+ *                     [0, num_axes) does not turn
+ * Angles are formed modulo one turn in 64-bit integers, so that a far position
+ * is as exact as a near one; sine, cosine and the products are fp32, and each
+ * result is rounded once to kv_dtype.  shape->out_dtype is checked and not
+ * used.  Two tokens of a call must not share a cache slot.
+ */
+pa_status pa_rope_append_kv(void* q_out, void* k_cache, void* v_cache, const void* q,
+                            const void* k_new, const void* v_new, const int32_t* rotary_positions,
+                            const int64_t* phases, const int32_t* axes,
+                            const int32_t* block_tables, const int32_t* context_lens,
+                            const pa_shape* shape, int32_t q_len, const pa_rope* rope,
+                            void* stream);
+
+/*
+ * Eviction from the cache by accumulated attention weight (the weights that
+ * pa_decode_accumulate keeps).  Every kv head of a sequence keeps at most
+ * `budget` of its min(context_lens[b], table reach) tokens: the first `sink`
+ * and the last `recent` ones, and of the others those of the largest weights,
+ * equal weights by the lowest index (NaN ranks below every number); tokens of
+ * masked pages are never kept.  Kept token number j, in the tokens' order, of
+ * each kv head moves to cache position j of new_block_tables[b]; the kv heads
+ * choose apart, and all keep the same number, which goes to new_lens[b].
+ *   weights           [batch, num_kv_heads, max_blocks_per_seq * block_size]      fp32
+ *   new_weights       [batch, num_kv_heads, new_max_blocks_per_seq * block_size]  fp32:
+ *                     the kept tokens' weights, zeros from new_lens[b] on
+ *   new_block_tables  [batch, new_max_blocks_per_seq]  int32
+ *   new_lens          [batch]  int32
+ *   kept              [batch, num_kv_heads, budget]  int32: the kept tokens'
+ *                     former positions, ascending, -1 from new_lens[b] on
+ * new_block_tables (and new_weights) may be block_tables (and weights)
+ * themselves: the tokens then move down within their own pages, which no
+ * other sequence may share.  Otherwise the new pages must not be among any
+ * sequence's old ones, which stay as they were.  A kept token whose new entry
+ * is masked is not stored.  budget >= sink + recent, and
+ * new_max_blocks_per_seq * block_size >= budget.  The num_heads and out_dtype
+ * of the shape are checked and not used.
+ */
+pa_status pa_evict_kv(void* k_cache, void* v_cache, const float* weights,
+                      const int32_t* block_tables, const int32_t* context_lens,
+                      const int32_t* new_block_tables, float* new_weights, int32_t* new_lens,
+                      int32_t* kept, const pa_shape* shape, int32_t new_max_blocks_per_seq,
+                      int32_t budget, int32_t sink, int32_t recent, void* stream);
+
 /*
  * Test export of the page walk (MiniVLLM docs "Decoding Benchmark", "Block
  * table lookup mechanics"): out_phys[b][j] (device, int32, [batch,

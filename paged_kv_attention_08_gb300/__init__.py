@@ -14,6 +14,11 @@ or a call is rejected, an exception is raised.
     decode_multi(out, q, k_cache, v_cache, block_tables, context_lens, scale,
                  max_context_len, partition_tokens=0, workspace=None)
     append_kv(k_cache, v_cache, k_new, v_new, block_tables, positions)
+    rope_phases(inv_freq)
+    rope_append_kv(q_out, k_cache, v_cache, q, k_new, v_new, rotary_positions, phases, axes,
+                   block_tables, context_lens, interleaved=False)
+    evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables,
+             new_weights, new_lens, kept, sink=0, recent=0)
     workspace_size(q, k_cache, block_tables, out_dtype, max_context_len, partition_tokens=0)
     workspace_size_multi(q, k_cache, block_tables, out_dtype, max_context_len, partition_tokens=0)
     plan_info(q, k_cache, block_tables, max_context_len, partition_tokens=0)
@@ -28,13 +33,14 @@ Every launching call also takes ``stream=`` (default: the current torch stream).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
 import torch
 
 __all__ = ["PaError", "decode", "decode_splitkv", "decode_splitkv_noalloc", "decode_multi",
-           "append_kv", "workspace_size", "workspace_size_multi", "plan_info", "choose_partition_tokens",
+           "append_kv", "rope_phases", "rope_append_kv", "evict_kv", "workspace_size", "workspace_size_multi", "plan_info", "choose_partition_tokens",
            "resolve_blocks", "selftest_wait_timeout", "device_error", "library_path", "F16",
            "BF16", "F32", "PARTITION_BALANCED", "set_switch", "get_switch", "SWITCH_MULTI_KERNEL",
            "SWITCH_TILE_COMPACT_Q", "KERNEL_AUTO", "KERNEL_MMA", "KERNEL_TILE"]
@@ -66,6 +72,13 @@ class _Shape(ctypes.Structure):
                 ("block_size", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
                 ("num_blocks", ctypes.c_int64), ("kv_dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -103,6 +116,10 @@ def _load():
             lib.pa_resolve_blocks.restype = ctypes.c_int
             lib.pa_append_kv.argtypes = [P, P, P, P, P, P, S, P]
             lib.pa_append_kv.restype = ctypes.c_int
+            lib.pa_rope_append_kv.argtypes = [P] * 11 + [S, i32, ctypes.POINTER(_Rope), P]
+            lib.pa_rope_append_kv.restype = ctypes.c_int
+            lib.pa_evict_kv.argtypes = [P] * 9 + [S, i32, i32, i32, i32, P]
+            lib.pa_evict_kv.restype = ctypes.c_int
             lib.pa_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P]
             lib.pa_selftest_wait_timeout.restype = ctypes.c_int
             lib.pa_device_error.argtypes = [ctypes.POINTER(i32), P]
@@ -344,6 +361,158 @@ def append_kv(k_cache, v_cache, k_new, v_new, block_tables, positions, stream=No
     _check(_load().pa_append_kv(k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(),
                                 v_new.data_ptr(), block_tables.data_ptr(), positions.data_ptr(),
                                 ctypes.byref(shape), _stream_ptr(stream)), "pa_append_kv")
+
+
+class _launch_on:
+    """Makes the tensors' device the current one for a call, and names the
+    stream to launch on: the given one, or that device's current stream."""
+
+    def __init__(self, tensor, stream):
+        self._guard = torch.cuda.device(tensor.device)
+        if stream is not None and stream.device != tensor.device:
+            raise ValueError("stream is on another device than the tensors")
+        self._stream = stream if stream is not None else torch.cuda.current_stream(tensor.device)
+
+    def __enter__(self):
+        self._guard.__enter__()
+        return self._stream
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def rope_phases(inv_freq: torch.Tensor) -> torch.Tensor:
+    """The int64 table that ``rope_append_kv`` takes for the rotary frequencies
+    ``inv_freq`` (float64, radians per position, one per pair; 1-D): each as a
+    fraction of a turn, times 2^64.  Made once, kept by the caller."""
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be a 1-D float64 tensor")
+    if not bool(torch.isfinite(inv_freq).all()):
+        raise ValueError("inv_freq must be finite")
+    turns = inv_freq / (2 * math.pi)
+    turns = turns - torch.floor(turns + 0.5)  # in [-1/2, 1/2)
+    return (turns * 2.0 ** 64).to(torch.int64)
+
+
+def _token_stride(t, name, heads, head_dim, batch, q_len):
+    """Elements between consecutive tokens of a [batch, q_len, heads, head_dim]
+    view whose tokens lie evenly apart and whose rows are contiguous."""
+    if tuple(t.shape) != (batch, q_len, heads, head_dim):
+        raise ValueError(f"{name} {tuple(t.shape)} must be {(batch, q_len, heads, head_dim)}")
+    s = t.stride()
+    if s[3] != 1 or (heads > 1 and s[2] != head_dim):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    if q_len == 1:
+        return s[0] if batch > 1 else max(s[0], heads * head_dim)
+    if batch > 1 and s[0] != q_len * s[1]:
+        raise ValueError(f"{name}'s tokens must lie evenly apart")
+    return s[1]
+
+
+def rope_append_kv(q_out, k_cache, v_cache, q, k_new, v_new, rotary_positions, phases, axes,
+                   block_tables, context_lens, interleaved: bool = False, stream=None):
+    """Turn the new tokens' queries into ``q_out`` (may be ``q``) and write
+    their turned keys and their values into the paged cache.
+
+    q, q_out [B, Q, H, D]; k_new, v_new [B, Q, Hkv, D] (views of one fused
+    projection are fine); rotary_positions int32 [axes, B, Q]; phases from
+    ``rope_phases`` and axes int32, one per rotary pair (2 * pairs <= D).
+    context_lens counts the Q new tokens.  For one token per sequence the
+    tensors may leave out their Q dimension."""
+    if q.dim() == 3:
+        if q_out.dim() != 3 or k_new.dim() != 3 or v_new.dim() != 3 or rotary_positions.dim() != 2:
+            raise ValueError("q, q_out, k_new, v_new and rotary_positions must all leave out "
+                             "the query-token dimension, or none")
+        rope_append_kv(q_out.unsqueeze(1), k_cache, v_cache, q.unsqueeze(1), k_new.unsqueeze(1),
+                       v_new.unsqueeze(1), rotary_positions.unsqueeze(2), phases, axes,
+                       block_tables, context_lens, interleaved, stream)
+        return q_out
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, q_len, num_heads, head_dim]")
+    if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
+                         "num_kv_heads, head_dim]")
+    if any(t.dtype != k_cache.dtype for t in (v_cache, q, q_out, k_new, v_new)):
+        raise TypeError("queries, new keys/values and both caches must have one dtype")
+    B, Q, H, D = q.shape
+    NB, bs, Hkv, cache_d = k_cache.shape
+    if cache_d != D:
+        raise ValueError(f"q's head_dim {D} differs from the cache's {cache_d}")
+    if Q < 1:
+        raise ValueError("q_len must be at least 1")
+    rope = _Rope(0, 0, int(bool(interleaved)), 0, _token_stride(q, "q", H, D, B, Q),
+                 _token_stride(q_out, "q_out", H, D, B, Q),
+                 _token_stride(k_new, "k_new", Hkv, D, B, Q),
+                 _token_stride(v_new, "v_new", Hkv, D, B, Q))
+    if rotary_positions.dim() != 3 or tuple(rotary_positions.shape[1:]) != (B, Q):
+        raise ValueError("rotary_positions must be [axes, batch, q_len]")
+    if rotary_positions.dtype != torch.int32 or axes.dtype != torch.int32:
+        raise TypeError("rotary_positions and axes must be int32")
+    if phases.dtype != torch.int64:
+        raise TypeError("phases must be the int64 table of rope_phases")
+    if phases.dim() != 1 or tuple(axes.shape) != tuple(phases.shape):
+        raise ValueError("phases and axes must hold one value per rotary pair")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq], context_lens [batch]")
+    _ints(block_tables, context_lens)
+    _dev_tensors(k_cache, v_cache, rotary_positions, phases, axes, block_tables, context_lens)
+    for t in (q, q_out, k_new, v_new):
+        if t.device != k_cache.device:
+            raise ValueError("all tensors must be on one device")
+    rope.rotary_dim, rope.num_axes = 2 * phases.numel(), rotary_positions.shape[0]
+    shape = _Shape(B, H, Hkv, D, bs, block_tables.shape[1], NB, _dtype_code(k_cache.dtype), F32)
+    with _launch_on(k_cache, stream) as on:
+        _check(_load().pa_rope_append_kv(
+            q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), q.data_ptr(),
+            k_new.data_ptr(), v_new.data_ptr(), rotary_positions.data_ptr(), phases.data_ptr(),
+            axes.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), ctypes.byref(shape),
+            Q, ctypes.byref(rope), on.cuda_stream), "pa_rope_append_kv")
+    return q_out
+
+
+def evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, new_weights,
+             new_lens, kept, sink: int = 0, recent: int = 0, stream=None):
+    """Cut every kv head of every sequence down to ``kept.shape[2]`` tokens: the
+    first ``sink`` and last ``recent`` ones and those of the largest
+    accumulated ``weights`` ([B, Hkv, max_blocks * block_size] fp32, ties to
+    the lowest index), moved in their order to the front of
+    ``new_block_tables``' pages.  Passing ``block_tables`` / ``weights``
+    themselves as the new ones works in place.  ``kept`` (int32 [B, Hkv,
+    budget]) receives the kept tokens' former positions, ``new_lens`` (int32
+    [B]) the new lengths."""
+    if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
+                         "num_kv_heads, head_dim]")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("v_cache must have k_cache's dtype")
+    NB, bs, Hkv, D = k_cache.shape
+    if block_tables.dim() != 2 or new_block_tables.dim() != 2 or \
+            new_block_tables.shape[0] != block_tables.shape[0]:
+        raise ValueError("block_tables and new_block_tables must be [batch, max_blocks_per_seq]")
+    B, mb = block_tables.shape
+    new_mb = new_block_tables.shape[1]
+    if tuple(weights.shape) != (B, Hkv, mb * bs) or tuple(new_weights.shape) != (B, Hkv, new_mb * bs):
+        raise ValueError("weights and new_weights must be [batch, num_kv_heads, their table's "
+                         "max_blocks * block_size]")
+    if weights.dtype != torch.float32 or new_weights.dtype != torch.float32:
+        raise TypeError("weights and new_weights must be float32")
+    if tuple(context_lens.shape) != (B,) or tuple(new_lens.shape) != (B,):
+        raise ValueError("context_lens and new_lens must be [batch]")
+    if kept.dim() != 3 or tuple(kept.shape[:2]) != (B, Hkv):
+        raise ValueError("kept must be [batch, num_kv_heads, budget]")
+    _ints(block_tables, context_lens)
+    if any(t.dtype != torch.int32 for t in (new_block_tables, new_lens, kept)):
+        raise TypeError("new_block_tables, new_lens and kept must be int32")
+    _dev_tensors(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables,
+                 new_weights, new_lens, kept)
+    shape = _Shape(B, Hkv, Hkv, D, bs, mb, NB, _dtype_code(k_cache.dtype), F32)
+    with _launch_on(k_cache, stream) as on:
+        _check(_load().pa_evict_kv(
+            k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), new_block_tables.data_ptr(), new_weights.data_ptr(),
+            new_lens.data_ptr(), kept.data_ptr(), ctypes.byref(shape), new_mb, kept.shape[2],
+            int(sink), int(recent), on.cuda_stream), "pa_evict_kv")
+    return new_lens
 
 
 def resolve_blocks(out_phys, block_tables, context_lens, block_size: int, num_blocks: int,

@@ -85,9 +85,9 @@ std::atomic<int> g_switch_compact_q{env_value("PA_TILE_COMPACT_Q", 1, parse_comp
 
 int elem_size(int dtype) { return dtype == PA_F32 ? 4 : 2; }
 
-bool aligned(const void* ptr, size_t a) { return reinterpret_cast<uintptr_t>(ptr) % a == 0; }
-
 bool pow2_group_ok(int g) { return g == 1 || g == 2 || g == 4 || g == 8 || g == 16; }
+
+}  // namespace
 
 pa_status check_shape(const pa_shape* s) {
     if (!s) return PA_ERR_INVALID_ARG;
@@ -106,6 +106,8 @@ pa_status check_shape(const pa_shape* s) {
         return PA_ERR_UNSUPPORTED;
     return PA_OK;
 }
+
+namespace {
 
 // The scores are scaled by `scale` before the softmax; the kernels take the
 // running maximum of the unscaled scores, which needs scale > 0.
@@ -163,6 +165,8 @@ pa_status query_sms(int32_t partition_tokens, int* sms) {
     return partition_tokens > 0 ? PA_OK : st;
 }
 
+}  // namespace
+
 // SM count and error-word address of the current device (cached).
 pa_status device_state(int* sms, int32_t** err) {
     int dev = 0, n = 0;
@@ -180,6 +184,8 @@ pa_status device_state(int* sms, int32_t** err) {
     if (err) *err = e;
     return PA_OK;
 }
+
+namespace {
 
 // Launch shape of the attention kernel for one problem: warps per stream
 // (head_dim 256 splits a page's output columns over two warps), streams per
@@ -226,8 +232,9 @@ int ctas_per_sm(const pa_shape* s, const Tune& t) {
 
 // Programmatic dependent launch lets each kernel's launch overlap the tail
 // of the previous one in the stream; PA_NO_PDL=1 launches plainly instead.
+}  // namespace
 bool use_pdl() { return !g_env.no_pdl; }
-
+namespace {
 
 int pages_for(const pa_shape* s, int32_t max_context_len) {
     int64_t t = max_context_len < 1 ? 1 : max_context_len;

@@ -58,6 +58,42 @@ struct CombineParams {
     int32_t num_ctas;  // balanced split: CTAs of the attention kernel (records [C][2][G])
 };
 
+// Rotary positions and the append to the cache (strides in elements, between
+// the tokens of the flattened [batch * q_len] order).
+struct RopeParams {
+    void* q_out;              // [tokens, H, D] kv dtype
+    void* k_cache;
+    void* v_cache;
+    const void* q;            // [tokens, H, D]
+    const void* k_new;        // [tokens, Hkv, D]
+    const void* v_new;
+    const int32_t* positions; // [num_axes, tokens]
+    const int64_t* phases;    // [rotary_dim / 2] turns per position, times 2^64
+    const int32_t* axes;      // [rotary_dim / 2] axis of each pair
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int64_t num_blocks, q_stride, k_stride, v_stride, q_out_stride;
+    int32_t batch, q_len, num_heads, num_kv_heads, head_dim, block_size, max_blocks;
+    int32_t rotary_dim, num_axes, interleaved;
+    int32_t max_cta_tokens;   // tokens that one CTA's run of items can touch
+};
+
+// Eviction by accumulated weight.
+struct EvictParams {
+    void* k_cache;
+    void* v_cache;
+    const float* weights;     // [B, Hkv, max_blocks * block_size]
+    float* new_weights;       // [B, Hkv, new_max_blocks * block_size]
+    const int32_t* block_tables;
+    const int32_t* new_block_tables;
+    const int32_t* context_lens;
+    int32_t* new_lens;        // [B]
+    int32_t* kept;            // [B, Hkv, budget]
+    int64_t num_blocks;
+    int32_t batch, num_kv_heads, head_dim, block_size, max_blocks, new_max_blocks;
+    int32_t budget, sink, recent;
+};
+
 // Largest batch the balanced split handles (its per-sequence page counts live
 // in shared memory).
 constexpr int kMaxBalancedBatch = 512;
@@ -309,9 +345,20 @@ cudaError_t launch_append(void* k_cache, void* v_cache, const void* k_new, const
                           const int32_t* block_tables, const int32_t* positions, int32_t batch,
                           int32_t max_blocks, int32_t block_size, int64_t num_blocks,
                           int32_t row_bytes, bool pdl, cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeParams& p, bool bf16, int num_sms, bool pdl,
+                               cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams& p, bool in_place, bool pdl, cudaStream_t stream);
 cudaError_t launch_wait_timeout(int32_t* err, uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t launch_resolve(int32_t* out_phys, const int32_t* block_tables,
                            const int32_t* context_lens, int32_t batch, int32_t max_blocks,
                            int32_t block_size, int64_t num_blocks, cudaStream_t stream);
+
+// Host state and checks that every entry point shares (pa_api.cu).
+pa_status check_shape(const pa_shape* s);
+// SM count and error-word address of the current device (cached; either may be null).
+pa_status device_state(int* sms, int32_t** err);
+// Whether launches carry the programmatic stream serialization attribute.
+bool use_pdl();
+inline bool aligned(const void* ptr, size_t a) { return reinterpret_cast<uintptr_t>(ptr) % a == 0; }
 
 }  // namespace pa
