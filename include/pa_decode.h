@@ -300,6 +300,72 @@ pa_status pa_rope_append_kv(void* q_out, void* k_cache, void* v_cache, const voi
                             void* stream);
 
 /*
+ * Attention of sequences that share a prefix, whose pages are read once for
+ * all of them.  The batch's sequences fall into num_prefixes groups of equal
+ * size n = batch / num_prefixes, in order: sequence b has prefix b / n.  The
+ * softmax of a sequence's query tokens runs over its prefix's tokens and its
+ * own as over one sequence, prefix_lens[b / n] + context_lens[b] tokens long:
+ *   prefix_tables  [num_prefixes, max_prefix_blocks]  int32: the prefixes' pages
+ *   prefix_lens    [num_prefixes]  int32: any length; the last page may be partial
+ *   block_tables, context_lens: the sequences' own pages and lengths, which
+ *                  count the q_len query tokens (as in pa_decode_multi); own
+ *                  tokens start at slot 0 of the first own page
+ *   q, out         [batch, q_len, num_heads, head_dim]
+ * Query token i of sequence b attends to the whole prefix and to its own
+ * tokens t <= context_lens[b] - q_len + i; where a sequence is shorter than
+ * q_len its first query tokens stand for the prefix's last tokens and see no
+ * further than they would.  Masked entries, lengths past a table's reach and
+ * rows with no token as in pa_decode.
+ * The query rows of a prefix's sequences (n * q_len * group per kv head) go
+ * through the prefix's pages together, on the kernel that pa_decode_multi
+ * takes for as many rows; the sequences' own pages as in pa_decode_multi; a
+ * third launch joins the two by their softmax statistics.  max_prefix_len and
+ * max_context_len bound the lengths, as in pa_decode_splitkv; the workspace
+ * must hold pa_workspace_size_shared_prefix(...) bytes (device, 16-byte
+ * aligned, free again once the stream has passed the call).
+ */
+pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* prefix_tables,
+                                  const int32_t* prefix_lens, const int32_t* block_tables,
+                                  const int32_t* context_lens, const pa_shape* shape,
+                                  int32_t num_prefixes, int32_t max_prefix_blocks, int32_t q_len,
+                                  float scale, int32_t max_prefix_len, int32_t max_context_len,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of pa_decode_shared_prefix on the current device (0 for
+ * invalid arguments or without a device; SIZE_MAX when no size_t holds it). */
+size_t pa_workspace_size_shared_prefix(const pa_shape* shape, int32_t num_prefixes,
+                                       int32_t max_prefix_blocks, int32_t q_len,
+                                       int32_t max_prefix_len, int32_t max_context_len);
+
+/*
+ * pa_decode_multi (q_len = 1: pa_decode_splitkv) that also adds every cached
+ * token's attention weight to a running sum per kv head, from which
+ * pa_evict_kv chooses:
+ *   weights_out[b][kvh][t] = weights_in[b][kvh][t]
+ *                            + sum over the group's heads h and query tokens i of p[b][i][h][t]
+ * for t < min(context_lens[b], table reach), p the softmax weights of the
+ * call's attention (0 for tokens that a row does not attend to); entries from
+ * there on are not written.
+ *   weights_in, weights_out  [batch, num_kv_heads, max_blocks_per_seq * block_size]
+ *                            fp32; may be the same array, else apart
+ * Weights are fp32; each is summed over the rows by one thread quad in a fixed
+ * order, so that equal calls give equal bits.  The other arguments are those
+ * of pa_decode_multi with an automatic split; the workspace must hold
+ * pa_workspace_size_accumulate(...) bytes.
+ */
+pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weights_in,
+                               const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, const int32_t* context_lens,
+                               const pa_shape* shape, int32_t q_len, float scale,
+                               int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Workspace bytes of pa_decode_accumulate on the current device (0 for
+ * invalid arguments or without a device; SIZE_MAX when no size_t holds it). */
+size_t pa_workspace_size_accumulate(const pa_shape* shape, int32_t q_len, int32_t max_context_len);
+
+/*
  * Eviction from the cache by accumulated attention weight (the weights that
  * pa_decode_accumulate keeps).  Every kv head of a sequence keeps at most
  * `budget` of its min(context_lens[b], table reach) tokens: the first `sink`

@@ -17,6 +17,13 @@ or a call is rejected, an exception is raised.
     rope_phases(inv_freq)
     rope_append_kv(q_out, k_cache, v_cache, q, k_new, v_new, rotary_positions, phases, axes,
                    block_tables, context_lens, interleaved=False)
+    decode_shared_prefix(out, q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables,
+                         context_lens, scale, max_prefix_len, max_context_len, workspace=None)
+    workspace_size_shared_prefix(q, k_cache, prefix_tables, block_tables, out_dtype,
+                                 max_prefix_len, max_context_len)
+    decode_accumulate(out, new_weights, q, k_cache, v_cache, block_tables, context_lens, scale,
+                      max_context_len, weights=None, workspace=None)
+    workspace_size_accumulate(q, k_cache, block_tables, out_dtype, max_context_len)
     evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables,
              new_weights, new_lens, kept, sink=0, recent=0)
     workspace_size(q, k_cache, block_tables, out_dtype, max_context_len, partition_tokens=0)
@@ -40,7 +47,9 @@ import threading
 import torch
 
 __all__ = ["PaError", "decode", "decode_splitkv", "decode_splitkv_noalloc", "decode_multi",
-           "append_kv", "rope_phases", "rope_append_kv", "evict_kv", "workspace_size", "workspace_size_multi", "plan_info", "choose_partition_tokens",
+           "append_kv", "rope_phases", "rope_append_kv", "decode_shared_prefix",
+           "workspace_size_shared_prefix", "decode_accumulate", "workspace_size_accumulate",
+           "evict_kv", "workspace_size", "workspace_size_multi", "plan_info", "choose_partition_tokens",
            "resolve_blocks", "selftest_wait_timeout", "device_error", "library_path", "F16",
            "BF16", "F32", "PARTITION_BALANCED", "set_switch", "get_switch", "SWITCH_MULTI_KERNEL",
            "SWITCH_TILE_COMPACT_Q", "KERNEL_AUTO", "KERNEL_MMA", "KERNEL_TILE"]
@@ -118,6 +127,14 @@ def _load():
             lib.pa_append_kv.restype = ctypes.c_int
             lib.pa_rope_append_kv.argtypes = [P] * 11 + [S, i32, ctypes.POINTER(_Rope), P]
             lib.pa_rope_append_kv.restype = ctypes.c_int
+            lib.pa_decode_shared_prefix.argtypes = [P] * 8 + [S, i32, i32, i32, f32, i32, i32, P, sz, P]
+            lib.pa_decode_shared_prefix.restype = ctypes.c_int
+            lib.pa_workspace_size_shared_prefix.argtypes = [S, i32, i32, i32, i32, i32]
+            lib.pa_workspace_size_shared_prefix.restype = sz
+            lib.pa_decode_accumulate.argtypes = [P] * 8 + [S, i32, f32, i32, P, sz, P]
+            lib.pa_decode_accumulate.restype = ctypes.c_int
+            lib.pa_workspace_size_accumulate.argtypes = [S, i32, i32]
+            lib.pa_workspace_size_accumulate.restype = sz
             lib.pa_evict_kv.argtypes = [P] * 9 + [S, i32, i32, i32, i32, P]
             lib.pa_evict_kv.restype = ctypes.c_int
             lib.pa_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P]
@@ -468,6 +485,116 @@ def rope_append_kv(q_out, k_cache, v_cache, q, k_new, v_new, rotary_positions, p
             axes.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), ctypes.byref(shape),
             Q, ctypes.byref(rope), on.cuda_stream), "pa_rope_append_kv")
     return q_out
+
+
+def _any_shape(q, k_cache, block_tables, out_dtype):
+    """pa_shape and q_len of a one-token or a multi-token query."""
+    if q.dim() == 4:
+        return _multi_shape(q, k_cache, block_tables, out_dtype)
+    return make_shape(q, k_cache, block_tables, out_dtype), 1
+
+
+def _workspace(workspace, need, like, on):
+    """The caller's workspace, or one from torch's allocator on the launch's stream."""
+    if workspace is None:
+        if need > 1 << 62:
+            raise PaError(3, "workspace")
+        with torch.cuda.stream(on):
+            return torch.empty(max(int(need), 16), dtype=torch.uint8, device=like.device)
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != like.device:
+        raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
+    return workspace
+
+
+def _check_prefixes(prefix_tables, prefix_lens, batch):
+    if prefix_tables.dim() != 2 or prefix_tables.shape[0] < 1 or batch % prefix_tables.shape[0]:
+        raise ValueError("prefix_tables must be [prefixes, max_prefix_blocks], with as many "
+                         "sequences for each prefix")
+    if prefix_lens is not None and tuple(prefix_lens.shape) != (prefix_tables.shape[0],):
+        raise ValueError("prefix_lens must be [prefixes]")
+    if prefix_tables.dtype != torch.int32 or \
+            (prefix_lens is not None and prefix_lens.dtype != torch.int32):
+        raise TypeError("prefix_tables and prefix_lens must be int32")
+
+
+def workspace_size_shared_prefix(q, k_cache, prefix_tables, block_tables, out_dtype,
+                                 max_prefix_len: int, max_context_len: int) -> int:
+    """Bytes of workspace that ``decode_shared_prefix`` takes, on the tensors' device."""
+    shape, q_len = _any_shape(q, k_cache, block_tables, out_dtype)
+    _check_prefixes(prefix_tables, None, shape.batch)
+    _dev_tensors(q, k_cache)
+    with _launch_on(k_cache, None):
+        return int(_load().pa_workspace_size_shared_prefix(
+            ctypes.byref(shape), prefix_tables.shape[0], prefix_tables.shape[1], q_len,
+            int(max_prefix_len), int(max_context_len)))
+
+
+def decode_shared_prefix(out, q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables,
+                         context_lens, scale: float, max_prefix_len: int, max_context_len: int,
+                         workspace=None, stream=None):
+    """Attention of a batch over shared prefixes and each sequence's own pages,
+    as over one sequence.  q, out [B, H, D] or [B, Q, H, D]; prefix_tables int32
+    [P, max_prefix_blocks] and prefix_lens int32 [P], sequence b having prefix
+    b // (B // P); block_tables and context_lens are the sequences' own (the
+    lengths count the Q new tokens, causal among themselves).  ``workspace``: a
+    CUDA byte tensor of ``workspace_size_shared_prefix(...)`` bytes, else one
+    is taken from torch's allocator."""
+    _check_args(out, q, k_cache, v_cache, block_tables, context_lens, multi=q.dim() == 4)
+    shape, q_len = _any_shape(q, k_cache, block_tables, out.dtype)
+    _check_prefixes(prefix_tables, prefix_lens, shape.batch)
+    _dev_tensors(out, q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables, context_lens)
+    lib, (P, mpb) = _load(), prefix_tables.shape
+    with _launch_on(k_cache, stream) as on:
+        need = 0 if workspace is not None else lib.pa_workspace_size_shared_prefix(
+            ctypes.byref(shape), P, mpb, q_len, int(max_prefix_len), int(max_context_len))
+        ws = _workspace(workspace, need, k_cache, on)
+        _check(lib.pa_decode_shared_prefix(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            prefix_tables.data_ptr(), prefix_lens.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), ctypes.byref(shape), P, mpb, q_len, float(scale),
+            int(max_prefix_len), int(max_context_len), ws.data_ptr(),
+            ws.numel() * ws.element_size(), on.cuda_stream), "pa_decode_shared_prefix")
+    return out
+
+
+def workspace_size_accumulate(q, k_cache, block_tables, out_dtype, max_context_len: int) -> int:
+    """Bytes of workspace that ``decode_accumulate`` takes, on the tensors' device."""
+    shape, q_len = _any_shape(q, k_cache, block_tables, out_dtype)
+    _dev_tensors(q, k_cache)
+    with _launch_on(k_cache, None):
+        return int(_load().pa_workspace_size_accumulate(ctypes.byref(shape), q_len,
+                                                        int(max_context_len)))
+
+
+def decode_accumulate(out, new_weights, q, k_cache, v_cache, block_tables, context_lens,
+                      scale: float, max_context_len: int, weights=None, workspace=None,
+                      stream=None):
+    """``decode_splitkv`` (q [B, H, D]) or ``decode_multi`` (q [B, Q, H, D]) that also
+    adds every cached token's attention weight, summed over the kv head's
+    query heads and the query tokens: new_weights[b, kvh, t] = weights[b, kvh, t] +
+    sum p (fp32 [B, Hkv, max_blocks * block_size]; ``weights`` omitted: in place).
+    Entries past a sequence's tokens are not written."""
+    weights = new_weights if weights is None else weights
+    _check_args(out, q, k_cache, v_cache, block_tables, context_lens, multi=q.dim() == 4)
+    shape, q_len = _any_shape(q, k_cache, block_tables, out.dtype)
+    want = (shape.batch, shape.num_kv_heads, shape.max_blocks_per_seq * shape.block_size)
+    if tuple(weights.shape) != want or tuple(new_weights.shape) != want:
+        raise ValueError(f"weights and new_weights must be {want}")
+    if weights.dtype != torch.float32 or new_weights.dtype != torch.float32:
+        raise TypeError("weights and new_weights must be float32")
+    _dev_tensors(out, q, k_cache, v_cache, block_tables, context_lens, weights, new_weights)
+    lib = _load()
+    with _launch_on(k_cache, stream) as on:
+        need = 0 if workspace is not None else lib.pa_workspace_size_accumulate(
+            ctypes.byref(shape), q_len, int(max_context_len))
+        ws = _workspace(workspace, need, k_cache, on)
+        _check(lib.pa_decode_accumulate(
+            out.data_ptr(), new_weights.data_ptr(), weights.data_ptr(), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), ctypes.byref(shape), q_len, float(scale),
+            int(max_context_len), ws.data_ptr(), ws.numel() * ws.element_size(), on.cuda_stream),
+            "pa_decode_accumulate")
+    return out
 
 
 def evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables, new_weights,

@@ -256,6 +256,10 @@ struct Plan {
     bool tile;       // several query tokens on the tcgen05 tile kernel (128-row tiles)
     int tile_qr;     // tile kernel: Q rows staged in shared memory (128, or 16: compact)
     bool persistent; // tile kernel, one pass: num_ctas CTAs take the units in turn, whole
+    bool partials = false;              // leave (m, l, acc) in the workspace even of one partition
+    const int32_t* own_lens = nullptr;  // a shared prefix: see AttnParams
+    int32_t own_q = 0;
+    float* lse = nullptr;               // row statistics wanted: see AttnParams
 };
 
 Plan plan_with(const pa_shape* s, int pages, int pp, bool cluster_ok,
@@ -765,10 +769,13 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     p.nh = t.nh;
     p.ns = t.ns;
     p.out_dtype = s->out_dtype;
-    p.final_out = plan.num_parts <= 1 ? 1 : 0;
+    p.final_out = plan.num_parts <= 1 && !plan.partials ? 1 : 0;
     p.cluster_reduce = plan.cluster ? 1 : 0;
     p.balanced = plan.balanced ? 1 : 0;
     if (plan.balanced) p.final_out = 0;
+    p.own_lens = plan.own_lens;
+    p.own_q = plan.own_q;
+    p.lse = plan.lse;
     p.timeout_ns = kDefaultTimeoutNs;
     L.head_dim = s->head_dim;
     L.block_size = s->block_size;
@@ -822,8 +829,11 @@ pa_status launch_tile(void* out, const void* q, const void* k, const void* v, co
     p.part_pages = plan.part_pages;
     p.num_parts = plan.num_parts;
     p.out_dtype = s->out_dtype;
-    p.final_out = plan.num_parts <= 1 ? 1 : 0;
+    p.final_out = plan.num_parts <= 1 && !plan.partials ? 1 : 0;
     p.cluster_reduce = plan.cluster ? 1 : 0;
+    p.own_lens = plan.own_lens;
+    p.own_q = plan.own_q;
+    p.lse = plan.lse;
     p.timeout_ns = kDefaultTimeoutNs;
     L.head_dim = s->head_dim;
     L.block_size = s->block_size;
@@ -859,6 +869,143 @@ pa_status launch_tile(void* out, const void* q, const void* k, const void* v, co
         case 128: e = launch_tile_d128(L, stream); break;
         default: e = compact ? launch_tile_d256_compact(L, stream) : launch_tile_d256(L, stream); break;
     }
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// ---- attention with a shared prefix ----
+
+// The two attention launches and where their partials go.
+struct PrefixPlan {
+    pa_shape pre;      // the prefixes as sequences of n * q_len query tokens each
+    int32_t pre_q;     // n * q_len
+    Plan prefix, own;
+    size_t pre_ml, own_acc, own_ml, bytes;  // workspace offsets and size
+};
+
+pa_status check_prefix(const pa_shape* s, int32_t num_prefixes, int32_t max_prefix_blocks,
+                       int32_t q_len, int32_t max_prefix_len, int32_t max_context_len,
+                       pa_shape* pre) {
+    pa_status st = check_shape(s);
+    if (st != PA_OK) return st;
+    if (q_len < 1 || num_prefixes < 1 || s->batch % num_prefixes != 0 || max_prefix_blocks < 1 ||
+        max_prefix_len < 0 || max_context_len < 0)
+        return PA_ERR_INVALID_ARG;
+    *pre = *s;
+    pre->batch = num_prefixes;
+    pre->max_blocks_per_seq = max_prefix_blocks;
+    st = check_shape(pre);
+    if (st != PA_OK) return st;
+    // rows of a prefix and of a launch in 31 bits
+    const int64_t rows = (int64_t)(s->batch / num_prefixes) * q_len * s->num_heads;
+    return rows > 0x7fffffff ? PA_ERR_UNSUPPORTED : PA_OK;
+}
+
+pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
+                      int32_t max_prefix_len, int32_t max_context_len, int sms, PrefixPlan* pp) {
+    pp->pre = *pre;
+    pp->pre_q = s->batch / pre->batch * q_len;
+    // the library's own split of each part, its partials always left in the
+    // workspace for the join
+    auto split = [&](const pa_shape* sh, int32_t max_len, int32_t q) {
+        Plan p = make_plan(sh, max_len, 0, sms, q);
+        if (p.balanced) p = plan_with(sh, pages_for(sh, max_len), pages_for(sh, max_len), false);
+        p.cluster = p.persistent = false;
+        p.partials = true;
+        return p;
+    };
+    pp->prefix = split(&pp->pre, max_prefix_len, pp->pre_q);
+    pp->own = split(s, max_context_len, q_len);
+    size_t at = 0;
+    bool ok = true;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        ok = ok && n <= SIZE_MAX - 255 && !__builtin_add_overflow(at, (n + 255) / 256 * 256, &at);
+        return o;
+    };
+    auto rows = [&](const pa_shape* sh, int32_t q, const Plan& p) {
+        size_t r = (size_t)sh->batch;
+        ok = ok && !__builtin_mul_overflow(r, (size_t)sh->num_heads, &r) &&
+             !__builtin_mul_overflow(r, (size_t)q, &r) &&
+             !__builtin_mul_overflow(r, (size_t)p.num_parts, &r) &&
+             r <= SIZE_MAX / 4 / (size_t)sh->head_dim;
+        return ok ? r : 0;
+    };
+    const size_t rp = rows(&pp->pre, pp->pre_q, pp->prefix), ro = rows(s, q_len, pp->own);
+    (void)take(rp * s->head_dim * sizeof(float));
+    pp->pre_ml = take(rp * 2 * sizeof(float));
+    pp->own_acc = take(ro * s->head_dim * sizeof(float));
+    pp->own_ml = take(ro * 2 * sizeof(float));
+    pp->bytes = ok ? at : SIZE_MAX;
+    return PA_OK;
+}
+
+// ---- attention that accumulates the tokens' weights ----
+
+// Workspace: what pa_decode_multi takes, then the rows' statistics [B, Q, H].
+size_t accumulate_bytes(const pa_shape* s, const Plan& plan, int32_t q_len, size_t* lse_off) {
+    const size_t attn = workspace_bytes_for(s, plan, nullptr, q_len);
+    if (attn > SIZE_MAX / 2) return SIZE_MAX;
+    const size_t off = (attn + 255) / 256 * 256;
+    if (lse_off) *lse_off = off;
+    size_t rows = (size_t)s->batch;
+    if (__builtin_mul_overflow(rows, (size_t)s->num_heads * sizeof(float), &rows) ||
+        __builtin_mul_overflow(rows, (size_t)q_len, &rows) || rows > SIZE_MAX / 4)
+        return SIZE_MAX;
+    return off + rows;
+}
+
+// pa_decode_multi after its checks; lse: row statistics wanted (or null).
+pa_status run_multi(void* out, const void* q, const void* k_cache, const void* v_cache,
+                    const int32_t* block_tables, const int32_t* context_lens,
+                    const pa_shape* shape, int32_t q_len, float scale, int32_t max_context_len,
+                    int32_t partition_tokens, void* workspace, size_t workspace_bytes, float* lse,
+                    cudaStream_t cs) {
+    int sms = 0;
+    int32_t* err = nullptr;
+    pa_status st = device_state(&sms, &err);
+    if (st != PA_OK) return st;
+    Plan plan = make_plan(shape, max_context_len, partition_tokens, sms, q_len);
+    plan.lse = lse;
+    if (plan.tile && !plan.balanced && (plan.num_parts <= 1 || plan.cluster))
+        return launch_tile(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale, plan,
+                           nullptr, nullptr, err, cs, q_len);
+    if (!plan.tile && !plan.balanced && (plan.num_parts <= 1 || plan.cluster))
+        return launch_attention(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale,
+                                plan, nullptr, nullptr, err, cs, q_len);
+
+    size_t ml_off = 0;
+    const size_t need = workspace_bytes_for(shape, plan, &ml_off, q_len);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return PA_ERR_WORKSPACE;
+    if ((size_t)plan.num_parts * 2 * sizeof(float) > 200u * 1024u) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)q_len * shape->num_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    float* part_acc = static_cast<float*>(workspace);
+    float* part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_off);
+    st = plan.tile ? launch_tile(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale,
+                                 plan, part_acc, part_ml, err, cs, q_len)
+                   : launch_attention(out, q, k_cache, v_cache, block_tables, context_lens, shape,
+                                      scale, plan, part_acc, part_ml, err, cs, q_len);
+    if (st != PA_OK) return st;
+    CombineParams c;
+    c.out = out;
+    c.context_lens = context_lens;
+    c.part_acc = part_acc;
+    c.part_ml = part_ml;
+    c.batch = shape->batch;
+    c.num_heads = shape->num_heads;
+    c.num_kv_heads = shape->num_kv_heads;
+    c.group = shape->num_heads / shape->num_kv_heads;
+    c.max_blocks = shape->max_blocks_per_seq;
+    c.block_size = shape->block_size;
+    c.q_len = q_len;
+    c.part_pages = plan.part_pages;
+    c.num_parts = plan.num_parts;
+    c.out_dtype = shape->out_dtype;
+    c.num_ctas = plan.num_ctas;
+    c.lse = lse;
+    const dim3 cgrid((unsigned)(q_len * shape->num_heads), (unsigned)shape->batch);
+    const cudaError_t e = plan.balanced ? launch_combine_balanced(c, shape->head_dim, cgrid,
+                                                                  use_pdl(), cs)
+                                        : launch_combine(c, shape->head_dim, cgrid, use_pdl(), cs);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -948,52 +1095,9 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_cache, const v
     if (shape->batch == 0) return PA_OK;
     st = check_ptrs(out, q, k_cache, v_cache, block_tables, context_lens);
     if (st != PA_OK) return st;
-    int sms = 0;
-    int32_t* err = nullptr;
-    st = device_state(&sms, &err);
-    if (st != PA_OK) return st;
-    const Plan plan = make_plan(shape, max_context_len, partition_tokens, sms, q_len);
-    cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (plan.tile && !plan.balanced && (plan.num_parts <= 1 || plan.cluster))
-        return launch_tile(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale, plan,
-                           nullptr, nullptr, err, cs, q_len);
-    if (!plan.tile && !plan.balanced && (plan.num_parts <= 1 || plan.cluster))
-        return launch_attention(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale,
-                                plan, nullptr, nullptr, err, cs, q_len);
-
-    size_t ml_off = 0;
-    const size_t need = workspace_bytes_for(shape, plan, &ml_off, q_len);
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return PA_ERR_WORKSPACE;
-    if ((size_t)plan.num_parts * 2 * sizeof(float) > 200u * 1024u) return PA_ERR_UNSUPPORTED;
-    if ((int64_t)q_len * shape->num_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;
-    float* part_acc = static_cast<float*>(workspace);
-    float* part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_off);
-    st = plan.tile ? launch_tile(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale,
-                                 plan, part_acc, part_ml, err, cs, q_len)
-                   : launch_attention(out, q, k_cache, v_cache, block_tables, context_lens, shape,
-                                      scale, plan, part_acc, part_ml, err, cs, q_len);
-    if (st != PA_OK) return st;
-    CombineParams c;
-    c.out = out;
-    c.context_lens = context_lens;
-    c.part_acc = part_acc;
-    c.part_ml = part_ml;
-    c.batch = shape->batch;
-    c.num_heads = shape->num_heads;
-    c.num_kv_heads = shape->num_kv_heads;
-    c.group = shape->num_heads / shape->num_kv_heads;
-    c.max_blocks = shape->max_blocks_per_seq;
-    c.block_size = shape->block_size;
-    c.q_len = q_len;
-    c.part_pages = plan.part_pages;
-    c.num_parts = plan.num_parts;
-    c.out_dtype = shape->out_dtype;
-    c.num_ctas = plan.num_ctas;
-    const dim3 cgrid((unsigned)(q_len * shape->num_heads), (unsigned)shape->batch);
-    const cudaError_t e = plan.balanced ? launch_combine_balanced(c, shape->head_dim, cgrid,
-                                                                  use_pdl(), cs)
-                                        : launch_combine(c, shape->head_dim, cgrid, use_pdl(), cs);
-    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return run_multi(out, q, k_cache, v_cache, block_tables, context_lens, shape, q_len, scale,
+                     max_context_len, partition_tokens, workspace, workspace_bytes, nullptr,
+                     static_cast<cudaStream_t>(stream));
 }
 
 pa_status pa_decode_splitkv(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -1146,6 +1250,155 @@ pa_status pa_decode_splitkv_noalloc(void* out, const void* q, const void* k_cach
     return pa_decode_splitkv(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale,
                              max_context_len, partition_tokens, scratch, kNoAllocScratchBytes,
                              stream);
+}
+
+size_t pa_workspace_size_shared_prefix(const pa_shape* shape, int32_t num_prefixes,
+                                       int32_t max_prefix_blocks, int32_t q_len,
+                                       int32_t max_prefix_len, int32_t max_context_len) {
+    pa_shape pre;
+    if (check_prefix(shape, num_prefixes, max_prefix_blocks, q_len, max_prefix_len,
+                     max_context_len, &pre) != PA_OK || shape->batch == 0)
+        return 0;
+    int sms = 0;
+    if (device_state(&sms, nullptr) != PA_OK) return 0;
+    PrefixPlan pp;
+    (void)plan_prefix(shape, &pre, q_len, max_prefix_len, max_context_len, sms, &pp);
+    return pp.bytes;
+}
+
+pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* prefix_tables,
+                                  const int32_t* prefix_lens, const int32_t* block_tables,
+                                  const int32_t* context_lens, const pa_shape* shape,
+                                  int32_t num_prefixes, int32_t max_prefix_blocks, int32_t q_len,
+                                  float scale, int32_t max_prefix_len, int32_t max_context_len,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    pa_shape pre;
+    pa_status st = check_prefix(shape, num_prefixes, max_prefix_blocks, q_len, max_prefix_len,
+                                max_context_len, &pre);
+    if (st != PA_OK) return st;
+    if (!scale_ok(scale)) return PA_ERR_INVALID_ARG;
+    if (shape->batch == 0) return PA_OK;
+    st = check_ptrs(out, q, k_cache, v_cache, block_tables, context_lens);
+    if (st != PA_OK) return st;
+    if (!prefix_tables || !prefix_lens || !aligned(prefix_tables, 4) || !aligned(prefix_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    int sms = 0;
+    int32_t* err = nullptr;
+    st = device_state(&sms, &err);
+    if (st != PA_OK) return st;
+    PrefixPlan pp;
+    st = plan_prefix(shape, &pre, q_len, max_prefix_len, max_context_len, sms, &pp);
+    if (st != PA_OK) return st;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < pp.bytes) return PA_ERR_WORKSPACE;
+    if ((int64_t)pp.prefix.num_parts + pp.own.num_parts > 8192) return PA_ERR_UNSUPPORTED;
+    char* ws = static_cast<char*>(workspace);
+    auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    pp.prefix.own_lens = context_lens;
+    pp.prefix.own_q = q_len;
+    auto attend = [&](const int32_t* bt, const int32_t* lens, const pa_shape* s, int32_t ql,
+                      const Plan& plan, float* acc, float* ml) {
+        return plan.tile ? launch_tile(out, q, k_cache, v_cache, bt, lens, s, scale, plan, acc, ml,
+                                       err, cs, ql)
+                         : launch_attention(out, q, k_cache, v_cache, bt, lens, s, scale, plan, acc,
+                                            ml, err, cs, ql);
+    };
+    st = attend(prefix_tables, prefix_lens, &pp.pre, pp.pre_q, pp.prefix, f(0), f(pp.pre_ml));
+    if (st != PA_OK) return st;
+    st = attend(block_tables, context_lens, shape, q_len, pp.own, f(pp.own_acc), f(pp.own_ml));
+    if (st != PA_OK) return st;
+    PrefixCombineParams c;
+    c.out = out;
+    c.prefix_lens = prefix_lens;
+    c.context_lens = context_lens;
+    c.prefix_acc = f(0);
+    c.prefix_ml = f(pp.pre_ml);
+    c.own_acc = f(pp.own_acc);
+    c.own_ml = f(pp.own_ml);
+    c.num_heads = shape->num_heads;
+    c.num_kv_heads = shape->num_kv_heads;
+    c.group = shape->num_heads / shape->num_kv_heads;
+    c.block_size = shape->block_size;
+    c.q_len = q_len;
+    c.per_prefix = shape->batch / num_prefixes;
+    c.max_prefix_blocks = max_prefix_blocks;
+    c.max_blocks = shape->max_blocks_per_seq;
+    c.prefix_parts = pp.prefix.num_parts;
+    c.prefix_part_pages = pp.prefix.part_pages;
+    c.own_parts = pp.own.num_parts;
+    c.own_part_pages = pp.own.part_pages;
+    c.out_dtype = shape->out_dtype;
+    return launch_prefix_combine(c, shape->head_dim, shape->batch, use_pdl(), cs) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+size_t pa_workspace_size_accumulate(const pa_shape* shape, int32_t q_len, int32_t max_context_len) {
+    if (check_shape(shape) != PA_OK || max_context_len < 0 || q_len < 1) return 0;
+    int sms = 0;
+    if (device_state(&sms, nullptr) != PA_OK) return 0;
+    return accumulate_bytes(shape, make_plan(shape, max_context_len, 0, sms, q_len), q_len, nullptr);
+}
+
+pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weights_in,
+                               const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, const int32_t* context_lens,
+                               const pa_shape* shape, int32_t q_len, float scale,
+                               int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    pa_status st = check_shape(shape);
+    if (st != PA_OK) return st;
+    if (q_len < 1 || !scale_ok(scale) || max_context_len < 0) return PA_ERR_INVALID_ARG;
+    if ((int64_t)q_len * shape->num_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    if (shape->batch == 0) return PA_OK;
+    st = check_ptrs(out, q, k_cache, v_cache, block_tables, context_lens);
+    if (st != PA_OK) return st;
+    if (!weights_out || !weights_in || !aligned(weights_out, 4) || !aligned(weights_in, 4))
+        return PA_ERR_INVALID_ARG;
+    const size_t w_bytes = (size_t)shape->batch * shape->num_kv_heads *
+                           ((size_t)shape->max_blocks_per_seq * shape->block_size) * sizeof(float);
+    const uintptr_t w_out = reinterpret_cast<uintptr_t>(weights_out);
+    const uintptr_t w_in = reinterpret_cast<uintptr_t>(weights_in);
+    if (w_out != w_in && w_out < w_in + w_bytes && w_in < w_out + w_bytes) return PA_ERR_INVALID_ARG;
+    int sms = 0;
+    st = device_state(&sms, nullptr);
+    if (st != PA_OK) return st;
+    const Plan plan = make_plan(shape, max_context_len, 0, sms, q_len);
+    size_t lse_off = 0;
+    const size_t need = accumulate_bytes(shape, plan, q_len, &lse_off);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return PA_ERR_WORKSPACE;
+    float* lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + lse_off);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    st = run_multi(out, q, k_cache, v_cache, block_tables, context_lens, shape, q_len, scale,
+                   max_context_len, 0, workspace, lse_off, lse, cs);
+    if (st != PA_OK) return st;
+    WeightParams w;
+    w.q = q;
+    w.k_cache = k_cache;
+    w.weights_in = weights_in;
+    w.weights_out = weights_out;
+    w.lse = lse;
+    w.block_tables = block_tables;
+    w.context_lens = context_lens;
+    w.num_blocks = shape->num_blocks;
+    w.qscale = scale * 1.4426950408889634f;
+    w.batch = shape->batch;
+    w.q_len = q_len;
+    w.num_heads = shape->num_heads;
+    w.num_kv_heads = shape->num_kv_heads;
+    w.group = shape->num_heads / shape->num_kv_heads;
+    w.block_size = shape->block_size;
+    w.max_blocks = shape->max_blocks_per_seq;
+    // a split covers max_context_len, one pass everything the table reaches
+    const int64_t covered = (int64_t)plan.num_parts * plan.part_pages * shape->block_size;
+    w.token_limit = plan.num_parts <= 1 || plan.balanced || covered > 0x7fffffff ? 0x7fffffff
+                                                                                 : (int32_t)covered;
+    return launch_weights(w, shape->head_dim, shape->kv_dtype,
+                          pages_for(shape, max_context_len) * shape->block_size, use_pdl(),
+                          cs) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -238,9 +238,15 @@ __global__ void __launch_bounds__(256, 1)
         // the table's reach (with one query token, every row attends T).
         int lim0 = T, lim1 = T;
         if constexpr (MULTI) {
-            const int ctx = max(__ldg(p.context_lens + b), 0);
-            lim0 = min(T, ctx - Q + qi0 + (g >> gshift) + 1);
-            lim1 = min(T, ctx - Q + qi0 + ((g + 8) >> gshift) + 1);
+            if (p.own_lens) {
+                if (real0) lim0 = prefix_limit(T, b, qi0 + (g >> gshift), Q, p.own_q, p.own_lens);
+                if (real1)
+                    lim1 = prefix_limit(T, b, qi0 + ((g + 8) >> gshift), Q, p.own_q, p.own_lens);
+            } else {
+                const int ctx = max(__ldg(p.context_lens + b), 0);
+                lim0 = min(T, ctx - Q + qi0 + (g >> gshift) + 1);
+                lim1 = min(T, ctx - Q + qi0 + ((g + 8) >> gshift) + 1);
+            }
         }
 
         // Running state of rows g and g+8 (padded rows stay at m = 0, p = 0).
@@ -473,6 +479,7 @@ __global__ void __launch_bounds__(256, 1)
         return [&, b, kvh](int idx, float A, float M, float Ls) {
             store_out(p.out, row_off(b, kvh, idx / D) + idx % D, Ls > 0.f ? A / Ls : 0.f,
                       p.out_dtype);
+            if (p.lse && idx % D == 0) p.lse[row_off(b, kvh, idx / D) / D] = row_lse(M, Ls);
         };
     };
     // (m, l, acc) of the CTA's rows into workspace row `row0 + r`.
@@ -580,6 +587,7 @@ __global__ void __launch_bounds__(256, 1)
         if (p.final_out) {
             for (int idx = tid; idx < R * D; idx += blockDim.x)
                 store_out(p.out, row_off(b, kvh, idx / D) + idx % D, 0.f, p.out_dtype);
+            if (p.lse && tid < R) p.lse[row_off(b, kvh, tid) / D] = INFINITY;
         }
         return;
     }
@@ -646,6 +654,7 @@ __global__ void __launch_bounds__(256, 1)
                 }
                 store_out(p.out, row_off(b, kvh, r) + idx % D, Ls > 0.f ? A / Ls : 0.f,
                           p.out_dtype);
+                if (p.lse && idx % D == 0) p.lse[row_off(b, kvh, r) / D] = row_lse(M, Ls);
             }
         };
         if (P <= kMaxClusterParts)

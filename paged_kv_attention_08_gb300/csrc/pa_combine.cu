@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
         }
         const float inv = empty ? 0.f : 1.f / ls;
         const size_t o = (((size_t)b * p.q_len + qi) * p.num_heads + h) * D + sl * 4;
+        if (p.lse && sl == 0) p.lse[o / D] = empty ? INFINITY : row_lse(mx, ls);
         store_out(p.out, o, a.x * inv, p.out_dtype);
         store_out(p.out, o + 1, a.y * inv, p.out_dtype);
         store_out(p.out, o + 2, a.z * inv, p.out_dtype);
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_balanced_kernel(const
     const size_t o = (((size_t)b * p.q_len + qi) * p.num_heads + h) * D;
     if (np == 0) {  // no page, no CTA: the empty-context result
         for (int d = tid; d < D; d += kCombineThreads) store_out(p.out, o + d, 0.f, p.out_dtype);
+        if (p.lse && tid == 0) p.lse[o / D] = INFINITY;
         return;
     }
     const long long Cn = p.num_ctas;
@@ -233,10 +235,110 @@ __global__ void __launch_bounds__(kCombineThreads) combine_balanced_kernel(const
             a.w += x.w;
         }
         const float inv = empty ? 0.f : 1.f / ls;
+        if (p.lse && sl == 0) p.lse[o / D] = empty ? INFINITY : row_lse(mx, ls);
         store_out(p.out, o + sl * 4, a.x * inv, p.out_dtype);
         store_out(p.out, o + sl * 4 + 1, a.y * inv, p.out_dtype);
         store_out(p.out, o + sl * 4 + 2, a.z * inv, p.out_dtype);
         store_out(p.out, o + sl * 4 + 3, a.w * inv, p.out_dtype);
+    }
+}
+
+// Joining a shared prefix with the sequences' own tokens: a query row has
+// partials (m, l, acc) of the prefix's partitions, in the prefix's rows (its
+// n sequences' query tokens in order), and of its own sequence's.  With x over
+// both, out = sum_x 2^(m_x - M) acc_x / sum_x 2^(m_x - M) l_x: the softmax over
+// the tokens of prefix and sequence as one.  One CTA per row, as in
+// combine_kernel; partitions past the tokens are never read.
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) prefix_combine_kernel(const PrefixCombineParams p) {
+    constexpr int SLICES = D / 4;
+    constexpr int PGRP = kCombineThreads / SLICES;
+    constexpr float NEG_INF = -INFINITY;
+    extern __shared__ float weight[];                  // [prefix_parts + own_parts]
+    __shared__ float red[kCombineThreads / 32];
+    __shared__ float4 part[PGRP][SLICES];
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = (int)blockIdx.x % p.num_heads, qi = (int)blockIdx.x / p.num_heads;
+    const int b = blockIdx.y, pre = b / p.per_prefix;
+    const int kvh = h / p.group, hg = h % p.group;
+    const int own_rows = p.q_len * p.group, pre_rows = p.per_prefix * own_rows;
+    const int Tp = reachable_tokens(p.prefix_lens, pre, p.max_prefix_blocks, p.block_size);
+    const int To = reachable_tokens(p.context_lens, b, p.max_blocks, p.block_size);
+    const int np_pages = (Tp + p.block_size - 1) / p.block_size;
+    const int no_pages = (To + p.block_size - 1) / p.block_size;
+    const int np = min((np_pages + p.prefix_part_pages - 1) / p.prefix_part_pages, p.prefix_parts);
+    const int no = min((no_pages + p.own_part_pages - 1) / p.own_part_pages, p.own_parts);
+    // rows of partition q of the prefix, and of the sequence
+    const size_t rp = ((size_t)pre * p.num_kv_heads + kvh) * p.prefix_parts * pre_rows +
+                      ((b - pre * p.per_prefix) * p.q_len + qi) * p.group + hg;
+    const size_t ro = ((size_t)b * p.num_kv_heads + kvh) * p.own_parts * own_rows + qi * p.group + hg;
+    auto ml = [&](int q) {
+        return q < np ? reinterpret_cast<const float2*>(p.prefix_ml)[rp + (size_t)q * pre_rows]
+                      : reinterpret_cast<const float2*>(p.own_ml)[ro + (size_t)(q - np) * own_rows];
+    };
+    const int parts = np + no;
+
+    float mx = NEG_INF;
+    for (int q = tid; q < parts; q += kCombineThreads) mx = fmaxf(mx, ml(q).x);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, m));
+    if (lane == 0) red[warp] = mx;
+    __syncthreads();
+    mx = red[0];
+#pragma unroll
+    for (int w = 1; w < kCombineThreads / 32; ++w) mx = fmaxf(mx, red[w]);
+    __syncthreads();
+    float ls = 0.f;
+    for (int q = tid; q < parts; q += kCombineThreads) {
+        const float2 v = ml(q);
+        const float w = (v.x == NEG_INF) ? 0.f : exp2f(v.x - mx);
+        weight[q] = w;
+        ls = fmaf(w, v.y, ls);
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) ls += __shfl_xor_sync(kFullMask, ls, m);
+    if (lane == 0) red[warp] = ls;
+    __syncthreads();  // also publishes `weight`
+    ls = 0.f;
+#pragma unroll
+    for (int w = 0; w < kCombineThreads / 32; ++w) ls += red[w];
+
+    const bool empty = (mx == NEG_INF) || !(ls > 0.f);
+    const int pg = tid / SLICES, sl = tid % SLICES;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!empty) {
+#pragma unroll 4
+        for (int q = pg; q < parts; q += PGRP) {
+            const float w = weight[q];
+            const float4 x =
+                q < np ? reinterpret_cast<const float4*>(p.prefix_acc + (rp + (size_t)q * pre_rows) * D)[sl]
+                       : reinterpret_cast<const float4*>(
+                             p.own_acc + (ro + (size_t)(q - np) * own_rows) * D)[sl];
+            a.x = fmaf(w, x.x, a.x);
+            a.y = fmaf(w, x.y, a.y);
+            a.z = fmaf(w, x.z, a.z);
+            a.w = fmaf(w, x.w, a.w);
+        }
+    }
+    part[pg][sl] = a;
+    __syncthreads();
+    if (pg == 0) {
+        for (int k = 1; k < PGRP; ++k) {
+            const float4 x = part[k][sl];
+            a.x += x.x;
+            a.y += x.y;
+            a.z += x.z;
+            a.w += x.w;
+        }
+        const float inv = empty ? 0.f : 1.f / ls;
+        const size_t o = (((size_t)b * p.q_len + qi) * p.num_heads + h) * D + sl * 4;
+        store_out(p.out, o, a.x * inv, p.out_dtype);
+        store_out(p.out, o + 1, a.y * inv, p.out_dtype);
+        store_out(p.out, o + 2, a.z * inv, p.out_dtype);
+        store_out(p.out, o + 3, a.w * inv, p.out_dtype);
     }
 }
 
@@ -339,6 +441,27 @@ cudaError_t launch_combine_balanced(const CombineParams& p, int head_dim, dim3 g
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kCombineThreads);
     cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+cudaError_t launch_prefix_combine(const PrefixCombineParams& p, int head_dim, int batch, bool pdl,
+                                  cudaStream_t stream) {
+    void (*kern)(const PrefixCombineParams);
+    switch (head_dim) {
+        case 64: kern = prefix_combine_kernel<64>; break;
+        case 128: kern = prefix_combine_kernel<128>; break;
+        default: kern = prefix_combine_kernel<256>; break;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.q_len * p.num_heads), (unsigned)batch);
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.dynamicSmemBytes = (size_t)(p.prefix_parts + p.own_parts) * sizeof(float);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -36,6 +36,22 @@ __device__ __forceinline__ int page_phys(const int32_t* table_row, int j, int np
     return (e >= 0 && (int64_t)e < num_blocks) ? e : -1;
 }
 
+// Tokens of a shared prefix of T reachable tokens that query token x of its
+// q_len / own_q sequences attends to: all of them, unless the sequence is
+// shorter than its own_q query tokens, whose first then stand for the
+// prefix's last tokens.
+__device__ __forceinline__ int prefix_limit(int T, int prefix, int x, int q_len, int own_q,
+                                            const int32_t* own_lens) {
+    const int s = x / own_q, i = x - s * own_q;
+    const int own = max(__ldg(own_lens + prefix * (q_len / own_q) + s), 0);
+    return T + min(0, own - own_q + i + 1);
+}
+
+// m + log2 l of a row; +inf (no weight on any token) for an empty one.
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l > 0.f ? m + log2f(l) : INFINITY;
+}
+
 // ---------------------------------------------------------------------------
 // mbarrier / TMA
 // ---------------------------------------------------------------------------

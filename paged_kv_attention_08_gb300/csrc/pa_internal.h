@@ -27,6 +27,12 @@ struct AttnParams {
     int32_t q_chunk;          // query tokens per CTA (q_chunk * group <= 16 MMA rows);
                               // gridDim.y = num_kv_heads * ceil(Q / q_chunk)
     int32_t unit_rows;        // Q * group: workspace rows of one (sequence, kv head, partition)
+    // A shared prefix in place of a sequence (null otherwise): its q_len query
+    // tokens are those of q_len / own_q sequences, whose own tokens follow the
+    // prefix.  Each sees the whole prefix, but for padding (see prefix_limit).
+    const int32_t* own_lens;
+    int32_t own_q;
+    float* lse;               // [B, Q, H] or null: m + log2 l of each row (+inf for an empty one)
     int64_t num_blocks;
     float qscale;             // scale * log2(e): scores are kept in base-2 units
     int32_t part_pages;       // pages per partition
@@ -56,6 +62,38 @@ struct CombineParams {
     int32_t q_len;     // query tokens per sequence; gridDim.x = q_len * num_heads
     int32_t part_pages, num_parts, out_dtype;
     int32_t num_ctas;  // balanced split: CTAs of the attention kernel (records [C][2][G])
+    float* lse;        // [B, Q, H] or null, as in AttnParams
+};
+
+// Joining the partials of a shared prefix and of the sequences' own tokens.
+struct PrefixCombineParams {
+    void* out;
+    const int32_t* prefix_lens;   // [num_prefixes]
+    const int32_t* context_lens;  // [B]
+    const float* prefix_acc;      // [num_prefixes, Hkv, prefix_parts, n * Q * G, D]
+    const float* prefix_ml;
+    const float* own_acc;         // [B, Hkv, own_parts, Q * G, D]
+    const float* own_ml;
+    int32_t num_heads, num_kv_heads, group, block_size, q_len;
+    int32_t per_prefix;           // n: sequences that share a prefix
+    int32_t max_prefix_blocks, max_blocks;
+    int32_t prefix_parts, prefix_part_pages, own_parts, own_part_pages;
+    int32_t out_dtype;
+};
+
+// Adding each token's attention weight to its running sum.
+struct WeightParams {
+    const void* q;            // [B, Q, H, D]
+    const void* k_cache;
+    const float* weights_in;  // [B, Hkv, max_blocks * block_size]
+    float* weights_out;
+    const float* lse;         // [B, Q, H], log2 units
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int64_t num_blocks;
+    float qscale;             // scale * log2(e)
+    int32_t batch, q_len, num_heads, num_kv_heads, group, block_size, max_blocks;
+    int32_t token_limit;      // tokens from here on were not attended
 };
 
 // Rotary positions and the append to the cache (strides in elements, between
@@ -341,6 +379,10 @@ cudaError_t launch_combine(const CombineParams& p, int head_dim, dim3 grid, bool
                            cudaStream_t stream);
 cudaError_t launch_combine_balanced(const CombineParams& p, int head_dim, dim3 grid, bool pdl,
                                     cudaStream_t stream);
+cudaError_t launch_prefix_combine(const PrefixCombineParams& p, int head_dim, int batch, bool pdl,
+                                  cudaStream_t stream);
+cudaError_t launch_weights(const WeightParams& p, int head_dim, int kv_dtype, int max_tokens,
+                           bool pdl, cudaStream_t stream);
 cudaError_t launch_append(void* k_cache, void* v_cache, const void* k_new, const void* v_new,
                           const int32_t* block_tables, const int32_t* positions, int32_t batch,
                           int32_t max_blocks, int32_t block_size, int64_t num_blocks,

@@ -330,6 +330,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
 #pragma unroll
             for (int q = 0; q < kMaxClusterParts; ++q) cl_w[t * 8 + q] = w[q] * inv;
+            if (p.lse && seg0.tile * kTileRows + r < U)
+                p.lse[row_off(seg0.b, seg0.kvh, seg0.tile * kTileRows + r) / D] = row_lse(M, Ls);
         }
         __syncthreads();
         for (int idx = tid; idx < (r1 - r0) * (D / 4); idx += kTileThreads) {
@@ -374,6 +376,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int idx = tid; idx < kTileRows * D; idx += kTileThreads) {
                 const int u = seg0.tile * kTileRows + idx / D;
                 if (u < U) store_out(p.out, row_off(seg0.b, seg0.kvh, u) + idx % D, 0.f, p.out_dtype);
+                if (p.lse && u < U && idx % D == 0) p.lse[row_off(seg0.b, seg0.kvh, u) / D] = INFINITY;
             }
         }
         return;
@@ -722,6 +725,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int idx = sr; idx < kTileRows * D; idx += 256) {
                     const int uu = g.tile * kTileRows + idx / D;
                     if (uu < U) store_out(p.out, row_off(g.b, g.kvh, uu) + idx % D, 0.f, p.out_dtype);
+                    if (p.lse && uu < U && idx % D == 0) p.lse[row_off(g.b, g.kvh, uu) / D] = INFINITY;
                 }
             }
         }
@@ -736,7 +740,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int tend = min(g.T, g.pe * BS);  // tokens of this segment end here
             const int ctx = max(__ldg(p.context_lens + g.b), 0);
             // tokens t < lim: the row's causal limit, the table's reach, the segment's end
-            const int lim = u < U ? min(tend, ctx - Q + (u >> gshift) + 1) : 0;
+            const int lim =
+                u >= U ? 0
+                       : min(tend, p.own_lens ? prefix_limit(g.T, g.b, u >> gshift, Q, p.own_q, p.own_lens)
+                                              : ctx - Q + (u >> gshift) + 1);
             const int32_t* table_row = p.block_tables + (size_t)g.b * p.max_blocks;
             // which pages of the segment's block k hold data: bit q for page q
             // (read from the table here; the K stage's record may already
@@ -958,6 +965,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         orow = (((size_t)blockIdx.x * 2 + (s == 0 ? 0 : 1)) * U + u) * D;
                     else
                         orow = ((((size_t)g.b * Hkv + g.kvh) * p.num_parts + part) * U + u) * D;
+                    if (fin && p.lse && wg == 0) p.lse[orow / D] = row_lse(m, l);
                     if (!fin && wg == 0) {
                         p.part_ml[(orow / D) * 2] = l > 0.f ? m : NEG_INF;
                         p.part_ml[(orow / D) * 2 + 1] = l;

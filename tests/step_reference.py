@@ -150,3 +150,36 @@ def shared_prefix(q, k_cache, v_cache, prefix_tables, prefix_lens, table, lens, 
             p = _softmax(x, torch.cat([tp, plen + ts]) < end[:, None])
             out[b, :, h * G:(h + 1) * G] = (p @ torch.cat([vp, vs])).reshape(Q, G, D)
     return out
+
+
+def score_error(q, k_cache, scale):
+    """Bound on the error, in log2 units, of one score formed from these 16-bit
+    values in fp32: exact products, D sums and two scalings of 2^-23 each, of
+    terms of at most |q| |k| in all."""
+    D = q.shape[-1]
+    biggest = q.double().norm(dim=-1).max() * torch.nan_to_num(k_cache.double()).norm(dim=-1).max()
+    return (D + 4) * 2.0 ** -23 * biggest.item() * scale * 1.4427
+
+
+def weight_slack(q, k_cache, scale, tokens):
+    """Relative error of one softmax weight 2^(s - m) / l: the score's and the
+    normaliser's scores' errors (times ln 2), the normaliser's sum over the
+    tokens, and the exponentials (2^-22 each, of the weight and of l)."""
+    return 2 * 0.6932 * score_error(q, k_cache, scale) + (tokens + 8) * 2.0 ** -23
+
+
+def out_slack(q, k_cache, v_cache, scale, tokens):
+    """Absolute error of an attention output before its own rounding: every
+    weight's relative error, twice (numerator and normaliser), of the largest
+    value; the weights' own rounding on the way into the second product: fp16
+    once (2^-11), bf16 as a high and a low part (2^-16)."""
+    rounding = 2.0 ** -11 if q.dtype == torch.float16 else 2.0 ** -16
+    return (2 * weight_slack(q, k_cache, scale, tokens) + 2 * rounding) * \
+        torch.nan_to_num(v_cache.double()).abs().max().item()
+
+
+def close_out(got, want, slack):
+    assert torch.isfinite(got).all(), "non-finite output"
+    half = torch.finfo(got.dtype).eps / 2
+    err = (got.double() - want).abs() - half * want.abs() - slack
+    assert err.max().item() <= 0, f"{err.max().item():.3e} over the bound, slack {slack:.3e}"

@@ -1,0 +1,149 @@
+"""GPU tests of pa.decode_shared_prefix against the 64-bit definition: the
+softmax over a sequence's prefix and own tokens as one (the bound is derived
+in step_reference)."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_attention_08_gb300 as pa
+import step_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def case(seed, n, Q, H, Hkv, D, bs, plens, lens, dtype):
+    B = n * len(plens)
+    assert len(lens) == B
+    ptable, first = ref.tables(plens, bs, seed)
+    table, pool = ref.tables(lens, bs, seed + 1, first=first)
+    return dict(q=ref.normal((B, Q, H, D), dtype, seed + 2),
+                k_cache=ref.normal((pool, bs, Hkv, D), dtype, seed + 3),
+                v_cache=ref.normal((pool, bs, Hkv, D), dtype, seed + 4), ptable=ptable,
+                plens=torch.tensor(plens, dtype=torch.int32), table=table,
+                lens=torch.tensor(lens, dtype=torch.int32))
+
+
+def run(c, scale, out_dtype=None, max_p=None, max_own=None, stream=None, own_workspace=True):
+    d = {k: v.to(DEV) for k, v in c.items()}
+    out = torch.full(c["q"].shape, float("nan"), dtype=out_dtype or c["q"].dtype, device=DEV)
+    mp = max_p if max_p is not None else max(0, int(c["plens"].max()))
+    mo = max_own if max_own is not None else max(0, int(c["lens"].max()))
+    ws = None
+    if own_workspace:
+        need = pa.workspace_size_shared_prefix(d["q"], d["k_cache"], d["ptable"], d["table"],
+                                               out.dtype, mp, mo)
+        ws = torch.full((need // 4 + 1,), float("nan"), device=DEV)
+    torch.cuda.synchronize()
+    pa.decode_shared_prefix(out, d["q"], d["k_cache"], d["v_cache"], d["ptable"], d["plens"],
+                            d["table"], d["lens"], scale, mp, mo, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    return out.cpu()
+
+
+def check(c, scale=None, **kw):
+    scale = scale or 1 / math.sqrt(c["q"].shape[-1])
+    want = ref.shared_prefix(c["q"], c["k_cache"], c["v_cache"], c["ptable"], c["plens"],
+                             c["table"], c["lens"], scale)
+    tokens = c["ptable"].shape[1] * c["k_cache"].shape[1] + c["table"].shape[1] * c["k_cache"].shape[1]
+    ref.close_out(run(c, scale, **kw), want,
+                  ref.out_slack(c["q"], c["k_cache"], c["v_cache"], scale, tokens))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n,Q,H,Hkv,D,bs,plens,lens", [
+    (1, 1, 1, 1, 64, 16, [1], [1]),
+    (1, 1, 4, 2, 128, 16, [100], [30]),
+    (3, 1, 8, 2, 128, 16, [77], [1, 50, 16]),          # up to 16 rows: the warp-level kernel
+    (8, 1, 8, 2, 128, 16, [1000], [5 * b + 1 for b in range(8)]),
+    (40, 1, 32, 8, 128, 16, [333], [b % 7 + 1 for b in range(40)]),   # two row tiles
+    (2, 1, 16, 1, 256, 32, [500], [33, 64]),
+    (1, 1, 16, 1, 256, 16, [500], [100]),              # a compact tile
+    (5, 2, 4, 4, 64, 32, [65, 64, 1, 300], [2 + b for b in range(20)]),
+    (3, 4, 16, 2, 256, 16, [40, 129], [4, 9, 30, 4, 100, 5]),
+    (2, 70, 8, 2, 128, 16, [200], [70, 90]),
+])
+def test_matches_definition(n, Q, H, Hkv, D, bs, plens, lens, dtype):
+    check(case(n * 100 + Q, n, Q, H, Hkv, D, bs, plens, lens, dtype))
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_output_types(out_dtype):
+    check(case(31, 6, 1, 8, 2, 128, 16, [400], [10 * b + 1 for b in range(6)], torch.bfloat16),
+          out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("Q", [1, 3, 12])
+def test_empty_prefixes_empty_sequences_and_padding(Q):
+    lens = [Q, 0, max(0, Q - 2), -4, 50, Q + 1, 0, 1]
+    c = case(32 + Q, 4, Q, 8, 2, 128, 16, [0, 45], [max(t, 0) for t in lens], torch.bfloat16)
+    c["lens"] = torch.tensor(lens, dtype=torch.int32)
+    check(c)
+    c["plens"][1] = -2
+    check(c, max_p=45)
+
+
+@pytest.mark.parametrize("n", [2, 20])
+def test_masked_pages_and_nan_in_unread_places(n):
+    c = case(40 + n, n, 1, 8, 2, 128, 16, [150], [40 + b for b in range(n)], torch.bfloat16)
+    c["ptable"][0, 3] = -1
+    c["ptable"][0, 9] = c["k_cache"].shape[0] + 5
+    c["table"][0, 1] = -1
+    c["table"][1, :] = -1
+    used = torch.cat([c["ptable"].flatten(), c["table"].flatten()])
+    dead = torch.ones(c["k_cache"].shape[0], dtype=torch.bool)
+    dead[used[(used >= 0) & (used < len(dead))].unique().long()] = False
+    c["plens"][0] = 135                        # ends inside page 8
+    for cache in (c["k_cache"], c["v_cache"]):
+        cache[dead] = float("nan")
+        cache[int(c["ptable"][0, 8]), 7:] = float("nan")
+    check(c, max_p=150)
+
+
+def test_lengths_past_the_tables():
+    c = case(51, 5, 1, 8, 2, 64, 16, [64], [32] * 5, torch.float16)
+    c["plens"][0], c["lens"][2] = 1 << 30, 1 << 30
+    check(c, max_p=64, max_own=32)
+
+
+@pytest.mark.parametrize("n,plen,own", [(2, 30000, 5), (12, 9000, 700), (150, 600, 40)])
+def test_every_split(n, plen, own):
+    check(case(60 + n, n, 1, 8, 2, 64, 16, [plen], [own + b % 5 for b in range(n)], torch.bfloat16))
+
+
+def test_equals_attention_over_one_table():
+    """The same tokens behind one table each: decode_multi over prefix and own pages."""
+    n, Q, bs = 4, 3, 16
+    c = case(70, n, Q, 8, 2, 128, bs, [64], [20, 3, 33, 16], torch.bfloat16)
+    d = {k: v.to(DEV) for k, v in c.items()}
+    whole = torch.cat([d["ptable"].expand(n, -1), d["table"]], 1).contiguous()
+    want = torch.zeros(c["q"].shape, device=DEV)
+    pa.decode_multi(want, d["q"], d["k_cache"], d["v_cache"], whole, d["lens"] + 64, 0.1, 97)
+    got = run(c, 0.1, out_dtype=torch.float32)
+    slack = 2 * ref.out_slack(c["q"], c["k_cache"], c["v_cache"], 0.1, 97)
+    assert (got - want.cpu()).abs().max().item() <= slack
+
+
+def test_same_bits_twice_other_stream_one_token_form_and_graph():
+    c = case(80, 20, 1, 32, 8, 128, 16, [2000], [3 * b + 1 for b in range(20)], torch.bfloat16)
+    want = run(c, 0.1)
+    for kw in (dict(), dict(stream=torch.cuda.Stream(DEV)),
+               dict(stream=torch.cuda.Stream(DEV), own_workspace=False)):
+        assert torch.equal(run(c, 0.1, **kw), want)
+    d = {k: v.to(DEV) for k, v in c.items()}
+    q, out = d["q"][:, 0].contiguous(), torch.zeros((20, 32, 128), dtype=torch.bfloat16, device=DEV)
+    args = (out, q, d["k_cache"], d["v_cache"], d["ptable"], d["plens"], d["table"], d["lens"], 0.1,
+            2000, 58)
+    pa.decode_shared_prefix(*args)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want[:, 0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.decode_shared_prefix(*args)
+    out.zero_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want[:, 0])

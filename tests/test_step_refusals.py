@@ -178,3 +178,105 @@ def evict_args(**kw):
 def test_binding_refuses_evict(kw, error):
     with pytest.raises(error):
         pa.evict_kv(**evict_args(**kw))
+
+
+def call_prefix(lib, s, ptrs=None, num_prefixes=2, max_prefix_blocks=100, q_len=1, scale=0.1,
+                max_prefix_len=100, max_len=100, ws=FAKE, ws_bytes=1 << 20):
+    p = [FAKE] * 8
+    for i, v in (ptrs or {}).items():
+        p[i] = v
+    return lib.pa_decode_shared_prefix(*p, ctypes.byref(s), num_prefixes, max_prefix_blocks, q_len,
+                                       scale, max_prefix_len, max_len, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(num_prefixes=0), 1), (dict(num_prefixes=3), 1), (dict(num_prefixes=-1), 1),
+    (dict(max_prefix_blocks=0), 1), (dict(q_len=0), 1), (dict(scale=0.0), 1),
+    (dict(scale=float("nan")), 1), (dict(max_prefix_len=-1), 1), (dict(max_len=-1), 1),
+    (dict(max_prefix_blocks=1 << 28), 2), (dict(q_len=1 << 27), 2),
+])
+def test_prefix_refuses_arguments(lib, kw, code):
+    assert call_prefix(lib, shape(), **kw) == code
+
+
+def test_prefix_refuses_the_rest(lib):
+    for i in range(8):
+        assert call_prefix(lib, shape(), {i: None}) == 1
+        assert call_prefix(lib, shape(), {i: FAR + 2}) == 1
+    for i in range(4):
+        assert call_prefix(lib, shape(), {i: FAR + 8}) == 1
+    assert call_prefix(lib, shape(num_heads=24)) == 2
+    assert call_prefix(lib, shape(batch=0), {i: None for i in range(8)}, ws=None) == 0
+    assert lib.pa_workspace_size_shared_prefix(ctypes.byref(shape()), 3, 100, 1, 100, 100) == 0
+    assert lib.pa_workspace_size_shared_prefix(ctypes.byref(shape(batch=0)), 1, 100, 1, 100, 100) == 0
+
+
+def call_accumulate(lib, s, ptrs=None, q_len=1, scale=0.1, max_len=100, ws=FAKE, ws_bytes=1 << 20):
+    p = [FAKE] * 8
+    for i, v in (ptrs or {}).items():
+        p[i] = v
+    return lib.pa_decode_accumulate(*p, ctypes.byref(s), q_len, scale, max_len, ws, ws_bytes, None)
+
+
+def test_accumulate_refuses(lib):
+    s = shape()
+    for kw in (dict(q_len=0), dict(scale=-1.0), dict(scale=float("inf")), dict(max_len=-1)):
+        assert call_accumulate(lib, s, **kw) == 1
+    assert call_accumulate(lib, s, q_len=1 << 27) == 2
+    for i in range(8):
+        assert call_accumulate(lib, s, {i: None}) == 1
+        assert call_accumulate(lib, s, {i: FAR + 2}) == 1
+    # weights that overlap in part
+    assert call_accumulate(lib, s, {1: FAR + 16, 2: FAR}) == 1
+    assert call_accumulate(lib, shape(kv_dtype=pa.F32)) == 2
+    assert call_accumulate(lib, shape(batch=0), {i: None for i in range(8)}, ws=None) == 0
+    assert lib.pa_workspace_size_accumulate(ctypes.byref(shape(head_dim=80)), 1, 100) == 0
+    assert lib.pa_workspace_size_accumulate(ctypes.byref(s), 0, 100) == 0
+
+
+def attention_args(**kw):
+    B, H, Hkv, D = 4, 4, 2, 64
+    t = dict(out=torch.zeros(B, H, D, dtype=torch.float16), q=torch.zeros(B, H, D, dtype=torch.float16),
+             k_cache=torch.zeros(4, 16, Hkv, D, dtype=torch.float16),
+             v_cache=torch.zeros(4, 16, Hkv, D, dtype=torch.float16),
+             block_tables=torch.zeros(B, 2, dtype=torch.int32),
+             context_lens=torch.zeros(B, dtype=torch.int32), scale=0.1, max_context_len=32)
+    t.update(kw)
+    return t
+
+
+@pytest.mark.parametrize("kw,error", [
+    (dict(prefix_tables=torch.zeros(3, 5, dtype=torch.int32), prefix_lens=torch.zeros(3, dtype=torch.int32)), ValueError),
+    (dict(prefix_tables=torch.zeros(0, 5, dtype=torch.int32), prefix_lens=torch.zeros(0, dtype=torch.int32)), ValueError),
+    (dict(prefix_tables=torch.zeros(5, dtype=torch.int32)), ValueError),
+    (dict(prefix_tables=torch.zeros(2, 5)), TypeError),
+    (dict(prefix_lens=torch.zeros(1, dtype=torch.int32)), ValueError),
+    (dict(prefix_lens=torch.zeros(2, dtype=torch.int64)), TypeError),
+    (dict(out=torch.zeros(4, 4, 128, dtype=torch.float16)), ValueError),
+    (dict(out=torch.zeros(4, 4, 64, dtype=torch.bfloat16)), TypeError),
+    (dict(context_lens=torch.zeros(3, dtype=torch.int32)), ValueError),
+    (dict(), ValueError),   # not on a GPU
+])
+def test_binding_refuses_prefix(kw, error):
+    args = attention_args(prefix_tables=torch.zeros(2, 5, dtype=torch.int32),
+                          prefix_lens=torch.zeros(2, dtype=torch.int32), max_prefix_len=50)
+    args.update(kw)
+    with pytest.raises(error):
+        pa.decode_shared_prefix(**args)
+
+
+@pytest.mark.parametrize("kw,error", [
+    (dict(new_weights=torch.zeros(4, 2, 31)), ValueError),
+    (dict(new_weights=torch.zeros(4, 4, 32)), ValueError),
+    (dict(new_weights=torch.zeros(4, 2, 32, dtype=torch.float16)), TypeError),
+    (dict(weights=torch.zeros(4, 2, 16)), ValueError),
+    (dict(weights=torch.zeros(4, 2, 32, dtype=torch.float64)), TypeError),
+    (dict(q=torch.zeros(4, 4, 64)), TypeError),
+    (dict(q=torch.zeros(4, 1, 4, 64, dtype=torch.float16)), ValueError),
+    (dict(), ValueError),   # not on a GPU
+])
+def test_binding_refuses_accumulate(kw, error):
+    args = attention_args(new_weights=torch.zeros(4, 2, 32))
+    args.update(kw)
+    with pytest.raises(error):
+        pa.decode_accumulate(**args)
