@@ -260,6 +260,8 @@ struct Plan {
     const int32_t* own_lens = nullptr;  // a shared prefix: see AttnParams
     int32_t own_q = 0;
     float* lse = nullptr;               // row statistics wanted: see AttnParams
+    float* scores = nullptr;            // scores wanted: see AttnParams
+    int64_t score_width = 0;
 };
 
 Plan plan_with(const pa_shape* s, int pages, int pp, bool cluster_ok,
@@ -776,6 +778,8 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     p.own_lens = plan.own_lens;
     p.own_q = plan.own_q;
     p.lse = plan.lse;
+    p.scores = plan.scores;
+    p.score_width = plan.score_width;
     p.timeout_ns = kDefaultTimeoutNs;
     L.head_dim = s->head_dim;
     L.block_size = s->block_size;
@@ -789,9 +793,9 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     L.smem_bytes = sm.total + kSmemAlignSlack;
     cudaError_t e;
     switch (s->head_dim) {
-        case 64: e = launch_attn_d64(L, stream); break;
-        case 128: e = launch_attn_d128(L, stream); break;
-        default: e = launch_attn_d256(L, stream); break;
+        case 64: e = p.scores ? launch_attn_d64_scores(L, stream) : launch_attn_d64(L, stream); break;
+        case 128: e = p.scores ? launch_attn_d128_scores(L, stream) : launch_attn_d128(L, stream); break;
+        default: e = p.scores ? launch_attn_d256_scores(L, stream) : launch_attn_d256(L, stream); break;
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -941,31 +945,61 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
 
 // ---- attention that accumulates the tokens' weights ----
 
-// Workspace: what pa_decode_multi takes, then the rows' statistics [B, Q, H].
-size_t accumulate_bytes(const pa_shape* s, const Plan& plan, int32_t q_len, size_t* lse_off) {
-    const size_t attn = workspace_bytes_for(s, plan, nullptr, q_len);
-    if (attn > SIZE_MAX / 2) return SIZE_MAX;
-    const size_t off = (attn + 255) / 256 * 256;
-    if (lse_off) *lse_off = off;
-    size_t rows = (size_t)s->batch;
-    if (__builtin_mul_overflow(rows, (size_t)s->num_heads * sizeof(float), &rows) ||
-        __builtin_mul_overflow(rows, (size_t)q_len, &rows) || rows > SIZE_MAX / 4)
-        return SIZE_MAX;
-    return off + rows;
+// How the attention of a call is split: as pa_decode_multi splits it, except
+// that more units than SMs, on the warp-level kernel, are cut into partitions
+// of 64 pages even where all of them are resident at once.  The lengths are
+// not known here, and one pass lasts as long as its longest sequence: 32
+// sequences of 1 .. 8192 tokens took 124 us in one pass, 95 us in partitions
+// of 1024 tokens.  A call's partitions cover max_context_len and no more, so
+// that the scores stay inside their array.
+Plan accumulate_plan(const pa_shape* s, int32_t max_context_len, int sms, int32_t q_len) {
+    Plan p = make_plan(s, max_context_len, 0, sms, q_len);
+    const int pages = pages_for(s, max_context_len);
+    const int64_t units = (int64_t)s->batch * s->num_kv_heads * (p.tile ? 1 : q_chunks_for(s, q_len));
+    if (p.balanced || (!p.tile && p.num_parts <= 1 && units > sms && pages > 64)) {
+        const bool tile = p.tile;
+        const int qr = p.tile_qr;
+        p = plan_with(s, pages, tile ? pages : 64, false);
+        p.tile = tile;
+        p.tile_qr = qr;
+        p.many_ctas = units * p.num_parts > sms;
+    }
+    if (p.num_parts <= 1) p.part_pages = pages;
+    return p;
 }
 
-// pa_decode_multi after its checks; lse: row statistics wanted (or null).
+// Whether the attention leaves its scores (up to 16 query rows on the
+// warp-level kernel, 4 bytes each) or the keys are read again (the rows of
+// the tile kernel share one read of a key by up to 128 rows).
+bool accumulate_scores(const pa_shape* s, const Plan& plan, int32_t q_len) {
+    return !plan.tile && (int64_t)q_len * (s->num_heads / s->num_kv_heads) <= 16;
+}
+
+// Workspace: what the attention takes; the rows' statistics [B, Q, H]; the
+// scores [B, Hkv, Q * group, tokens of max_context_len's pages].
+size_t accumulate_bytes(const pa_shape* s, const Plan& plan, int32_t q_len, int32_t max_context_len,
+                        size_t* lse_off, size_t* score_off) {
+    const size_t attn = workspace_bytes_for(s, plan, nullptr, q_len);
+    size_t rows = (size_t)s->batch, bytes = 0;
+    if (attn > SIZE_MAX / 4 || __builtin_mul_overflow(rows, (size_t)s->num_heads * sizeof(float), &rows) ||
+        __builtin_mul_overflow(rows, (size_t)q_len, &rows) || rows > SIZE_MAX / 4)
+        return SIZE_MAX;
+    const size_t lse = (attn + 255) / 256 * 256, scores = lse + (rows + 255) / 256 * 256;
+    if (lse_off) *lse_off = lse;
+    if (score_off) *score_off = scores;
+    if (!accumulate_scores(s, plan, q_len)) return lse + rows;
+    if (__builtin_mul_overflow(rows, (size_t)pages_for(s, max_context_len) * s->block_size, &bytes) ||
+        bytes > SIZE_MAX - scores)
+        return SIZE_MAX;
+    return scores + bytes;
+}
+
+// pa_decode_multi after its checks and its plan.
 pa_status run_multi(void* out, const void* q, const void* k_cache, const void* v_cache,
                     const int32_t* block_tables, const int32_t* context_lens,
-                    const pa_shape* shape, int32_t q_len, float scale, int32_t max_context_len,
-                    int32_t partition_tokens, void* workspace, size_t workspace_bytes, float* lse,
-                    cudaStream_t cs) {
-    int sms = 0;
-    int32_t* err = nullptr;
-    pa_status st = device_state(&sms, &err);
-    if (st != PA_OK) return st;
-    Plan plan = make_plan(shape, max_context_len, partition_tokens, sms, q_len);
-    plan.lse = lse;
+                    const pa_shape* shape, int32_t q_len, float scale, const Plan& plan,
+                    void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t cs) {
+    pa_status st;
     if (plan.tile && !plan.balanced && (plan.num_parts <= 1 || plan.cluster))
         return launch_tile(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale, plan,
                            nullptr, nullptr, err, cs, q_len);
@@ -1001,7 +1035,7 @@ pa_status run_multi(void* out, const void* q, const void* k_cache, const void* v
     c.num_parts = plan.num_parts;
     c.out_dtype = shape->out_dtype;
     c.num_ctas = plan.num_ctas;
-    c.lse = lse;
+    c.lse = plan.lse;
     const dim3 cgrid((unsigned)(q_len * shape->num_heads), (unsigned)shape->batch);
     const cudaError_t e = plan.balanced ? launch_combine_balanced(c, shape->head_dim, cgrid,
                                                                   use_pdl(), cs)
@@ -1095,9 +1129,13 @@ pa_status pa_decode_multi(void* out, const void* q, const void* k_cache, const v
     if (shape->batch == 0) return PA_OK;
     st = check_ptrs(out, q, k_cache, v_cache, block_tables, context_lens);
     if (st != PA_OK) return st;
+    int sms = 0;
+    int32_t* err = nullptr;
+    st = device_state(&sms, &err);
+    if (st != PA_OK) return st;
     return run_multi(out, q, k_cache, v_cache, block_tables, context_lens, shape, q_len, scale,
-                     max_context_len, partition_tokens, workspace, workspace_bytes, nullptr,
-                     static_cast<cudaStream_t>(stream));
+                     make_plan(shape, max_context_len, partition_tokens, sms, q_len), workspace,
+                     workspace_bytes, err, static_cast<cudaStream_t>(stream));
 }
 
 pa_status pa_decode_splitkv(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -1338,7 +1376,8 @@ size_t pa_workspace_size_accumulate(const pa_shape* shape, int32_t q_len, int32_
     if (check_shape(shape) != PA_OK || max_context_len < 0 || q_len < 1) return 0;
     int sms = 0;
     if (device_state(&sms, nullptr) != PA_OK) return 0;
-    return accumulate_bytes(shape, make_plan(shape, max_context_len, 0, sms, q_len), q_len, nullptr);
+    return accumulate_bytes(shape, accumulate_plan(shape, max_context_len, sms, q_len), q_len,
+                            max_context_len, nullptr, nullptr);
 }
 
 pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weights_in,
@@ -1362,23 +1401,31 @@ pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weigh
     const uintptr_t w_in = reinterpret_cast<uintptr_t>(weights_in);
     if (w_out != w_in && w_out < w_in + w_bytes && w_in < w_out + w_bytes) return PA_ERR_INVALID_ARG;
     int sms = 0;
-    st = device_state(&sms, nullptr);
+    int32_t* err = nullptr;
+    st = device_state(&sms, &err);
     if (st != PA_OK) return st;
-    const Plan plan = make_plan(shape, max_context_len, 0, sms, q_len);
-    size_t lse_off = 0;
-    const size_t need = accumulate_bytes(shape, plan, q_len, &lse_off);
+    Plan plan = accumulate_plan(shape, max_context_len, sms, q_len);
+    size_t lse_off = 0, score_off = 0;
+    const size_t need =
+        accumulate_bytes(shape, plan, q_len, max_context_len, &lse_off, &score_off);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return PA_ERR_WORKSPACE;
-    float* lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + lse_off);
+    const bool scores = accumulate_scores(shape, plan, q_len);
+    char* ws = static_cast<char*>(workspace);
+    plan.lse = reinterpret_cast<float*>(ws + lse_off);
+    plan.scores = scores ? reinterpret_cast<float*>(ws + score_off) : nullptr;
+    plan.score_width = (int64_t)pages_for(shape, max_context_len) * shape->block_size;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    st = run_multi(out, q, k_cache, v_cache, block_tables, context_lens, shape, q_len, scale,
-                   max_context_len, 0, workspace, lse_off, lse, cs);
+    st = run_multi(out, q, k_cache, v_cache, block_tables, context_lens, shape, q_len, scale, plan,
+                   workspace, lse_off, err, cs);
     if (st != PA_OK) return st;
     WeightParams w;
     w.q = q;
     w.k_cache = k_cache;
     w.weights_in = weights_in;
     w.weights_out = weights_out;
-    w.lse = lse;
+    w.lse = plan.lse;
+    w.scores = plan.scores;
+    w.score_width = plan.score_width;
     w.block_tables = block_tables;
     w.context_lens = context_lens;
     w.num_blocks = shape->num_blocks;
@@ -1390,15 +1437,13 @@ pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weigh
     w.group = shape->num_heads / shape->num_kv_heads;
     w.block_size = shape->block_size;
     w.max_blocks = shape->max_blocks_per_seq;
-    // a split covers max_context_len, one pass everything the table reaches
-    const int64_t covered = (int64_t)plan.num_parts * plan.part_pages * shape->block_size;
-    w.token_limit = plan.num_parts <= 1 || plan.balanced || covered > 0x7fffffff ? 0x7fffffff
-                                                                                 : (int32_t)covered;
-    return launch_weights(w, shape->head_dim, shape->kv_dtype,
-                          pages_for(shape, max_context_len) * shape->block_size, use_pdl(),
-                          cs) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    // what the partitions cover (persistent CTAs walk their sequences whole)
+    w.token_limit = plan.persistent ? 0x7fffffff : (int32_t)plan.score_width;
+    const cudaError_t e =
+        scores ? launch_weights_of_scores(w, use_pdl(), cs)
+               : launch_weights(w, shape->head_dim, shape->kv_dtype, (int)plan.score_width,
+                                use_pdl(), cs);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -72,7 +72,10 @@ enum SegOut { kOutFinal = 0, kOutPartial = 1, kOutCluster = 2, kOutRecord = 3 };
 
 // MULTI: several query tokens per sequence (rows are (query token, head)
 // pairs with a causal limit each); otherwise one token, rows = the group's heads.
-template <int D, int BS, typename KV, bool MULTI>
+// SCORES: every score also goes to p.scores, from which the tokens' attention
+// weights are summed once the rows' statistics are known (4 bytes a row and
+// token written and read again, against reading a key of 2 D bytes again).
+template <int D, int BS, typename KV, bool MULTI, bool SCORES = false>
 __global__ void __launch_bounds__(256, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
@@ -319,6 +322,22 @@ __global__ void __launch_bounds__(256, 1)
                         mx0 = fmaxf(mx0, s[nt][e]);
                         mx1 = fmaxf(mx1, s[nt][2 + e]);
                     }
+                if constexpr (SCORES) {
+                    if (ds == 0) {  // (the two warps of a page at head_dim 256 form the same scores)
+                        const size_t rows = ((size_t)b * Hkv + kvh) * (MULTI ? p.unit_rows : G) +
+                                            (size_t)qi0 * G;
+                        float* at = p.scores + rows * p.score_width + (size_t)j * BS + tig * 2;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (real0)
+                                *reinterpret_cast<float2*>(at + (size_t)g * p.score_width + nt * 8) =
+                                    make_float2(s[nt][0], s[nt][1]);
+                            if (real1)
+                                *reinterpret_cast<float2*>(at + (size_t)(g + 8) * p.score_width + nt * 8) =
+                                    make_float2(s[nt][2], s[nt][3]);
+                        }
+                    }
+                }
                 mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 1));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 1));
                 mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2));
@@ -666,16 +685,16 @@ __global__ void __launch_bounds__(256, 1)
 }
 
 // Per-instantiation flags of the attributes set once per device.
-template <int D, int BS, typename KV, bool MULTI>
+template <int D, int BS, typename KV, bool MULTI, bool SCORES = false>
 struct AttnAttrs {
     static inline AttrFlags smem;
     static inline AttrFlags nonportable;
 };
 
-template <int D, int BS, typename KV, bool MULTI>
+template <int D, int BS, typename KV, bool MULTI, bool SCORES>
 cudaError_t launch_attn_inst(const AttnLaunch& L, cudaStream_t stream) {
-    auto kern = attn_kernel<D, BS, KV, MULTI>;
-    using Attrs = AttnAttrs<D, BS, KV, MULTI>;
+    auto kern = attn_kernel<D, BS, KV, MULTI, SCORES>;
+    using Attrs = AttnAttrs<D, BS, KV, MULTI, SCORES>;
     cudaError_t e = raise_smem_limit_once(kern, Attrs::smem);
     if (e != cudaSuccess) return e;
     if (L.cluster > kMaxClusterParts) {
@@ -751,15 +770,15 @@ int attn_max_clusters_for_d(int block_size, int kv_dtype, int cluster, int threa
               : attn_max_clusters_inst<D, 32, __half>(cluster, threads, smem_bytes);
 }
 
-template <int D, bool MULTI>
+template <int D, bool MULTI, bool SCORES = false>
 cudaError_t launch_attn_for_d(const AttnLaunch& L, cudaStream_t stream) {
     const bool bf = L.kv_dtype == PA_BF16;
     if (L.block_size == 16)
-        return bf ? launch_attn_inst<D, 16, __nv_bfloat16, MULTI>(L, stream)
-                  : launch_attn_inst<D, 16, __half, MULTI>(L, stream);
+        return bf ? launch_attn_inst<D, 16, __nv_bfloat16, MULTI, SCORES>(L, stream)
+                  : launch_attn_inst<D, 16, __half, MULTI, SCORES>(L, stream);
     if (L.block_size == 32)
-        return bf ? launch_attn_inst<D, 32, __nv_bfloat16, MULTI>(L, stream)
-                  : launch_attn_inst<D, 32, __half, MULTI>(L, stream);
+        return bf ? launch_attn_inst<D, 32, __nv_bfloat16, MULTI, SCORES>(L, stream)
+                  : launch_attn_inst<D, 32, __half, MULTI, SCORES>(L, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -19,52 +19,83 @@ namespace pa {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kMaxSelCluster = 8;
+constexpr int kBins = 2048;           // digits of 11, 11 and 10 bits; four per thread
+constexpr int kSelShare = 4096;       // tokens a CTA takes before a row gets a larger cluster
+constexpr int kMaxCached = 50 * 1024; // tokens whose keys fit in a CTA's shared memory
 
-// Integers that order as the weights do: NaN below everything, -0 as +0.
+// Keys of tokens that the selection does not weigh.
+constexpr uint32_t kKeyAlways = 0xffffffffu;  // kept whatever the weight
+constexpr uint32_t kKeyAbsent = 0u;           // of a masked page: never kept
+
+// Integers that order as the weights do: NaN below every number, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-    if (w != w) return 0u;
+    if (w != w) return 1u;
     const uint32_t u = __float_as_uint(w + 0.f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive sum over the block of one int per thread; *total gets the sum.
-// `scratch` holds 33 ints; a barrier follows its last read.
-__device__ __forceinline__ int block_exclusive(int v, int* scratch, int* total) {
+// Exclusive sum over the block of one number per thread; *total gets the sum.
+// `scratch` holds 33 numbers; a barrier follows its last read.
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* scratch, uint32_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    uint32_t x = v;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int y = __shfl_up_sync(kFullMask, x, m);
+        const uint32_t y = __shfl_up_sync(kFullMask, x, m);
         if (lane >= m) x += y;
     }
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int s = lane < (int)(blockDim.x >> 5) ? scratch[lane] : 0;
-        const int own = s;
+        uint32_t s = lane < (int)(blockDim.x >> 5) ? scratch[lane] : 0;
+        const uint32_t own = s;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const int y = __shfl_up_sync(kFullMask, s, m);
+            const uint32_t y = __shfl_up_sync(kFullMask, s, m);
             if (lane >= m) s += y;
         }
         scratch[lane] = s - own;
         if (lane == 31) scratch[32] = s;
     }
     __syncthreads();
-    const int r = x - v + scratch[warp];
+    const uint32_t r = x - v + scratch[warp];
     *total = scratch[32];
     __syncthreads();
     return r;
 }
 
-// One CTA per (kv head, sequence).
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
-    __shared__ int hist[256];
-    __shared__ int scratch[33];
-    __shared__ int chosen[2];  // digit of the threshold, tokens still wanted of it
-    const int tid = threadIdx.x;
-    const int kvh = blockIdx.x, b = blockIdx.y;
+// Word of a cached key: one word in 33 is skipped, so that threads that each
+// walk a run of keys meet in no bank.
+__device__ __forceinline__ int key_word(int i) { return i + (i >> 5); }
+
+// One cluster of up to 8 CTAs per (kv head, sequence), each with a run of the
+// row's tokens.  A CTA turns its weights into keys once and keeps them in
+// shared memory (CACHED; a row too long for that is read again by every
+// pass).  Three passes find the threshold, the want-th largest key among the
+// tokens that are not kept anyway: each counts a digit of the keys that agree
+// with the digits found so far, and every CTA adds up the cluster's counts
+// through distributed shared memory, four bins to a thread, all ranks' loads
+// in flight.  Then each thread counts what it keeps of its own run of keys;
+// one scan over the CTA, and the counts of the CTAs before it, tell it where
+// to write them.
+//
+// What bounds it: the barriers and the round trips to the cluster's counts,
+// a few of each per pass; 32 rows of 128K weights are 17 MB.
+template <bool CACHED>
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictParams p) {
+    extern __shared__ uint32_t keys[];
+    __shared__ __align__(16) uint32_t hist[kBins];
+    __shared__ uint32_t scratch[33];
+    __shared__ uint32_t chosen[2];  // digit of the threshold, tokens still wanted of it
+    // this CTA's share, read by the cluster: tokens held, of them kept
+    // whatever their weight; above the threshold (those included), equal to it
+    __shared__ uint32_t share[4];
+    __shared__ uint32_t shares[kMaxSelCluster][2];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int C = (int)p.cluster, rank = (int)blockIdx.x % C;
+    const int kvh = (int)blockIdx.x / C, b = blockIdx.y;
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -73,71 +104,210 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     int32_t* kept = p.kept + ((size_t)b * p.num_kv_heads + kvh) * p.budget;
     const int32_t* row = p.block_tables + (size_t)b * p.max_blocks;
     const int npages = (T + p.block_size - 1) / p.block_size;
-    auto held = [&](int t) { return page_phys(row, t / p.block_size, npages, p.num_blocks) >= 0; };
-    auto always = [&](int t) { return t < p.sink || t >= T - p.recent; };
+    const int bshift = __ffs(p.block_size) - 1;
+    const int recent = T - p.recent;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.weights) & 15) == 0;
+    // tokens [t0, t1) of the row, t0 a multiple of 4
+    const int per = ((T + 3) / 4 + C - 1) / C * 4;
+    const int t0 = min(rank * per, T), t1 = min(t0 + per, T), len = t1 - t0;
 
-    // tokens of readable pages, and those kept whatever their weight
-    int mine = 0, forced = 0;
-    for (int t = tid; t < T; t += kSelThreads)
-        if (held(t)) {
-            ++mine;
-            forced += always(t);
+    auto key_of = [&](int t, float x) {
+        return t < p.sink || t >= recent ? kKeyAlways : weight_key(x);
+    };
+    auto page_held = [&](int t) { return page_phys(row, t >> bshift, npages, p.num_blocks) >= 0; };
+    // key of the CTA's token i
+    auto key_at = [&](int i) {
+        if constexpr (CACHED) return keys[key_word(i)];
+        else return page_held(t0 + i) ? key_of(t0 + i, w[t0 + i]) : kKeyAbsent;
+    };
+    auto gather_shares = [&](int first) {  // after a cluster barrier; a block barrier follows
+        if (tid < C * 2)
+            shares[tid >> 1][tid & 1] =
+                ld_cluster_u32(map_cluster_rank(smem_u32(&share[first + (tid & 1)]), tid >> 1));
+        __syncthreads();
+    };
+
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    if (tid < 4) share[tid] = 0;
+    __syncthreads();
+    uint32_t held = 0, must = 0;
+    auto count_first = [&](uint32_t k) {  // the first pass's counts
+        held += k != kKeyAbsent;
+        must += k == kKeyAlways;
+        if (k != kKeyAbsent && k != kKeyAlways) atomicAdd(&hist[k >> 21], 1u);
+    };
+    if constexpr (CACHED) {
+        // a quad of tokens, which lies in one page, at a time; four quads in flight
+        const int quads = (len + 3) / 4;
+        for (int base = tid; base < quads; base += kSelThreads * 4) {
+            float4 x[4];
+            bool ok[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int q = base + u * kSelThreads;
+                ok[u] = q < quads && page_held(t0 + q * 4);
+                if (!ok[u]) continue;
+                const float* v = w + t0 + q * 4;  // inside the row: its width is a multiple of 16
+                x[u] = wide ? *reinterpret_cast<const float4*>(v) : make_float4(v[0], v[1], v[2], v[3]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int q = base + u * kSelThreads;
+                if (q >= quads) continue;
+                const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (q * 4 + e < len) {
+                        const uint32_t k = ok[u] ? key_of(t0 + q * 4 + e, v[e]) : kKeyAbsent;
+                        keys[key_word(q * 4 + e)] = k;
+                        count_first(k);
+                    }
+            }
         }
-    int valid, must;
-    (void)block_exclusive(mine, scratch, &valid);
-    (void)block_exclusive(forced, scratch, &must);
-    const int n = min(valid, p.budget);
-    int want = n - must;  // to be chosen by weight
+    } else {
+        for (int i = tid; i < len; i += kSelThreads) count_first(key_at(i));
+    }
+    held = __reduce_add_sync(kFullMask, held);
+    must = __reduce_add_sync(kFullMask, must);
+    if (lane == 0) {
+        atomicAdd(&share[0], held);
+        atomicAdd(&share[1], must);
+    }
 
-    // the largest key of which at least `want` free tokens are as large, digit by digit
-    uint32_t prefix = 0, mask = 0;
-    const bool all = valid <= p.budget;
-    if (!all) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
-            __syncthreads();
-            for (int t = tid; t < T; t += kSelThreads) {
-                if (always(t) || !held(t)) continue;
-                const uint32_t k = weight_key(w[t]);
-                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    uint32_t prefix = 0, mask = 0, want = 0, n = 0;
+    bool all = false;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+        const uint32_t digit = pass == 2 ? 1023u : 2047u;
+        if (pass > 0) {
+#pragma unroll 8
+            for (int i = tid; i < len; i += kSelThreads) {
+                const uint32_t k = key_at(i);
+                if ((k & mask) == prefix && k != kKeyAbsent && k != kKeyAlways)
+                    atomicAdd(&hist[(k >> shift) & digit], 1u);
             }
-            __syncthreads();
-            if (tid == 0) {
-                int left = want, d = 255;
-                for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-                chosen[0] = d;
-                chosen[1] = left;
+        }
+        cluster_sync_release_acquire();  // every CTA's counts are in place
+        // the cluster's counts of bins 4 tid .. 4 tid + 3
+        uint4 c = make_uint4(0, 0, 0, 0);
+        {
+            const uint32_t at = smem_u32(hist) + 16u * tid;
+            uint4 x[kMaxSelCluster];
+#pragma unroll
+            for (int r = 0; r < kMaxSelCluster; ++r)
+                x[r] = r < C ? ld_cluster_v4u32(map_cluster_rank(at, r)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < kMaxSelCluster; ++r) {
+                c.x += x[r].x;
+                c.y += x[r].y;
+                c.z += x[r].z;
+                c.w += x[r].w;
             }
-            __syncthreads();
-            prefix |= (uint32_t)chosen[0] << shift;
-            mask |= 255u << shift;
-            want = chosen[1];
+        }
+        if (pass == 0) {
+            gather_shares(0);
+            uint32_t valid = 0, fixed = 0;
+            for (int r = 0; r < C; ++r) {
+                valid += shares[r][0];
+                fixed += shares[r][1];
+            }
+            n = min(valid, (uint32_t)p.budget);
+            want = n - fixed;
+            all = valid <= (uint32_t)p.budget;
+            if (all) break;  // (the same in every CTA of the cluster)
+        }
+        // the want-th largest: its rank from below among the cluster's counts
+        uint32_t total;
+        const uint32_t before = block_exclusive(c.x + c.y + c.z + c.w, scratch, &total);
+        if (tid == 0 && want == 0) {  // nothing is wanted: above every key
+            chosen[0] = digit;
+            chosen[1] = 0;
+        }
+        const uint32_t below = total - want;  // candidates left out
+        if (want > 0 && below >= before && below < before + c.x + c.y + c.z + c.w) {
+            const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+            uint32_t s = before;
+            int d = 0;
+            while (d < 3 && below >= s + cs[d]) s += cs[d++];
+            chosen[0] = (uint32_t)(4 * tid + d);
+            chosen[1] = s + cs[d] - below;
+        }
+        __syncthreads();
+        prefix |= chosen[0] << shift;
+        mask |= digit << shift;
+        want = chosen[1];
+        if (pass < 2) {
+            cluster_sync_release_acquire();  // the counts have been read
+            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
             __syncthreads();
         }
     }
-    // the kept tokens in order; `want` of those equal to the threshold, lowest first
-    int at = 0, equals = 0;
-    for (int t0 = 0; t0 < T; t0 += kSelThreads) {
-        const int t = t0 + tid;
-        bool keep = false, equal = false;
-        if (t < T && held(t)) {
-            keep = all || always(t);
-            if (!keep) {
-                const uint32_t k = weight_key(w[t]);
-                keep = k > prefix;
-                equal = k == prefix;
+
+    // this thread's run of the CTA's keys: how many it surely keeps, how many
+    // equal the threshold, of which the row keeps its lowest `want`
+    const int run = (len + kSelThreads - 1) / kSelThreads;
+    const int i0 = min(tid * run, len), i1 = min(i0 + run, len);
+    // (a bit for each of 32 tokens; with `all`, prefix is 0 = absent: no token equals it)
+    auto masks = [&](int i, uint32_t& s, uint32_t& e) {
+        s = e = 0;
+#pragma unroll 8
+        for (int u = 0; u < 32; ++u) {
+            if (i + u >= i1) break;
+            const uint32_t k = key_at(i + u);
+            s |= (uint32_t)(k > prefix) << u;
+            e |= (uint32_t)(k == prefix) << u;
+        }
+        // (with nothing wanted the threshold is the key of the tokens always kept)
+        if (prefix == kKeyAlways) s = e;
+        if (prefix == kKeyAbsent || prefix == kKeyAlways) e = 0;
+    };
+    uint32_t sure = 0, equal = 0, s0 = 0, e0 = 0;
+    for (int i = i0; i < i1; i += 32) {
+        uint32_t s, e;
+        masks(i, s, e);
+        if (i == i0) {
+            s0 = s;
+            e0 = e;
+        }
+        sure += __popc(s);
+        equal += __popc(e);
+    }
+    uint32_t sures, equals;
+    sure = block_exclusive(sure, scratch, &sures);
+    equal = block_exclusive(equal, scratch, &equals);
+    if (tid == 0) {
+        share[2] = sures;
+        share[3] = equals;
+    }
+    cluster_sync_release_acquire();
+    gather_shares(2);
+    uint32_t begin = 0, left = want;  // where this CTA's list begins; equal tokens still wanted
+    for (int r = 0; r < rank; ++r) {
+        const uint32_t eq = min(left, shares[r][1]);
+        begin += shares[r][0] + eq;
+        left -= eq;
+    }
+    uint32_t j = begin + sure;  // plus the kept ones of the equal tokens before
+    for (int i = i0; i < i1; i += 32) {
+        uint32_t s = s0, e = e0;
+        if (i > i0) masks(i, s, e);
+        for (uint32_t any = s | e; any; any &= any - 1) {
+            const int u = __ffs(any) - 1;
+            if ((s >> u) & 1u) {
+                kept[j + min(equal, left)] = t0 + i + u;
+                ++j;
+            } else {
+                if (equal < left) kept[j + equal] = t0 + i + u;
+                ++equal;
             }
         }
-        int total;
-        const int rank = equals + block_exclusive(equal, scratch, &total);
-        equals += total;
-        keep = keep || (equal && rank < want);
-        const int j = at + block_exclusive(keep, scratch, &total);
-        at += total;
-        if (keep) kept[j] = t;
     }
-    for (int j = n + tid; j < p.budget; j += kSelThreads) kept[j] = -1;
-    if (kvh == 0 && tid == 0) p.new_lens[b] = n;
+    if (rank == 0) {
+        for (int i = (int)n + tid; i < p.budget; i += kSelThreads) kept[i] = -1;
+        if (kvh == 0 && tid == 0) p.new_lens[b] = (int32_t)n;
+    }
+    cluster_sync_relaxed();  // no CTA leaves while others still read its counts
 }
 
 // A row (slot) of the cache, in 16-byte vectors, of token t of a table row;
@@ -182,12 +352,24 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
     }
     __syncthreads();
     const long long row = (long long)p.num_kv_heads * vecs;
-    for (int i = tid; i < kCopyRows * 2 * vecs; i += kCopyThreads) {
-        const int r = i / (2 * vecs), c = i % (2 * vecs);
-        if (src[r] < 0 || dst[r] < 0) continue;
-        uint4* cache = static_cast<uint4*>(c < vecs ? p.k_cache : p.v_cache);
-        const int at = kvh * vecs + (c < vecs ? c : c - vecs);
-        cache[dst[r] * row + at] = cache[src[r] * row + at];
+    // eight vectors of a thread in flight at a time
+    const int vshift = __ffs(vecs) - 1;  // (8, 16 or 32 vectors a head)
+    for (int i0 = tid; i0 < kCopyRows * 2 * vecs; i0 += kCopyThreads * 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kCopyThreads, r = i >> (vshift + 1), c = i & (2 * vecs - 1);
+            if (r >= kCopyRows || src[r] < 0 || dst[r] < 0) continue;
+            const uint4* cache = static_cast<const uint4*>(c < vecs ? p.k_cache : p.v_cache);
+            v[k] = cache[src[r] * row + kvh * vecs + (c & (vecs - 1))];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kCopyThreads, r = i >> (vshift + 1), c = i & (2 * vecs - 1);
+            if (r >= kCopyRows || src[r] < 0 || dst[r] < 0) continue;
+            uint4* cache = static_cast<uint4*>(c < vecs ? p.k_cache : p.v_cache);
+            cache[dst[r] * row + kvh * vecs + (c & (vecs - 1))] = v[k];
+        }
     }
 }
 
@@ -253,25 +435,47 @@ __global__ void __launch_bounds__(kPackThreads) evict_pack_kernel(const EvictPar
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams& p, bool in_place, bool pdl, cudaStream_t stream) {
+cudaError_t launch_evict(EvictParams p, bool in_place, bool pdl, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    const int64_t width = (int64_t)p.max_blocks * p.block_size;
+    int cluster = 1;
+    while (cluster < kMaxSelCluster && cluster * (int64_t)kSelShare < width) cluster *= 2;
+    p.cluster = cluster;
+    const int64_t per = (width / 4 + cluster - 1) / cluster * 4;  // tokens of a CTA at most
+    const bool cached = per <= kMaxCached;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    cfg.gridDim = dim3((unsigned)p.num_kv_heads, (unsigned)p.batch);
+    cfg.numAttrs = pdl ? 2 : 1;
+    cfg.gridDim = dim3((unsigned)(p.num_kv_heads * cluster), (unsigned)p.batch);
     cfg.blockDim = dim3(kSelThreads);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+    cudaError_t e;
+    if (cached) {
+        static AttrFlags smem_limit;
+        e = raise_smem_limit_once(evict_select_kernel<true>, smem_limit);
+        if (e != cudaSuccess) return e;
+        cfg.dynamicSmemBytes = (size_t)(per + per / 32 + 1) * sizeof(uint32_t);
+        e = cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p);
+    } else {
+        e = cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);
+    }
     if (e != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = pdl ? 1 : 0;
     if (in_place) {
         cfg.gridDim = dim3((unsigned)(2 * p.head_dim / 64), (unsigned)p.num_kv_heads, (unsigned)p.batch);
         cfg.blockDim = dim3(kPackThreads);
         return cudaLaunchKernelEx(&cfg, evict_pack_kernel, p);
     }
-    const int width = max(p.budget, p.new_max_blocks * p.block_size);
-    cfg.gridDim = dim3((unsigned)((width + kCopyRows - 1) / kCopyRows), (unsigned)p.num_kv_heads,
+    // (the new pages hold at least the budget)
+    const int new_width = p.new_max_blocks * p.block_size;
+    cfg.gridDim = dim3((unsigned)((new_width + kCopyRows - 1) / kCopyRows), (unsigned)p.num_kv_heads,
                        (unsigned)p.batch);
     cfg.blockDim = dim3(kCopyThreads);
     return cudaLaunchKernelEx(&cfg, evict_copy_kernel, p);

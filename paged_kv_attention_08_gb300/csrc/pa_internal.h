@@ -32,6 +32,9 @@ struct AttnParams {
     // prefix.  Each sees the whole prefix, but for padding (see prefix_limit).
     const int32_t* own_lens;
     int32_t own_q;
+    float* scores;            // warp-level kernel: [B, Hkv, Q * group, score_width] or null: q . K
+                              // of every token of a read page, -inf where masked
+    int64_t score_width;
     float* lse;               // [B, Q, H] or null: m + log2 l of each row (+inf for an empty one)
     int64_t num_blocks;
     float qscale;             // scale * log2(e): scores are kept in base-2 units
@@ -94,6 +97,8 @@ struct WeightParams {
     float qscale;             // scale * log2(e)
     int32_t batch, q_len, num_heads, num_kv_heads, group, block_size, max_blocks;
     int32_t token_limit;      // tokens from here on were not attended
+    const float* scores;      // as in AttnParams
+    int64_t score_width;
 };
 
 // Rotary positions and the append to the cache (strides in elements, between
@@ -130,6 +135,7 @@ struct EvictParams {
     int64_t num_blocks;
     int32_t batch, num_kv_heads, head_dim, block_size, max_blocks, new_max_blocks;
     int32_t budget, sink, recent;
+    int32_t cluster;          // CTAs that select one row together
 };
 
 // Largest batch the balanced split handles (its per-sequence page counts live
@@ -356,6 +362,10 @@ cudaError_t launch_attn_d64(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_attn_d128(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_attn_d256(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_attn_d64_multi(const AttnLaunch& L, cudaStream_t stream);
+// Instantiations that also store the scores (p.scores).
+cudaError_t launch_attn_d64_scores(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_attn_d128_scores(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_attn_d256_scores(const AttnLaunch& L, cudaStream_t stream);
 // Clusters of `cluster` one-token attention CTAs (tune: `threads`, `smem_bytes`)
 // resident at once on the current device (0 if the query fails).
 int attn_max_clusters_d64(int block_size, int kv_dtype, int cluster, int threads, uint32_t smem_bytes);
@@ -381,6 +391,8 @@ cudaError_t launch_combine_balanced(const CombineParams& p, int head_dim, dim3 g
                                     cudaStream_t stream);
 cudaError_t launch_prefix_combine(const PrefixCombineParams& p, int head_dim, int batch, bool pdl,
                                   cudaStream_t stream);
+// The same from stored scores (p.scores), up to 16 rows per kv head.
+cudaError_t launch_weights_of_scores(const WeightParams& p, bool pdl, cudaStream_t stream);
 cudaError_t launch_weights(const WeightParams& p, int head_dim, int kv_dtype, int max_tokens,
                            bool pdl, cudaStream_t stream);
 cudaError_t launch_append(void* k_cache, void* v_cache, const void* k_new, const void* v_new,
@@ -389,7 +401,7 @@ cudaError_t launch_append(void* k_cache, void* v_cache, const void* k_new, const
                           int32_t row_bytes, bool pdl, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams& p, bool bf16, int num_sms, bool pdl,
                                cudaStream_t stream);
-cudaError_t launch_evict(const EvictParams& p, bool in_place, bool pdl, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams p, bool in_place, bool pdl, cudaStream_t stream);
 cudaError_t launch_wait_timeout(int32_t* err, uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t launch_resolve(int32_t* out_phys, const int32_t* block_tables,
                            const int32_t* context_lens, int32_t batch, int32_t max_blocks,

@@ -111,6 +111,54 @@ __global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightParams p
     }
 }
 
+// From scores that the attention left: one thread per four neighbouring tokens
+// of a kv head.  Bound: memory, 4 bytes per (row, token) and 8 per token.
+constexpr int kSThreads = 256;
+
+__global__ void __launch_bounds__(kSThreads) weights_of_scores_kernel(const WeightParams p) {
+    __shared__ float ls[16];
+    const int tid = threadIdx.x;
+    const int kvh = blockIdx.y, b = blockIdx.z;
+    const int G = p.group, rows = p.q_len * G;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int T = reachable_tokens(p.context_lens, b, p.max_blocks, p.block_size);
+    const int t0 = blockIdx.x * (kSThreads * 4) + tid * 4;
+    if (tid < rows)
+        ls[tid] = p.lse[((size_t)b * p.q_len + tid / G) * p.num_heads + kvh * G + tid % G];
+    __syncthreads();
+    if (t0 >= T) return;
+    const int npages = (T + p.block_size - 1) / p.block_size;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t0 < p.token_limit && page_phys(p.block_tables + (size_t)b * p.max_blocks, t0 / p.block_size,
+                                        npages, p.num_blocks) >= 0) {
+        const float* s = p.scores + ((size_t)b * p.num_kv_heads + kvh) * rows * p.score_width + t0;
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) {
+            const float4 x = __ldcs(reinterpret_cast<const float4*>(s + (size_t)r * p.score_width));
+            const float l = ls[r];  // (+inf where the row attends to nothing: weight 0)
+            sum.x += fast_exp2(fmaf(x.x, p.qscale, -l));
+            sum.y += fast_exp2(fmaf(x.y, p.qscale, -l));
+            sum.z += fast_exp2(fmaf(x.z, p.qscale, -l));
+            sum.w += fast_exp2(fmaf(x.w, p.qscale, -l));
+        }
+    }
+    const size_t at = ((size_t)b * p.num_kv_heads + kvh) * p.max_blocks * p.block_size + t0;
+    const float* in = p.weights_in + at;
+    float* out = p.weights_out + at;
+    if (t0 + 4 <= T && ((reinterpret_cast<uintptr_t>(p.weights_in) |
+                         reinterpret_cast<uintptr_t>(p.weights_out)) & 15) == 0) {
+        const float4 w = *reinterpret_cast<const float4*>(in);
+        *reinterpret_cast<float4*>(out) =
+            make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
+    } else {
+        const float d[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (t0 + e < T) out[e] = in[e] + d[e];
+    }
+}
+
 template <int D>
 cudaError_t launch_d(const WeightParams& p, int kv_dtype, const cudaLaunchConfig_t& cfg) {
     return kv_dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, weights_kernel<D, __nv_bfloat16>, p)
@@ -118,6 +166,22 @@ cudaError_t launch_d(const WeightParams& p, int kv_dtype, const cudaLaunchConfig
 }
 
 }  // namespace
+
+cudaError_t launch_weights_of_scores(const WeightParams& p, bool pdl, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    // every token of the table: those past the scores take a weight of 0
+    const int64_t tokens = (int64_t)p.max_blocks * p.block_size;
+    cfg.gridDim = dim3((unsigned)((tokens + kSThreads * 4 - 1) / (kSThreads * 4)),
+                       (unsigned)p.num_kv_heads, (unsigned)p.batch);
+    cfg.blockDim = dim3(kSThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, weights_of_scores_kernel, p);
+}
 
 cudaError_t launch_weights(const WeightParams& p, int head_dim, int kv_dtype, int max_tokens,
                            bool pdl, cudaStream_t stream) {
