@@ -1439,10 +1439,18 @@ pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weigh
     w.max_blocks = shape->max_blocks_per_seq;
     // what the partitions cover (persistent CTAs walk their sequences whole)
     w.token_limit = plan.persistent ? 0x7fffffff : (int32_t)plan.score_width;
-    const cudaError_t e =
-        scores ? launch_weights_of_scores(w, use_pdl(), cs)
-               : launch_weights(w, shape->head_dim, shape->kv_dtype, (int)plan.score_width,
-                                use_pdl(), cs);
+    w.err = err;
+    w.timeout_ns = kDefaultTimeoutNs;
+    cudaError_t e;
+    if (scores) {
+        e = launch_weights_of_scores(w, use_pdl(), cs);
+    } else {
+        CUtensorMap mk, mv, mq;
+        st = encode_maps(shape, k_cache, v_cache, &mk, &mv);
+        if (st == PA_OK) st = encode_q_map(shape, q, q_len, weights_tile_chunk(shape->head_dim), &mq);
+        if (st != PA_OK) return st;
+        e = launch_weights_tile(w, shape->head_dim, shape->kv_dtype, mk, mq, use_pdl(), cs);
+    }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -23,7 +23,7 @@ constexpr int kSelThreads = 512;
 constexpr int kMaxSelCluster = 8;
 constexpr int kBins = 2048;           // digits of 11, 11 and 10 bits; four per thread
 constexpr int kSelShare = 4096;       // tokens a CTA takes before a row gets a larger cluster
-constexpr int kMaxCached = 50 * 1024; // tokens whose keys fit in a CTA's shared memory
+constexpr int kMaxCached = 40 * 1024; // tokens whose keys fit in a CTA's shared memory
 
 // Keys of tokens that the selection does not weigh.
 constexpr uint32_t kKeyAlways = 0xffffffffu;  // kept whatever the weight
@@ -36,9 +36,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive sum over the block of one number per thread; *total gets the sum.
-// `scratch` holds 33 numbers; a barrier follows its last read.
+// Exclusive sum over the CTA of one number per thread; *total gets the sum.
+// One barrier: `scratch` holds a number per warp and is not used again.
 __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* scratch, uint32_t* total) {
+    constexpr int W = kSelThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t x = v;
 #pragma unroll
@@ -48,54 +49,63 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* scratc
     }
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        uint32_t s = lane < (int)(blockDim.x >> 5) ? scratch[lane] : 0;
-        const uint32_t own = s;
+    uint32_t s = lane < W ? scratch[lane] : 0;
+    const uint32_t own = s;
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const uint32_t y = __shfl_up_sync(kFullMask, s, m);
-            if (lane >= m) s += y;
-        }
-        scratch[lane] = s - own;
-        if (lane == 31) scratch[32] = s;
+    for (int m = 1; m < W; m <<= 1) {
+        const uint32_t y = __shfl_up_sync(kFullMask, s, m);
+        if (lane >= m) s += y;
     }
-    __syncthreads();
-    const uint32_t r = x - v + scratch[warp];
-    *total = scratch[32];
-    __syncthreads();
-    return r;
+    *total = __shfl_sync(kFullMask, s, W - 1);
+    return x - v + __shfl_sync(kFullMask, s - own, warp);
 }
 
-// Word of a cached key: one word in 33 is skipped, so that threads that each
-// walk a run of keys meet in no bank.
-__device__ __forceinline__ int key_word(int i) { return i + (i >> 5); }
+// Stores and adds to the same place in another CTA's shared memory.
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_cluster_add(uint32_t addr, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Word of cached quad q: four words in 36 are skipped, so that threads that
+// each walk a run of eight quads meet in no bank.
+__device__ __forceinline__ int quad_word(int q) { return q * 4 + (q >> 3) * 4; }
 
 // One cluster of up to 8 CTAs per (kv head, sequence), each with a run of the
-// row's tokens.  A CTA turns its weights into keys once and keeps them in
-// shared memory (CACHED; a row too long for that is read again by every
-// pass).  Three passes find the threshold, the want-th largest key among the
-// tokens that are not kept anyway: each counts a digit of the keys that agree
-// with the digits found so far, and every CTA adds up the cluster's counts
-// through distributed shared memory, four bins to a thread, all ranks' loads
-// in flight.  Then each thread counts what it keeps of its own run of keys;
-// one scan over the CTA, and the counts of the CTAs before it, tell it where
-// to write them.
+// row's tokens, handled in quads (which lie in one page).  A CTA turns its
+// weights into keys once and keeps them in shared memory (CACHED; a row too
+// long for that is read again by every pass).  Three passes find the
+// threshold, the want-th largest key among the tokens that are not kept
+// anyway: each counts a digit of the keys that agree with the digits found so
+// far in bins of its own and then adds its non-empty bins to those of every
+// CTA of the cluster through distributed shared memory (weights fill a hundred
+// or two of the 2048 bins; reading all bins of all ranks instead took 7 us a
+// pass).  Then each thread marks what it keeps of its own run of quads in a
+// bit mask; one scan over the CTA, and the counts of the CTAs before it, tell
+// it where to write them.
 //
-// What bounds it: the barriers and the round trips to the cluster's counts,
-// a few of each per pass; 32 rows of 128K weights are 17 MB.
+// What bounds it: the latency of its steps, not the 17 MB that 32 rows of 128K
+// weights are.
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictParams p) {
-    extern __shared__ uint32_t keys[];
-    __shared__ __align__(16) uint32_t hist[kBins];
-    __shared__ uint32_t scratch[33];
-    __shared__ uint32_t chosen[2];  // digit of the threshold, tokens still wanted of it
-    // this CTA's share, read by the cluster: tokens held, of them kept
-    // whatever their weight; above the threshold (those included), equal to it
-    __shared__ uint32_t share[4];
-    __shared__ uint32_t shares[kMaxSelCluster][2];
+    extern __shared__ __align__(16) uint32_t keys[];
+    __shared__ __align__(16) uint32_t hist[kBins];     // this CTA's counts
+    __shared__ __align__(16) uint32_t sums[3][kBins];  // the cluster's, of each pass
+    __shared__ uint32_t scratch[5][kSelThreads / 32];
+    __shared__ uint32_t chosen[3][2];  // of each pass: the threshold's digit, tokens still wanted of it
+    // every CTA's tokens held, and of them those kept whatever their weight;
+    // those above the threshold (the latter included), and those equal to it
+    __shared__ uint32_t shares[kMaxSelCluster][4];
+    __shared__ uint32_t counted[2];
     const int tid = threadIdx.x, lane = tid & 31;
     const int C = (int)p.cluster, rank = (int)blockIdx.x % C;
     const int kvh = (int)blockIdx.x / C, b = blockIdx.y;
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = sums[0][i] = sums[1][i] = sums[2][i] = 0;
+    if (tid < 2) counted[tid] = 0;
+    // (the others' adds may come from here on: every CTA waits for this before its first)
+    if (C > 1) cluster_arrive_release();
+    else __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -107,72 +117,88 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     const int bshift = __ffs(p.block_size) - 1;
     const int recent = T - p.recent;
     const bool wide = (reinterpret_cast<uintptr_t>(p.weights) & 15) == 0;
-    // tokens [t0, t1) of the row, t0 a multiple of 4
-    const int per = ((T + 3) / 4 + C - 1) / C * 4;
-    const int t0 = min(rank * per, T), t1 = min(t0 + per, T), len = t1 - t0;
+    // quads [q0, q0 + nq) of the row
+    const int quads = (T + 3) / 4, per = (quads + C - 1) / C;
+    const int q0 = min(rank * per, quads), nq = min(per, quads - q0);
 
-    auto key_of = [&](int t, float x) {
-        return t < p.sink || t >= recent ? kKeyAlways : weight_key(x);
+    // a quad's page, and its weights (inside the row: its width is a multiple of 16)
+    auto quad_held = [&](int q) { return page_phys(row, (q * 4) >> bshift, npages, p.num_blocks) >= 0; };
+    auto quad_load = [&](int q) {
+        const float* v = w + (size_t)q * 4;
+        return wide ? *reinterpret_cast<const float4*>(v) : make_float4(v[0], v[1], v[2], v[3]);
     };
-    auto page_held = [&](int t) { return page_phys(row, t >> bshift, npages, p.num_blocks) >= 0; };
-    // key of the CTA's token i
-    auto key_at = [&](int i) {
-        if constexpr (CACHED) return keys[key_word(i)];
-        else return page_held(t0 + i) ? key_of(t0 + i, w[t0 + i]) : kKeyAbsent;
-    };
-    auto gather_shares = [&](int first) {  // after a cluster barrier; a block barrier follows
-        if (tid < C * 2)
-            shares[tid >> 1][tid & 1] =
-                ld_cluster_u32(map_cluster_rank(smem_u32(&share[first + (tid & 1)]), tid >> 1));
-        __syncthreads();
-    };
-
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-    if (tid < 4) share[tid] = 0;
-    __syncthreads();
-    uint32_t held = 0, must = 0;
-    auto count_first = [&](uint32_t k) {  // the first pass's counts
-        held += k != kKeyAbsent;
-        must += k == kKeyAlways;
-        if (k != kKeyAbsent && k != kKeyAlways) atomicAdd(&hist[k >> 21], 1u);
-    };
-    if constexpr (CACHED) {
-        // a quad of tokens, which lies in one page, at a time; four quads in flight
-        const int quads = (len + 3) / 4;
-        for (int base = tid; base < quads; base += kSelThreads * 4) {
-            float4 x[4];
-            bool ok[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int q = base + u * kSelThreads;
-                ok[u] = q < quads && page_held(t0 + q * 4);
-                if (!ok[u]) continue;
-                const float* v = w + t0 + q * 4;  // inside the row: its width is a multiple of 16
-                x[u] = wide ? *reinterpret_cast<const float4*>(v) : make_float4(v[0], v[1], v[2], v[3]);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int q = base + u * kSelThreads;
-                if (q >= quads) continue;
-                const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (q * 4 + e < len) {
-                        const uint32_t k = ok[u] ? key_of(t0 + q * 4 + e, v[e]) : kKeyAbsent;
-                        keys[key_word(q * 4 + e)] = k;
-                        count_first(k);
-                    }
-            }
+    auto quad_keys = [&](int q, bool held, const float4& x) {
+        if (!held) return make_uint4(0, 0, 0, 0);
+        uint4 k = make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
+        const int t = q * 4;
+        if (t < p.sink || t + 3 >= recent) {  // at the row's ends: token by token
+            auto end = [&](int u, uint32_t v) {
+                return u >= T ? kKeyAbsent : (u < p.sink || u >= recent ? kKeyAlways : v);
+            };
+            k = make_uint4(end(t, k.x), end(t + 1, k.y), end(t + 2, k.z), end(t + 3, k.w));
         }
-    } else {
-        for (int i = tid; i < len; i += kSelThreads) count_first(key_at(i));
+        return k;
+    };
+    // keys of the CTA's quad i
+    auto keys_at = [&](int i) {
+        if constexpr (CACHED) return *reinterpret_cast<const uint4*>(keys + quad_word(i));
+        const bool held = quad_held(q0 + i);
+        return quad_keys(q0 + i, held, held ? quad_load(q0 + i) : make_float4(0.f, 0.f, 0.f, 0.f));
+    };
+    auto cluster_barrier = [&]() {
+        if (C > 1) cluster_sync_release_acquire();
+        else __syncthreads();
+    };
+    // the same number to every CTA of the cluster, before a cluster barrier
+    auto tell = [&](int which, uint32_t v) {
+        for (int r = 0; r < C; ++r)
+            st_cluster_u32(map_cluster_rank(smem_u32(&shares[rank][which]), r), v);
+    };
+
+    // the keys, and the first pass's counts: eight quads in flight (the
+    // weights of a masked page are loaded like the others, and not used)
+    uint32_t held = 0, must = 0;
+    auto count_first = [&](uint32_t k) {
+        if (k == kKeyAlways) ++must;
+        else if (k != kKeyAbsent) {
+            ++held;
+            atomicAdd(&hist[k >> 21], 1u);
+        }
+    };
+    if (C > 1) cluster_wait_acquire();  // (also a barrier of the CTA: hist is zero)
+    for (int base = tid; base < nq; base += kSelThreads * 8) {
+        float4 x[8];
+        bool ok[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int q = base + u * kSelThreads;
+            x[u] = q < nq ? quad_load(q0 + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+            ok[u] = q < nq && quad_held(q0 + q);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int q = base + u * kSelThreads;
+            if (q >= nq) continue;
+            const uint4 k = quad_keys(q0 + q, ok[u], x[u]);
+            if constexpr (CACHED) *reinterpret_cast<uint4*>(keys + quad_word(q)) = k;
+            count_first(k.x);
+            count_first(k.y);
+            count_first(k.z);
+            count_first(k.w);
+        }
     }
     held = __reduce_add_sync(kFullMask, held);
     must = __reduce_add_sync(kFullMask, must);
     if (lane == 0) {
-        atomicAdd(&share[0], held);
-        atomicAdd(&share[1], must);
+        atomicAdd(&counted[0], held + must);
+        atomicAdd(&counted[1], must);
     }
+
+    // a thread's run of quads: a power of two up to eight, then whole eights
+    int run = 1;
+    while (run < 8 && run * kSelThreads < nq) run *= 2;
+    if (run == 8) run = ((nq + kSelThreads - 1) / kSelThreads + 7) / 8 * 8;
+    const int i0 = min(tid * run, nq), i1 = min(i0 + run, nq);
 
     uint32_t prefix = 0, mask = 0, want = 0, n = 0;
     bool all = false;
@@ -181,32 +207,37 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
         const uint32_t digit = pass == 2 ? 1023u : 2047u;
         if (pass > 0) {
-#pragma unroll 8
-            for (int i = tid; i < len; i += kSelThreads) {
-                const uint32_t k = key_at(i);
+            auto count = [&](uint32_t k) {
                 if ((k & mask) == prefix && k != kKeyAbsent && k != kKeyAlways)
                     atomicAdd(&hist[(k >> shift) & digit], 1u);
+            };
+#pragma unroll 4
+            for (int i = i0; i < i1; ++i) {
+                const uint4 k = keys_at(i);
+                count(k.x);
+                count(k.y);
+                count(k.z);
+                count(k.w);
             }
         }
-        cluster_sync_release_acquire();  // every CTA's counts are in place
-        // the cluster's counts of bins 4 tid .. 4 tid + 3
-        uint4 c = make_uint4(0, 0, 0, 0);
-        {
-            const uint32_t at = smem_u32(hist) + 16u * tid;
-            uint4 x[kMaxSelCluster];
-#pragma unroll
-            for (int r = 0; r < kMaxSelCluster; ++r)
-                x[r] = r < C ? ld_cluster_v4u32(map_cluster_rank(at, r)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < kMaxSelCluster; ++r) {
-                c.x += x[r].x;
-                c.y += x[r].y;
-                c.z += x[r].z;
-                c.w += x[r].w;
+        __syncthreads();  // this CTA's counts are complete
+        uint4 c = *reinterpret_cast<const uint4*>(hist + 4 * tid);
+        if (C > 1) {
+            // the non-empty ones of this thread's four bins, to every CTA
+            for (int r = 0; r < C; ++r) {
+                const uint32_t at = map_cluster_rank(smem_u32(&sums[pass][4 * tid]), r);
+                if (c.x) red_cluster_add(at, c.x);
+                if (c.y) red_cluster_add(at + 4, c.y);
+                if (c.z) red_cluster_add(at + 8, c.z);
+                if (c.w) red_cluster_add(at + 12, c.w);
             }
         }
+        // (read by this thread alone, and counted into again after the barrier)
+        *reinterpret_cast<uint4*>(hist + 4 * tid) = make_uint4(0, 0, 0, 0);
+        if (pass == 0 && tid < 2) tell(tid, counted[tid]);
+        cluster_barrier();
+        if (C > 1) c = *reinterpret_cast<const uint4*>(&sums[pass][4 * tid]);
         if (pass == 0) {
-            gather_shares(0);
             uint32_t valid = 0, fixed = 0;
             for (int r = 0; r < C; ++r) {
                 valid += shares[r][0];
@@ -219,10 +250,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         }
         // the want-th largest: its rank from below among the cluster's counts
         uint32_t total;
-        const uint32_t before = block_exclusive(c.x + c.y + c.z + c.w, scratch, &total);
+        const uint32_t before = block_exclusive(c.x + c.y + c.z + c.w, scratch[pass], &total);
         if (tid == 0 && want == 0) {  // nothing is wanted: above every key
-            chosen[0] = digit;
-            chosen[1] = 0;
+            chosen[pass][0] = digit;
+            chosen[pass][1] = 0;
         }
         const uint32_t below = total - want;  // candidates left out
         if (want > 0 && below >= before && below < before + c.x + c.y + c.z + c.w) {
@@ -230,40 +261,34 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
             uint32_t s = before;
             int d = 0;
             while (d < 3 && below >= s + cs[d]) s += cs[d++];
-            chosen[0] = (uint32_t)(4 * tid + d);
-            chosen[1] = s + cs[d] - below;
+            chosen[pass][0] = (uint32_t)(4 * tid + d);
+            chosen[pass][1] = s + cs[d] - below;
         }
         __syncthreads();
-        prefix |= chosen[0] << shift;
+        prefix |= chosen[pass][0] << shift;
         mask |= digit << shift;
-        want = chosen[1];
-        if (pass < 2) {
-            cluster_sync_release_acquire();  // the counts have been read
-            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
-        }
+        want = chosen[pass][1];
     }
 
-    // this thread's run of the CTA's keys: how many it surely keeps, how many
-    // equal the threshold, of which the row keeps its lowest `want`
-    const int run = (len + kSelThreads - 1) / kSelThreads;
-    const int i0 = min(tid * run, len), i1 = min(i0 + run, len);
-    // (a bit for each of 32 tokens; with `all`, prefix is 0 = absent: no token equals it)
+    // what this thread surely keeps of its run, and what equals the threshold,
+    // of which the row keeps its lowest `want`: a bit for each token of eight quads
+    // (with `all` the prefix is 0 = absent: every other key is above it)
     auto masks = [&](int i, uint32_t& s, uint32_t& e) {
         s = e = 0;
-#pragma unroll 8
-        for (int u = 0; u < 32; ++u) {
-            if (i + u >= i1) break;
-            const uint32_t k = key_at(i + u);
-            s |= (uint32_t)(k > prefix) << u;
-            e |= (uint32_t)(k == prefix) << u;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint4 k = i + u < i1 ? keys_at(i + u) : make_uint4(0, 0, 0, 0);
+            s |= ((uint32_t)(k.x > prefix) | (uint32_t)(k.y > prefix) << 1 |
+                  (uint32_t)(k.z > prefix) << 2 | (uint32_t)(k.w > prefix) << 3) << (4 * u);
+            e |= ((uint32_t)(k.x == prefix) | (uint32_t)(k.y == prefix) << 1 |
+                  (uint32_t)(k.z == prefix) << 2 | (uint32_t)(k.w == prefix) << 3) << (4 * u);
         }
         // (with nothing wanted the threshold is the key of the tokens always kept)
         if (prefix == kKeyAlways) s = e;
         if (prefix == kKeyAbsent || prefix == kKeyAlways) e = 0;
     };
     uint32_t sure = 0, equal = 0, s0 = 0, e0 = 0;
-    for (int i = i0; i < i1; i += 32) {
+    for (int i = i0; i < i1; i += 8) {
         uint32_t s, e;
         masks(i, s, e);
         if (i == i0) {
@@ -274,31 +299,37 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         equal += __popc(e);
     }
     uint32_t sures, equals;
-    sure = block_exclusive(sure, scratch, &sures);
-    equal = block_exclusive(equal, scratch, &equals);
-    if (tid == 0) {
-        share[2] = sures;
-        share[3] = equals;
+    if constexpr (CACHED) {  // both below 2^16: one scan
+        static_assert(kMaxCached < 65536, "packed counts");
+        const uint32_t at = block_exclusive(sure | equal << 16, scratch[3], &sures);
+        sure = at & 0xffffu;
+        equal = at >> 16;
+        equals = sures >> 16;
+        sures &= 0xffffu;
+    } else {
+        sure = block_exclusive(sure, scratch[3], &sures);
+        equal = block_exclusive(equal, scratch[4], &equals);
     }
-    cluster_sync_release_acquire();
-    gather_shares(2);
+    if (tid < 2) tell(2 + tid, tid == 0 ? sures : equals);
+    cluster_barrier();  // (the last access to another CTA's memory is before it)
     uint32_t begin = 0, left = want;  // where this CTA's list begins; equal tokens still wanted
     for (int r = 0; r < rank; ++r) {
-        const uint32_t eq = min(left, shares[r][1]);
-        begin += shares[r][0] + eq;
+        const uint32_t eq = min(left, shares[r][3]);
+        begin += shares[r][2] + eq;
         left -= eq;
     }
     uint32_t j = begin + sure;  // plus the kept ones of the equal tokens before
-    for (int i = i0; i < i1; i += 32) {
+    for (int i = i0; i < i1; i += 8) {
         uint32_t s = s0, e = e0;
         if (i > i0) masks(i, s, e);
+        const int t = (q0 + i) * 4;
         for (uint32_t any = s | e; any; any &= any - 1) {
             const int u = __ffs(any) - 1;
             if ((s >> u) & 1u) {
-                kept[j + min(equal, left)] = t0 + i + u;
+                kept[j + min(equal, left)] = t + u;
                 ++j;
             } else {
-                if (equal < left) kept[j + equal] = t0 + i + u;
+                if (equal < left) kept[j + equal] = t + u;
                 ++equal;
             }
         }
@@ -307,7 +338,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         for (int i = (int)n + tid; i < p.budget; i += kSelThreads) kept[i] = -1;
         if (kvh == 0 && tid == 0) p.new_lens[b] = (int32_t)n;
     }
-    cluster_sync_relaxed();  // no CTA leaves while others still read its counts
 }
 
 // A row (slot) of the cache, in 16-byte vectors, of token t of a table row;
@@ -459,7 +489,7 @@ cudaError_t launch_evict(EvictParams p, bool in_place, bool pdl, cudaStream_t st
         static AttrFlags smem_limit;
         e = raise_smem_limit_once(evict_select_kernel<true>, smem_limit);
         if (e != cudaSuccess) return e;
-        cfg.dynamicSmemBytes = (size_t)(per + per / 32 + 1) * sizeof(uint32_t);
+        cfg.dynamicSmemBytes = (size_t)(per + (per / 32 + 1) * 4) * sizeof(uint32_t);
         e = cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p);
     } else {
         e = cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p);

@@ -99,6 +99,8 @@ struct WeightParams {
     int32_t token_limit;      // tokens from here on were not attended
     const float* scores;      // as in AttnParams
     int64_t score_width;
+    int32_t* err;             // device error word, bound on every wait (tile kernel)
+    uint64_t timeout_ns;
 };
 
 // Rotary positions and the append to the cache (strides in elements, between
@@ -393,8 +395,12 @@ cudaError_t launch_prefix_combine(const PrefixCombineParams& p, int head_dim, in
                                   cudaStream_t stream);
 // The same from stored scores (p.scores), up to 16 rows per kv head.
 cudaError_t launch_weights_of_scores(const WeightParams& p, bool pdl, cudaStream_t stream);
-cudaError_t launch_weights(const WeightParams& p, int head_dim, int kv_dtype, int max_tokens,
-                           bool pdl, cudaStream_t stream);
+// On the tensor cores, for many rows; k: the keys' pages, q: boxes of 64 columns
+// and weights_tile_chunk(head_dim) query rows.
+int weights_tile_chunk(int head_dim);
+cudaError_t launch_weights_tile(const WeightParams& p, int head_dim, int kv_dtype,
+                                const CUtensorMap& k, const CUtensorMap& q, bool pdl,
+                                cudaStream_t stream);
 cudaError_t launch_append(void* k_cache, void* v_cache, const void* k_new, const void* v_new,
                           const int32_t* block_tables, const int32_t* positions, int32_t batch,
                           int32_t max_blocks, int32_t block_size, int64_t num_blocks,

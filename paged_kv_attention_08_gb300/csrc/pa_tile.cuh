@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     // high and a low part, hi in columns [0, BN/2) and lo in [BN/2, BN)
                     // of the buffer; for fp16 the high part alone
                     const float me = (m == NEG_INF) ? 0.f : m;
-                    if (!dead) {
+                    auto form_p = [&](auto exact_l) {
 #pragma unroll
                         for (int c0 = 0; c0 < BH; c0 += 16) {
                             uint32_t ph[8], pl[8];
@@ -846,6 +846,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                     Mma<KV>::unpack(h, h0, h1);
                                     l += x0 + x1;
                                     pl[c / 2] = Mma<KV>::pack(x0 - h0, x1 - h1);
+                                } else if constexpr (decltype(exact_l)::value) {
+                                    l += x0 + x1;
                                 } else {
                                     l = Mma<KV>::add2(h, l);  // the weights the MMA uses
                                 }
@@ -860,6 +862,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             tc::st_32x32b_x8(sb + col_hi, ph);
                             if (kSplitP) tc::st_32x32b_x8(sb + col_lo, pl);
                         }
+                    };
+                    // (row statistics wanted: the normaliser of the weights as they
+                    // are, since those of the tokens are formed from it)
+                    if (!dead) {
+                        if (!kSplitP && p.lse) form_p(std::true_type{});
+                        else form_p(std::false_type{});
                     }
                     tc::wait_st();
                     // zero the V rows of masked pages and past the segment's last
