@@ -380,22 +380,86 @@ def append_kv(k_cache, v_cache, k_new, v_new, block_tables, positions, stream=No
                                 ctypes.byref(shape), _stream_ptr(stream)), "pa_append_kv")
 
 
-class _launch_on:
-    """Makes the tensors' device the current one for a call, and names the
-    stream to launch on: the given one, or that device's current stream."""
+# The serving-step entry points below run once per layer and step, where the
+# binding's own time shows: they check with as few calls as that takes, and
+# launch on the tensors' device whatever the current one is.
 
-    def __init__(self, tensor, stream):
-        self._guard = torch.cuda.device(tensor.device)
-        if stream is not None and stream.device != tensor.device:
-            raise ValueError("stream is on another device than the tensors")
-        self._stream = stream if stream is not None else torch.cuda.current_stream(tensor.device)
+def _device_of(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    return dev
 
-    def __enter__(self):
-        self._guard.__enter__()
-        return self._stream
 
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+def _same_device(dev: int, ts, contiguous: bool = True):
+    for t in ts:
+        if t.get_device() != dev:
+            raise ValueError("all tensors must be CUDA tensors on one device")
+        if contiguous and not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+
+
+def _stream_on(dev: int, stream) -> int:
+    """The given stream, or the device's current one, for the C ABI."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError("stream is on another device than the tensors")
+    return stream.cuda_stream
+
+
+_KV_CODE = {torch.float16: F16, torch.bfloat16: BF16}
+
+
+def _attention_shape(out, q, k_cache, v_cache, block_tables, context_lens):
+    """Checks what ``_check_args`` checks; pa_shape and q_len of a one-token
+    ([B, H, D]) or several-token ([B, Q, H, D]) query."""
+    qs, ks, bts = q.shape, k_cache.shape, block_tables.shape
+    if len(qs) == 3:
+        B, H, D = qs
+        Q = 1
+    elif len(qs) == 4:
+        B, Q, H, D = qs
+        if Q < 1:
+            raise ValueError("q_len must be at least 1")
+    else:
+        raise ValueError("q must be [batch, num_heads, head_dim] or "
+                         "[batch, q_len, num_heads, head_dim]")
+    if len(ks) != 4 or v_cache.shape != ks:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
+                         "num_kv_heads, head_dim]")
+    dt, odt = k_cache.dtype, out.dtype
+    if q.dtype != dt or v_cache.dtype != dt:
+        raise TypeError("q and both caches must have one dtype")
+    if dt not in _KV_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    if D != ks[3]:
+        raise ValueError(f"q's head_dim {D} differs from the cache's {ks[3]}")
+    if out.shape != qs:
+        raise ValueError(f"out {tuple(out.shape)} must be shaped like q {tuple(qs)}")
+    if odt != dt and odt != torch.float32:
+        raise TypeError("out must be float32 or q's dtype")
+    if len(bts) != 2 or bts[0] != B:
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq]")
+    if context_lens.shape != (B,):
+        raise ValueError("context_lens must be [batch]")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    code = _KV_CODE[dt]
+    return _Shape(B, H, ks[2], D, ks[1], bts[1], ks[0], code, code if odt == dt else F32), Q
+
+
+def _workspace_for(workspace, need, dev: int, stream):
+    """The caller's workspace, or one from torch's allocator: (tensor, bytes).
+    One taken here belongs to the stream that the call launches on."""
+    if workspace is None:
+        if need > 1 << 62:
+            raise PaError(3, "workspace")
+        with torch.cuda.stream(stream):  # (None: the current stream)
+            workspace = torch.empty(max(int(need), 16), dtype=torch.uint8, device=f"cuda:{dev}")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def rope_phases(inv_freq: torch.Tensor) -> torch.Tensor:
@@ -411,19 +475,20 @@ def rope_phases(inv_freq: torch.Tensor) -> torch.Tensor:
     return (turns * 2.0 ** 64).to(torch.int64)
 
 
-def _token_stride(t, name, heads, head_dim, batch, q_len):
+def _token_stride(t, name, shape):
     """Elements between consecutive tokens of a [batch, q_len, heads, head_dim]
     view whose tokens lie evenly apart and whose rows are contiguous."""
-    if tuple(t.shape) != (batch, q_len, heads, head_dim):
-        raise ValueError(f"{name} {tuple(t.shape)} must be {(batch, q_len, heads, head_dim)}")
-    s = t.stride()
-    if s[3] != 1 or (heads > 1 and s[2] != head_dim):
+    if t.shape != shape:
+        raise ValueError(f"{name} {tuple(t.shape)} must be {tuple(shape)}")
+    batch, q_len, heads, head_dim = shape
+    sb, sq, sh, sd = t.stride()
+    if sd != 1 or (heads > 1 and sh != head_dim):
         raise ValueError(f"{name}'s heads must be contiguous")
     if q_len == 1:
-        return s[0] if batch > 1 else max(s[0], heads * head_dim)
-    if batch > 1 and s[0] != q_len * s[1]:
+        return sb if batch > 1 else heads * head_dim
+    if batch > 1 and sb != q_len * sq:
         raise ValueError(f"{name}'s tokens must lie evenly apart")
-    return s[1]
+    return sq
 
 
 def rope_append_kv(q_out, k_cache, v_cache, q, k_new, v_new, rotary_positions, phases, axes,
@@ -444,89 +509,84 @@ def rope_append_kv(q_out, k_cache, v_cache, q, k_new, v_new, rotary_positions, p
                        v_new.unsqueeze(1), rotary_positions.unsqueeze(2), phases, axes,
                        block_tables, context_lens, interleaved, stream)
         return q_out
-    if q.dim() != 4:
+    qs, ks, bts, rs = q.shape, k_cache.shape, block_tables.shape, rotary_positions.shape
+    if len(qs) != 4:
         raise ValueError("q must be [batch, q_len, num_heads, head_dim]")
-    if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape):
+    if len(ks) != 4 or v_cache.shape != ks:
         raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
                          "num_kv_heads, head_dim]")
-    if any(t.dtype != k_cache.dtype for t in (v_cache, q, q_out, k_new, v_new)):
+    dt = k_cache.dtype
+    if v_cache.dtype != dt or q.dtype != dt or q_out.dtype != dt or k_new.dtype != dt or \
+            v_new.dtype != dt:
         raise TypeError("queries, new keys/values and both caches must have one dtype")
-    B, Q, H, D = q.shape
-    NB, bs, Hkv, cache_d = k_cache.shape
+    if dt not in _KV_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    B, Q, H, D = qs
+    NB, bs, Hkv, cache_d = ks
     if cache_d != D:
         raise ValueError(f"q's head_dim {D} differs from the cache's {cache_d}")
     if Q < 1:
         raise ValueError("q_len must be at least 1")
-    rope = _Rope(0, 0, int(bool(interleaved)), 0, _token_stride(q, "q", H, D, B, Q),
-                 _token_stride(q_out, "q_out", H, D, B, Q),
-                 _token_stride(k_new, "k_new", Hkv, D, B, Q),
-                 _token_stride(v_new, "v_new", Hkv, D, B, Q))
-    if rotary_positions.dim() != 3 or tuple(rotary_positions.shape[1:]) != (B, Q):
+    if len(rs) != 3 or rs[1] != B or rs[2] != Q:
         raise ValueError("rotary_positions must be [axes, batch, q_len]")
+    pairs = phases.numel()
     if rotary_positions.dtype != torch.int32 or axes.dtype != torch.int32:
         raise TypeError("rotary_positions and axes must be int32")
     if phases.dtype != torch.int64:
         raise TypeError("phases must be the int64 table of rope_phases")
-    if phases.dim() != 1 or tuple(axes.shape) != tuple(phases.shape):
+    if phases.dim() != 1 or axes.shape != (pairs,):
         raise ValueError("phases and axes must hold one value per rotary pair")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+    if len(bts) != 2 or bts[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [batch, max_blocks_per_seq], context_lens [batch]")
-    _ints(block_tables, context_lens)
-    _dev_tensors(k_cache, v_cache, rotary_positions, phases, axes, block_tables, context_lens)
-    for t in (q, q_out, k_new, v_new):
-        if t.device != k_cache.device:
-            raise ValueError("all tensors must be on one device")
-    rope.rotary_dim, rope.num_axes = 2 * phases.numel(), rotary_positions.shape[0]
-    shape = _Shape(B, H, Hkv, D, bs, block_tables.shape[1], NB, _dtype_code(k_cache.dtype), F32)
-    with _launch_on(k_cache, stream) as on:
-        _check(_load().pa_rope_append_kv(
-            q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), q.data_ptr(),
-            k_new.data_ptr(), v_new.data_ptr(), rotary_positions.data_ptr(), phases.data_ptr(),
-            axes.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), ctypes.byref(shape),
-            Q, ctypes.byref(rope), on.cuda_stream), "pa_rope_append_kv")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    rope = _Rope(2 * pairs, rs[0], 1 if interleaved else 0, 0,
+                 _token_stride(q, "q", qs), _token_stride(q_out, "q_out", qs),
+                 _token_stride(k_new, "k_new", (B, Q, Hkv, D)),
+                 _token_stride(v_new, "v_new", (B, Q, Hkv, D)))
+    dev = _device_of(k_cache)
+    _same_device(dev, (k_cache, v_cache, rotary_positions, phases, axes, block_tables, context_lens))
+    _same_device(dev, (q, q_out, k_new, v_new), contiguous=False)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rope_append_kv(q_out, k_cache, v_cache, q, k_new, v_new, rotary_positions,
+                                  phases, axes, block_tables, context_lens, interleaved, stream)
+    _check((_lib or _load()).pa_rope_append_kv(
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), q.data_ptr(), k_new.data_ptr(),
+        v_new.data_ptr(), rotary_positions.data_ptr(), phases.data_ptr(), axes.data_ptr(),
+        block_tables.data_ptr(), context_lens.data_ptr(),
+        _Shape(B, H, Hkv, D, bs, bts[1], NB, _KV_CODE[dt], F32), Q, rope,
+        _stream_on(dev, stream)), "pa_rope_append_kv")
     return q_out
 
 
-def _any_shape(q, k_cache, block_tables, out_dtype):
-    """pa_shape and q_len of a one-token or a multi-token query."""
+def _sizing_shape(q, k_cache, block_tables, out_dtype):
+    """pa_shape, q_len and device for a workspace query."""
     if q.dim() == 4:
-        return _multi_shape(q, k_cache, block_tables, out_dtype)
-    return make_shape(q, k_cache, block_tables, out_dtype), 1
+        shape, q_len = _multi_shape(q, k_cache, block_tables, out_dtype)
+    else:
+        shape, q_len = make_shape(q, k_cache, block_tables, out_dtype), 1
+    return shape, q_len, _device_of(k_cache)
 
 
-def _workspace(workspace, need, like, on):
-    """The caller's workspace, or one from torch's allocator on the launch's stream."""
-    if workspace is None:
-        if need > 1 << 62:
-            raise PaError(3, "workspace")
-        with torch.cuda.stream(on):
-            return torch.empty(max(int(need), 16), dtype=torch.uint8, device=like.device)
-    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != like.device:
-        raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
-    return workspace
-
-
-def _check_prefixes(prefix_tables, prefix_lens, batch):
-    if prefix_tables.dim() != 2 or prefix_tables.shape[0] < 1 or batch % prefix_tables.shape[0]:
+def _check_prefixes(prefix_tables, batch):
+    shape = prefix_tables.shape
+    if len(shape) != 2 or shape[0] < 1 or batch % shape[0]:
         raise ValueError("prefix_tables must be [prefixes, max_prefix_blocks], with as many "
                          "sequences for each prefix")
-    if prefix_lens is not None and tuple(prefix_lens.shape) != (prefix_tables.shape[0],):
-        raise ValueError("prefix_lens must be [prefixes]")
-    if prefix_tables.dtype != torch.int32 or \
-            (prefix_lens is not None and prefix_lens.dtype != torch.int32):
-        raise TypeError("prefix_tables and prefix_lens must be int32")
+    if prefix_tables.dtype != torch.int32:
+        raise TypeError("prefix_tables must be int32")
+    return shape
 
 
 def workspace_size_shared_prefix(q, k_cache, prefix_tables, block_tables, out_dtype,
                                  max_prefix_len: int, max_context_len: int) -> int:
     """Bytes of workspace that ``decode_shared_prefix`` takes, on the tensors' device."""
-    shape, q_len = _any_shape(q, k_cache, block_tables, out_dtype)
-    _check_prefixes(prefix_tables, None, shape.batch)
-    _dev_tensors(q, k_cache)
-    with _launch_on(k_cache, None):
+    shape, q_len, dev = _sizing_shape(q, k_cache, block_tables, out_dtype)
+    P, mpb = _check_prefixes(prefix_tables, shape.batch)
+    with torch.cuda.device(dev):
         return int(_load().pa_workspace_size_shared_prefix(
-            ctypes.byref(shape), prefix_tables.shape[0], prefix_tables.shape[1], q_len,
-            int(max_prefix_len), int(max_context_len)))
+            shape, P, mpb, q_len, int(max_prefix_len), int(max_context_len)))
 
 
 def decode_shared_prefix(out, q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables,
@@ -539,31 +599,37 @@ def decode_shared_prefix(out, q, k_cache, v_cache, prefix_tables, prefix_lens, b
     lengths count the Q new tokens, causal among themselves).  ``workspace``: a
     CUDA byte tensor of ``workspace_size_shared_prefix(...)`` bytes, else one
     is taken from torch's allocator."""
-    _check_args(out, q, k_cache, v_cache, block_tables, context_lens, multi=q.dim() == 4)
-    shape, q_len = _any_shape(q, k_cache, block_tables, out.dtype)
-    _check_prefixes(prefix_tables, prefix_lens, shape.batch)
-    _dev_tensors(out, q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables, context_lens)
-    lib, (P, mpb) = _load(), prefix_tables.shape
-    with _launch_on(k_cache, stream) as on:
-        need = 0 if workspace is not None else lib.pa_workspace_size_shared_prefix(
-            ctypes.byref(shape), P, mpb, q_len, int(max_prefix_len), int(max_context_len))
-        ws = _workspace(workspace, need, k_cache, on)
-        _check(lib.pa_decode_shared_prefix(
-            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            prefix_tables.data_ptr(), prefix_lens.data_ptr(), block_tables.data_ptr(),
-            context_lens.data_ptr(), ctypes.byref(shape), P, mpb, q_len, float(scale),
-            int(max_prefix_len), int(max_context_len), ws.data_ptr(),
-            ws.numel() * ws.element_size(), on.cuda_stream), "pa_decode_shared_prefix")
+    shape, q_len = _attention_shape(out, q, k_cache, v_cache, block_tables, context_lens)
+    P, mpb = _check_prefixes(prefix_tables, shape.batch)
+    if prefix_lens.shape != (P,):
+        raise ValueError("prefix_lens must be [prefixes]")
+    if prefix_lens.dtype != torch.int32:
+        raise TypeError("prefix_lens must be int32")
+    dev = _device_of(k_cache)
+    _same_device(dev, (out, q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables,
+                       context_lens))
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return decode_shared_prefix(out, q, k_cache, v_cache, prefix_tables, prefix_lens,
+                                        block_tables, context_lens, scale, max_prefix_len,
+                                        max_context_len, workspace, stream)
+    lib = _lib or _load()
+    need = 0 if workspace is not None else lib.pa_workspace_size_shared_prefix(
+        shape, P, mpb, q_len, max_prefix_len, max_context_len)
+    ws, ws_bytes = _workspace_for(workspace, need, dev, stream)
+    _check(lib.pa_decode_shared_prefix(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        prefix_tables.data_ptr(), prefix_lens.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), shape, P, mpb, q_len, scale, max_prefix_len, max_context_len,
+        ws.data_ptr(), ws_bytes, _stream_on(dev, stream)), "pa_decode_shared_prefix")
     return out
 
 
 def workspace_size_accumulate(q, k_cache, block_tables, out_dtype, max_context_len: int) -> int:
     """Bytes of workspace that ``decode_accumulate`` takes, on the tensors' device."""
-    shape, q_len = _any_shape(q, k_cache, block_tables, out_dtype)
-    _dev_tensors(q, k_cache)
-    with _launch_on(k_cache, None):
-        return int(_load().pa_workspace_size_accumulate(ctypes.byref(shape), q_len,
-                                                        int(max_context_len)))
+    shape, q_len, dev = _sizing_shape(q, k_cache, block_tables, out_dtype)
+    with torch.cuda.device(dev):
+        return int(_load().pa_workspace_size_accumulate(shape, q_len, int(max_context_len)))
 
 
 def decode_accumulate(out, new_weights, q, k_cache, v_cache, block_tables, context_lens,
@@ -575,25 +641,28 @@ def decode_accumulate(out, new_weights, q, k_cache, v_cache, block_tables, conte
     sum p (fp32 [B, Hkv, max_blocks * block_size]; ``weights`` omitted: in place).
     Entries past a sequence's tokens are not written."""
     weights = new_weights if weights is None else weights
-    _check_args(out, q, k_cache, v_cache, block_tables, context_lens, multi=q.dim() == 4)
-    shape, q_len = _any_shape(q, k_cache, block_tables, out.dtype)
+    shape, q_len = _attention_shape(out, q, k_cache, v_cache, block_tables, context_lens)
     want = (shape.batch, shape.num_kv_heads, shape.max_blocks_per_seq * shape.block_size)
-    if tuple(weights.shape) != want or tuple(new_weights.shape) != want:
+    if weights.shape != want or new_weights.shape != want:
         raise ValueError(f"weights and new_weights must be {want}")
     if weights.dtype != torch.float32 or new_weights.dtype != torch.float32:
         raise TypeError("weights and new_weights must be float32")
-    _dev_tensors(out, q, k_cache, v_cache, block_tables, context_lens, weights, new_weights)
-    lib = _load()
-    with _launch_on(k_cache, stream) as on:
-        need = 0 if workspace is not None else lib.pa_workspace_size_accumulate(
-            ctypes.byref(shape), q_len, int(max_context_len))
-        ws = _workspace(workspace, need, k_cache, on)
-        _check(lib.pa_decode_accumulate(
-            out.data_ptr(), new_weights.data_ptr(), weights.data_ptr(), q.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            context_lens.data_ptr(), ctypes.byref(shape), q_len, float(scale),
-            int(max_context_len), ws.data_ptr(), ws.numel() * ws.element_size(), on.cuda_stream),
-            "pa_decode_accumulate")
+    dev = _device_of(k_cache)
+    _same_device(dev, (out, q, k_cache, v_cache, block_tables, context_lens, weights, new_weights))
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return decode_accumulate(out, new_weights, q, k_cache, v_cache, block_tables,
+                                     context_lens, scale, max_context_len, weights, workspace,
+                                     stream)
+    lib = _lib or _load()
+    need = 0 if workspace is not None else lib.pa_workspace_size_accumulate(
+        shape, q_len, max_context_len)
+    ws, ws_bytes = _workspace_for(workspace, need, dev, stream)
+    _check(lib.pa_decode_accumulate(
+        out.data_ptr(), new_weights.data_ptr(), weights.data_ptr(), q.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+        shape, q_len, scale, max_context_len, ws.data_ptr(), ws_bytes, _stream_on(dev, stream)),
+        "pa_decode_accumulate")
     return out
 
 
@@ -607,38 +676,46 @@ def evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_ta
     themselves as the new ones works in place.  ``kept`` (int32 [B, Hkv,
     budget]) receives the kept tokens' former positions, ``new_lens`` (int32
     [B]) the new lengths."""
-    if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape):
+    ks, bts, nbts, kts = k_cache.shape, block_tables.shape, new_block_tables.shape, kept.shape
+    if len(ks) != 4 or v_cache.shape != ks:
         raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
                          "num_kv_heads, head_dim]")
-    if v_cache.dtype != k_cache.dtype:
+    dt = k_cache.dtype
+    if v_cache.dtype != dt:
         raise TypeError("v_cache must have k_cache's dtype")
-    NB, bs, Hkv, D = k_cache.shape
-    if block_tables.dim() != 2 or new_block_tables.dim() != 2 or \
-            new_block_tables.shape[0] != block_tables.shape[0]:
+    if dt not in _KV_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    if len(bts) != 2 or len(nbts) != 2 or nbts[0] != bts[0]:
         raise ValueError("block_tables and new_block_tables must be [batch, max_blocks_per_seq]")
-    B, mb = block_tables.shape
-    new_mb = new_block_tables.shape[1]
-    if tuple(weights.shape) != (B, Hkv, mb * bs) or tuple(new_weights.shape) != (B, Hkv, new_mb * bs):
+    NB, bs, Hkv, D = ks
+    B, mb = bts
+    new_mb = nbts[1]
+    if weights.shape != (B, Hkv, mb * bs) or new_weights.shape != (B, Hkv, new_mb * bs):
         raise ValueError("weights and new_weights must be [batch, num_kv_heads, their table's "
                          "max_blocks * block_size]")
     if weights.dtype != torch.float32 or new_weights.dtype != torch.float32:
         raise TypeError("weights and new_weights must be float32")
-    if tuple(context_lens.shape) != (B,) or tuple(new_lens.shape) != (B,):
+    if context_lens.shape != (B,) or new_lens.shape != (B,):
         raise ValueError("context_lens and new_lens must be [batch]")
-    if kept.dim() != 3 or tuple(kept.shape[:2]) != (B, Hkv):
+    if len(kts) != 3 or kts[0] != B or kts[1] != Hkv:
         raise ValueError("kept must be [batch, num_kv_heads, budget]")
-    _ints(block_tables, context_lens)
-    if any(t.dtype != torch.int32 for t in (new_block_tables, new_lens, kept)):
-        raise TypeError("new_block_tables, new_lens and kept must be int32")
-    _dev_tensors(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables,
-                 new_weights, new_lens, kept)
-    shape = _Shape(B, Hkv, Hkv, D, bs, mb, NB, _dtype_code(k_cache.dtype), F32)
-    with _launch_on(k_cache, stream) as on:
-        _check(_load().pa_evict_kv(
-            k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_tables.data_ptr(),
-            context_lens.data_ptr(), new_block_tables.data_ptr(), new_weights.data_ptr(),
-            new_lens.data_ptr(), kept.data_ptr(), ctypes.byref(shape), new_mb, kept.shape[2],
-            int(sink), int(recent), on.cuda_stream), "pa_evict_kv")
+    i32 = torch.int32
+    if block_tables.dtype != i32 or context_lens.dtype != i32 or new_block_tables.dtype != i32 or \
+            new_lens.dtype != i32 or kept.dtype != i32:
+        raise TypeError("block tables, lengths and kept must be int32")
+    dev = _device_of(k_cache)
+    _same_device(dev, (k_cache, v_cache, weights, block_tables, context_lens, new_block_tables,
+                       new_weights, new_lens, kept))
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return evict_kv(k_cache, v_cache, weights, block_tables, context_lens,
+                            new_block_tables, new_weights, new_lens, kept, sink, recent, stream)
+    _check((_lib or _load()).pa_evict_kv(
+        k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), new_block_tables.data_ptr(), new_weights.data_ptr(),
+        new_lens.data_ptr(), kept.data_ptr(),
+        _Shape(B, Hkv, Hkv, D, bs, mb, NB, _KV_CODE[dt], F32), new_mb, kts[2], sink, recent,
+        _stream_on(dev, stream)), "pa_evict_kv")
     return new_lens
 
 
