@@ -259,6 +259,7 @@ struct Plan {
     bool partials = false;              // leave (m, l, acc) in the workspace even of one partition
     const int32_t* own_lens = nullptr;  // a shared prefix: see AttnParams
     int32_t own_q = 0;
+    bool late_wait = false;             // see AttnParams
     float* lse = nullptr;               // row statistics wanted: see AttnParams
     float* scores = nullptr;            // scores wanted: see AttnParams
     int64_t score_width = 0;
@@ -777,6 +778,7 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     if (plan.balanced) p.final_out = 0;
     p.own_lens = plan.own_lens;
     p.own_q = plan.own_q;
+    p.late_wait = plan.late_wait ? 1 : 0;
     p.lse = plan.lse;
     p.scores = plan.scores;
     p.score_width = plan.score_width;
@@ -837,6 +839,7 @@ pa_status launch_tile(void* out, const void* q, const void* k, const void* v, co
     p.cluster_reduce = plan.cluster ? 1 : 0;
     p.own_lens = plan.own_lens;
     p.own_q = plan.own_q;
+    p.late_wait = plan.late_wait ? 1 : 0;
     p.lse = plan.lse;
     p.timeout_ns = kDefaultTimeoutNs;
     L.head_dim = s->head_dim;
@@ -908,17 +911,35 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
                       int32_t max_prefix_len, int32_t max_context_len, int sms, PrefixPlan* pp) {
     pp->pre = *pre;
     pp->pre_q = s->batch / pre->batch * q_len;
-    // the library's own split of each part, its partials always left in the
-    // workspace for the join
+    // The library's split of each part, its partials always left in the
+    // workspace for the join.  No cluster reduces here, so the tile kernel takes
+    // as many partitions as fit in one wave (16 units of 8191 tokens: 9 each, not
+    // the 6 of a cluster split); and where the own pages' units run in several
+    // waves anyway, partitions of 128 pages, not 64, leave fewer partials (1024
+    // units of up to 2048 tokens: 92 us against 98).
     auto split = [&](const pa_shape* sh, int32_t max_len, int32_t q) {
         Plan p = make_plan(sh, max_len, 0, sms, q);
-        if (p.balanced) p = plan_with(sh, pages_for(sh, max_len), pages_for(sh, max_len), false);
-        p.cluster = p.persistent = false;
+        const int pages = pages_for(sh, max_len);
+        const int64_t rows = (int64_t)q * (sh->num_heads / sh->num_kv_heads);
+        const int64_t units = (int64_t)sh->batch * sh->num_kv_heads *
+                              (p.tile ? (rows + kTileRows - 1) / kTileRows : q_chunks_for(sh, q));
+        const int64_t slots =
+            (int64_t)sms * (p.tile ? tile_ctas_per_sm(sh, p.tile_qr) : ctas_per_sm(sh, pick_tune(sh, true)));
+        int64_t parts = p.balanced ? 1 : p.num_parts;
+        if (p.tile) parts = std::max<int64_t>(1, std::min<int64_t>(slots / units, (pages + 3) / 4));
+        else if (units > slots) parts = (pages + 127) / 128;
+        const bool tile = p.tile;
+        const int qr = p.tile_qr;
+        p = plan_with(sh, pages, (int)((pages + parts - 1) / parts), false);
+        p.many_ctas = units * p.num_parts > sms;
+        p.tile = tile;
+        p.tile_qr = qr;
         p.partials = true;
         return p;
     };
     pp->prefix = split(&pp->pre, max_prefix_len, pp->pre_q);
     pp->own = split(s, max_context_len, q_len);
+    pp->own.late_wait = true;  // (it needs nothing of the prefix's launch)
     size_t at = 0;
     bool ok = true;
     auto take = [&](size_t n) {
@@ -1329,7 +1350,6 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
     st = plan_prefix(shape, &pre, q_len, max_prefix_len, max_context_len, sms, &pp);
     if (st != PA_OK) return st;
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < pp.bytes) return PA_ERR_WORKSPACE;
-    if ((int64_t)pp.prefix.num_parts + pp.own.num_parts > 8192) return PA_ERR_UNSUPPORTED;
     char* ws = static_cast<char*>(workspace);
     auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
     cudaStream_t cs = static_cast<cudaStream_t>(stream);

@@ -32,6 +32,11 @@ struct AttnParams {
     // prefix.  Each sees the whole prefix, but for padding (see prefix_limit).
     const int32_t* own_lens;
     int32_t own_q;
+    // 1: this launch needs nothing of the one before it in the stream, only of
+    // those before that, so it waits for it at its end and not at its start.
+    // (The launch before must let its dependents go no earlier than after its
+    // own wait, as the attention kernels do: then what came before it is done.)
+    int32_t late_wait;
     float* scores;            // warp-level kernel: [B, Hkv, Q * group, score_width] or null: q . K
                               // of every token of a read page, -inf where masked
     int64_t score_width;
@@ -121,6 +126,7 @@ struct RopeParams {
     int32_t batch, q_len, num_heads, num_kv_heads, head_dim, block_size, max_blocks;
     int32_t rotary_dim, num_axes, interleaved;
     int32_t max_cta_tokens;   // tokens that one CTA's run of items can touch
+    uint32_t per_token_inverse;  // 2^32 / items of a token, rounded up
 };
 
 // Eviction by accumulated weight.

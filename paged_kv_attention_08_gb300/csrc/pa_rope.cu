@@ -53,8 +53,12 @@ __device__ __forceinline__ void turn8(uint4& lo, uint4& hi, const float4* cs, in
 }
 
 // IPT: items per thread (1 spreads a decode step's few tokens over the SMs).
+//
+// Four CTAs to an SM: with the item's place kept in registers instead of found
+// again after the barrier, and four items to a thread, only two fitted (92
+// registers), and 24,002 tokens of 24 heads took 37.6 us.
 template <typename T, int IPT>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const RopeParams p) {
     extern __shared__ float4 cs[];  // [tokens of the CTA][4][pair octets] (cos, sin) x 2
     const int tid = threadIdx.x;
     const int per_head = p.head_dim / 16;                    // items of a head
@@ -65,7 +69,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
 
     const long long tokens = (long long)p.batch * p.q_len;
     const long long first = (long long)blockIdx.x * (kRopeThreads * IPT);
-    const long long t0 = first / per_token;                  // the CTA's first token
+    const long long t0 = first < (1ll << 31) ? (int)first / per_token  // the CTA's first token
+                                             : first / per_token;
     const int skip = (int)(first - t0 * per_token);
     int ntok = (skip + kRopeThreads * IPT + per_token - 1) / per_token;
     if (ntok > tokens - t0) ntok = (int)(tokens - t0);
@@ -73,33 +78,39 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
     grid_dependency_wait();
     grid_launch_dependents();
 
+    // token of the CTA, head and octet of its item number i (below per_token + 512):
+    // a head has a power of two of items; a token's are divided by as a product
+    const int hshift = __ffs(per_head) - 1;
+    auto place = [&](int k, int& tok, int& head, int& oct) {
+        const int i = skip + tid + k * kRopeThreads;
+        tok = per_token >= 512 ? (i >= per_token) : (int)__umulhi((uint32_t)i, p.per_token_inverse);
+        const int rem = i - tok * per_token;
+        head = rem >> hshift;
+        oct = rem & (per_head - 1);
+    };
+
     uint4 lo[IPT], hi[IPT];
-    int tok[IPT], head[IPT], oct[IPT];
 #pragma unroll
     for (int k = 0; k < IPT; ++k) {
-        const int i = skip + tid + k * kRopeThreads;
-        tok[k] = i / per_token;
-        const int rem = i - tok[k] * per_token;
-        head[k] = rem / per_head;
-        oct[k] = rem - head[k] * per_head;
-        if (tok[k] >= ntok) continue;
+        int tok, h, oct;
+        place(k, tok, h, oct);
+        if (tok >= ntok) continue;
         // the two 8-element vectors of the item: both halves of the rotary
         // part, or 16 neighbours (interleaved pairs, the untouched rest, values)
         const T* src;
-        int h = head[k];
-        bool turned = oct[k] < octets;
+        bool turned = oct < octets;
         if (h < p.num_heads) {
-            src = static_cast<const T*>(p.q) + (t0 + tok[k]) * p.q_stride;
+            src = static_cast<const T*>(p.q) + (t0 + tok) * p.q_stride;
         } else if (h < p.num_heads + p.num_kv_heads) {
             h -= p.num_heads;
-            src = static_cast<const T*>(p.k_new) + (t0 + tok[k]) * p.k_stride;
+            src = static_cast<const T*>(p.k_new) + (t0 + tok) * p.k_stride;
         } else {
             h -= p.num_heads + p.num_kv_heads;
             turned = false;
-            src = static_cast<const T*>(p.v_new) + (t0 + tok[k]) * p.v_stride;
+            src = static_cast<const T*>(p.v_new) + (t0 + tok) * p.v_stride;
         }
         const bool split = turned && !p.interleaved;
-        src += h * p.head_dim + (split ? oct[k] * 8 : oct[k] * 16);
+        src += h * p.head_dim + (split ? oct * 8 : oct * 16);
         lo[k] = *reinterpret_cast<const uint4*>(src);
         hi[k] = *reinterpret_cast<const uint4*>(src + (split ? p.rotary_dim / 2 : 8));
     }
@@ -137,24 +148,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
 
 #pragma unroll
     for (int k = 0; k < IPT; ++k) {
-        if (tok[k] >= ntok) continue;
-        int h = head[k];
+        int tok, h, oct;
+        place(k, tok, h, oct);
+        if (tok >= ntok) continue;
         const bool is_q = h < p.num_heads, is_k = !is_q && h < p.num_heads + p.num_kv_heads;
-        const bool turned = oct[k] < octets && (is_q || is_k);
+        const bool turned = oct < octets && (is_q || is_k);
         if (turned)
-            turn8<T>(lo[k], hi[k], cs + tok[k] * 4 * octets + oct[k], octets, p.interleaved);
+            turn8<T>(lo[k], hi[k], cs + tok * 4 * octets + oct, octets, p.interleaved);
         T* dst;
         if (is_q) {
-            dst = static_cast<T*>(p.q_out) + (t0 + tok[k]) * p.q_out_stride;
+            dst = static_cast<T*>(p.q_out) + (t0 + tok) * p.q_out_stride;
         } else {
-            const long long slot = slot_of[tok[k]];
+            const long long slot = slot_of[tok];
             if (slot < 0) continue;
             h -= is_k ? p.num_heads : p.num_heads + p.num_kv_heads;
             dst = static_cast<T*>(is_k ? p.k_cache : p.v_cache) +
                   slot * ((long long)p.num_kv_heads * p.head_dim);
         }
         const bool split = turned && !p.interleaved;
-        dst += h * p.head_dim + (split ? oct[k] * 8 : oct[k] * 16);
+        dst += h * p.head_dim + (split ? oct * 8 : oct * 16);
         *reinterpret_cast<uint4*>(dst) = lo[k];
         *reinterpret_cast<uint4*>(dst + (split ? p.rotary_dim / 2 : 8)) = hi[k];
     }
@@ -164,8 +176,10 @@ template <typename T, int IPT>
 cudaError_t launch_inst(RopeParams p, long long items, int per_token, bool pdl,
                         cudaStream_t stream) {
     const int span = kRopeThreads * IPT;
+    // floor(i / per_token) = (i * inverse) >> 32 for i < 1024 and per_token < 512
+    p.per_token_inverse = (uint32_t)((0x100000000ull + per_token - 1) / per_token);
     p.max_cta_tokens = (span + per_token - 2) / per_token + 1;
-    // at most (1024 / (3 D / 16) + 2) tokens of D / 2 pairs: 24 KB
+    // at most (512 / (3 D / 16) + 2) tokens of D / 2 pairs: 13 KB
     const size_t smem = (size_t)p.max_cta_tokens * (p.rotary_dim / 16 * 4 * sizeof(float4) + 8);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((items + span - 1) / span));
@@ -186,11 +200,11 @@ cudaError_t launch_rope_append(const RopeParams& p, bool bf16, int num_sms, bool
                                cudaStream_t stream) {
     const int per_token = (p.num_heads + 2 * p.num_kv_heads) * (p.head_dim / 16);
     const long long items = (long long)p.batch * p.q_len * per_token;
-    const bool wide = items > (long long)num_sms * kRopeThreads * 4;
+    const bool wide = items > (long long)num_sms * kRopeThreads * 4;  // more than a wave of one each
     if (bf16)
-        return wide ? launch_inst<__nv_bfloat16, 4>(p, items, per_token, pdl, stream)
+        return wide ? launch_inst<__nv_bfloat16, 2>(p, items, per_token, pdl, stream)
                     : launch_inst<__nv_bfloat16, 1>(p, items, per_token, pdl, stream);
-    return wide ? launch_inst<__half, 4>(p, items, per_token, pdl, stream)
+    return wide ? launch_inst<__half, 2>(p, items, per_token, pdl, stream)
                 : launch_inst<__half, 1>(p, items, per_token, pdl, stream);
 }
 

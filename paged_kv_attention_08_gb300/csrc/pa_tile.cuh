@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int part = blockIdx.x;
     const int tiles = (U + kTileRows - 1) / kTileRows;  // 128-row tiles of a unit
 
-    grid_dependency_wait();
+    if (!p.late_wait) grid_dependency_wait();
     grid_launch_dependents();
 
     // Element offset of unit row u's query / output vector ([B, Q, H, D]).
@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (p.lse && u < U && idx % D == 0) p.lse[row_off(seg0.b, seg0.kvh, u) / D] = INFINITY;
             }
         }
+        if (p.late_wait) grid_dependency_wait();
         return;
     }
 
@@ -1029,6 +1030,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc::tmem_dealloc(tmem, kCols);
     }
     if (p.cluster_reduce) cluster_merge();
+    if (p.late_wait) grid_dependency_wait();
 }
 
 // Per-instantiation flag of the shared-memory limit set once per device.
