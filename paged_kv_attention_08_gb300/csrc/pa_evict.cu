@@ -23,7 +23,7 @@ constexpr int kSelThreads = 512;
 constexpr int kMaxSelCluster = 8;
 constexpr int kBins = 2048;           // digits of 11, 11 and 10 bits; four per thread
 constexpr int kSelShare = 4096;       // tokens a CTA takes before a row gets a larger cluster
-constexpr int kMaxCached = 40 * 1024; // tokens whose keys fit in a CTA's shared memory
+constexpr int kMaxCached = 38 * 1024; // tokens whose keys fit in a CTA's shared memory
 
 // Keys of tokens that the selection does not weigh.
 constexpr uint32_t kKeyAlways = 0xffffffffu;  // kept whatever the weight
@@ -31,9 +31,8 @@ constexpr uint32_t kKeyAbsent = 0u;           // of a masked page: never kept
 
 // Integers that order as the weights do: NaN below every number, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-    if (w != w) return 1u;
     const uint32_t u = __float_as_uint(w + 0.f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return w != w ? 1u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // Exclusive sum over the CTA of one number per thread; *total gets the sum.
@@ -75,33 +74,41 @@ __device__ __forceinline__ int quad_word(int q) { return q * 4 + (q >> 3) * 4; }
 // One cluster of up to 8 CTAs per (kv head, sequence), each with a run of the
 // row's tokens, handled in quads (which lie in one page).  A CTA turns its
 // weights into keys once and keeps them in shared memory (CACHED; a row too
-// long for that is read again by every pass).  Three passes find the
-// threshold, the want-th largest key among the tokens that are not kept
-// anyway: each counts a digit of the keys that agree with the digits found so
-// far in bins of its own and then adds its non-empty bins to those of every
-// CTA of the cluster through distributed shared memory (weights fill a hundred
-// or two of the 2048 bins; reading all bins of all ranks instead took 7 us a
-// pass).  Then each thread marks what it keeps of its own run of quads in a
-// bit mask; one scan over the CTA, and the counts of the CTAs before it, tell
-// it where to write them.
+// long for that is read again where its keys are needed).  The threshold, the
+// want-th largest key among the tokens that are not kept anyway, is found by
+// digits of 11, 11 and 10 bits:
+//   - each CTA counts its keys' first digits (four copies of the bins, a lane
+//     takes copy lane % 4: weights meet in few bins) and adds its non-empty
+//     bins to those of every CTA of the cluster through distributed shared
+//     memory; all of them then know the threshold's first digit;
+//   - the keys with that digit, a few in a hundred as a rule, are sent to
+//     every CTA, each of which finds the other two digits by itself;
+//   - where they are too many for that (ties), the CTAs count and add up the
+//     other digits as they did the first.
+// Then each thread marks what it keeps of its own run of quads in a bit mask;
+// one scan over the CTA, and the counts of the CTAs before it, tell it where
+// to write them.
 //
-// What bounds it: the latency of its steps, not the 17 MB that 32 rows of 128K
-// weights are.
+// What bounds it: the latency of its steps (a cluster barrier 1 to 2 us with
+// the skew of its CTAs), not the 17 MB that 32 rows of 128K weights are.
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictParams p) {
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ __align__(16) uint32_t hist[kBins];     // this CTA's counts
-    __shared__ __align__(16) uint32_t sums[3][kBins];  // the cluster's, of each pass
-    __shared__ uint32_t scratch[5][kSelThreads / 32];
+    __shared__ __align__(16) uint32_t hist[kBins * 4];  // this CTA's counts; later the candidates' keys
+    __shared__ __align__(16) uint32_t sums[kBins];      // the cluster's counts
+    __shared__ uint32_t scratch[6][kSelThreads / 32];
     __shared__ uint32_t chosen[3][2];  // of each pass: the threshold's digit, tokens still wanted of it
     // every CTA's tokens held, and of them those kept whatever their weight;
-    // those above the threshold (the latter included), and those equal to it
-    __shared__ uint32_t shares[kMaxSelCluster][4];
+    // those above the threshold (the latter included), and those equal to it;
+    // those that share the threshold's first digit
+    __shared__ uint32_t shares[kMaxSelCluster][5];
     __shared__ uint32_t counted[2];
     const int tid = threadIdx.x, lane = tid & 31;
     const int C = (int)p.cluster, rank = (int)blockIdx.x % C;
     const int kvh = (int)blockIdx.x / C, b = blockIdx.y;
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = sums[0][i] = sums[1][i] = sums[2][i] = 0;
+    const uint4 zeros = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < kBins; i += kSelThreads) reinterpret_cast<uint4*>(hist)[i] = zeros;
+    reinterpret_cast<uint4*>(sums)[tid] = zeros;
     if (tid < 2) counted[tid] = 0;
     // (the others' adds may come from here on: every CTA waits for this before its first)
     if (C > 1) cluster_arrive_release();
@@ -158,11 +165,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     // the keys, and the first pass's counts: eight quads in flight (the
     // weights of a masked page are loaded like the others, and not used)
     uint32_t held = 0, must = 0;
+    uint32_t* const copy = hist + (lane & 3);
     auto count_first = [&](uint32_t k) {
         if (k == kKeyAlways) ++must;
         else if (k != kKeyAbsent) {
             ++held;
-            atomicAdd(&hist[k >> 21], 1u);
+            atomicAdd(&copy[(k >> 21) * 4], 1u);
         }
     };
     if (C > 1) cluster_wait_acquire();  // (also a barrier of the CTA: hist is zero)
@@ -181,10 +189,19 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
             if (q >= nq) continue;
             const uint4 k = quad_keys(q0 + q, ok[u], x[u]);
             if constexpr (CACHED) *reinterpret_cast<uint4*>(keys + quad_word(q)) = k;
-            count_first(k.x);
-            count_first(k.y);
-            count_first(k.z);
-            count_first(k.w);
+            const int t = (q0 + q) * 4;
+            if (ok[u] && t >= p.sink && t + 3 < recent) {  // four tokens to weigh
+                held += 4;
+                atomicAdd(&copy[(k.x >> 21) * 4], 1u);
+                atomicAdd(&copy[(k.y >> 21) * 4], 1u);
+                atomicAdd(&copy[(k.z >> 21) * 4], 1u);
+                atomicAdd(&copy[(k.w >> 21) * 4], 1u);
+            } else {
+                count_first(k.x);
+                count_first(k.y);
+                count_first(k.z);
+                count_first(k.w);
+            }
         }
     }
     held = __reduce_add_sync(kFullMask, held);
@@ -201,59 +218,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     const int i0 = min(tid * run, nq), i1 = min(i0 + run, nq);
 
     uint32_t prefix = 0, mask = 0, want = 0, n = 0;
-    bool all = false;
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-        const uint32_t digit = pass == 2 ? 1023u : 2047u;
-        if (pass > 0) {
-            auto count = [&](uint32_t k) {
-                if ((k & mask) == prefix && k != kKeyAbsent && k != kKeyAlways)
-                    atomicAdd(&hist[(k >> shift) & digit], 1u);
-            };
-#pragma unroll 4
-            for (int i = i0; i < i1; ++i) {
-                const uint4 k = keys_at(i);
-                count(k.x);
-                count(k.y);
-                count(k.z);
-                count(k.w);
-            }
-        }
-        __syncthreads();  // this CTA's counts are complete
-        uint4 c = *reinterpret_cast<const uint4*>(hist + 4 * tid);
-        if (C > 1) {
-            // the non-empty ones of this thread's four bins, to every CTA
-            for (int r = 0; r < C; ++r) {
-                const uint32_t at = map_cluster_rank(smem_u32(&sums[pass][4 * tid]), r);
-                if (c.x) red_cluster_add(at, c.x);
-                if (c.y) red_cluster_add(at + 4, c.y);
-                if (c.z) red_cluster_add(at + 8, c.z);
-                if (c.w) red_cluster_add(at + 12, c.w);
-            }
-        }
-        // (read by this thread alone, and counted into again after the barrier)
-        *reinterpret_cast<uint4*>(hist + 4 * tid) = make_uint4(0, 0, 0, 0);
-        if (pass == 0 && tid < 2) tell(tid, counted[tid]);
-        cluster_barrier();
-        if (C > 1) c = *reinterpret_cast<const uint4*>(&sums[pass][4 * tid]);
-        if (pass == 0) {
-            uint32_t valid = 0, fixed = 0;
-            for (int r = 0; r < C; ++r) {
-                valid += shares[r][0];
-                fixed += shares[r][1];
-            }
-            n = min(valid, (uint32_t)p.budget);
-            want = n - fixed;
-            all = valid <= (uint32_t)p.budget;
-            if (all) break;  // (the same in every CTA of the cluster)
-        }
-        // the want-th largest: its rank from below among the cluster's counts
+    int steps = 0;
+    // the digit of the want-th largest key among those counted: thread tid has
+    // the counts of bins 4 tid .. 4 tid + 3
+    auto find_digit = [&](const uint4& c, int shift, uint32_t digit) {
         uint32_t total;
-        const uint32_t before = block_exclusive(c.x + c.y + c.z + c.w, scratch[pass], &total);
+        const uint32_t before = block_exclusive(c.x + c.y + c.z + c.w, scratch[steps], &total);
         if (tid == 0 && want == 0) {  // nothing is wanted: above every key
-            chosen[pass][0] = digit;
-            chosen[pass][1] = 0;
+            chosen[steps][0] = digit;
+            chosen[steps][1] = 0;
         }
         const uint32_t below = total - want;  // candidates left out
         if (want > 0 && below >= before && below < before + c.x + c.y + c.z + c.w) {
@@ -261,13 +234,123 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
             uint32_t s = before;
             int d = 0;
             while (d < 3 && below >= s + cs[d]) s += cs[d++];
-            chosen[pass][0] = (uint32_t)(4 * tid + d);
-            chosen[pass][1] = s + cs[d] - below;
+            chosen[steps][0] = (uint32_t)(4 * tid + d);
+            chosen[steps][1] = s + cs[d] - below;
         }
         __syncthreads();
-        prefix |= chosen[pass][0] << shift;
+        prefix |= chosen[steps][0] << shift;
         mask |= digit << shift;
-        want = chosen[pass][1];
+        want = chosen[steps][1];
+        ++steps;
+    };
+    // this CTA's counts of this thread's bins, the non-empty ones to every CTA
+    auto send_counts = [&](const uint4& c) {
+        if ((c.x | c.y | c.z | c.w) == 0) return;
+        for (int r = 0; r < C; ++r) {
+            const uint32_t at = map_cluster_rank(smem_u32(&sums[4 * tid]), r);
+            if (c.x) red_cluster_add(at, c.x);
+            if (c.y) red_cluster_add(at + 4, c.y);
+            if (c.z) red_cluster_add(at + 8, c.z);
+            if (c.w) red_cluster_add(at + 12, c.w);
+        }
+    };
+    uint4* const my_sums = reinterpret_cast<uint4*>(sums) + tid;
+
+    __syncthreads();  // this CTA's counts are complete
+    uint4 c;
+    {
+        const uint4* h = reinterpret_cast<const uint4*>(hist) + 4 * tid;
+        const uint4 h0 = h[0], h1 = h[1], h2 = h[2], h3 = h[3];
+        c = make_uint4(h0.x + h0.y + h0.z + h0.w, h1.x + h1.y + h1.z + h1.w,
+                       h2.x + h2.y + h2.z + h2.w, h3.x + h3.y + h3.z + h3.w);
+    }
+    if (C > 1) send_counts(c);
+    if (tid < 2) tell(tid, counted[tid]);
+    cluster_barrier();
+    if (C > 1) c = *my_sums;
+    uint32_t valid = 0, fixed = 0;
+    for (int r = 0; r < C; ++r) {
+        valid += shares[r][0];
+        fixed += shares[r][1];
+    }
+    n = min(valid, (uint32_t)p.budget);
+    want = n - fixed;
+    const bool all = valid <= (uint32_t)p.budget;  // (the same in every CTA of the cluster)
+    if (!all) {
+        find_digit(c, 21, 2047u);
+        *my_sums = zeros;
+        auto each_key = [&](auto&& fn) {  // of this thread's run
+#pragma unroll 4
+            for (int i = i0; i < i1; ++i) {
+                const uint4 k = keys_at(i);
+                fn(k.x);
+                fn(k.y);
+                fn(k.z);
+                fn(k.w);
+            }
+        };
+        auto candidate = [&](uint32_t k) {
+            return (k & mask) == prefix && k != kKeyAbsent && k != kKeyAlways;
+        };
+        // the keys with the threshold's first digit, into this CTA's part of the list
+        // (a row of one CTA counts its keys again instead)
+        const uint32_t room = kBins * 4 / C;
+        bool fits = C > 1;
+        if (C > 1) {
+            uint32_t* const mine = hist + rank * room;
+            uint32_t count = 0;
+            each_key([&](uint32_t k) { count += candidate(k); });
+            uint32_t sent;
+            uint32_t at = block_exclusive(count, scratch[4], &sent);
+            if (count > 0 && sent <= room)
+                each_key([&](uint32_t k) {
+                    if (candidate(k)) mine[at++] = k;
+                });
+            if (tid == 0) tell(4, sent);
+            __syncthreads();
+            if (sent <= room)
+                for (int r = 0; r < C; ++r) {
+                    if (r == rank) continue;
+                    const uint32_t to = map_cluster_rank(smem_u32(mine), r);
+                    for (uint32_t i = tid; i < sent; i += kSelThreads) st_cluster_u32(to + 4u * i, mine[i]);
+                }
+            cluster_barrier();
+            for (int r = 0; r < C; ++r) fits = fits && shares[r][4] <= room;
+        }
+        for (int step = 0; step < 2; ++step) {
+            const int shift = step == 0 ? 10 : 0;
+            const uint32_t digit = step == 0 ? 2047u : 1023u;
+            if (fits) {
+                // (an equal share of the threads to each CTA's part)
+                const int r = tid / (kSelThreads / C);
+                const uint32_t len = shares[r][4];
+                for (uint32_t i = tid % (kSelThreads / C); i < len; i += kSelThreads / C) {
+                    const uint32_t k = hist[r * room + i];
+                    if (candidate(k)) atomicAdd(&sums[(k >> shift) & digit], 1u);
+                }
+                __syncthreads();
+                c = *my_sums;
+                *my_sums = zeros;
+                find_digit(c, shift, digit);  // (its barriers order the zeros before the next counts)
+            } else {
+                // (the list is not used: its first words hold this CTA's counts)
+                reinterpret_cast<uint4*>(hist)[tid] = zeros;
+                __syncthreads();
+                each_key([&](uint32_t k) {
+                    if (candidate(k)) atomicAdd(&hist[(k >> shift) & digit], 1u);
+                });
+                __syncthreads();
+                c = reinterpret_cast<const uint4*>(hist)[tid];
+                if (C > 1) {
+                    send_counts(c);
+                    cluster_barrier();
+                    c = *my_sums;
+                    *my_sums = zeros;
+                    cluster_barrier();  // zero before the next step's counts arrive
+                }
+                find_digit(c, shift, digit);
+            }
+        }
     }
 
     // what this thread surely keeps of its run, and what equals the threshold,
@@ -308,7 +391,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         sures &= 0xffffu;
     } else {
         sure = block_exclusive(sure, scratch[3], &sures);
-        equal = block_exclusive(equal, scratch[4], &equals);
+        equal = block_exclusive(equal, scratch[5], &equals);
     }
     if (tid < 2) tell(2 + tid, tid == 0 ? sures : equals);
     cluster_barrier();  // (the last access to another CTA's memory is before it)

@@ -145,3 +145,18 @@ def test_attention_over_what_is_kept():
     after = pa.decode(torch.zeros((2, 8, 128), device=DEV), q, d["k_cache"], d["v_cache"],
                       d["new_table"], lens, 0.09)
     assert torch.equal(lens, d["lens"]) and torch.equal(before, after)
+
+
+@pytest.mark.parametrize("T,kind", [(9000, "distinct"), (70000, "distinct"), (70000, "ties"),
+                                    (70000, "equal"), (70000, "one digit"), (320000, "ties"),
+                                    (320000, "equal")])
+def test_rows_that_several_ctas_share(T, kind):
+    """Long rows: a cluster of CTAs, lists of candidates that fit and that do not
+    (many keys with one first digit), rows too long for the key cache."""
+    c = case(20, 1, 1 if T > 100000 else 2, 64, 16, torch.float16, [T - 5], 700,
+             ties=0.3 if kind == "ties" else 0.0)
+    if kind == "equal":
+        c["weights"].fill_(0.5)
+    if kind == "one digit":   # 1 .. 1.25: the first eleven bits agree
+        c["weights"] = 1 + c["weights"] / c["weights"].max() * 0.24
+    check(c, 700, 4, 100, False)
