@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(256, 1)
                 store_out(p.out, row_off(b, kvh, idx / D) + idx % D, 0.f, p.out_dtype);
             if (p.lse && tid < R) p.lse[row_off(b, kvh, tid) / D] = INFINITY;
         }
-        if (p.late_wait) grid_dependency_wait();
+        late_dependency_wait(p.late_wait);
         return;
     }
     __syncthreads();  // barrier initialisation visible to every warp
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(256, 1)
             merge(std::integral_constant<int, kMaxDecodeClusterParts>{});
         cluster_sync_relaxed();  // no CTA leaves while others still read its shared memory
     }
-    if (p.late_wait) grid_dependency_wait();
+    late_dependency_wait(p.late_wait);
 }
 
 // Per-instantiation flags of the attributes set once per device.

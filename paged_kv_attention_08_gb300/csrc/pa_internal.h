@@ -33,7 +33,8 @@ struct AttnParams {
     const int32_t* own_lens;
     int32_t own_q;
     // 1: this launch needs nothing of the one before it in the stream, only of
-    // those before that, so it waits for it at its end and not at its start.
+    // those before that, so its last CTA waits for it at its end instead of
+    // every CTA at its start.
     // (The launch before must let its dependents go no earlier than after its
     // own wait, as the attention kernels do: then what came before it is done.)
     int32_t late_wait;

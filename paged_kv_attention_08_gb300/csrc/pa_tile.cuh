@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (p.lse && u < U && idx % D == 0) p.lse[row_off(seg0.b, seg0.kvh, u) / D] = INFINITY;
             }
         }
-        if (p.late_wait) grid_dependency_wait();
+        late_dependency_wait(p.late_wait);
         return;
     }
 
@@ -1030,7 +1030,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc::tmem_dealloc(tmem, kCols);
     }
     if (p.cluster_reduce) cluster_merge();
-    if (p.late_wait) grid_dependency_wait();
+    late_dependency_wait(p.late_wait);
 }
 
 // Per-instantiation flag of the shared-memory limit set once per device.
