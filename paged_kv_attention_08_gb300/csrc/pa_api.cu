@@ -911,34 +911,76 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
                       int32_t max_prefix_len, int32_t max_context_len, int sms, PrefixPlan* pp) {
     pp->pre = *pre;
     pp->pre_q = s->batch / pre->batch * q_len;
-    // The library's split of each part, its partials always left in the
-    // workspace for the join.  No cluster reduces here, so the tile kernel takes
-    // as many partitions as fit in one wave (16 units of 8191 tokens: 9 each, not
-    // the 6 of a cluster split); and where the own pages' units run in several
-    // waves anyway, partitions of 128 pages, not 64, leave fewer partials (1024
-    // units of up to 2048 tokens: 92 us against 98).
-    auto split = [&](const pa_shape* sh, int32_t max_len, int32_t q) {
-        Plan p = make_plan(sh, max_len, 0, sms, q);
-        const int pages = pages_for(sh, max_len);
+    // The library's kernel choice for each part; the partials always stay in
+    // the workspace for the join, and no cluster reduces.
+    struct Part {
+        Plan p;
+        int pages;
+        int64_t units, slots, parts;
+    };
+    auto part_of = [&](const pa_shape* sh, int32_t max_len, int32_t q) {
+        Part x;
+        x.p = make_plan(sh, max_len, 0, sms, q);
+        x.pages = pages_for(sh, max_len);
         const int64_t rows = (int64_t)q * (sh->num_heads / sh->num_kv_heads);
-        const int64_t units = (int64_t)sh->batch * sh->num_kv_heads *
-                              (p.tile ? (rows + kTileRows - 1) / kTileRows : q_chunks_for(sh, q));
-        const int64_t slots =
-            (int64_t)sms * (p.tile ? tile_ctas_per_sm(sh, p.tile_qr) : ctas_per_sm(sh, pick_tune(sh, true)));
-        int64_t parts = p.balanced ? 1 : p.num_parts;
-        if (p.tile) parts = std::max<int64_t>(1, std::min<int64_t>(slots / units, (pages + 3) / 4));
-        else if (units > slots) parts = (pages + 127) / 128;
-        const bool tile = p.tile;
-        const int qr = p.tile_qr;
-        p = plan_with(sh, pages, (int)((pages + parts - 1) / parts), false);
-        p.many_ctas = units * p.num_parts > sms;
-        p.tile = tile;
-        p.tile_qr = qr;
+        x.units = (int64_t)sh->batch * sh->num_kv_heads *
+                  (x.p.tile ? (rows + kTileRows - 1) / kTileRows : q_chunks_for(sh, q));
+        x.slots = (int64_t)sms * (x.p.tile ? tile_ctas_per_sm(sh, x.p.tile_qr)
+                                           : ctas_per_sm(sh, pick_tune(sh, true)));
+        x.parts = x.p.balanced ? 1 : x.p.num_parts;
+        return x;
+    };
+    Part pre_part = part_of(&pp->pre, max_prefix_len, pp->pre_q);
+    Part own_part = part_of(s, max_context_len, q_len);
+    // What a tile CTA takes: its blocks, and a start and an end (measured on
+    // GB300: 1.5 us a block of 128 tokens, 2 us one of 64 at head_dim 256; 10 us).
+    const double block_us = s->head_dim == 256 ? 2.0 : 1.5, ends_us = 10.0;
+    const int block_pages = tile_block_tokens(s->head_dim) / s->block_size;
+    auto tile_us = [&](const Part& x, int64_t parts) {
+        const int64_t pages = (x.pages + parts - 1) / parts;
+        return (double)((pages + block_pages - 1) / block_pages) * block_us + ends_us;
+    };
+    if (own_part.p.tile) {
+        // few blocks are not worth another CTA's start and end (64 units of 300
+        // tokens at head_dim 256: 41.4 us for the call with one partition, 46.0 with two)
+        own_part.parts = std::max<int64_t>(
+            1, std::min<int64_t>(own_part.slots / own_part.units, own_part.pages / (8 * block_pages)));
+    } else if (own_part.units > own_part.slots) {
+        // several waves of units anyway: partitions of 128 pages, not 64, leave fewer
+        // partials (1024 units of up to 2048 tokens: 92 us against 98)
+        own_part.parts = (own_part.pages + 127) / 128;
+    }
+    if (pre_part.p.tile) {
+        // The two launches share the SMs.  A CTA more for the prefix shortens it
+        // but costs a start and an end, and takes an SM from the sequences' own
+        // pages; so the prefix is cut only until it ends well before the whole
+        // call can (lengths are not known here: the own pages count as half of
+        // max_context_len, read at 33 GB/s an SM).  16 units of 8191 tokens beside
+        // 64 sequences of up to 1024: 57.5 us with 9 partitions (one wave), 50.0
+        // with 4; 32 units of 65536 beside 128 sequences of up to 2048: 255 us
+        // with 4, 279 with 3.
+        const double own_us =
+            own_part.p.tile ? own_part.units * own_part.parts * tile_us(own_part, own_part.parts)
+                            : (double)own_part.units * max_context_len * s->head_dim * 2.0 / 33e3;
+        const int64_t most = std::max<int64_t>(
+            1, std::min<int64_t>(pre_part.slots / pre_part.units, (pre_part.pages + 3) / 4));
+        int64_t parts = 1;
+        for (; parts < most; ++parts) {
+            const double cta = tile_us(pre_part, parts);
+            if (cta <= 0.85 * (pre_part.units * parts * cta + own_us) / sms) break;
+        }
+        pre_part.parts = parts;
+    }
+    auto finish = [&](const pa_shape* sh, const Part& x) {
+        Plan p = plan_with(sh, x.pages, (int)((x.pages + x.parts - 1) / x.parts), false);
+        p.many_ctas = x.units * p.num_parts > sms;
+        p.tile = x.p.tile;
+        p.tile_qr = x.p.tile_qr;
         p.partials = true;
         return p;
     };
-    pp->prefix = split(&pp->pre, max_prefix_len, pp->pre_q);
-    pp->own = split(s, max_context_len, q_len);
+    pp->prefix = finish(&pp->pre, pre_part);
+    pp->own = finish(s, own_part);
     pp->own.late_wait = true;  // (it needs nothing of the prefix's launch)
     size_t at = 0;
     bool ok = true;
