@@ -1488,6 +1488,13 @@ pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weigh
     w.lse = plan.lse;
     w.scores = plan.scores;
     w.score_width = plan.score_width;
+    const bool partials = scores && plan.num_parts > 1 && !plan.cluster;
+    size_t ml_off = 0;
+    (void)workspace_bytes_for(shape, plan, &ml_off, q_len);
+    w.part_ml = partials ? reinterpret_cast<const float*>(ws + ml_off) : nullptr;
+    w.num_parts = plan.num_parts;
+    w.part_pages = plan.part_pages;
+    w.late_wait = partials ? 1 : 0;
     w.block_tables = block_tables;
     w.context_lens = context_lens;
     w.num_blocks = shape->num_blocks;

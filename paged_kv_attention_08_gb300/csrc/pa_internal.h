@@ -105,6 +105,12 @@ struct WeightParams {
     int32_t token_limit;      // tokens from here on were not attended
     const float* scores;      // as in AttnParams
     int64_t score_width;
+    // Stored scores of a call whose partitions' statistics are in part_ml
+    // [B, Hkv, num_parts, Q * group, 2] (else null: lse is filled): the rows'
+    // statistics are formed from those, so that the launch need not wait for
+    // the combine kernel that runs before it (late_wait as in AttnParams).
+    const float* part_ml;
+    int32_t num_parts, part_pages, late_wait;
     int32_t* err;             // device error word, bound on every wait (tile kernel)
     uint64_t timeout_ns;
 };

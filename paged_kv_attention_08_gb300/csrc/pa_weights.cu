@@ -17,15 +17,41 @@ __global__ void __launch_bounds__(kSThreads) weights_of_scores_kernel(const Weig
     const int tid = threadIdx.x;
     const int kvh = blockIdx.y, b = blockIdx.z;
     const int G = p.group, rows = p.q_len * G;
-    grid_dependency_wait();
+    if (!p.late_wait) grid_dependency_wait();
     grid_launch_dependents();
+    late_dependency_wait(p.late_wait);  // (the last CTA: the launch ends after the one before)
     const int T = reachable_tokens(p.context_lens, b, p.max_blocks, p.block_size);
     const int t0 = blockIdx.x * (kSThreads * 4) + tid * 4;
-    if (tid < rows)
+    if ((int)blockIdx.x * (kSThreads * 4) >= T) return;
+    const int npages = (T + p.block_size - 1) / p.block_size;
+    if (p.part_ml) {
+        // m + log2 l over the partitions that hold tokens: a warp per row in turn
+        const int parts = min((npages + p.part_pages - 1) / p.part_pages, p.num_parts);
+        const float2* ml = reinterpret_cast<const float2*>(p.part_ml) +
+                           ((size_t)b * p.num_kv_heads + kvh) * p.num_parts * rows;
+        const int lane = tid & 31;
+        for (int r = tid >> 5; r < rows; r += kSThreads / 32) {
+            float m = -INFINITY, l = 0.f;
+            for (int q = lane; q < parts; q += 32) {
+                const float2 v = ml[(size_t)q * rows + r];
+                if (v.x == -INFINITY) continue;
+                const float n = fmaxf(m, v.x);
+                l = l * (m == -INFINITY ? 0.f : exp2f(m - n)) + v.y * exp2f(v.x - n);
+                m = n;
+            }
+            float M = m;
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, d));
+            l *= m == -INFINITY ? 0.f : exp2f(m - M);
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(kFullMask, l, d);
+            if (lane == 0) ls[r] = row_lse(M, l);
+        }
+    } else if (tid < rows) {
         ls[tid] = p.lse[((size_t)b * p.q_len + tid / G) * p.num_heads + kvh * G + tid % G];
+    }
     __syncthreads();
     if (t0 >= T) return;
-    const int npages = (T + p.block_size - 1) / p.block_size;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t0 < p.token_limit && page_phys(p.block_tables + (size_t)b * p.max_blocks, t0 / p.block_size,
                                         npages, p.num_blocks) >= 0) {
