@@ -903,8 +903,18 @@ pa_status check_prefix(const pa_shape* s, int32_t num_prefixes, int32_t max_pref
     st = check_shape(pre);
     if (st != PA_OK) return st;
     // rows of a prefix and of a launch in 31 bits
-    const int64_t rows = (int64_t)(s->batch / num_prefixes) * q_len * s->num_heads;
-    return rows > 0x7fffffff ? PA_ERR_UNSUPPORTED : PA_OK;
+    const int64_t tokens = (int64_t)(s->batch / num_prefixes) * q_len;
+    if (tokens * s->num_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    if (s->batch == 0) return PA_OK;
+    // both launches' grids, before the first of them is made
+    for (int64_t q : {tokens, (int64_t)q_len}) {
+        const pa_shape* sh = q == tokens ? pre : s;
+        const int64_t per_head = use_tile(sh, (int32_t)q, 0)
+                                     ? (q * (s->num_heads / s->num_kv_heads) + kTileRows - 1) / kTileRows
+                                     : q_chunks_for(sh, (int32_t)q);
+        if (per_head * s->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    }
+    return PA_OK;
 }
 
 pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,

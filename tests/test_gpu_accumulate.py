@@ -154,3 +154,23 @@ def test_output_is_that_of_plain_decode():
     # the same sums, possibly split elsewhere: twice the error of either
     slack = 2 * ref.out_slack(c["q"], c["k_cache"], c["v_cache"], 0.1, 900)
     assert (out - plain).abs().max().item() <= slack
+
+
+@pytest.mark.parametrize("kernel", ["mma", "tile"])
+@pytest.mark.parametrize("Q,H,Hkv,D", [(1, 8, 2, 128), (3, 8, 2, 64), (12, 8, 2, 128), (2, 16, 1, 256)])
+def test_either_kernel_forced(kernel, Q, H, Hkv, D, switches):
+    switches(kernel=kernel)
+    check(case(100 + Q, 2, Q, H, Hkv, D, 16, [50, 400], torch.float16))
+
+
+def test_contexts_longer_than_announced_drop_the_rest():
+    """Tokens past max_context_len's pages are in neither the output nor the weights."""
+    c = case(110, 2, 1, 8, 2, 128, 16, [200, 90], torch.bfloat16)
+    short = {k: v.clone() for k, v in c.items()}
+    short["lens"] = torch.clamp(c["lens"], max=96)
+    out, new = run(c, 0.1, max_len=96)
+    want_out, want = run(short, 0.1, max_len=96)
+    assert torch.equal(out, want_out)
+    assert torch.equal(new[:, :, :96], torch.where(torch.arange(96) < short["lens"].view(2, 1, 1),
+                                                   want[:, :, :96], new[:, :, :96]))
+    assert torch.equal(new[0, :, 96:200], c["weights"][0, :, 96:200])   # added weight: none

@@ -147,3 +147,32 @@ def test_same_bits_twice_other_stream_one_token_form_and_graph():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out.cpu(), want[:, 0])
+
+
+@pytest.mark.parametrize("kernel", ["mma", "tile"])
+def test_either_kernel_forced(kernel, switches):
+    switches(kernel=kernel)
+    check(case(90, 5, 3, 8, 2, 128, 16, [150, 33], [3 + 7 * b for b in range(10)], torch.bfloat16))
+    check(case(91, 20, 1, 16, 1, 256, 16, [100], [5 + b for b in range(20)], torch.float16))
+
+
+def test_two_graphs_share_a_workspace():
+    cs = [case(92, 20, 1, 8, 2, 128, 16, [700], [40] * 20, torch.bfloat16),
+          case(93, 3, 4, 8, 2, 128, 16, [90], [9, 30, 70], torch.bfloat16)]
+    want = [run(c, 0.1) for c in cs]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    graphs, outs, keep = [], [], []
+    for c in cs:
+        d = {k: v.to(DEV) for k, v in c.items()}
+        out = torch.zeros(c["q"].shape, dtype=c["q"].dtype, device=DEV)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pa.decode_shared_prefix(out, d["q"], d["k_cache"], d["v_cache"], d["ptable"], d["plens"],
+                                    d["table"], d["lens"], 0.1, int(c["plens"].max()),
+                                    int(c["lens"].max()), workspace=ws)
+        graphs.append(graph), outs.append(out), keep.append(d)
+    for i in (0, 1, 0, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i].cpu(), want[i])
