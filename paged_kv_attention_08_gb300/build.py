@@ -19,10 +19,14 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa_decode.so")
 
-SOURCES = ["pa_api.cu", "pa_step_api.cu", "pa_rope.cu", "pa_evict.cu", "pa_weights.cu", "pa_weights_tile.cu", "pa_combine.cu", "pa_attn_d64.cu", "pa_attn_d128.cu", "pa_attn_d256.cu",
+SOURCES = ["pa_api.cu", "pa_step_api.cu", "pa_combine.cu", "pa_rope.cu", "pa_evict.cu",
+           "pa_weights.cu", "pa_weights_tile.cu",
+           "pa_attn_d64.cu", "pa_attn_d128.cu", "pa_attn_d256.cu",
            "pa_attn_d64_multi.cu", "pa_attn_d128_multi.cu", "pa_attn_d256_multi.cu",
-           "pa_attn_d64_scores.cu", "pa_attn_d128_scores.cu", "pa_attn_d256_scores.cu",
-           "pa_tile_d64.cu", "pa_tile_d128.cu", "pa_tile_d256.cu", "pa_tile_d256_compact.cu"]
+           "pa_attn_d64_extended.cu", "pa_attn_d128_extended.cu", "pa_attn_d256_extended.cu",
+           "pa_tile_d64.cu", "pa_tile_d128.cu", "pa_tile_d256.cu", "pa_tile_d256_compact.cu",
+           "pa_tile_d64_extended.cu", "pa_tile_d128_extended.cu", "pa_tile_d256_extended.cu",
+           "pa_tile_d256_compact_extended.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          f"-I{INCLUDE}"] + ARCH

@@ -346,7 +346,8 @@ bool clusters_enabled();
 
 Plan auto_plan(const pa_shape* s, int32_t max_context_len, int num_sms, int q_chunks = 1) {
     const int pages = pages_for(s, max_context_len);
-    const int64_t units = (int64_t)s->batch * s->num_kv_heads * q_chunks;
+    // (an empty batch is planned like one sequence)
+    const int64_t units = (int64_t)std::max(s->batch, 1) * s->num_kv_heads * q_chunks;
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const bool can_balance =
         s->batch <= kMaxBalancedBatch && q_chunks == 1 && balanced_mode() > 0;
@@ -504,7 +505,8 @@ Plan tile_plan(const pa_shape* s, int32_t max_context_len, int32_t partition_tok
         pp = partition_tokens / s->block_size;
     } else {
         const int64_t rows = (int64_t)q_len * (s->num_heads / s->num_kv_heads);
-        const int64_t units = (int64_t)s->batch * s->num_kv_heads * ((rows + kTileRows - 1) / kTileRows);
+        const int64_t units =
+            (int64_t)std::max(s->batch, 1) * s->num_kv_heads * ((rows + kTileRows - 1) / kTileRows);
         const int64_t slots = (int64_t)num_sms * tile_ctas_per_sm(s, qr);
         int64_t parts = slots / units;  // whole waves: one partition more would add a wave
         const int64_t max_parts = (pages + 3) / 4;
@@ -793,11 +795,12 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
                                   (unsigned)s->batch);
     L.threads = 32 * t.nt * t.nh;
     L.smem_bytes = sm.total + kSmemAlignSlack;
+    const bool ext = extended(p);
     cudaError_t e;
     switch (s->head_dim) {
-        case 64: e = p.scores ? launch_attn_d64_scores(L, stream) : launch_attn_d64(L, stream); break;
-        case 128: e = p.scores ? launch_attn_d128_scores(L, stream) : launch_attn_d128(L, stream); break;
-        default: e = p.scores ? launch_attn_d256_scores(L, stream) : launch_attn_d256(L, stream); break;
+        case 64: e = ext ? launch_attn_d64_extended(L, stream) : launch_attn_d64(L, stream); break;
+        case 128: e = ext ? launch_attn_d128_extended(L, stream) : launch_attn_d128(L, stream); break;
+        default: e = ext ? launch_attn_d256_extended(L, stream) : launch_attn_d256(L, stream); break;
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -870,11 +873,17 @@ pa_status launch_tile(void* out, const void* q, const void* k, const void* v, co
     }
     L.threads = kTileThreads;
     L.smem_bytes = tile_smem_layout(s->head_dim, s->block_size, plan.tile_qr).total + kSmemAlignSlack;
+    const bool ext = extended(p);
     cudaError_t e;
     switch (s->head_dim) {
-        case 64: e = launch_tile_d64(L, stream); break;
-        case 128: e = launch_tile_d128(L, stream); break;
-        default: e = compact ? launch_tile_d256_compact(L, stream) : launch_tile_d256(L, stream); break;
+        case 64: e = ext ? launch_tile_d64_extended(L, stream) : launch_tile_d64(L, stream); break;
+        case 128: e = ext ? launch_tile_d128_extended(L, stream) : launch_tile_d128(L, stream); break;
+        default:
+            if (ext)
+                e = compact ? launch_tile_d256_compact_extended(L, stream) : launch_tile_d256_extended(L, stream);
+            else
+                e = compact ? launch_tile_d256_compact(L, stream) : launch_tile_d256(L, stream);
+            break;
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -72,10 +72,13 @@ enum SegOut { kOutFinal = 0, kOutPartial = 1, kOutCluster = 2, kOutRecord = 3 };
 
 // MULTI: several query tokens per sequence (rows are (query token, head)
 // pairs with a causal limit each); otherwise one token, rows = the group's heads.
-// SCORES: every score also goes to p.scores, from which the tokens' attention
-// weights are summed once the rows' statistics are known (4 bytes a row and
-// token written and read again, against reading a key of 2 D bytes again).
-template <int D, int BS, typename KV, bool MULTI, bool SCORES = false>
+// EXT: a launch may also ask for the row statistics (p.lse), a shared prefix
+// (p.own_lens), a late wait, and the scores: with p.scores every score is
+// stored, and the tokens' attention weights are summed from them once the rows'
+// statistics are known (4 bytes a row and token written and read again,
+// against reading a key of 2 D bytes again).  The plain instantiations know
+// nothing of these: as run-time questions they cost the short calls 2.4 %.
+template <int D, int BS, typename KV, bool MULTI, bool EXT = false>
 __global__ void __launch_bounds__(256, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(256, 1)
         prefetch_tensormap(&tmap_v);
     }
     // Inputs may come from the previous kernel in the stream.
-    if (!p.late_wait) grid_dependency_wait();
+    if (!EXT || !p.late_wait) grid_dependency_wait();
     grid_launch_dependents();
 
     const int g = lane >> 2, tig = lane & 3;
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(256, 1)
         // the table's reach (with one query token, every row attends T).
         int lim0 = T, lim1 = T;
         if constexpr (MULTI) {
-            if (p.own_lens) {
+            if (EXT && p.own_lens) {
                 if (real0) lim0 = prefix_limit(T, b, qi0 + (g >> gshift), Q, p.own_q, p.own_lens);
                 if (real1)
                     lim1 = prefix_limit(T, b, qi0 + ((g + 8) >> gshift), Q, p.own_q, p.own_lens);
@@ -322,8 +325,8 @@ __global__ void __launch_bounds__(256, 1)
                         mx0 = fmaxf(mx0, s[nt][e]);
                         mx1 = fmaxf(mx1, s[nt][2 + e]);
                     }
-                if constexpr (SCORES) {
-                    if (ds == 0) {  // (the two warps of a page at head_dim 256 form the same scores)
+                if constexpr (EXT) {
+                    if (p.scores && ds == 0) {  // (the two warps of a page at head_dim 256 form the same scores)
                         const size_t rows = ((size_t)b * Hkv + kvh) * (MULTI ? p.unit_rows : G) +
                                             (size_t)qi0 * G;
                         float* at = p.scores + rows * p.score_width + (size_t)j * BS + tig * 2;
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(256, 1)
         return [&, b, kvh](int idx, float A, float M, float Ls) {
             store_out(p.out, row_off(b, kvh, idx / D) + idx % D, Ls > 0.f ? A / Ls : 0.f,
                       p.out_dtype);
-            if (p.lse && idx % D == 0) p.lse[row_off(b, kvh, idx / D) / D] = row_lse(M, Ls);
+            if (EXT && p.lse && idx % D == 0) p.lse[row_off(b, kvh, idx / D) / D] = row_lse(M, Ls);
         };
     };
     // (m, l, acc) of the CTA's rows into workspace row `row0 + r`.
@@ -606,9 +609,9 @@ __global__ void __launch_bounds__(256, 1)
         if (p.final_out) {
             for (int idx = tid; idx < R * D; idx += blockDim.x)
                 store_out(p.out, row_off(b, kvh, idx / D) + idx % D, 0.f, p.out_dtype);
-            if (p.lse && tid < R) p.lse[row_off(b, kvh, tid) / D] = INFINITY;
+            if (EXT && p.lse && tid < R) p.lse[row_off(b, kvh, tid) / D] = INFINITY;
         }
-        late_dependency_wait(p.late_wait);
+        if constexpr (EXT) late_dependency_wait(p.late_wait);
         return;
     }
     __syncthreads();  // barrier initialisation visible to every warp
@@ -674,7 +677,7 @@ __global__ void __launch_bounds__(256, 1)
                 }
                 store_out(p.out, row_off(b, kvh, r) + idx % D, Ls > 0.f ? A / Ls : 0.f,
                           p.out_dtype);
-                if (p.lse && idx % D == 0) p.lse[row_off(b, kvh, r) / D] = row_lse(M, Ls);
+                if (EXT && p.lse && idx % D == 0) p.lse[row_off(b, kvh, r) / D] = row_lse(M, Ls);
             }
         };
         if (P <= kMaxClusterParts)
@@ -683,20 +686,20 @@ __global__ void __launch_bounds__(256, 1)
             merge(std::integral_constant<int, kMaxDecodeClusterParts>{});
         cluster_sync_relaxed();  // no CTA leaves while others still read its shared memory
     }
-    late_dependency_wait(p.late_wait);
+    if constexpr (EXT) late_dependency_wait(p.late_wait);
 }
 
 // Per-instantiation flags of the attributes set once per device.
-template <int D, int BS, typename KV, bool MULTI, bool SCORES = false>
+template <int D, int BS, typename KV, bool MULTI, bool EXT = false>
 struct AttnAttrs {
     static inline AttrFlags smem;
     static inline AttrFlags nonportable;
 };
 
-template <int D, int BS, typename KV, bool MULTI, bool SCORES>
+template <int D, int BS, typename KV, bool MULTI, bool EXT>
 cudaError_t launch_attn_inst(const AttnLaunch& L, cudaStream_t stream) {
-    auto kern = attn_kernel<D, BS, KV, MULTI, SCORES>;
-    using Attrs = AttnAttrs<D, BS, KV, MULTI, SCORES>;
+    auto kern = attn_kernel<D, BS, KV, MULTI, EXT>;
+    using Attrs = AttnAttrs<D, BS, KV, MULTI, EXT>;
     cudaError_t e = raise_smem_limit_once(kern, Attrs::smem);
     if (e != cudaSuccess) return e;
     if (L.cluster > kMaxClusterParts) {
@@ -772,15 +775,15 @@ int attn_max_clusters_for_d(int block_size, int kv_dtype, int cluster, int threa
               : attn_max_clusters_inst<D, 32, __half>(cluster, threads, smem_bytes);
 }
 
-template <int D, bool MULTI, bool SCORES = false>
+template <int D, bool MULTI, bool EXT = false>
 cudaError_t launch_attn_for_d(const AttnLaunch& L, cudaStream_t stream) {
     const bool bf = L.kv_dtype == PA_BF16;
     if (L.block_size == 16)
-        return bf ? launch_attn_inst<D, 16, __nv_bfloat16, MULTI, SCORES>(L, stream)
-                  : launch_attn_inst<D, 16, __half, MULTI, SCORES>(L, stream);
+        return bf ? launch_attn_inst<D, 16, __nv_bfloat16, MULTI, EXT>(L, stream)
+                  : launch_attn_inst<D, 16, __half, MULTI, EXT>(L, stream);
     if (L.block_size == 32)
-        return bf ? launch_attn_inst<D, 32, __nv_bfloat16, MULTI, SCORES>(L, stream)
-                  : launch_attn_inst<D, 32, __half, MULTI, SCORES>(L, stream);
+        return bf ? launch_attn_inst<D, 32, __nv_bfloat16, MULTI, EXT>(L, stream)
+                  : launch_attn_inst<D, 32, __half, MULTI, EXT>(L, stream);
     return cudaErrorInvalidValue;
 }
 

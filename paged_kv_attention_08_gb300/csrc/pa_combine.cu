@@ -23,7 +23,8 @@ namespace {
 // groups finishes the head.  Two dependent memory round trips in all.
 constexpr int kCombineThreads = 256;
 
-template <int D>
+// LSE: the rows' statistics are wanted too (p.lse).
+template <int D, bool LSE>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
     constexpr int SLICES = D / 4;                      // float4 slices of one row
     constexpr int PGRP = kCombineThreads / SLICES;     // partition groups
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
         }
         const float inv = empty ? 0.f : 1.f / ls;
         const size_t o = (((size_t)b * p.q_len + qi) * p.num_heads + h) * D + sl * 4;
-        if (p.lse && sl == 0) p.lse[o / D] = empty ? INFINITY : row_lse(mx, ls);
+        if (LSE && sl == 0) p.lse[o / D] = empty ? INFINITY : row_lse(mx, ls);
         store_out(p.out, o, a.x * inv, p.out_dtype);
         store_out(p.out, o + 1, a.y * inv, p.out_dtype);
         store_out(p.out, o + 2, a.z * inv, p.out_dtype);
@@ -160,7 +161,6 @@ __global__ void __launch_bounds__(kCombineThreads) combine_balanced_kernel(const
     const size_t o = (((size_t)b * p.q_len + qi) * p.num_heads + h) * D;
     if (np == 0) {  // no page, no CTA: the empty-context result
         for (int d = tid; d < D; d += kCombineThreads) store_out(p.out, o + d, 0.f, p.out_dtype);
-        if (p.lse && tid == 0) p.lse[o / D] = INFINITY;
         return;
     }
     const long long Cn = p.num_ctas;
@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(kCombineThreads) combine_balanced_kernel(const
             a.w += x.w;
         }
         const float inv = empty ? 0.f : 1.f / ls;
-        if (p.lse && sl == 0) p.lse[o / D] = empty ? INFINITY : row_lse(mx, ls);
         store_out(p.out, o + sl * 4, a.x * inv, p.out_dtype);
         store_out(p.out, o + sl * 4 + 1, a.y * inv, p.out_dtype);
         store_out(p.out, o + sl * 4 + 2, a.z * inv, p.out_dtype);
@@ -420,9 +419,9 @@ cudaError_t launch_combine(const CombineParams& p, int head_dim, dim3 grid, bool
                            cudaStream_t stream) {
     void (*kern)(const CombineParams);
     switch (head_dim) {
-        case 64: kern = combine_kernel<64>; break;
-        case 128: kern = combine_kernel<128>; break;
-        default: kern = combine_kernel<256>; break;
+        case 64: kern = p.lse ? combine_kernel<64, true> : combine_kernel<64, false>; break;
+        case 128: kern = p.lse ? combine_kernel<128, true> : combine_kernel<128, false>; break;
+        default: kern = p.lse ? combine_kernel<256, true> : combine_kernel<256, false>; break;
     }
     const uint32_t smem = (uint32_t)p.num_parts * sizeof(float);
     if (smem > 48 * 1024) {

@@ -228,6 +228,7 @@ constexpr uint32_t kSmemAlignSlack = 1024;
 // rings of their own (a K stage is free once S is computed, long before P V
 // has read the V stage), each fed by its own copy warp.
 constexpr int kTileRows = 128;
+enum TileMode { kPlain = 0, kExtended = 1, kExact = 2 };  // see tile_kernel
 constexpr int kTileThreads = 384;  // warp 0 copies K, warp 3 copies V, warp 1 issues
                                    // MMAs, warp 2 owns tensor memory, warps 4-11 softmax
                                    // (two warpgroups, one half of a block's columns each)
@@ -358,6 +359,9 @@ cudaError_t allow_nonportable_clusters_once(Kern kern, AttrFlags& done) {
     return e;
 }
 
+// Does a launch ask for more than attention?
+inline bool extended(const AttnParams& p) { return p.own_lens || p.late_wait || p.scores || p.lse; }
+
 struct AttnLaunch {
     AttnParams p;
     CUtensorMap tmap_k;
@@ -377,10 +381,10 @@ cudaError_t launch_attn_d64(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_attn_d128(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_attn_d256(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_attn_d64_multi(const AttnLaunch& L, cudaStream_t stream);
-// Instantiations that also store the scores (p.scores).
-cudaError_t launch_attn_d64_scores(const AttnLaunch& L, cudaStream_t stream);
-cudaError_t launch_attn_d128_scores(const AttnLaunch& L, cudaStream_t stream);
-cudaError_t launch_attn_d256_scores(const AttnLaunch& L, cudaStream_t stream);
+// Instantiations for launches that ask for more than attention (AttnParams).
+cudaError_t launch_attn_d64_extended(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_attn_d128_extended(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_attn_d256_extended(const AttnLaunch& L, cudaStream_t stream);
 // Clusters of `cluster` one-token attention CTAs (tune: `threads`, `smem_bytes`)
 // resident at once on the current device (0 if the query fails).
 int attn_max_clusters_d64(int block_size, int kv_dtype, int cluster, int threads, uint32_t smem_bytes);
@@ -394,6 +398,10 @@ cudaError_t launch_tile_d64(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d128(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d256(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d256_compact(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_tile_d64_extended(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_tile_d128_extended(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_tile_d256_extended(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_tile_d256_compact_extended(const AttnLaunch& L, cudaStream_t stream);
 // Clusters of `cluster` tile-kernel CTAs resident at once on the current device.
 int tile_max_clusters_d64(int block_size, int kv_dtype, int cluster, uint32_t smem_bytes);
 int tile_max_clusters_d128(int block_size, int kv_dtype, int cluster, uint32_t smem_bytes);

@@ -67,7 +67,17 @@ constexpr float kTileRescaleSlack = 8.0f;  // log2 units: P may reach 2^8 before
 // warp loads the Q of segment s >= 1 by TMA once the last S MMA of segment
 // s - 2 has completed), and the first P V MMA of a segment waits until the
 // previous segment's O has been read out.
-template <int D, int BS, typename KV, int QR>
+//
+// MODE: what a launch may ask for beyond the attention itself.  The plain
+// instantiations know nothing of it: as run-time questions in the one kernel it
+// cost the several-token workloads 1.5 %, and the exact normaliser's second
+// form of the inner loop the prefill chunk 3 %.
+//   kPlain     attention alone
+//   kExtended  row statistics (p.lse), a shared prefix (p.own_lens), a late wait
+//   kExact     kExtended, and fp16's normaliser sums the weights as they are, not
+//              as rounded for the P V MMA: the tokens' accumulated weights are
+//              formed from it
+template <int D, int BS, typename KV, int QR, int MODE = kPlain>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v,
@@ -79,6 +89,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int DBLK = D / 64;
     constexpr int KSTEPS = D / 16;
     constexpr float NEG_INF = -INFINITY;
+    constexpr bool EXT = MODE != kPlain;
     constexpr bool kBF = std::is_same<KV, __nv_bfloat16>::value;
     // P enters the P V MMA as 16-bit values.  bf16 keeps 8 significant bits,
     // so P is split into a high and a low part (two MMAs, ~16 bits); fp16
@@ -138,7 +149,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int part = blockIdx.x;
     const int tiles = (U + kTileRows - 1) / kTileRows;  // 128-row tiles of a unit
 
-    if (!p.late_wait) grid_dependency_wait();
+    if (!EXT || !p.late_wait) grid_dependency_wait();
     grid_launch_dependents();
 
     // Element offset of unit row u's query / output vector ([B, Q, H, D]).
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
 #pragma unroll
             for (int q = 0; q < kMaxClusterParts; ++q) cl_w[t * 8 + q] = w[q] * inv;
-            if (p.lse && seg0.tile * kTileRows + r < U)
+            if (EXT && p.lse && seg0.tile * kTileRows + r < U)
                 p.lse[row_off(seg0.b, seg0.kvh, seg0.tile * kTileRows + r) / D] = row_lse(M, Ls);
         }
         __syncthreads();
@@ -376,10 +387,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int idx = tid; idx < kTileRows * D; idx += kTileThreads) {
                 const int u = seg0.tile * kTileRows + idx / D;
                 if (u < U) store_out(p.out, row_off(seg0.b, seg0.kvh, u) + idx % D, 0.f, p.out_dtype);
-                if (p.lse && u < U && idx % D == 0) p.lse[row_off(seg0.b, seg0.kvh, u) / D] = INFINITY;
+                if (EXT && p.lse && u < U && idx % D == 0) p.lse[row_off(seg0.b, seg0.kvh, u) / D] = INFINITY;
             }
         }
-        late_dependency_wait(p.late_wait);
+        if constexpr (EXT) late_dependency_wait(p.late_wait);
         return;
     }
 
@@ -726,7 +737,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int idx = sr; idx < kTileRows * D; idx += 256) {
                     const int uu = g.tile * kTileRows + idx / D;
                     if (uu < U) store_out(p.out, row_off(g.b, g.kvh, uu) + idx % D, 0.f, p.out_dtype);
-                    if (p.lse && uu < U && idx % D == 0) p.lse[row_off(g.b, g.kvh, uu) / D] = INFINITY;
+                    if (EXT && p.lse && uu < U && idx % D == 0) p.lse[row_off(g.b, g.kvh, uu) / D] = INFINITY;
                 }
             }
         }
@@ -743,7 +754,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // tokens t < lim: the row's causal limit, the table's reach, the segment's end
             const int lim =
                 u >= U ? 0
-                       : min(tend, p.own_lens ? prefix_limit(g.T, g.b, u >> gshift, Q, p.own_q, p.own_lens)
+                       : min(tend, EXT && p.own_lens ? prefix_limit(g.T, g.b, u >> gshift, Q, p.own_q, p.own_lens)
                                               : ctx - Q + (u >> gshift) + 1);
             const int32_t* table_row = p.block_tables + (size_t)g.b * p.max_blocks;
             // which pages of the segment's block k hold data: bit q for page q
@@ -832,7 +843,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     // high and a low part, hi in columns [0, BN/2) and lo in [BN/2, BN)
                     // of the buffer; for fp16 the high part alone
                     const float me = (m == NEG_INF) ? 0.f : m;
-                    auto form_p = [&](auto exact_l) {
+                    if (!dead) {
 #pragma unroll
                         for (int c0 = 0; c0 < BH; c0 += 16) {
                             uint32_t ph[8], pl[8];
@@ -847,7 +858,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                     Mma<KV>::unpack(h, h0, h1);
                                     l += x0 + x1;
                                     pl[c / 2] = Mma<KV>::pack(x0 - h0, x1 - h1);
-                                } else if constexpr (decltype(exact_l)::value) {
+                                } else if constexpr (MODE == kExact) {
                                     l += x0 + x1;
                                 } else {
                                     l = Mma<KV>::add2(h, l);  // the weights the MMA uses
@@ -863,12 +874,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             tc::st_32x32b_x8(sb + col_hi, ph);
                             if (kSplitP) tc::st_32x32b_x8(sb + col_lo, pl);
                         }
-                    };
-                    // (row statistics wanted: the normaliser of the weights as they
-                    // are, since those of the tokens are formed from it)
-                    if (!dead) {
-                        if (!kSplitP && p.lse) form_p(std::true_type{});
-                        else form_p(std::false_type{});
                     }
                     tc::wait_st();
                     // zero the V rows of masked pages and past the segment's last
@@ -974,7 +979,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         orow = (((size_t)blockIdx.x * 2 + (s == 0 ? 0 : 1)) * U + u) * D;
                     else
                         orow = ((((size_t)g.b * Hkv + g.kvh) * p.num_parts + part) * U + u) * D;
-                    if (fin && p.lse && wg == 0) p.lse[orow / D] = row_lse(m, l);
+                    if (EXT && fin && p.lse && wg == 0) p.lse[orow / D] = row_lse(m, l);
                     if (!fin && wg == 0) {
                         p.part_ml[(orow / D) * 2] = l > 0.f ? m : NEG_INF;
                         p.part_ml[(orow / D) * 2 + 1] = l;
@@ -1030,19 +1035,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc::tmem_dealloc(tmem, kCols);
     }
     if (p.cluster_reduce) cluster_merge();
-    late_dependency_wait(p.late_wait);
+    if constexpr (EXT) late_dependency_wait(p.late_wait);
 }
 
 // Per-instantiation flag of the shared-memory limit set once per device.
-template <int D, int BS, typename KV, int QR>
+template <int D, int BS, typename KV, int QR, int MODE = kPlain>
 struct TileAttrs {
     static inline AttrFlags smem;
 };
 
-template <int D, int BS, typename KV, int QR>
+template <int D, int BS, typename KV, int QR, int MODE = kPlain>
 cudaError_t launch_tile_inst(const AttnLaunch& L, cudaStream_t stream) {
-    auto kern = tile_kernel<D, BS, KV, QR>;
-    cudaError_t e = raise_smem_limit_once(kern, TileAttrs<D, BS, KV, QR>::smem);
+    auto kern = tile_kernel<D, BS, KV, QR, MODE>;
+    cudaError_t e = raise_smem_limit_once(kern, TileAttrs<D, BS, KV, QR, MODE>::smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = L.grid;
@@ -1116,6 +1121,20 @@ cudaError_t launch_tile_for_d(const AttnLaunch& L, cudaStream_t stream) {
         return bf ? launch_tile_inst<D, 32, __nv_bfloat16, QR>(L, stream)
                   : launch_tile_inst<D, 32, __half, QR>(L, stream);
     return cudaErrorInvalidValue;
+}
+
+// The same with row statistics, a shared prefix or a late wait.
+template <int D, int QR>
+cudaError_t launch_tile_extended_for_d(const AttnLaunch& L, cudaStream_t stream) {
+    const bool bs16 = L.block_size == 16;
+    if (L.kv_dtype == PA_BF16)
+        return bs16 ? launch_tile_inst<D, 16, __nv_bfloat16, QR, kExtended>(L, stream)
+                    : launch_tile_inst<D, 32, __nv_bfloat16, QR, kExtended>(L, stream);
+    if (L.p.lse)
+        return bs16 ? launch_tile_inst<D, 16, __half, QR, kExact>(L, stream)
+                    : launch_tile_inst<D, 32, __half, QR, kExact>(L, stream);
+    return bs16 ? launch_tile_inst<D, 16, __half, QR, kExtended>(L, stream)
+                : launch_tile_inst<D, 32, __half, QR, kExtended>(L, stream);
 }
 
 }  // namespace pa

@@ -122,3 +122,27 @@ def test_samples_of_one_prompt():
         want = ref.shared_prefix(q_out.cpu(), kc.cpu(), vc.cpu(), ptable, plens.cpu(), own, lens, scale)
         ref.close_out(out.cpu(), want, ref.out_slack(q_out.cpu(), kc.cpu(), vc.cpu(), scale, P + 50))
     assert pa.device_error() == 0
+
+
+@pytest.mark.parametrize("Q", [1, 40])
+def test_an_empty_batch_launches_nothing(Q):
+    H, Hkv, D, bs = 8, 2, 64, 16
+    kc = torch.ones((4, bs, Hkv, D), dtype=torch.float16, device=DEV)
+    vc = kc.clone()
+
+    def none(*shape, dtype=torch.int32):
+        return torch.empty((0,) + shape, dtype=dtype, device=DEV)
+
+    q, kv = none(Q, H, D, dtype=torch.float16), none(Q, Hkv, D, dtype=torch.float16)
+    table, lens, w = none(3), none(), none(Hkv, 3 * bs, dtype=torch.float32)
+    phases = pa.rope_phases(torch.ones(32, dtype=torch.float64)).to(DEV)
+    pa.rope_append_kv(q, kc, vc, q, kv, kv, torch.empty((2, 0, Q), dtype=torch.int32, device=DEV), phases,
+                      torch.zeros(32, dtype=torch.int32, device=DEV), table, lens)
+    assert pa.workspace_size_accumulate(q, kc, table, torch.float16, 48) >= 0
+    pa.decode_accumulate(q.clone(), w, q, kc, vc, table, lens, 0.1, 48)
+    ptable, plens = torch.zeros((1, 2), dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert pa.workspace_size_shared_prefix(q, kc, ptable, table, torch.float16, 20, 48) == 0
+    pa.decode_shared_prefix(q.clone(), q, kc, vc, ptable, plens, table, lens, 0.1, 20, 48)
+    pa.evict_kv(kc, vc, w, table, lens, table, w, none(), none(Hkv, 7))
+    torch.cuda.synchronize()
+    assert (kc == 1).all() and (vc == 1).all()
