@@ -486,63 +486,116 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
     }
 }
 
-constexpr int kPackThreads = 256;
-constexpr int kPackRows = kPackThreads / 8;  // rows of 64 columns moved at a time
+constexpr int kPackThreads = 512;
+constexpr int kPackRows = kPackThreads / 8;          // rows of 64 columns moved by one step
 constexpr int kPackSteps = 8;
+constexpr int kPackChunk = kPackRows * kPackSteps;   // rows that are read before the first is written
+constexpr int kPackSegment = 8192;                   // rows whose places are in shared memory at a time
+constexpr uint32_t kPackSmem = kPackSegment * 8 + kPackSegment / 16 * 4;
 
 // In place: token j of the new row comes from slot kept[j] >= j of the same
 // row, so a chunk of rows may be written once all of it has been read, and
 // no later chunk reads what it writes.  One CTA per (64 columns of the keys
-// or of the values, kv head, sequence) takes the chunks in order; columns
-// do not meet, so the CTAs need no order among them.  The first slice's CTA
-// packs the weights as well.
-__global__ void __launch_bounds__(kPackThreads) evict_pack_kernel(const EvictParams p) {
+// or of the values, kv head, sequence) takes the chunks in order, the next
+// chunk's rows on their way while it writes this one's; columns do not meet,
+// so the CTAs need no order among them.  One more CTA packs the weights.
+//
+// Bound: the latency of a chunk (64 KB a CTA in flight), with few CTAs: 4
+// sequences, 8 kv heads and head_dim 128 are 128 of them.  The rows' places
+// are found for a segment at once: looked up chunk by chunk, 256 rows at a
+// time and none ahead, four sequences of 65,000 to 131,072 tokens cut to 8192
+// took 412 us.
+__global__ void __launch_bounds__(kPackThreads, 1) evict_pack_kernel(const EvictParams p) {
+    extern __shared__ long long src[];  // [segment] slot that a row comes from, -1: it stays
+    int32_t* page = reinterpret_cast<int32_t*>(src + kPackSegment);  // block of each new page, or -1
     const int tid = threadIdx.x;
     const int kvh = blockIdx.y, b = blockIdx.z;
     const int slices = p.head_dim / 64;
-    const int slice = blockIdx.x % slices;
-    uint4* cache = static_cast<uint4*>((int)blockIdx.x < slices ? p.k_cache : p.v_cache);
     grid_dependency_wait();
     grid_launch_dependents();
     const size_t unit = (size_t)b * p.num_kv_heads + kvh;
     const int32_t* kept = p.kept + unit * p.budget;
-    const int32_t* old_row = p.block_tables + (size_t)b * p.max_blocks;
-    const int32_t* new_row = p.new_block_tables + (size_t)b * p.new_max_blocks;
     const int n = p.new_lens[b];
-    const long long row = (long long)p.num_kv_heads * (p.head_dim / 8);
-    const int col = kvh * (p.head_dim / 8) + slice * 8 + (tid & 7);
-    for (int j0 = 0; j0 < n; j0 += kPackRows * kPackSteps) {
-        uint4 v[kPackSteps];
-        long long dst[kPackSteps];
-#pragma unroll
-        for (int k = 0; k < kPackSteps; ++k) {
-            const int j = j0 + k * kPackRows + (tid >> 3);
-            dst[k] = -1;
-            if (j < n) {
-                const long long s = slot_of(old_row, kept[j], p.block_size, p.max_blocks, p.num_blocks);
-                const long long d = slot_of(new_row, j, p.block_size, p.new_max_blocks, p.num_blocks);
-                if (s >= 0 && d >= 0 && s != d) {
-                    dst[k] = d;
-                    v[k] = cache[s * row + col];
-                }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kPackSteps; ++k)
-            if (dst[k] >= 0) cache[dst[k] * row + col] = v[k];
-    }
-    if (blockIdx.x == 0) {
+    if ((int)blockIdx.x == 2 * slices) {
+        // the weights, and zeros behind them
         const float* w = p.weights + unit * p.max_blocks * p.block_size;
         const int new_width = p.new_max_blocks * p.block_size;
         float* nw = p.new_weights + unit * new_width;
-        for (int j0 = 0; j0 < n; j0 += kPackThreads) {
-            const int j = j0 + tid;
-            const float x = j < n ? w[kept[j]] : 0.f;
+        for (int j0 = 0; j0 < n; j0 += kPackThreads * kPackSteps) {
+            float x[kPackSteps];
+#pragma unroll
+            for (int k = 0; k < kPackSteps; ++k) {
+                const int j = j0 + k * kPackThreads + tid;
+                if (j < n) x[k] = w[kept[j]];
+            }
             __syncthreads();
-            if (j < n) nw[j] = x;
+#pragma unroll
+            for (int k = 0; k < kPackSteps; ++k) {
+                const int j = j0 + k * kPackThreads + tid;
+                if (j < n) nw[j] = x[k];
+            }
         }
         for (int j = n + tid; j < new_width; j += kPackThreads) nw[j] = 0.f;
+        return;
+    }
+    uint4* cache = static_cast<uint4*>((int)blockIdx.x < slices ? p.k_cache : p.v_cache);
+    const int32_t* old_row = p.block_tables + (size_t)b * p.max_blocks;
+    const int32_t* new_row = p.new_block_tables + (size_t)b * p.new_max_blocks;
+    const long long row = (long long)p.num_kv_heads * (p.head_dim / 8);
+    const int col = kvh * (p.head_dim / 8) + (int)(blockIdx.x % slices) * 8 + (tid & 7);
+    const int bshift = __ffs(p.block_size) - 1;
+    for (int seg = 0; seg < n; seg += kPackSegment) {
+        const int count = min(n - seg, kPackSegment);
+        __syncthreads();  // the previous segment's places have been used
+        for (int i = tid; i < (count + p.block_size - 1) >> bshift; i += kPackThreads)
+            page[i] = page_phys(new_row, (seg >> bshift) + i, p.new_max_blocks, p.num_blocks);
+        for (int i0 = tid; i0 < count; i0 += kPackThreads * 4) {
+            int t[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * kPackThreads;
+                t[k] = i < count ? kept[seg + i] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * kPackThreads;
+                if (i < count) src[i] = slot_of(old_row, t[k], p.block_size, p.max_blocks, p.num_blocks);
+            }
+        }
+        __syncthreads();
+        auto to_of = [&](int i) -> long long {  // slot of the segment's row i, -1: it is not moved
+            if (i >= count || src[i] < 0) return -1;
+            const int e = page[i >> bshift];
+            const long long d = (long long)e * p.block_size + (i & (p.block_size - 1));
+            return e < 0 || d == src[i] ? -1 : d;
+        };
+        uint4 v[2][kPackSteps];
+        auto read = [&](int i0, uint4 (&x)[kPackSteps]) {
+#pragma unroll
+            for (int k = 0; k < kPackSteps; ++k) {
+                const int i = i0 + k * kPackRows + (tid >> 3);
+                if (to_of(i) >= 0) x[k] = cache[src[i] * row + col];
+            }
+        };
+        auto write = [&](int i0, const uint4 (&x)[kPackSteps]) {
+#pragma unroll
+            for (int k = 0; k < kPackSteps; ++k) {
+                const int i = i0 + k * kPackRows + (tid >> 3);
+                const long long d = to_of(i);
+                if (d >= 0) cache[d * row + col] = x[k];
+            }
+        };
+        read(0, v[0]);
+        for (int i0 = 0; i0 < count; i0 += 2 * kPackChunk) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = i0 + h * kPackChunk;
+                if (i >= count) break;  // (the same in every thread)
+                read(i + kPackChunk, v[1 - h]);
+                __syncthreads();  // the chunk has been read
+                write(i, v[h]);
+            }
+        }
     }
 }
 
@@ -582,7 +635,11 @@ cudaError_t launch_evict(EvictParams p, bool in_place, bool pdl, cudaStream_t st
     cfg.attrs = attr + 1;
     cfg.numAttrs = pdl ? 1 : 0;
     if (in_place) {
-        cfg.gridDim = dim3((unsigned)(2 * p.head_dim / 64), (unsigned)p.num_kv_heads, (unsigned)p.batch);
+        static AttrFlags smem_limit;
+        e = raise_smem_limit_once(evict_pack_kernel, smem_limit);
+        if (e != cudaSuccess) return e;
+        cfg.dynamicSmemBytes = kPackSmem;
+        cfg.gridDim = dim3((unsigned)(2 * p.head_dim / 64 + 1), (unsigned)p.num_kv_heads, (unsigned)p.batch);
         cfg.blockDim = dim3(kPackThreads);
         return cudaLaunchKernelEx(&cfg, evict_pack_kernel, p);
     }

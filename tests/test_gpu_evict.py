@@ -160,3 +160,17 @@ def test_rows_that_several_ctas_share(T, kind):
     if kind == "one digit":   # 1 .. 1.25: the first eleven bits agree
         c["weights"] = 1 + c["weights"] / c["weights"].max() * 0.24
     check(c, 700, 4, 100, False)
+
+
+@pytest.mark.parametrize("budget,T", [(513, 3000), (1500, 1501), (9000, 20000)])
+def test_in_place_over_several_chunks_and_segments(budget, T):
+    """Chunks of 512 rows whose sources the chunks before must not touch; a budget past one segment."""
+    c = case(40 + T, 2, 2, 128, 16, torch.bfloat16, [T, T - 7], budget)
+    check(c, budget, 3, 11, True)
+
+
+def test_in_place_keeps_an_untouched_front():
+    """Weights that fall with the index: the kept tokens are the first ones and none moves."""
+    c = case(50, 1, 2, 64, 16, torch.float16, [2000], 600)
+    c["weights"] = torch.arange(c["weights"].numel(), 0, -1).float().reshape(c["weights"].shape)
+    check(c, 600, 0, 0, True)
