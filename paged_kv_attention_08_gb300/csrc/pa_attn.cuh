@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(256, 1)
     uint64_t* empty = reinterpret_cast<uint64_t*>(smem + L.empty_off);
     int32_t* phys_of = reinterpret_cast<int32_t*>(smem + L.phys_off);
     int32_t* seq_pages = reinterpret_cast<int32_t*>(smem + L.seq_off);  // balanced split only
+    float* row_stat = reinterpret_cast<float*>(smem + L.seq_off);  // accumulated weights only: m + log2 l
     if (tid == 0) {
         for (int i = 0; i < p.nt * p.ns; ++i) {
             mbar_init(smem_u32(full + i), 1);
@@ -501,8 +502,49 @@ __global__ void __launch_bounds__(256, 1)
         return [&, b, kvh](int idx, float A, float M, float Ls) {
             store_out(p.out, row_off(b, kvh, idx / D) + idx % D, Ls > 0.f ? A / Ls : 0.f,
                       p.out_dtype);
-            if (EXT && p.lse && idx % D == 0) p.lse[row_off(b, kvh, idx / D) / D] = row_lse(M, Ls);
+            if (EXT && p.lse && idx % D == 0) {
+                p.lse[row_off(b, kvh, idx / D) / D] = row_lse(M, Ls);
+                row_stat[idx / D] = row_lse(M, Ls);
+            }
         };
+    };
+    // The weights of the CTA's tokens, from the scores that it has stored and
+    // the rows' statistics in row_stat (a barrier after both): pages [pb, pe),
+    // and with `rest` the tokens past them, which no row attended to.
+    auto add_weights = [&](int b, int kvh, int pb, int pe, int T, bool rest) {
+        const size_t unit = (size_t)b * Hkv + kvh;
+        const float* sc = p.scores + unit * R * p.score_width;
+        const float* in = p.weights_in + unit * p.max_blocks * BS;
+        float* out = p.weights_out + unit * p.max_blocks * BS;
+        const int32_t* row = p.block_tables + (size_t)b * p.max_blocks;
+        const bool wide = ((reinterpret_cast<uintptr_t>(p.weights_in) |
+                            reinterpret_cast<uintptr_t>(p.weights_out)) & 15) == 0;
+        const int end = min(pe * BS, T), last = rest ? T : end;
+        for (int t = pb * BS + tid * 4; t < last; t += blockDim.x * 4) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int e = t < end ? __ldg(row + t / BS) : -1;  // (four tokens lie in one page)
+            if (e >= 0 && (int64_t)e < p.num_blocks) {
+#pragma unroll 4
+                for (int r = 0; r < R; ++r) {
+                    const float4 x = *reinterpret_cast<const float4*>(sc + (size_t)r * p.score_width + t);
+                    const float l = row_stat[r];  // (+inf where the row attends to nothing: weight 0)
+                    sum.x += fast_exp2(fmaf(x.x, qscale, -l));
+                    sum.y += fast_exp2(fmaf(x.y, qscale, -l));
+                    sum.z += fast_exp2(fmaf(x.z, qscale, -l));
+                    sum.w += fast_exp2(fmaf(x.w, qscale, -l));
+                }
+            }
+            if (wide && t + 4 <= T) {
+                const float4 w = *reinterpret_cast<const float4*>(in + t);
+                *reinterpret_cast<float4*>(out + t) =
+                    make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
+            } else {
+                const float d[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (t + k < T) out[t + k] = in[t + k] + d[k];
+            }
+        }
     };
     // (m, l, acc) of the CTA's rows into workspace row `row0 + r`.
     auto emit_rows = [&](size_t row0) {
@@ -618,6 +660,7 @@ __global__ void __launch_bounds__(256, 1)
 
     if (p.final_out) {
         run_segment(b, kvh, pb, max(pb, pe), T, emit_final(b, kvh));
+        if (EXT && p.weights_out) add_weights(b, kvh, pb, max(pb, pe), T, true);
     } else if (p.cluster_reduce) {
         run_segment(b, kvh, pb, max(pb, pe), T, [&](int idx, float A, float M, float Ls) {
             cpart[idx] = A;
@@ -684,7 +727,24 @@ __global__ void __launch_bounds__(256, 1)
             merge(std::integral_constant<int, kMaxClusterParts>{});
         else
             merge(std::integral_constant<int, kMaxDecodeClusterParts>{});
+        if (EXT && p.weights_out) {
+            // every row's statistics, for this partition's weights
+            if (tid < R) {
+                float M = NEG_INF, Ls = 0.f;
+                for (int q = 0; q < P; ++q)
+                    M = fmaxf(M, ld_cluster_f32(map_cluster_rank(cp, (uint32_t)q) + 4u * (R * D + tid)));
+                for (int q = 0; q < P; ++q) {
+                    const uint32_t at = map_cluster_rank(cp, (uint32_t)q) + 4u * (R * D + tid);
+                    const float m = ld_cluster_f32(at);
+                    if (m != NEG_INF) Ls = fmaf(fast_exp2(m - M), ld_cluster_f32(at + 4u * R), Ls);
+                }
+                row_stat[tid] = row_lse(M, Ls);
+            }
+            __syncthreads();
+        }
         cluster_sync_relaxed();  // no CTA leaves while others still read its shared memory
+        if (EXT && p.weights_out)
+            add_weights(b, kvh, pb, max(pb, pe), T, part == p.num_parts - 1);
     }
     if constexpr (EXT) late_dependency_wait(p.late_wait);
 }

@@ -41,6 +41,10 @@ struct AttnParams {
     float* scores;            // warp-level kernel: [B, Hkv, Q * group, score_width] or null: q . K
                               // of every token of a read page, -inf where masked
     int64_t score_width;
+    // Beside scores, where a CTA or its cluster has the rows' final statistics
+    // (one pass, or a cluster's reduction), else null: the tokens' weights.
+    const float* weights_in;  // [B, Hkv, max_blocks * block_size]
+    float* weights_out;
     float* lse;               // [B, Q, H] or null: m + log2 l of each row (+inf for an empty one)
     int64_t num_blocks;
     float qscale;             // scale * log2(e): scores are kept in base-2 units
@@ -105,12 +109,11 @@ struct WeightParams {
     int32_t token_limit;      // tokens from here on were not attended
     const float* scores;      // as in AttnParams
     int64_t score_width;
-    // Stored scores of a call whose partitions' statistics are in part_ml
-    // [B, Hkv, num_parts, Q * group, 2] (else null: lse is filled): the rows'
-    // statistics are formed from those, so that the launch need not wait for
-    // the combine kernel that runs before it (late_wait as in AttnParams).
+    // Stored scores of a call whose partitions left their statistics [B, Hkv,
+    // num_parts, Q * group, 2] (else null: lse is filled): the rows' own are formed
+    // from those, so that the launch runs beside the combine kernel before it.
     const float* part_ml;
-    int32_t num_parts, part_pages, late_wait;
+    int32_t num_parts, part_pages;
     int32_t* err;             // device error word, bound on every wait (tile kernel)
     uint64_t timeout_ns;
 };

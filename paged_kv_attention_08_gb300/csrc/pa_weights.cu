@@ -17,9 +17,12 @@ __global__ void __launch_bounds__(kSThreads) weights_of_scores_kernel(const Weig
     const int tid = threadIdx.x;
     const int kvh = blockIdx.y, b = blockIdx.z;
     const int G = p.group, rows = p.q_len * G;
-    if (!p.late_wait) grid_dependency_wait();
+    // With part_ml only the attention kernel is needed, which is done once the
+    // combine kernel before this one has started; the last CTA waits for that
+    // one, so that this launch does not end before it.
+    if (!p.part_ml) grid_dependency_wait();
     grid_launch_dependents();
-    late_dependency_wait(p.late_wait);  // (the last CTA: the launch ends after the one before)
+    late_dependency_wait(p.part_ml != nullptr);
     const int T = reachable_tokens(p.context_lens, b, p.max_blocks, p.block_size);
     const int t0 = blockIdx.x * (kSThreads * 4) + tid * 4;
     if ((int)blockIdx.x * (kSThreads * 4) >= T) return;

@@ -174,3 +174,10 @@ def test_contexts_longer_than_announced_drop_the_rest():
     assert torch.equal(new[:, :, :96], torch.where(torch.arange(96) < short["lens"].view(2, 1, 1),
                                                    want[:, :, :96], new[:, :, :96]))
     assert torch.equal(new[0, :, 96:200], c["weights"][0, :, 96:200])   # added weight: none
+
+
+@pytest.mark.parametrize("B,T", [(1, 30000), (2, 9000), (4, 4096), (3, 60)])
+def test_weights_by_the_attention_kernel_or_apart(B, T):
+    """Cluster plans with long and short partitions, and one pass."""
+    check(case(120 + T, B, 1, 8, 2, 128, 16, [T - 100 * b if T > 1000 else T - b for b in range(B)],
+               torch.bfloat16))
