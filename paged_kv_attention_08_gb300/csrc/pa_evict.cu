@@ -13,6 +13,8 @@
 //   evict_pack_kernel    the same within the same pages.
 //
 // Bound: memory (the weights are read, each kept row is read and written).
+// Four sequences of 65,000 to 131,072 tokens, 8 kv heads of 128, cut to 8192 each:
+// 79 us to other pages (selection 26, copy 47 at 5.7 TB/s), 142 us in place.
 #include "pa_device.cuh"
 
 namespace pa {
@@ -90,7 +92,10 @@ __device__ __forceinline__ int quad_word(int q) { return q * 4 + (q >> 3) * 4; }
 // to write them.
 //
 // What bounds it: the latency of its steps (a cluster barrier 1 to 2 us with
-// the skew of its CTAs), not the 17 MB that 32 rows of 128K weights are.
+// the skew of its CTAs), not the 17 MB that 32 rows of 128K weights are.  The
+// 32 rows of up to 131,072 tokens take 26 us; one CTA to a row, reading the row
+// from global memory in four passes of 8 bits, took 460 us, and a cluster
+// whose CTAs read each other's whole bins 37 us.
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictParams p) {
     extern __shared__ __align__(16) uint32_t keys[];
@@ -436,7 +441,8 @@ __device__ __forceinline__ long long slot_of(const int32_t* row, int t, int bloc
 constexpr int kCopyThreads = 256;
 constexpr int kCopyRows = 64;  // tokens of one kv head per CTA
 
-// One CTA per (64 tokens of the new row, kv head, sequence).
+// One CTA per (64 tokens of the new row, kv head, sequence): 32 KB of keys and
+// values, eight 16-byte vectors of a thread on their way at a time.
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictParams p) {
     __shared__ long long src[kCopyRows], dst[kCopyRows];
     const int tid = threadIdx.x;

@@ -9,7 +9,9 @@ namespace pa {
 namespace {
 
 // One thread per four neighbouring tokens of a kv head.  Bound: memory, 4 bytes
-// per (row, token) and 8 per token.
+// per (row, token) and 8 per token: 4 rows of 1M (token, kv head) pairs, 25 MB, in
+// 10.7 us cold.  The scores are stored in fp32, as they were formed.  (Reading
+// the keys again instead took 79 us there, and 135 us for 2M pairs.)
 constexpr int kSThreads = 256;
 
 __global__ void __launch_bounds__(kSThreads) weights_of_scores_kernel(const WeightParams p) {
