@@ -261,6 +261,7 @@ struct Plan {
     int32_t own_q = 0;
     bool late_wait = false;             // see AttnParams
     float* lse = nullptr;               // row statistics wanted: see AttnParams
+    int32_t token_limit = 0;            // see AttnParams
     float* scores = nullptr;            // scores wanted: see AttnParams
     int64_t score_width = 0;
     const float* weights_in = nullptr;
@@ -783,6 +784,7 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     p.own_lens = plan.own_lens;
     p.own_q = plan.own_q;
     p.late_wait = plan.late_wait ? 1 : 0;
+    p.token_limit = plan.token_limit;
     p.lse = plan.lse;
     p.scores = plan.scores;
     p.score_width = plan.score_width;
@@ -847,6 +849,7 @@ pa_status launch_tile(void* out, const void* q, const void* k, const void* v, co
     p.own_lens = plan.own_lens;
     p.own_q = plan.own_q;
     p.late_wait = plan.late_wait ? 1 : 0;
+    p.token_limit = plan.token_limit;
     p.lse = plan.lse;
     p.timeout_ns = kDefaultTimeoutNs;
     L.head_dim = s->head_dim;
@@ -1036,8 +1039,9 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
 // of 64 pages even where all of them are resident at once.  The lengths are
 // not known here, and one pass lasts as long as its longest sequence: 32
 // sequences of 1 .. 8192 tokens took 124 us in one pass, 95 us in partitions
-// of 1024 tokens.  A call's partitions cover max_context_len and no more, so
-// that the scores stay inside their array.
+// of 1024 tokens.  Tokens past max_context_len's pages are left out (token_limit),
+// so that the scores stay inside their array.  The weights' launches are sized by
+// that too, not by the tables, which may be far wider than any sequence.
 Plan accumulate_plan(const pa_shape* s, int32_t max_context_len, int sms, int32_t q_len) {
     Plan p = make_plan(s, max_context_len, 0, sms, q_len);
     const int pages = pages_for(s, max_context_len);
@@ -1499,6 +1503,7 @@ pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weigh
     plan.lse = reinterpret_cast<float*>(ws + lse_off);
     plan.scores = scores ? reinterpret_cast<float*>(ws + score_off) : nullptr;
     plan.score_width = (int64_t)pages_for(shape, max_context_len) * shape->block_size;
+    plan.token_limit = (int32_t)std::min<int64_t>(plan.score_width, INT32_MAX);
     // Where the attention kernel ends with the rows' statistics (one pass, or a
     // cluster's reduction) it adds the weights itself, unless its CTAs have many
     // tokens each: a launch of the whole GPU is then faster at it (700 tokens:
@@ -1538,8 +1543,7 @@ pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weigh
     w.group = shape->num_heads / shape->num_kv_heads;
     w.block_size = shape->block_size;
     w.max_blocks = shape->max_blocks_per_seq;
-    // what the partitions cover (persistent CTAs walk their sequences whole)
-    w.token_limit = plan.persistent ? 0x7fffffff : (int32_t)plan.score_width;
+    w.token_limit = plan.token_limit;
     w.err = err;
     w.timeout_ns = kDefaultTimeoutNs;
     cudaError_t e;

@@ -509,8 +509,9 @@ __global__ void __launch_bounds__(256, 1)
         };
     };
     // The weights of the CTA's tokens, from the scores that it has stored and
-    // the rows' statistics in row_stat (a barrier after both): pages [pb, pe),
-    // and with `rest` the tokens past them, which no row attended to.
+    // the rows' statistics in row_stat (a barrier after both): pages [pb, pe)
+    // of a sequence of T tokens, and with `rest` the tokens past them, which no
+    // row attended to.
     auto add_weights = [&](int b, int kvh, int pb, int pe, int T, bool rest) {
         const size_t unit = (size_t)b * Hkv + kvh;
         const float* sc = p.scores + unit * R * p.score_width;
@@ -640,7 +641,8 @@ __global__ void __launch_bounds__(256, 1)
     // the table entries are fetched before the context length is known
     // (every index stays inside the table row); those past it are masked
     start_fetch(b, pb, min(pb + p.part_pages, p.max_blocks));
-    const int T = reachable_tokens(p.context_lens, b, p.max_blocks, BS);
+    const int reach = reachable_tokens(p.context_lens, b, p.max_blocks, BS);
+    const int T = EXT && p.token_limit ? min(reach, p.token_limit) : reach;
     const int npages = (T + BS - 1) / BS;
     const int pe = min(pb + p.part_pages, npages);
     if (pb >= pe && !p.cluster_reduce) {
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(256, 1)
 
     if (p.final_out) {
         run_segment(b, kvh, pb, max(pb, pe), T, emit_final(b, kvh));
-        if (EXT && p.weights_out) add_weights(b, kvh, pb, max(pb, pe), T, true);
+        if (EXT && p.weights_out) add_weights(b, kvh, pb, max(pb, pe), reach, true);
     } else if (p.cluster_reduce) {
         run_segment(b, kvh, pb, max(pb, pe), T, [&](int idx, float A, float M, float Ls) {
             cpart[idx] = A;
@@ -744,7 +746,7 @@ __global__ void __launch_bounds__(256, 1)
         }
         cluster_sync_relaxed();  // no CTA leaves while others still read its shared memory
         if (EXT && p.weights_out)
-            add_weights(b, kvh, pb, max(pb, pe), T, part == p.num_parts - 1);
+            add_weights(b, kvh, pb, max(pb, pe), reach, part == p.num_parts - 1);
     }
     if constexpr (EXT) late_dependency_wait(p.late_wait);
 }

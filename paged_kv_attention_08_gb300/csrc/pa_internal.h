@@ -38,6 +38,8 @@ struct AttnParams {
     // (The launch before must let its dependents go no earlier than after its
     // own wait, as the attention kernels do: then what came before it is done.)
     int32_t late_wait;
+    int32_t token_limit;      // 0, or tokens from here on are not attended to (a multiple of
+                              // block_size): what the scores and weights are sized for
     float* scores;            // warp-level kernel: [B, Hkv, Q * group, score_width] or null: q . K
                               // of every token of a read page, -inf where masked
     int64_t score_width;
@@ -363,7 +365,9 @@ cudaError_t allow_nonportable_clusters_once(Kern kern, AttrFlags& done) {
 }
 
 // Does a launch ask for more than attention?
-inline bool extended(const AttnParams& p) { return p.own_lens || p.late_wait || p.scores || p.lse; }
+inline bool extended(const AttnParams& p) {
+    return p.own_lens || p.late_wait || p.scores || p.lse || p.token_limit;
+}
 
 struct AttnLaunch {
     AttnParams p;

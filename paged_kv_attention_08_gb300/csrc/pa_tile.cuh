@@ -157,6 +157,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         return (((size_t)b * Q + (u >> gshift)) * p.num_heads + kvh * G + (u & (G - 1))) * D;
     };
 
+    // tokens of sequence b that are attended to
+    auto tokens_of = [&](int b) {
+        const int T = reachable_tokens(p.context_lens, b, p.max_blocks, BS);
+        return EXT && p.token_limit ? min(T, p.token_limit) : T;
+    };
+
     // ---- the CTA's segments ----
     struct Seg {
         int b, kvh, tile, pb, pe, T, np;  // pages [pb, pe) of the np of (b, kvh); T tokens
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const long long bk = x / tiles;
         g.kvh = (int)(bk % Hkv);
         g.b = (int)(bk / Hkv);
-        g.T = reachable_tokens(p.context_lens, g.b, p.max_blocks, BS);
+        g.T = tokens_of(g.b);
         g.np = (g.T + BS - 1) / BS;
         g.pb = 0;
         g.pe = g.np;
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         seg0.b = blockIdx.z;
         seg0.kvh = (int)blockIdx.y % Hkv;
         seg0.tile = (int)blockIdx.y / Hkv;
-        seg0.T = reachable_tokens(p.context_lens, seg0.b, p.max_blocks, BS);
+        seg0.T = tokens_of(seg0.b);
         seg0.np = (seg0.T + BS - 1) / BS;
         seg0.pb = part * p.part_pages;
         seg0.pe = min(seg0.pb + p.part_pages, seg0.np);

@@ -28,6 +28,10 @@ __global__ void __launch_bounds__(kSThreads) weights_of_scores_kernel(const Weig
     const int T = reachable_tokens(p.context_lens, b, p.max_blocks, p.block_size);
     const int t0 = blockIdx.x * (kSThreads * 4) + tid * 4;
     if ((int)blockIdx.x * (kSThreads * 4) >= T) return;
+    const size_t unit = ((size_t)b * p.num_kv_heads + kvh) * p.max_blocks * p.block_size;
+    if (blockIdx.x == gridDim.x - 1)  // tokens past the scores: nothing to add
+        for (int t = gridDim.x * (kSThreads * 4) + tid; t < T; t += kSThreads)
+            p.weights_out[unit + t] = p.weights_in[unit + t];
     const int npages = (T + p.block_size - 1) / p.block_size;
     if (p.part_ml) {
         // m + log2 l over the partitions that hold tokens: a warp per row in turn
@@ -71,9 +75,8 @@ __global__ void __launch_bounds__(kSThreads) weights_of_scores_kernel(const Weig
             sum.w += fast_exp2(fmaf(x.w, p.qscale, -l));
         }
     }
-    const size_t at = ((size_t)b * p.num_kv_heads + kvh) * p.max_blocks * p.block_size + t0;
-    const float* in = p.weights_in + at;
-    float* out = p.weights_out + at;
+    const float* in = p.weights_in + unit + t0;
+    float* out = p.weights_out + unit + t0;
     if (t0 + 4 <= T && ((reinterpret_cast<uintptr_t>(p.weights_in) |
                          reinterpret_cast<uintptr_t>(p.weights_out)) & 15) == 0) {
         const float4 w = *reinterpret_cast<const float4*>(in);
@@ -91,9 +94,7 @@ __global__ void __launch_bounds__(kSThreads) weights_of_scores_kernel(const Weig
 
 cudaError_t launch_weights_of_scores(const WeightParams& p, bool pdl, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    // every token of the table: those past the scores take a weight of 0
-    const int64_t tokens = (int64_t)p.max_blocks * p.block_size;
-    cfg.gridDim = dim3((unsigned)((tokens + kSThreads * 4 - 1) / (kSThreads * 4)),
+    cfg.gridDim = dim3((unsigned)((p.score_width + kSThreads * 4 - 1) / (kSThreads * 4)),
                        (unsigned)p.num_kv_heads, (unsigned)p.batch);
     cfg.blockDim = dim3(kSThreads);
     cfg.stream = stream;

@@ -255,6 +255,12 @@ __global__ void __launch_bounds__(WTile<D>::THREADS, 2)
         }
     }
 
+    if (blockIdx.x == gridDim.x - 1) {  // tokens past those attended to: nothing to add
+        const size_t unit = ((size_t)b * p.num_kv_heads + kvh) * p.max_blocks * BS;
+        for (int t = gridDim.x * (NT * 128) + tid; t < T; t += W::THREADS)
+            p.weights_out[unit + t] = p.weights_in[unit + t];
+    }
+
     // ---- release tensor memory once every role is done with it ----
     tc::fence_before_sync();
     __syncthreads();
@@ -273,9 +279,8 @@ cudaError_t launch_inst(const WeightParams& p, const CUtensorMap& k, const CUten
     cudaError_t e = raise_smem_limit_once(kern, smem_limit);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    const int64_t tokens = (int64_t)p.max_blocks * BS;
-    cfg.gridDim = dim3((unsigned)((tokens + W::NT * 128 - 1) / (W::NT * 128)), (unsigned)p.num_kv_heads,
-                       (unsigned)p.batch);
+    cfg.gridDim = dim3((unsigned)((p.token_limit + W::NT * 128 - 1) / (W::NT * 128)),
+                       (unsigned)p.num_kv_heads, (unsigned)p.batch);
     cfg.blockDim = dim3(W::THREADS);
     cfg.dynamicSmemBytes = W::SMEM;
     cfg.stream = stream;

@@ -163,17 +163,31 @@ def test_either_kernel_forced(kernel, Q, H, Hkv, D, switches):
     check(case(100 + Q, 2, Q, H, Hkv, D, 16, [50, 400], torch.float16))
 
 
-def test_contexts_longer_than_announced_drop_the_rest():
-    """Tokens past max_context_len's pages are in neither the output nor the weights."""
-    c = case(110, 2, 1, 8, 2, 128, 16, [200, 90], torch.bfloat16)
-    short = {k: v.clone() for k, v in c.items()}
-    short["lens"] = torch.clamp(c["lens"], max=96)
-    out, new = run(c, 0.1, max_len=96)
-    want_out, want = run(short, 0.1, max_len=96)
-    assert torch.equal(out, want_out)
-    assert torch.equal(new[:, :, :96], torch.where(torch.arange(96) < short["lens"].view(2, 1, 1),
-                                                   want[:, :, :96], new[:, :, :96]))
-    assert torch.equal(new[0, :, 96:200], c["weights"][0, :, 96:200])   # added weight: none
+@pytest.mark.parametrize("B,Q,T,limit", [(2, 1, 2000, 96), (1, 1, 30000, 9000), (40, 1, 3000, 1500),
+                                         (2, 20, 3000, 1000), (40, 33, 700, 500)])
+def test_contexts_longer_than_announced_drop_the_rest(B, Q, T, limit):
+    """Tokens past max_context_len's pages are in neither the output nor the
+    weights, which they keep; by every kernel and plan that adds weights."""
+    c = case(110 + B, B, Q, 8, 2, 128, 16, [T - b for b in range(B)], torch.bfloat16)
+    scale, end = 0.1, (limit + 15) // 16 * 16
+    out, new = run(c, scale, max_len=limit)
+    masked = {k: v.clone() for k, v in c.items()}
+    masked["table"][:, end // 16:] = -1      # the same tokens, left out by their pages
+    want_out, want = ref.accumulate(c["weights"], c["q"], c["k_cache"], c["v_cache"], masked["table"],
+                                    c["lens"], scale)
+    ref.close_out(out, want_out, ref.out_slack(c["q"], c["k_cache"], c["v_cache"], scale, T))
+    rel = ref.weight_slack(c["q"], c["k_cache"], scale, T)
+    for b in range(B):
+        t = T - b
+        added = want[b, :, :t] - c["weights"][b, :, :t].double()
+        err = (new[b, :, :t].double() - want[b, :, :t]).abs()
+        assert (err <= rel * added + (Q * 4 + 2) * 2.0 ** -23 * want[b, :, :t]).all()
+        assert torch.equal(new[b, :, end:t], c["weights"][b, :, end:t])
+
+
+@pytest.mark.parametrize("Q", [1, 20])
+def test_tables_far_wider_than_the_contexts(Q):
+    check(case(115 + Q, 2, Q, 8, 2, 64, 16, [200, 30], torch.float16, extra_pages=4000), max_len=200)
 
 
 @pytest.mark.parametrize("B,T", [(1, 30000), (2, 9000), (4, 4096), (3, 60)])
