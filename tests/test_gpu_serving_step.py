@@ -146,3 +146,16 @@ def test_an_empty_batch_launches_nothing(Q):
     pa.evict_kv(kc, vc, w, table, lens, table, w, none(), none(Hkv, 7))
     torch.cuda.synchronize()
     assert (kc == 1).all() and (vc == 1).all()
+
+
+def test_the_readme_example_runs():
+    import os
+    import re
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = re.search(r"```python\n(.*?)```", open(os.path.join(root, "README.md")).read(), re.S).group(1)
+    names = {}
+    exec(code, names)
+    torch.cuda.synchronize()
+    assert names["new_lens"].tolist() == [names["budget"]] * names["B"]
+    assert torch.isfinite(names["out"].float()).all() and pa.device_error() == 0
