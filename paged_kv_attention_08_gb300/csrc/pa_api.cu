@@ -262,6 +262,7 @@ struct Plan {
     bool late_wait = false;             // see AttnParams
     float* lse = nullptr;               // row statistics wanted: see AttnParams
     int32_t token_limit = 0;            // see AttnParams
+    bool pair = false;                  // (with tile) by the two-tile kernel
     float* scores = nullptr;            // scores wanted: see AttnParams
     int64_t score_width = 0;
     const float* weights_in = nullptr;
@@ -862,6 +863,20 @@ pa_status launch_tile(void* out, const void* q, const void* k, const void* v, co
     if (plan.cluster && !tile_cluster_fits(s, plan.tile_qr)) return PA_ERR_UNSUPPORTED;
     p.balanced = plan.balanced ? 1 : 0;
     p.persistent = plan.persistent ? 1 : 0;
+    if (plan.pair) {
+        if (s->head_dim > 128 || !plan.partials) return PA_ERR_UNSUPPORTED;
+        st = encode_q_map(s, q, q_len, kTileRows, &L.tmap_q);
+        if (st != PA_OK) return st;
+        L.grid = dim3((unsigned)plan.num_parts,
+                      (unsigned)(s->num_kv_heads * ((rows + 2 * kTileRows - 1) / (2 * kTileRows))),
+                      (unsigned)s->batch);
+        L.threads = kTileThreads;
+        L.smem_bytes = pair_smem_bytes(s->head_dim) + kSmemAlignSlack;
+        return (s->head_dim == 64 ? launch_pair_d64(L, stream) : launch_pair_d128(L, stream)) ==
+                       cudaSuccess
+                   ? PA_OK
+                   : PA_ERR_CUDA;
+    }
     if (plan.balanced) {
         if (!compact || plan.cluster) return PA_ERR_UNSUPPORTED;
         p.final_out = 0;
@@ -893,6 +908,17 @@ pa_status launch_tile(void* out, const void* q, const void* k, const void* v, co
             break;
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// Whether a tile plan's rows go two tiles to a CTA (pa_pair.cuh): units of more
+// than one tile that give every SM a few blocks.  With fewer, half as many CTAs
+// for the same rows cost more than their faster blocks save (256 rows of 8 kv
+// heads: prefixes of 4096 tokens, 1.7 blocks an SM, 33.5 us against 30.6 with a
+// tile to a CTA; of 16,384 tokens, 6.7 blocks, 50.3 against 56.1).
+bool use_pair(const pa_shape* s, const Plan& p, int64_t rows, int pages, int sms) {
+    if (!p.tile || p.balanced || s->head_dim > 128 || rows <= kTileRows) return false;
+    const int64_t units = (int64_t)s->batch * s->num_kv_heads * ((rows + 2 * kTileRows - 1) / (2 * kTileRows));
+    return units * ((int64_t)pages * s->block_size / kPairBlock) >= 3ll * sms;
 }
 
 // ---- attention with a shared prefix ----
@@ -941,6 +967,7 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
     // the workspace for the join, and no cluster reduces.
     struct Part {
         Plan p;
+        bool pair;
         int pages;
         int64_t units, slots, parts;
     };
@@ -949,22 +976,26 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
         x.p = make_plan(sh, max_len, 0, sms, q);
         x.pages = pages_for(sh, max_len);
         const int64_t rows = (int64_t)q * (sh->num_heads / sh->num_kv_heads);
+        x.pair = use_pair(sh, x.p, rows, x.pages, sms);
+        const int cta_rows = x.pair ? 2 * kTileRows : kTileRows;
         x.units = (int64_t)sh->batch * sh->num_kv_heads *
-                  (x.p.tile ? (rows + kTileRows - 1) / kTileRows : q_chunks_for(sh, q));
-        x.slots = (int64_t)sms * (x.p.tile ? tile_ctas_per_sm(sh, x.p.tile_qr)
-                                           : ctas_per_sm(sh, pick_tune(sh, true)));
+                  (x.p.tile ? (rows + cta_rows - 1) / cta_rows : q_chunks_for(sh, q));
+        x.slots = (int64_t)sms * (x.pair     ? 1
+                                  : x.p.tile ? tile_ctas_per_sm(sh, x.p.tile_qr)
+                                             : ctas_per_sm(sh, pick_tune(sh, true)));
         x.parts = x.p.balanced ? 1 : x.p.num_parts;
         return x;
     };
     Part pre_part = part_of(&pp->pre, max_prefix_len, pp->pre_q);
     Part own_part = part_of(s, max_context_len, q_len);
     // What a tile CTA takes: its blocks, and a start and an end (measured on
-    // GB300: 1.5 us a block of 128 tokens, 2 us one of 64 at head_dim 256; 10 us).
-    const double block_us = s->head_dim == 256 ? 2.0 : 1.5, ends_us = 10.0;
+    // GB300: 1.5 us a block of 128 tokens, 2 us one of 64 at head_dim 256, 3 us
+    // one of two tiles; 10 us, of which two tiles hide the most).
     const int block_pages = tile_block_tokens(s->head_dim) / s->block_size;
     auto tile_us = [&](const Part& x, int64_t parts) {
+        const double block_us = x.pair ? 3.0 : s->head_dim == 256 ? 2.0 : 1.5;
         const int64_t pages = (x.pages + parts - 1) / parts;
-        return (double)((pages + block_pages - 1) / block_pages) * block_us + ends_us;
+        return (double)((pages + block_pages - 1) / block_pages) * block_us + (x.pair ? 2.0 : 10.0);
     };
     if (own_part.p.tile) {
         // few blocks are not worth another CTA's start and end (64 units of 300
@@ -981,10 +1012,10 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
         // but costs a start and an end, and takes an SM from the sequences' own
         // pages; so the prefix is cut only until it ends well before the whole
         // call can (lengths are not known here: the own pages count as half of
-        // max_context_len, read at 33 GB/s an SM).  16 units of 8191 tokens beside
-        // 64 sequences of up to 1024: 57.5 us with 9 partitions (one wave), 50.0
-        // with 4; 32 units of 65536 beside 128 sequences of up to 2048: 255 us
-        // with 4, 279 with 3.
+        // max_context_len, read at 33 GB/s an SM).  Two tiles to a CTA, calls in a
+        // row: 8 units of 8191 tokens beside 64 sequences of up to 1024 take 49.9,
+        // 46.0, 48.5, 51.3 us with 5, 6, 7, 8 partitions; 16 units of 65536 beside 128
+        // of up to 2048 take 287, 249, 244 us with 6, 7, 8 (alone 260, 265, 267).
         const double own_us =
             own_part.p.tile ? own_part.units * own_part.parts * tile_us(own_part, own_part.parts)
                             : (double)own_part.units * max_context_len * s->head_dim * 2.0 / 33e3;
@@ -993,7 +1024,7 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
         int64_t parts = 1;
         for (; parts < most; ++parts) {
             const double cta = tile_us(pre_part, parts);
-            if (cta <= 0.85 * (pre_part.units * parts * cta + own_us) / sms) break;
+            if (cta <= (pre_part.pair ? 0.94 : 0.85) * (pre_part.units * parts * cta + own_us) / sms) break;
         }
         pre_part.parts = parts;
     }
@@ -1002,6 +1033,7 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
         p.many_ctas = x.units * p.num_parts > sms;
         p.tile = x.p.tile;
         p.tile_qr = x.p.tile_qr;
+        p.pair = x.pair;
         p.partials = true;
         return p;
     };

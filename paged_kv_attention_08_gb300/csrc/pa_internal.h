@@ -321,6 +321,19 @@ __host__ __device__ constexpr uint32_t tile_tmem_cols(int D) {
     return (uint32_t)D + kTileSBufs * tile_block_tokens(D) <= 256u ? 256u : 512u;
 }
 
+// Two-tile kernel (pa_pair.cuh): 256 rows to a CTA, KV blocks of 128 tokens, up
+// to head_dim 128 (tensor memory holds two O's and two S buffers).  Shared
+// memory: both Q tiles, the rings of K and V blocks, then mbarriers, flags and
+// the tensor-memory address.
+constexpr int kPairBlock = 128;
+__host__ __device__ constexpr int pair_k_stages(int D) { return D == 64 ? 3 : 2; }
+__host__ __device__ constexpr int pair_v_stages(int D) { return D == 64 ? 4 : 3; }
+__host__ __device__ constexpr uint32_t pair_smem_bytes(int D) {
+    return 2u * D * (2 * kTileRows + kPairBlock * (pair_k_stages(D) + pair_v_stages(D))) +
+           8u * (2 * pair_k_stages(D) + 3 * pair_v_stages(D) + 15) +
+           4u * (pair_k_stages(D) + pair_v_stages(D) + 2);
+}
+
 // ---------------------------------------------------------------------------
 // Host: kernel attributes set once per device.  A kernel's dynamic
 // shared-memory limit only caps what a launch may request (occupancy follows
@@ -409,6 +422,8 @@ cudaError_t launch_tile_d64_extended(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d128_extended(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d256_extended(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d256_compact_extended(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_pair_d64(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_pair_d128(const AttnLaunch& L, cudaStream_t stream);
 // Clusters of `cluster` tile-kernel CTAs resident at once on the current device.
 int tile_max_clusters_d64(int block_size, int kv_dtype, int cluster, uint32_t smem_bytes);
 int tile_max_clusters_d128(int block_size, int kv_dtype, int cluster, uint32_t smem_bytes);

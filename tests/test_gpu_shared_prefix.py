@@ -176,3 +176,82 @@ def test_two_graphs_share_a_workspace():
         graphs[i].replay()
         torch.cuda.synchronize()
         assert torch.equal(outs[i].cpu(), want[i])
+
+
+def widened(c, tokens):
+    """The same prefixes in tables of `tokens` tokens: announced so long, they
+    are given two tiles to a CTA from 129 rows of a kv head on."""
+    bs = c["k_cache"].shape[1]
+    wide = torch.full((c["ptable"].shape[0], tokens // bs), -1, dtype=torch.int32)
+    wide[:, :c["ptable"].shape[1]] = c["ptable"]
+    return dict(c, ptable=wide)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n,Q,H,Hkv,D,bs,plens", [
+    (33, 1, 32, 8, 64, 32, [1]),           # 132 rows
+    (40, 1, 32, 8, 128, 16, [127]),
+    (64, 1, 32, 8, 128, 32, [128]),        # 256
+    (65, 1, 32, 8, 128, 16, [129]),        # 260: a third tile
+    (96, 1, 32, 8, 64, 16, [333]),         # 384
+    (22, 3, 16, 8, 128, 16, [500, 0, 77]),
+    (11, 13, 8, 8, 64, 16, [400, 401]),    # a head to a kv head, padding
+    (9, 1, 16, 1, 128, 32, [5000]),        # 144 rows of one kv head, several partitions
+    (17, 2, 64, 8, 128, 16, [4999]),       # 272
+])
+def test_two_tiles_to_a_cta(n, Q, H, Hkv, D, bs, plens, dtype):
+    B = n * len(plens)
+    c = case(n * 1000 + D, n, Q, H, Hkv, D, bs, plens, [(b * 7) % 30 + 1 for b in range(B)], dtype)
+    check(widened(c, 65536), max_p=65536)
+
+
+def test_two_tiles_masked_pages_and_nan_in_unread_places():
+    c = case(900, 40, 1, 32, 8, 128, 16, [1000], [b % 9 + 1 for b in range(40)], torch.bfloat16)
+    c["ptable"][0, 3] = -1
+    c["ptable"][0, 20] = c["k_cache"].shape[0] + 5
+    c["ptable"][0, 24:34] = -1                 # a whole block of 8 pages among them
+    used = torch.cat([c["ptable"].flatten(), c["table"].flatten()])
+    dead = torch.ones(c["k_cache"].shape[0], dtype=torch.bool)
+    dead[used[(used >= 0) & (used < len(dead))].unique().long()] = False
+    c["plens"][0] = 985                        # ends inside a page
+    last = int(c["ptable"][0, 61])
+    for cache in (c["k_cache"], c["v_cache"]):
+        cache[dead] = float("nan")
+        cache[last, 9:] = float("nan")
+    check(widened(c, 65536), max_p=65536)
+    c["ptable"][0, :] = -1                     # no page at all
+    check(widened(c, 65536), max_p=65536)
+
+
+def test_two_tiles_scores_that_rise_and_fall():
+    """Maxima that move by more than the slack, up along the prefix and down again."""
+    c = case(901, 64, 1, 32, 8, 128, 16, [2000], [3] * 64, torch.float16)
+    ramp = 1 + 7 * torch.sin(torch.arange(c["k_cache"].shape[0]) / 9.0).abs()
+    c["k_cache"] = (c["k_cache"].float() * ramp.view(-1, 1, 1, 1)).to(torch.float16)
+    check(widened(c, 65536), scale=0.2, max_p=65536)
+
+
+def test_two_tiles_same_bits_twice_and_in_a_graph():
+    c = widened(case(902, 70, 1, 32, 8, 128, 16, [3000], [b % 20 + 1 for b in range(70)],
+                     torch.bfloat16), 65536)
+    first = run(c, 0.1, max_p=65536)
+    for own in (True, False):
+        assert torch.equal(run(c, 0.1, max_p=65536, own_workspace=own), first)
+    d = {k: v.to(DEV) for k, v in c.items()}
+    out = torch.empty_like(d["q"])
+    mo = int(c["lens"].max())
+    ws = torch.empty(pa.workspace_size_shared_prefix(d["q"], d["k_cache"], d["ptable"], d["table"],
+                                                     out.dtype, 65536, mo), dtype=torch.uint8, device=DEV)
+    call = lambda: pa.decode_shared_prefix(out, d["q"], d["k_cache"], d["v_cache"], d["ptable"],
+                                           d["plens"], d["table"], d["lens"], 0.1, 65536, mo, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+        call()
+    out.zero_()
+    ws.fill_(255)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), first) and pa.device_error() == 0
