@@ -385,7 +385,8 @@ size_t pa_workspace_size_accumulate(const pa_shape* shape, int32_t q_len, int32_
  * themselves: the tokens then move down within their own pages, which no
  * other sequence may share.  Otherwise the new pages must not be among any
  * sequence's old ones, which stay as they were.  A kept token whose new entry
- * is masked is not stored.  budget >= sink + recent, and
+ * is masked is not stored.  new_weights, new_lens and kept lie apart from each
+ * other and from the inputs.  budget >= sink + recent, and
  * new_max_blocks_per_seq * block_size >= budget.  The num_heads and out_dtype
  * of the shape are checked and not used.
  */

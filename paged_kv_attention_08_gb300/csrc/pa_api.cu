@@ -1015,7 +1015,9 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
         // max_context_len, read at 33 GB/s an SM).  Two tiles to a CTA, calls in a
         // row: 8 units of 8191 tokens beside 64 sequences of up to 1024 take 49.9,
         // 46.0, 48.5, 51.3 us with 5, 6, 7, 8 partitions; 16 units of 65536 beside 128
-        // of up to 2048 take 287, 249, 244 us with 6, 7, 8 (alone 260, 265, 267).
+        // of up to 2048 take 287, 249, 244 us with 6, 7, 8 (alone 260, 265, 267).  With
+        // one tile to a CTA the first took 50.0 us with 4 partitions of 16 units and 57.5
+        // with 9, the second 255 with 4 of 32 and 279 with 3.
         const double own_us =
             own_part.p.tile ? own_part.units * own_part.parts * tile_us(own_part, own_part.parts)
                             : (double)own_part.units * max_context_len * s->head_dim * 2.0 / 33e3;

@@ -125,14 +125,23 @@ pa_status pa_evict_kv(void* k_cache, void* v_cache, const float* weights,
     const size_t t_bytes = (size_t)shape->batch * shape->max_blocks_per_seq * 4;
     const size_t l_bytes = (size_t)shape->batch * 4, k_bytes = units * (size_t)budget * 4;
     if (!same_weights && overlap(weights, w_bytes, new_weights, nw_bytes)) return PA_ERR_INVALID_ARG;
-    // the outputs written before the inputs' last read lie apart from them
-    if (overlap(kept, k_bytes, weights, w_bytes) || overlap(kept, k_bytes, block_tables, t_bytes) ||
-        overlap(kept, k_bytes, context_lens, l_bytes) ||
-        overlap(new_lens, l_bytes, weights, w_bytes) ||
-        overlap(new_lens, l_bytes, block_tables, t_bytes) ||
-        overlap(new_lens, l_bytes, context_lens, l_bytes) ||
-        overlap(new_lens, l_bytes, kept, k_bytes))
-        return PA_ERR_INVALID_ARG;
+    // the outputs lie apart from each other and from every input
+    const size_t nt_bytes = (size_t)shape->batch * new_max_blocks_per_seq * 4;
+    const struct {
+        const void* p;
+        size_t n;
+    } outs[3] = {{kept, k_bytes}, {new_lens, l_bytes}, {new_weights, nw_bytes}},
+      ins[4] = {{block_tables, t_bytes},
+                {context_lens, l_bytes},
+                {new_block_tables, nt_bytes},
+                {weights, w_bytes}};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 4; ++i)
+            if (!(o == 2 && i == 3) && overlap(outs[o].p, outs[o].n, ins[i].p, ins[i].n))
+                return PA_ERR_INVALID_ARG;
+        for (int i = 0; i < o; ++i)
+            if (overlap(outs[o].p, outs[o].n, outs[i].p, outs[i].n)) return PA_ERR_INVALID_ARG;
+    }
     st = device_state(nullptr, nullptr);
     if (st != PA_OK) return st;
     EvictParams p;

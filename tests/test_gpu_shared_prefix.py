@@ -255,3 +255,14 @@ def test_two_tiles_same_bits_twice_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out.cpu(), first) and pa.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("Q,H,Hkv,D,bs", [(40, 32, 8, 128, 16), (150, 8, 8, 64, 32), (33, 32, 8, 64, 16)])
+def test_two_tiles_of_the_sequences_own_rows(Q, H, Hkv, D, bs, dtype):
+    """Own rows that go two tiles to a CTA, causal among themselves, with padding."""
+    lens = [Q, Q + 1, 700, Q - 2, 129, 0, 333, Q + 128]
+    c = case(Q * 10 + D, 4, Q, H, Hkv, D, bs, [60, 0], lens, dtype)
+    wide = torch.full((8, 65536 // bs), -1, dtype=torch.int32)
+    wide[:, :c["table"].shape[1]] = c["table"]
+    check(dict(c, table=wide), max_own=65536)

@@ -96,6 +96,17 @@ def test_evict_refuses_the_rest(lib):
     assert call_evict(lib, shape(batch=0), {i: None for i in range(9)}) == 0
 
 
+@pytest.mark.parametrize("out,size", [(6, 4 * 8 * 64 * 16 * 4), (7, 4 * 4), (8, 4 * 8 * 1024 * 4)])
+@pytest.mark.parametrize("other,length", [(3, 4 * 128 * 4), (4, 4 * 4), (5, 4 * 64 * 4), (6, 4 * 8 * 64 * 16 * 4),
+                                          (7, 4 * 4), (8, 4 * 8 * 1024 * 4)])
+def test_evict_refuses_outputs_that_overlap(lib, out, size, other, length):
+    if out == other:
+        return
+    far = 1 << 40
+    assert call_evict(lib, shape(), {out: far, other: far + size - 4}) == 1
+    assert call_evict(lib, shape(), {out: far + length - 4, other: far}) == 1
+
+
 def rope_args(**kw):
     B, Q, H, Hkv, D = 2, 3, 4, 2, 64
     t = dict(q_out=torch.zeros(B, Q, H, D, dtype=torch.float16),
