@@ -316,7 +316,9 @@ pa_status pa_rope_append_kv(void* q_out, void* k_cache, void* v_cache, const voi
  * q_len its first query tokens stand for the prefix's last tokens and see no
  * further than they would.  Masked entries, lengths past a table's reach and
  * rows with no token as in pa_decode.
- * The query rows of a prefix's sequences (n * q_len * group per kv head) go
+ * Where little is to be read, each sequence reads its prefix's pages before its
+ * own, in one launch.  Otherwise
+ * the query rows of a prefix's sequences (n * q_len * group per kv head) go
  * through the prefix's pages together, on the kernel that pa_decode_multi
  * takes for as many rows; the sequences' own pages as in pa_decode_multi; a
  * third launch joins the two by their softmax statistics.  max_prefix_len and
@@ -332,8 +334,8 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
                                   float scale, int32_t max_prefix_len, int32_t max_context_len,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of pa_decode_shared_prefix on the current device (0 for
- * invalid arguments or without a device; SIZE_MAX when no size_t holds it). */
+/* Workspace bytes of pa_decode_shared_prefix on the current device (0 where it
+ * needs none, for invalid arguments or without a device; SIZE_MAX when no size_t holds it). */
 size_t pa_workspace_size_shared_prefix(const pa_shape* shape, int32_t num_prefixes,
                                        int32_t max_prefix_blocks, int32_t q_len,
                                        int32_t max_prefix_len, int32_t max_context_len);

@@ -24,6 +24,7 @@ SOURCES = ["pa_api.cu", "pa_step_api.cu", "pa_combine.cu", "pa_rope.cu", "pa_evi
            "pa_attn_d64.cu", "pa_attn_d128.cu", "pa_attn_d256.cu",
            "pa_attn_d64_multi.cu", "pa_attn_d128_multi.cu", "pa_attn_d256_multi.cu",
            "pa_attn_d64_extended.cu", "pa_attn_d128_extended.cu", "pa_attn_d256_extended.cu",
+           "pa_attn_d64_prefixed.cu", "pa_attn_d128_prefixed.cu", "pa_attn_d256_prefixed.cu",
            "pa_tile_d64.cu", "pa_tile_d128.cu", "pa_tile_d256.cu", "pa_tile_d256_compact.cu",
            "pa_tile_d64_extended.cu", "pa_tile_d128_extended.cu", "pa_tile_d256_extended.cu",
            "pa_tile_d256_compact_extended.cu", "pa_pair_d64.cu", "pa_pair_d128.cu"]

@@ -263,6 +263,9 @@ struct Plan {
     float* lse = nullptr;               // row statistics wanted: see AttnParams
     int32_t token_limit = 0;            // see AttnParams
     bool pair = false;                  // (with tile) by the two-tile kernel
+    const int32_t* prefix_tables = nullptr;  // a prefix in front: see AttnParams
+    const int32_t* prefix_lens = nullptr;
+    int32_t max_prefix_blocks = 0, per_prefix = 0;
     float* scores = nullptr;            // scores wanted: see AttnParams
     int64_t score_width = 0;
     const float* weights_in = nullptr;
@@ -784,6 +787,10 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     if (plan.balanced) p.final_out = 0;
     p.own_lens = plan.own_lens;
     p.own_q = plan.own_q;
+    p.prefix_tables = plan.prefix_tables;
+    p.prefix_lens = plan.prefix_lens;
+    p.max_prefix_blocks = plan.max_prefix_blocks;
+    p.per_prefix = plan.per_prefix;
     p.late_wait = plan.late_wait ? 1 : 0;
     p.token_limit = plan.token_limit;
     p.lse = plan.lse;
@@ -804,6 +811,14 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     L.smem_bytes = sm.total + kSmemAlignSlack;
     const bool ext = extended(p);
     cudaError_t e;
+    if (p.prefix_tables) {
+        switch (s->head_dim) {
+            case 64: e = launch_attn_d64_prefixed(L, stream); break;
+            case 128: e = launch_attn_d128_prefixed(L, stream); break;
+            default: e = launch_attn_d256_prefixed(L, stream); break;
+        }
+        return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     switch (s->head_dim) {
         case 64: e = ext ? launch_attn_d64_extended(L, stream) : launch_attn_d64(L, stream); break;
         case 128: e = ext ? launch_attn_d128_extended(L, stream) : launch_attn_d128(L, stream); break;
@@ -928,6 +943,7 @@ struct PrefixPlan {
     pa_shape pre;      // the prefixes as sequences of n * q_len query tokens each
     int32_t pre_q;     // n * q_len
     Plan prefix, own;
+    bool joined;       // one launch: every sequence reads its prefix itself (by plan `own`)
     size_t pre_ml, own_acc, own_ml, bytes;  // workspace offsets and size
 };
 
@@ -959,10 +975,36 @@ pa_status check_prefix(const pa_shape* s, int32_t num_prefixes, int32_t max_pref
     return PA_OK;
 }
 
+// Bytes of keys and values up to which every sequence of a shared-prefix call
+// reads the prefix itself, in one launch instead of three (8 kv heads of 128, own
+// 64 tokens, us, one launch against three: 4 sequences behind 992 tokens, 16 MB, 8.9 and
+// 14.7; 8 behind 2000, 64 MB, 14.6 and 23.4; 64 behind 256, 80 MB, 19.5 and 22.9; 16
+// behind 2000, 129 MB, 22.0 and 24.8; 128 behind 192, 160 MB, 37.0 and 35.2; 4 behind
+// 16,000, 251 MB, 36.2 and 25.5).
+constexpr int64_t kJoinedBytes = 96ll << 20;
+
 pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
                       int32_t max_prefix_len, int32_t max_context_len, int sms, PrefixPlan* pp) {
     pp->pre = *pre;
     pp->pre_q = s->batch / pre->batch * q_len;
+    pp->joined = false;
+    // A short prefix of few sequences: each reads it in front of its own pages,
+    // mostly from L2, where that takes one launch (one pass, or a cluster's reduction).
+    const int64_t read_pages =
+        (int64_t)s->batch * s->num_kv_heads * (pages_for(pre, max_prefix_len) + pages_for(s, max_context_len));
+    if (read_pages * s->block_size * s->head_dim * 4 <= kJoinedBytes &&
+        (int64_t)s->max_blocks_per_seq + pre->max_blocks_per_seq < (1 << 26)) {
+        pa_shape both = *s;
+        both.max_blocks_per_seq += pre->max_blocks_per_seq;
+        const int pages = pages_for(pre, max_prefix_len) + pages_for(s, max_context_len);
+        Plan p = make_plan(&both, pages * s->block_size, 0, sms, q_len);
+        if (!p.tile && !p.balanced && (p.num_parts <= 1 || p.cluster)) {
+            pp->own = p;
+            pp->joined = true;
+            pp->pre_ml = pp->own_acc = pp->own_ml = pp->bytes = 0;
+            return PA_OK;
+        }
+    }
     // The library's kernel choice for each part; the partials always stay in
     // the workspace for the join, and no cluster reduces.
     struct Part {
@@ -1452,6 +1494,14 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
     PrefixPlan pp;
     st = plan_prefix(shape, &pre, q_len, max_prefix_len, max_context_len, sms, &pp);
     if (st != PA_OK) return st;
+    if (pp.joined) {
+        pp.own.prefix_tables = prefix_tables;
+        pp.own.prefix_lens = prefix_lens;
+        pp.own.max_prefix_blocks = max_prefix_blocks;
+        pp.own.per_prefix = shape->batch / num_prefixes;
+        return launch_attention(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale,
+                                pp.own, nullptr, nullptr, err, static_cast<cudaStream_t>(stream), q_len);
+    }
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < pp.bytes) return PA_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
     auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };

@@ -78,7 +78,10 @@ enum SegOut { kOutFinal = 0, kOutPartial = 1, kOutCluster = 2, kOutRecord = 3 };
 // statistics are known (4 bytes a row and token written and read again,
 // against reading a key of 2 D bytes again).  The plain instantiations know
 // nothing of these: as run-time questions they cost the short calls 2.4 %.
-template <int D, int BS, typename KV, bool MULTI, bool EXT = false>
+// PRE: a shared prefix (p.prefix_tables) in front of each sequence's own pages,
+// read by each of its sequences: one launch where little is to be read (in the
+// EXT instantiations it cost 128 sequences behind 65,536 tokens 4 %).
+template <int D, int BS, typename KV, bool MULTI, bool EXT = false, bool PRE = false>
 __global__ void __launch_bounds__(256, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
@@ -152,11 +155,16 @@ __global__ void __launch_bounds__(256, 1)
     // time, one per lane of the leader warp.
     const int32_t* table_row = nullptr;
     int seg_pb = 0, seg_fetch_end = 0;
+    // A prefix in front (PRE): its pages are pages 0 .. pre_pages - 1 of the
+    // sequence, the own ones follow; pre_tokens may end inside the last of them.
+    const int32_t* pre_row = nullptr;
+    int pre_pages = 0, pre_tokens = 0;
     int ent_cur = -1, ent_next = -1, cur_chunk = 0;
     auto fetch = [&](int chunk) -> int {
         const int li = chunk * 32 + lane;
         const int j = seg_pb + stream + li * p.nt;
-        return j < seg_fetch_end ? __ldg(table_row + j) : -1;
+        if (PRE && j < pre_pages) return j < seg_fetch_end ? __ldg(pre_row + j) : -1;
+        return j < seg_fetch_end ? __ldg(table_row + (PRE ? j - pre_pages : j)) : -1;
     };
     auto start_fetch = [&](int b, int pb, int fetch_end) {
         table_row = p.block_tables + (size_t)b * p.max_blocks;
@@ -175,7 +183,7 @@ __global__ void __launch_bounds__(256, 1)
     // row is handed to emit(idx = r*D + d, A, M, L).  Query token qi sits at
     // position ctx - Q + qi and attends to the tokens before and at it.
     auto run_segment = [&](int b, int kvh, int pb, int pe, int T, auto&& emit) {
-        const int npages = (T + BS - 1) / BS;
+        const int npages = (T + BS - 1) / BS + (PRE ? pre_pages : 0);
         const int span = pe - pb;
         const int n_s = span > stream ? (span - stream + p.nt - 1) / p.nt : 0;
         const int slot0 = slot;
@@ -244,6 +252,7 @@ __global__ void __launch_bounds__(256, 1)
         // Tokens each row attends: the causal limit of its query token, inside
         // the table's reach (with one query token, every row attends T).
         int lim0 = T, lim1 = T;
+        int pre_lim0 = 0, pre_lim1 = 0;  // and those of the prefix
         if constexpr (MULTI) {
             if (EXT && p.own_lens) {
                 if (real0) lim0 = prefix_limit(T, b, qi0 + (g >> gshift), Q, p.own_q, p.own_lens);
@@ -253,6 +262,10 @@ __global__ void __launch_bounds__(256, 1)
                 const int ctx = max(__ldg(p.context_lens + b), 0);
                 lim0 = min(T, ctx - Q + qi0 + (g >> gshift) + 1);
                 lim1 = min(T, ctx - Q + qi0 + ((g + 8) >> gshift) + 1);
+                if constexpr (PRE) {  // (all of it, but for padding: see prefix_limit)
+                    pre_lim0 = pre_tokens + min(0, ctx - Q + qi0 + (g >> gshift) + 1);
+                    pre_lim1 = pre_tokens + min(0, ctx - Q + qi0 + ((g + 8) >> gshift) + 1);
+                }
             }
         }
 
@@ -276,7 +289,9 @@ __global__ void __launch_bounds__(256, 1)
             const int phys = phys_of[sidx];
             if (phys >= 0) {
                 const int j = pb + stream + i * p.nt;
-                const int nvalid = min(BS, T - j * BS);
+                const bool pre = PRE && j < pre_pages;
+                const int first = (PRE && !pre ? j - pre_pages : j) * BS;  // the page's first token
+                const int nvalid = min(BS, (pre ? pre_tokens : T) - first);
                 uint8_t* kt = smem + L.stages_off + (size_t)sidx * L.stage_bytes;
                 uint8_t* vt = kt + L.tile_bytes;
                 const uint32_t kbase = smem_u32(kt), vbase = smem_u32(vt);
@@ -313,8 +328,8 @@ __global__ void __launch_bounds__(256, 1)
 
                 // ---- page max per row, conditional rescale ----
                 // this page's attended tokens of rows g and g + 8
-                const int v0 = MULTI ? lim0 - j * BS : nvalid;
-                const int v1 = MULTI ? lim1 - j * BS : nvalid;
+                const int v0 = MULTI ? (pre ? pre_lim0 : lim0) - first : nvalid;
+                const int v1 = MULTI ? (pre ? pre_lim1 : lim1) - first : nvalid;
                 float mx0 = NEG_INF, mx1 = NEG_INF;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -640,10 +655,18 @@ __global__ void __launch_bounds__(256, 1)
     const int pb = part * p.part_pages;
     // the table entries are fetched before the context length is known
     // (every index stays inside the table row); those past it are masked
-    start_fetch(b, pb, min(pb + p.part_pages, p.max_blocks));
+    if (!PRE) start_fetch(b, pb, min(pb + p.part_pages, p.max_blocks));
     const int reach = reachable_tokens(p.context_lens, b, p.max_blocks, BS);
     const int T = EXT && p.token_limit ? min(reach, p.token_limit) : reach;
-    const int npages = (T + BS - 1) / BS;
+    int npages = (T + BS - 1) / BS;
+    if constexpr (PRE) {
+        const int x = b / p.per_prefix;
+        pre_row = p.prefix_tables + (size_t)x * p.max_prefix_blocks;
+        pre_tokens = reachable_tokens(p.prefix_lens, x, p.max_prefix_blocks, BS);
+        pre_pages = (pre_tokens + BS - 1) / BS;
+        npages += pre_pages;
+        start_fetch(b, pb, min(pb + p.part_pages, npages));
+    }
     const int pe = min(pb + p.part_pages, npages);
     if (pb >= pe && !p.cluster_reduce) {
         // Nothing of this sequence falls in the partition.  The single pass
@@ -752,16 +775,16 @@ __global__ void __launch_bounds__(256, 1)
 }
 
 // Per-instantiation flags of the attributes set once per device.
-template <int D, int BS, typename KV, bool MULTI, bool EXT = false>
+template <int D, int BS, typename KV, bool MULTI, bool EXT = false, bool PRE = false>
 struct AttnAttrs {
     static inline AttrFlags smem;
     static inline AttrFlags nonportable;
 };
 
-template <int D, int BS, typename KV, bool MULTI, bool EXT>
+template <int D, int BS, typename KV, bool MULTI, bool EXT, bool PRE>
 cudaError_t launch_attn_inst(const AttnLaunch& L, cudaStream_t stream) {
-    auto kern = attn_kernel<D, BS, KV, MULTI, EXT>;
-    using Attrs = AttnAttrs<D, BS, KV, MULTI, EXT>;
+    auto kern = attn_kernel<D, BS, KV, MULTI, EXT, PRE>;
+    using Attrs = AttnAttrs<D, BS, KV, MULTI, EXT, PRE>;
     cudaError_t e = raise_smem_limit_once(kern, Attrs::smem);
     if (e != cudaSuccess) return e;
     if (L.cluster > kMaxClusterParts) {
@@ -837,15 +860,15 @@ int attn_max_clusters_for_d(int block_size, int kv_dtype, int cluster, int threa
               : attn_max_clusters_inst<D, 32, __half>(cluster, threads, smem_bytes);
 }
 
-template <int D, bool MULTI, bool EXT = false>
+template <int D, bool MULTI, bool EXT = false, bool PRE = false>
 cudaError_t launch_attn_for_d(const AttnLaunch& L, cudaStream_t stream) {
     const bool bf = L.kv_dtype == PA_BF16;
     if (L.block_size == 16)
-        return bf ? launch_attn_inst<D, 16, __nv_bfloat16, MULTI, EXT>(L, stream)
-                  : launch_attn_inst<D, 16, __half, MULTI, EXT>(L, stream);
+        return bf ? launch_attn_inst<D, 16, __nv_bfloat16, MULTI, EXT, PRE>(L, stream)
+                  : launch_attn_inst<D, 16, __half, MULTI, EXT, PRE>(L, stream);
     if (L.block_size == 32)
-        return bf ? launch_attn_inst<D, 32, __nv_bfloat16, MULTI, EXT>(L, stream)
-                  : launch_attn_inst<D, 32, __half, MULTI, EXT>(L, stream);
+        return bf ? launch_attn_inst<D, 32, __nv_bfloat16, MULTI, EXT, PRE>(L, stream)
+                  : launch_attn_inst<D, 32, __half, MULTI, EXT, PRE>(L, stream);
     return cudaErrorInvalidValue;
 }
 

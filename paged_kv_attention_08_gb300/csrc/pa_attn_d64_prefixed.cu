@@ -1,0 +1,10 @@
+// Instantiations of the decode kernel for head_dim 64 with a shared prefix in
+// front of each sequence's own pages.
+#include "pa_attn.cuh"
+
+namespace pa {
+cudaError_t launch_attn_d64_prefixed(const AttnLaunch& L, cudaStream_t stream) {
+    return L.p.q_len > 1 ? launch_attn_for_d<64, true, false, true>(L, stream)
+                         : launch_attn_for_d<64, false, false, true>(L, stream);
+}
+}  // namespace pa

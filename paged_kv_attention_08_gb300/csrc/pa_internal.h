@@ -38,6 +38,11 @@ struct AttnParams {
     // (The launch before must let its dependents go no earlier than after its
     // own wait, as the attention kernels do: then what came before it is done.)
     int32_t late_wait;
+    // Warp-level kernel: a shared prefix read by each of its sequences in front
+    // of its own pages (null otherwise), sequence b after prefix b / per_prefix.
+    const int32_t* prefix_tables;
+    const int32_t* prefix_lens;
+    int32_t max_prefix_blocks, per_prefix;
     int32_t token_limit;      // 0, or tokens from here on are not attended to (a multiple of
                               // block_size): what the scores and weights are sized for
     float* scores;            // warp-level kernel: [B, Hkv, Q * group, score_width] or null: q . K
@@ -418,6 +423,9 @@ cudaError_t launch_tile_d64(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d128(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d256(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d256_compact(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_attn_d64_prefixed(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_attn_d128_prefixed(const AttnLaunch& L, cudaStream_t stream);
+cudaError_t launch_attn_d256_prefixed(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d64_extended(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d128_extended(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_tile_d256_extended(const AttnLaunch& L, cudaStream_t stream);

@@ -47,7 +47,8 @@ def check(c, scale=None, **kw):
     scale = scale or 1 / math.sqrt(c["q"].shape[-1])
     want = ref.shared_prefix(c["q"], c["k_cache"], c["v_cache"], c["ptable"], c["plens"],
                              c["table"], c["lens"], scale)
-    tokens = c["ptable"].shape[1] * c["k_cache"].shape[1] + c["table"].shape[1] * c["k_cache"].shape[1]
+    pages = [int((c[t] >= 0).sum(1).max()) for t in ("ptable", "table")]  # attended at most
+    tokens = max(1, sum(pages)) * c["k_cache"].shape[1]
     ref.close_out(run(c, scale, **kw), want,
                   ref.out_slack(c["q"], c["k_cache"], c["v_cache"], scale, tokens))
 
@@ -266,3 +267,70 @@ def test_two_tiles_of_the_sequences_own_rows(Q, H, Hkv, D, bs, dtype):
     wide = torch.full((8, 65536 // bs), -1, dtype=torch.int32)
     wide[:, :c["table"].shape[1]] = c["table"]
     check(dict(c, table=wide), max_own=65536)
+
+
+APART = 1 << 20   # announced so long, a prefix is never read by each sequence itself
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n,Q,H,Hkv,D,bs,plens,lens", [
+    (1, 1, 4, 2, 128, 16, [100], [30]),
+    (3, 1, 8, 2, 128, 16, [77], [1, 50, 16]),
+    (8, 1, 8, 2, 64, 32, [1000], [5 * b + 1 for b in range(8)]),
+    (2, 1, 16, 1, 256, 32, [500], [33, 64]),
+    (5, 2, 4, 4, 64, 32, [65, 64, 1, 300], [2 + b for b in range(20)]),
+    (3, 4, 16, 2, 256, 16, [40, 129], [4, 9, 30, 4, 100, 5]),
+    (4, 3, 8, 2, 128, 16, [0, 45], [3, 0, 1, -4, 50, 4, 0, 1]),    # empty ones and padding
+])
+def test_in_launches_of_their_own(n, Q, H, Hkv, D, bs, plens, lens, dtype):
+    """The prefix and the own pages apart, and joined, at sizes that go in one launch too."""
+    c = case(n * 10 + Q, n, Q, H, Hkv, D, bs, plens, [max(t, 0) for t in lens], dtype)
+    c["lens"] = torch.tensor(lens, dtype=torch.int32)
+    check(c)
+    check(widened(c, APART), max_p=APART)
+
+
+def test_in_launches_of_their_own_masked_pages_and_nan_in_unread_places():
+    c = case(950, 3, 1, 8, 2, 128, 16, [150], [40, 41, 42], torch.bfloat16)
+    c["ptable"][0, 3] = -1
+    c["ptable"][0, 6] = c["k_cache"].shape[0] + 5
+    c["table"][0, 1] = -1
+    c["table"][1, :] = -1
+    used = torch.cat([c["ptable"].flatten(), c["table"].flatten()])
+    dead = torch.ones(c["k_cache"].shape[0], dtype=torch.bool)
+    dead[used[(used >= 0) & (used < len(dead))].unique().long()] = False
+    c["plens"][0] = 135
+    for cache in (c["k_cache"], c["v_cache"]):
+        cache[dead] = float("nan")
+        cache[int(c["ptable"][0, 8]), 7:] = float("nan")
+    check(c, max_p=150)
+    check(widened(c, APART), max_p=APART)
+
+
+def test_contexts_longer_than_announced_stay_in_bounds():
+    """Lengths past those announced: tokens are left out, nothing else is touched."""
+    for n, Q in ((4, 1), (4, 3), (40, 4)):
+        c = case(960 + n, n, Q, 8, 2, 128, 16, [900], [70 + b for b in range(n)], torch.bfloat16)
+        out = run(c, 0.1, max_p=200, max_own=20)
+        assert torch.isfinite(out.float()).all()
+
+
+def test_two_graphs_share_a_workspace_of_launches_apart():
+    cs = [widened(case(94, 20, 1, 8, 2, 128, 16, [700], [40] * 20, torch.bfloat16), APART),
+          widened(case(95, 3, 4, 8, 2, 128, 16, [90], [9, 30, 70], torch.bfloat16), APART)]
+    want = [run(c, 0.1, max_p=APART) for c in cs]
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    graphs, outs, keep = [], [], []
+    for c in cs:
+        d = {k: v.to(DEV) for k, v in c.items()}
+        out = torch.zeros(c["q"].shape, dtype=c["q"].dtype, device=DEV)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pa.decode_shared_prefix(out, d["q"], d["k_cache"], d["v_cache"], d["ptable"], d["plens"],
+                                    d["table"], d["lens"], 0.1, APART, int(c["lens"].max()), workspace=ws)
+        graphs.append(graph), outs.append(out), keep.append(d)
+    for i in (0, 1, 0, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i].cpu(), want[i])
