@@ -18,7 +18,7 @@
 // follows once P V has read P, which lies over S.
 //
 // Bound: no one unit.  A block of two tiles takes 5300 cycles, of which the MMAs
-// (bf16: 48 of 64 cycles) are 3072 and the exponentials (16 a cycle) 2048; the
+// (bf16: 48 of 64 cycles) are 58 % and the exponentials (16 a cycle) 39 %; the
 // rest is a tile's own chain.  512 rows of 8 kv heads of 128 on a prefix of 65,536
 // (152 SMs, with the join): bf16 180 us, 765 TFLOP/s, fp16 145 us, 946 (a tile to a CTA:
 // 203 and 156).  Also measured, bf16: P in two pieces 192; both tiles in step 186;
