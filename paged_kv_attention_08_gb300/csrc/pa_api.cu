@@ -1160,11 +1160,13 @@ size_t accumulate_bytes(const pa_shape* s, const Plan& plan, int32_t q_len, int3
     return scores + bytes;
 }
 
-// pa_decode_multi after its checks and its plan.
+// pa_decode_multi after its checks and its plan; with `weights` the launch that
+// combines the partitions adds the tokens' weights too (a plan that leaves partials).
 pa_status run_multi(void* out, const void* q, const void* k_cache, const void* v_cache,
                     const int32_t* block_tables, const int32_t* context_lens,
                     const pa_shape* shape, int32_t q_len, float scale, const Plan& plan,
-                    void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t cs) {
+                    void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t cs,
+                    const WeightParams* weights = nullptr) {
     pa_status st;
     if (plan.tile && !plan.balanced && (plan.num_parts <= 1 || plan.cluster))
         return launch_tile(out, q, k_cache, v_cache, block_tables, context_lens, shape, scale, plan,
@@ -1202,6 +1204,10 @@ pa_status run_multi(void* out, const void* q, const void* k_cache, const void* v
     c.out_dtype = shape->out_dtype;
     c.num_ctas = plan.num_ctas;
     c.lse = plan.lse;
+    if (weights)
+        return launch_combine_weights(c, *weights, shape->head_dim, use_pdl(), cs) == cudaSuccess
+                   ? PA_OK
+                   : PA_ERR_CUDA;
     const dim3 cgrid((unsigned)(q_len * shape->num_heads), (unsigned)shape->batch);
     const cudaError_t e = plan.balanced ? launch_combine_balanced(c, shape->head_dim, cgrid,
                                                                   use_pdl(), cs)
@@ -1600,9 +1606,6 @@ pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weigh
         plan.weights_out = weights_out;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    st = run_multi(out, q, k_cache, v_cache, block_tables, context_lens, shape, q_len, scale, plan,
-                   workspace, lse_off, err, cs);
-    if (st != PA_OK || joined) return st;
     WeightParams w;
     w.q = q;
     w.k_cache = k_cache;
@@ -1630,6 +1633,12 @@ pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weigh
     w.token_limit = plan.token_limit;
     w.err = err;
     w.timeout_ns = kDefaultTimeoutNs;
+    // (partitions' statistics serve where there is no row's: then no lse is written)
+    const bool beside = scores && !known;
+    if (beside) plan.lse = nullptr;
+    st = run_multi(out, q, k_cache, v_cache, block_tables, context_lens, shape, q_len, scale, plan,
+                   workspace, lse_off, err, cs, beside ? &w : nullptr);
+    if (st != PA_OK || joined || beside) return st;
     cudaError_t e;
     if (scores) {
         e = launch_weights_of_scores(w, use_pdl(), cs);

@@ -10,6 +10,7 @@
 // (m = -inf, l = 0, acc = 0) contributes nothing; a sequence with no attended
 // token gets zeros.
 #include "pa_device.cuh"
+#include "pa_weights.cuh"
 
 namespace pa {
 
@@ -23,21 +24,18 @@ namespace {
 // groups finishes the head.  Two dependent memory round trips in all.
 constexpr int kCombineThreads = 256;
 
-// LSE: the rows' statistics are wanted too (p.lse).
+// x: query token and head; LSE: the rows' statistics are wanted too (p.lse).
 template <int D, bool LSE>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
+__device__ __forceinline__ void combine_row(const CombineParams& p, int x, int b) {
     constexpr int SLICES = D / 4;                      // float4 slices of one row
     constexpr int PGRP = kCombineThreads / SLICES;     // partition groups
     constexpr float NEG_INF = -INFINITY;
     extern __shared__ float weight[];                  // [num_parts]
     __shared__ float red[kCombineThreads / 32];
     __shared__ float4 part[PGRP][SLICES];
-    grid_dependency_wait();                            // partials come from the attention kernel
-    grid_launch_dependents();
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = (int)blockIdx.x % p.num_heads, qi = (int)blockIdx.x / p.num_heads;
-    const int b = blockIdx.y;
+    const int h = x % p.num_heads, qi = x / p.num_heads;
     const int kvh = h / p.group;
     const int U = p.q_len * p.group, u = qi * p.group + h % p.group;  // rows of a unit; this row
     const int T = reachable_tokens(p.context_lens, b, p.max_blocks, p.block_size);
@@ -107,6 +105,28 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
         store_out(p.out, o + 2, a.z * inv, p.out_dtype);
         store_out(p.out, o + 3, a.w * inv, p.out_dtype);
     }
+}
+
+template <int D, bool LSE>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
+    grid_dependency_wait();                            // partials come from the attention kernel
+    grid_launch_dependents();
+    combine_row<D, LSE>(p, blockIdx.x, blockIdx.y);
+}
+
+// The combine and, beside it in the same launch, the tokens' weights from the
+// scores and the partitions' statistics: both need the attention kernel alone,
+// and both wait for it.
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_weights_kernel(const CombineParams p, const WeightParams w) {
+    static_assert(kCombineThreads == kSThreads, "CTAs of both kinds");
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int rows = p.q_len * p.num_heads;
+    const int x = (int)blockIdx.x - rows, tiles = weight_tiles(w);
+    if (x < 0) combine_row<D, false>(p, blockIdx.x, blockIdx.y);
+    else add_scored_weights(w, x % tiles, tiles, x / tiles, blockIdx.y);
 }
 
 // Combine for the balanced split: the attention kernel's CTA c covered pages
@@ -440,6 +460,36 @@ cudaError_t launch_combine(const CombineParams& p, int head_dim, dim3 grid, bool
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+cudaError_t launch_combine_weights(const CombineParams& p, const WeightParams& w, int head_dim,
+                                   bool pdl, cudaStream_t stream) {
+    void (*kern)(const CombineParams, const WeightParams);
+    switch (head_dim) {
+        case 64: kern = combine_weights_kernel<64>; break;
+        case 128: kern = combine_weights_kernel<128>; break;
+        default: kern = combine_weights_kernel<256>; break;
+    }
+    const uint32_t smem = (uint32_t)p.num_parts * sizeof(float);
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t ctas =
+        (int64_t)p.q_len * p.num_heads + (int64_t)weight_tiles(w) * p.num_kv_heads;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)p.batch);
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p, w);
 }
 
 cudaError_t launch_combine_balanced(const CombineParams& p, int head_dim, dim3 grid, bool pdl,

@@ -118,7 +118,7 @@ struct WeightParams {
     int64_t score_width;
     // Stored scores of a call whose partitions left their statistics [B, Hkv,
     // num_parts, Q * group, 2] (else null: lse is filled): the rows' own are formed
-    // from those, so that the launch runs beside the combine kernel before it.
+    // from those, so that one launch does this and the combine.
     const float* part_ml;
     int32_t num_parts, part_pages;
     int32_t* err;             // device error word, bound on every wait (tile kernel)
@@ -442,9 +442,12 @@ cudaError_t launch_combine(const CombineParams& p, int head_dim, dim3 grid, bool
                            cudaStream_t stream);
 cudaError_t launch_combine_balanced(const CombineParams& p, int head_dim, dim3 grid, bool pdl,
                                     cudaStream_t stream);
+// The combine and launch_weights_of_scores in one launch (w.part_ml set, p.lse not).
+cudaError_t launch_combine_weights(const CombineParams& p, const WeightParams& w, int head_dim,
+                                   bool pdl, cudaStream_t stream);
 cudaError_t launch_prefix_combine(const PrefixCombineParams& p, int head_dim, int batch, bool pdl,
                                   cudaStream_t stream);
-// The same from stored scores (p.scores), up to 16 rows per kv head.
+// The tokens' weights from stored scores (p.scores), up to 16 rows per kv head.
 cudaError_t launch_weights_of_scores(const WeightParams& p, bool pdl, cudaStream_t stream);
 // On the tensor cores, for many rows; k: the keys' pages, q: boxes of 64 columns
 // and weights_tile_chunk(head_dim) query rows.
