@@ -46,7 +46,8 @@
  * device memory.  Entry points may be called from several host threads; the
  * shared state is a per-device cache of the SM count, of the device error
  * word's address and of which cluster sizes fit, per-thread caches of tensor
- * maps, and the two test switches of pa_set_switch.  No call reads the
+ * maps, streams of the library's own (pa_decode_shared_prefix), and the two test
+ * switches of pa_set_switch.  No call reads the
  * environment (the tuning variables are read once, when the library loads).
  *
  * Supported shapes: head_dim in {64, 128, 256}; block_size in {16, 32};
@@ -321,7 +322,10 @@ pa_status pa_rope_append_kv(void* q_out, void* k_cache, void* v_cache, const voi
  * the query rows of a prefix's sequences (n * q_len * group per kv head) go
  * through the prefix's pages together, on the kernel that pa_decode_multi
  * takes for as many rows; the sequences' own pages as in pa_decode_multi; a
- * third launch joins the two by their softmax statistics.  max_prefix_len and
+ * third launch joins the two by their softmax statistics.  The first two run
+ * beside each other, the second on a stream of the library's own that starts
+ * from `stream` and that `stream` waits for before the third (under capture: a
+ * branch of the caller's graph).  max_prefix_len and
  * max_context_len bound the lengths, as in pa_decode_splitkv; the workspace
  * must hold pa_workspace_size_shared_prefix(...) bytes (device, 16-byte
  * aligned, free again once the stream has passed the call).

@@ -13,6 +13,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <vector>
 
 #include "pa_internal.h"
 
@@ -187,6 +188,92 @@ pa_status device_state(int* sms, int32_t** err) {
 
 namespace {
 
+// A stream of the library's own on which a call runs a launch beside those of
+// the caller's stream: its work starts after what that stream held when the
+// lane was taken (fork), and the stream goes on after it (join).  Under capture
+// both become edges of the caller's graph.  Lanes are kept for the life of the
+// process, as many a device as calls need at once: a call takes one that
+// served the same stream before or is idle, so that no caller's stream comes
+// to wait for another's, and that is not being captured into another graph.
+struct Lane {
+    cudaStream_t stream = nullptr;
+    cudaEvent_t fork = nullptr, join = nullptr;
+    cudaStream_t served = nullptr;  // the caller's stream of the last call
+};
+
+std::mutex g_lane_mutex;
+std::vector<Lane> g_lanes[kMaxDevices];  // not in use by a call
+
+bool capture_of(cudaStream_t s, bool* active, unsigned long long* id) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    *id = 0;
+    if (cudaStreamGetCaptureInfo(s, &st, id) != cudaSuccess) return false;
+    *active = st == cudaStreamCaptureStatusActive;
+    return st != cudaStreamCaptureStatusInvalidated;
+}
+
+// A lane of the current device forked from `cs`; false: none, nothing was done.
+bool take_lane(cudaStream_t cs, Lane* lane) {
+    // (a query or creation must not touch a capture that another thread has under way)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return false;
+    int dev = 0;
+    bool active = false, found = false;
+    unsigned long long id = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices &&
+        capture_of(cs, &active, &id)) {
+        {
+            std::lock_guard<std::mutex> lock(g_lane_mutex);
+            std::vector<Lane>& free = g_lanes[dev];
+            for (size_t i = free.size(); i-- > 0 && !found;) {
+                bool lane_active = false;
+                unsigned long long lane_id = 0;
+                if (!capture_of(free[i].stream, &lane_active, &lane_id)) continue;
+                if (lane_active ? !(active && lane_id == id && free[i].served == cs)
+                                : free[i].served != cs && cudaStreamQuery(free[i].stream) != cudaSuccess)
+                    continue;
+                *lane = free[i];
+                free.erase(free.begin() + (long)i);
+                found = true;
+            }
+        }
+        if (!found) {
+            *lane = Lane();
+            found = cudaStreamCreateWithFlags(&lane->stream, cudaStreamNonBlocking) == cudaSuccess &&
+                    cudaEventCreateWithFlags(&lane->fork, cudaEventDisableTiming) == cudaSuccess &&
+                    cudaEventCreateWithFlags(&lane->join, cudaEventDisableTiming) == cudaSuccess;
+            if (!found) {
+                if (lane->fork) (void)cudaEventDestroy(lane->fork);
+                if (lane->stream) (void)cudaStreamDestroy(lane->stream);
+            }
+        }
+    }
+    if (found) {
+        lane->served = cs;
+        found = cudaEventRecord(lane->fork, cs) == cudaSuccess &&
+                cudaStreamWaitEvent(lane->stream, lane->fork, 0) == cudaSuccess;
+        if (!found) {
+            std::lock_guard<std::mutex> lock(g_lane_mutex);
+            g_lanes[dev].push_back(*lane);
+        }
+    }
+    (void)cudaThreadExchangeStreamCaptureMode(&mode);
+    if (!found) (void)cudaGetLastError();
+    return found;
+}
+
+// Lets `cs` go on after the lane's work, and gives the lane back.
+bool join_lane(cudaStream_t cs, const Lane& lane) {
+    const bool ok = cudaEventRecord(lane.join, lane.stream) == cudaSuccess &&
+                    cudaStreamWaitEvent(cs, lane.join, 0) == cudaSuccess;
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) {
+        std::lock_guard<std::mutex> lock(g_lane_mutex);
+        g_lanes[dev].push_back(lane);
+    }
+    return ok;
+}
+
 // Launch shape of the attention kernel for one problem: warps per stream
 // (head_dim 256 splits a page's output columns over two warps), streams per
 // CTA and stages per stream.
@@ -256,10 +343,11 @@ struct Plan {
     bool tile;       // several query tokens on the tcgen05 tile kernel (128-row tiles)
     int tile_qr;     // tile kernel: Q rows staged in shared memory (128, or 16: compact)
     bool persistent; // tile kernel, one pass: num_ctas CTAs take the units in turn, whole
+    bool on_lane = false;               // launched on a lane (no programmatic launch: it is not the
+                                        // stream's last kernel that it depends on)
     bool partials = false;              // leave (m, l, acc) in the workspace even of one partition
     const int32_t* own_lens = nullptr;  // a shared prefix: see AttnParams
     int32_t own_q = 0;
-    bool late_wait = false;             // see AttnParams
     float* lse = nullptr;               // row statistics wanted: see AttnParams
     int32_t token_limit = 0;            // see AttnParams
     bool pair = false;                  // (with tile) by the two-tile kernel
@@ -791,7 +879,6 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     p.prefix_lens = plan.prefix_lens;
     p.max_prefix_blocks = plan.max_prefix_blocks;
     p.per_prefix = plan.per_prefix;
-    p.late_wait = plan.late_wait ? 1 : 0;
     p.token_limit = plan.token_limit;
     p.lse = plan.lse;
     p.scores = plan.scores;
@@ -802,7 +889,7 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     L.head_dim = s->head_dim;
     L.block_size = s->block_size;
     L.kv_dtype = s->kv_dtype;
-    L.pdl = use_pdl();
+    L.pdl = use_pdl() && !plan.on_lane;
     L.cluster = p.cluster_reduce ? plan.num_parts : 1;
     L.grid = plan.balanced ? dim3((unsigned)plan.num_ctas)
                            : dim3((unsigned)plan.num_parts, (unsigned)grid_y,
@@ -864,14 +951,13 @@ pa_status launch_tile(void* out, const void* q, const void* k, const void* v, co
     p.cluster_reduce = plan.cluster ? 1 : 0;
     p.own_lens = plan.own_lens;
     p.own_q = plan.own_q;
-    p.late_wait = plan.late_wait ? 1 : 0;
     p.token_limit = plan.token_limit;
     p.lse = plan.lse;
     p.timeout_ns = kDefaultTimeoutNs;
     L.head_dim = s->head_dim;
     L.block_size = s->block_size;
     L.kv_dtype = s->kv_dtype;
-    L.pdl = use_pdl();
+    L.pdl = use_pdl() && !plan.on_lane;
     L.cluster = plan.cluster ? plan.num_parts : 1;
     const bool compact = plan.tile_qr == kTileCompactQRows;
     if (compact && (s->head_dim != 256 || rows > kTileCompactQRows)) return PA_ERR_UNSUPPORTED;
@@ -1083,7 +1169,6 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
     };
     pp->prefix = finish(&pp->pre, pre_part);
     pp->own = finish(s, own_part);
-    pp->own.late_wait = true;  // (it needs nothing of the prefix's launch)
     size_t at = 0;
     bool ok = true;
     auto take = [&](size_t n) {
@@ -1515,15 +1600,26 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
     pp.prefix.own_lens = context_lens;
     pp.prefix.own_q = q_len;
     auto attend = [&](const int32_t* bt, const int32_t* lens, const pa_shape* s, int32_t ql,
-                      const Plan& plan, float* acc, float* ml) {
+                      const Plan& plan, float* acc, float* ml, cudaStream_t on) {
         return plan.tile ? launch_tile(out, q, k_cache, v_cache, bt, lens, s, scale, plan, acc, ml,
-                                       err, cs, ql)
+                                       err, on, ql)
                          : launch_attention(out, q, k_cache, v_cache, bt, lens, s, scale, plan, acc,
-                                            ml, err, cs, ql);
+                                            ml, err, on, ql);
     };
-    st = attend(prefix_tables, prefix_lens, &pp.pre, pp.pre_q, pp.prefix, f(0), f(pp.pre_ml));
-    if (st != PA_OK) return st;
-    st = attend(block_tables, context_lens, shape, q_len, pp.own, f(pp.own_acc), f(pp.own_ml));
+    // The own pages' launch needs nothing of the prefix's: it runs beside it, on a
+    // lane.  (As a programmatic launch behind the prefix's in one stream it would
+    // start before that has ended too, but what earlier launches wrote is only
+    // sure to be visible to CTAs that wait for the prefix's end; one after the
+    // other the two take 64 us where side by side they take 48, 64 sequences of up
+    // to 1024 tokens behind 8191.)
+    Lane lane;
+    const bool beside = take_lane(cs, &lane);
+    st = attend(prefix_tables, prefix_lens, &pp.pre, pp.pre_q, pp.prefix, f(0), f(pp.pre_ml), cs);
+    pp.own.on_lane = beside;
+    if (st == PA_OK)
+        st = attend(block_tables, context_lens, shape, q_len, pp.own, f(pp.own_acc), f(pp.own_ml),
+                    beside ? lane.stream : cs);
+    if (beside && !join_lane(cs, lane) && st == PA_OK) st = PA_ERR_CUDA;
     if (st != PA_OK) return st;
     PrefixCombineParams c;
     c.out = out;
@@ -1546,7 +1642,7 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
     c.own_parts = pp.own.num_parts;
     c.own_part_pages = pp.own.part_pages;
     c.out_dtype = shape->out_dtype;
-    return launch_prefix_combine(c, shape->head_dim, shape->batch, use_pdl(), cs) == cudaSuccess
+    return launch_prefix_combine(c, shape->head_dim, shape->batch, use_pdl() && !beside, cs) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }

@@ -73,7 +73,7 @@ enum SegOut { kOutFinal = 0, kOutPartial = 1, kOutCluster = 2, kOutRecord = 3 };
 // MULTI: several query tokens per sequence (rows are (query token, head)
 // pairs with a causal limit each); otherwise one token, rows = the group's heads.
 // EXT: a launch may also ask for the row statistics (p.lse), a shared prefix
-// (p.own_lens), a late wait, and the scores: with p.scores every score is
+// (p.own_lens), a limit of the tokens, and the scores: with p.scores every score is
 // stored, and the tokens' attention weights are summed from them once the rows'
 // statistics are known (4 bytes a row and token written and read again,
 // against reading a key of 2 D bytes again).  The plain instantiations know
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256, 1)
         prefetch_tensormap(&tmap_v);
     }
     // Inputs may come from the previous kernel in the stream.
-    if (!EXT || !p.late_wait) grid_dependency_wait();
+    grid_dependency_wait();
     grid_launch_dependents();
 
     const int g = lane >> 2, tig = lane & 3;
@@ -678,7 +678,6 @@ __global__ void __launch_bounds__(256, 1)
                 store_out(p.out, row_off(b, kvh, idx / D) + idx % D, 0.f, p.out_dtype);
             if (EXT && p.lse && tid < R) p.lse[row_off(b, kvh, tid) / D] = INFINITY;
         }
-        if constexpr (EXT) late_dependency_wait(p.late_wait);
         return;
     }
     __syncthreads();  // barrier initialisation visible to every warp
@@ -771,7 +770,6 @@ __global__ void __launch_bounds__(256, 1)
         if (EXT && p.weights_out)
             add_weights(b, kvh, pb, max(pb, pe), reach, part == p.num_parts - 1);
     }
-    if constexpr (EXT) late_dependency_wait(p.late_wait);
 }
 
 // Per-instantiation flags of the attributes set once per device.

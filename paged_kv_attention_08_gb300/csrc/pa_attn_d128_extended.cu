@@ -1,5 +1,5 @@
 // Instantiations of the decode kernel for head_dim 128 with row statistics,
-// scores, a shared prefix or a late wait.
+// scores, a shared prefix or a limit of the tokens.
 #include "pa_attn.cuh"
 
 namespace pa {

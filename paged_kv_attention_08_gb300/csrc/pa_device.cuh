@@ -169,15 +169,6 @@ __device__ __forceinline__ void grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// The wait of a launch that ran beside its predecessor, at its end: the last
-// CTA alone takes it, so that the grid ends no earlier than the predecessor
-// while every other CTA makes room for the next.
-__device__ __forceinline__ void late_dependency_wait(int late) {
-    if (late && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 &&
-        blockIdx.z == gridDim.z - 1)
-        grid_dependency_wait();
-}
-
 // Allow the next kernel in the stream to begin launching (it still waits for
 // this grid's completion before it reads anything this grid writes).
 __device__ __forceinline__ void grid_launch_dependents() {

@@ -32,12 +32,6 @@ struct AttnParams {
     // prefix.  Each sees the whole prefix, but for padding (see prefix_limit).
     const int32_t* own_lens;
     int32_t own_q;
-    // 1: this launch needs nothing of the one before it in the stream, only of
-    // those before that, so its last CTA waits for it at its end instead of
-    // every CTA at its start.
-    // (The launch before must let its dependents go no earlier than after its
-    // own wait, as the attention kernels do: then what came before it is done.)
-    int32_t late_wait;
     // Warp-level kernel: a shared prefix read by each of its sequences in front
     // of its own pages (null otherwise), sequence b after prefix b / per_prefix.
     const int32_t* prefix_tables;
@@ -384,7 +378,7 @@ cudaError_t allow_nonportable_clusters_once(Kern kern, AttrFlags& done) {
 
 // Does a launch ask for more than attention?
 inline bool extended(const AttnParams& p) {
-    return p.own_lens || p.late_wait || p.scores || p.lse || p.token_limit;
+    return p.own_lens || p.scores || p.lse || p.token_limit;
 }
 
 struct AttnLaunch {

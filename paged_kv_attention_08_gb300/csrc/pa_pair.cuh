@@ -80,16 +80,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int part = blockIdx.x, kvh = (int)blockIdx.y % Hkv, b = blockIdx.z;
     const int row0 = ((int)blockIdx.y / Hkv) * (2 * kTileRows);  // the CTA's first row of the unit
     const int ntile = U - row0 > kTileRows ? 2 : 1;
-    if (!p.late_wait) grid_dependency_wait();
+    grid_dependency_wait();
     grid_launch_dependents();
 
     const int T = reachable_tokens(p.context_lens, b, p.max_blocks, BS);
     const int pb = part * p.part_pages, pe = min(pb + p.part_pages, (T + BS - 1) / BS);
     const int32_t* table_row = p.block_tables + (size_t)b * p.max_blocks;
-    if (pe <= pb) {  // no page of the sequence: the join reads nothing of such a partition
-        late_dependency_wait(p.late_wait);
-        return;
-    }
+    if (pe <= pb) return;  // no page of the sequence: the join reads nothing of such a partition
     const int nblk = (pe - pb + NPB - 1) / NPB;
     const int tend = min(T, pe * BS);  // the partition's tokens end here
 
@@ -445,7 +442,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 512);
     }
-    late_dependency_wait(p.late_wait);
 }
 
 template <int D, int BS, typename KV>

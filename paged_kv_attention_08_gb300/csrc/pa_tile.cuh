@@ -73,7 +73,7 @@ constexpr float kTileRescaleSlack = 8.0f;  // log2 units: P may reach 2^8 before
 // cost the several-token workloads 1.5 %, and the exact normaliser's second
 // form of the inner loop the prefill chunk 3 %.
 //   kPlain     attention alone
-//   kExtended  row statistics (p.lse), a shared prefix (p.own_lens), a late wait
+//   kExtended  row statistics (p.lse), a shared prefix (p.own_lens), a limit of the tokens
 //   kExact     kExtended, and fp16's normaliser sums the weights as they are, not
 //              as rounded for the P V MMA: the tokens' accumulated weights are
 //              formed from it
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int part = blockIdx.x;
     const int tiles = (U + kTileRows - 1) / kTileRows;  // 128-row tiles of a unit
 
-    if (!EXT || !p.late_wait) grid_dependency_wait();
+    grid_dependency_wait();
     grid_launch_dependents();
 
     // Element offset of unit row u's query / output vector ([B, Q, H, D]).
@@ -396,7 +396,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (EXT && p.lse && u < U && idx % D == 0) p.lse[row_off(seg0.b, seg0.kvh, u) / D] = INFINITY;
             }
         }
-        if constexpr (EXT) late_dependency_wait(p.late_wait);
         return;
     }
 
@@ -1041,7 +1040,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc::tmem_dealloc(tmem, kCols);
     }
     if (p.cluster_reduce) cluster_merge();
-    if constexpr (EXT) late_dependency_wait(p.late_wait);
 }
 
 // Per-instantiation flag of the shared-memory limit set once per device.
@@ -1129,7 +1127,7 @@ cudaError_t launch_tile_for_d(const AttnLaunch& L, cudaStream_t stream) {
     return cudaErrorInvalidValue;
 }
 
-// The same with row statistics, a shared prefix or a late wait.
+// The same with row statistics, a shared prefix or a limit of the tokens.
 template <int D, int QR>
 cudaError_t launch_tile_extended_for_d(const AttnLaunch& L, cudaStream_t stream) {
     const bool bs16 = L.block_size == 16;

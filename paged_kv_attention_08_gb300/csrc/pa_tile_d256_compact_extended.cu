@@ -1,5 +1,5 @@
 // Instantiations of the tcgen05 tile kernel for compact units (head_dim 256, at
-// most 16 rows) with row statistics, a shared prefix or a late wait.
+// most 16 rows) with row statistics, a shared prefix or a limit of the tokens.
 #include "pa_tile.cuh"
 
 namespace pa {

@@ -1,5 +1,5 @@
 // Instantiations of the tcgen05 tile kernel for head_dim 64 with row
-// statistics, a shared prefix or a late wait.
+// statistics, a shared prefix or a limit of the tokens.
 #include "pa_tile.cuh"
 
 namespace pa {

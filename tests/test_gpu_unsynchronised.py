@@ -73,3 +73,160 @@ def test_accumulate_in_partitions(B, H, Hkv, D, longest):
     for a, b in zip(alone, together):
         assert torch.isfinite(a[0].float()).all()
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+APART = 1 << 20   # announced so long, a prefix is read in a launch of its own
+
+
+def prefix_loop(n, Q, H, Hkv, D, own, prefix, wide=0):
+    """(turn(i), reset()) of samples behind one prefix, everything rewritten before each call."""
+    bs, dtype = 16, torch.bfloat16
+    vs, first = variants(4, n, H, Hkv, D, bs, own, dtype, 0, Q)
+    if wide:
+        for v in vs:
+            table = torch.full((n, wide // bs), -1, dtype=torch.int32, device=DEV)
+            table[:, :v["table"].shape[1]] = v["table"]
+            v["table"] = table
+    pages = (prefix + bs - 1) // bs
+    for i, v in enumerate(vs):
+        g = torch.Generator().manual_seed(i)
+        v["ptable"] = torch.full((1, APART // bs), -1, dtype=torch.int32)
+        v["ptable"][0, :pages] = (torch.randperm(pages, generator=g) + first).to(torch.int32)
+        v["ptable"] = v["ptable"].to(DEV)
+        v["plens"] = torch.tensor([prefix - 37 * i], dtype=torch.int32, device=DEV)
+    phases, axes = rotary(D)
+    k0, v0 = (ref.normal((first + pages, bs, Hkv, D), dtype, s).to(DEV) for s in (93, 94))
+    kc, vc = k0.clone(), v0.clone()
+    state = {x: torch.empty_like(vs[0][x]) for x in vs[0]}
+    q, out = (torch.empty((n, Q, H, D), dtype=dtype, device=DEV) for _ in range(2))
+    max_own = wide or own
+    need = pa.workspace_size_shared_prefix(q, kc, state["ptable"], state["table"], dtype, APART, max_own)
+    assert need > 0                                  # launches of their own
+    ws = torch.empty((need // 4 + 1,), device=DEV)
+
+    def reset():
+        kc.copy_(k0)
+        vc.copy_(v0)
+        ws.fill_(float("nan"))
+
+    def turn(i):
+        for x, t in state.items():
+            t.copy_(vs[i % len(vs)][x])
+        qkv = state["qkv"]
+        pa.rope_append_kv(q, kc, vc, qkv[:, :, :H], qkv[:, :, H:H + Hkv], qkv[:, :, H + Hkv:],
+                          state["pos"], phases, axes, state["table"], state["lens"])
+        pa.decode_shared_prefix(out, q, kc, vc, state["ptable"], state["plens"], state["table"],
+                                state["lens"], D ** -0.5, APART, max_own, workspace=ws)
+        return out.clone()
+
+    return turn, reset
+
+
+# own pages on the warp-level kernel, on the tile kernel, and two tiles to a CTA
+LOOPS = [(20, 1, 32, 8, 128, 300, 3000, 0), (4, 40, 8, 2, 128, 200, 3000, 0),
+         (4, 40, 32, 8, 128, 200, 3000, 65536), (3, 8, 16, 1, 256, 100, 500, 0)]
+
+
+@pytest.mark.parametrize("args", LOOPS)
+def test_shared_prefix_in_launches_of_their_own(args):
+    turn, reset = prefix_loop(*args)
+    reset()
+    alone = []
+    for i in range(TURNS):
+        alone.append(turn(i))
+        torch.cuda.synchronize()
+    reset()
+    torch.cuda.synchronize()
+    together = [turn(i) for i in range(TURNS)]
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    for a, b in zip(alone, together):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+def test_shared_prefix_captured_with_what_surrounds_it():
+    """Several calls and their inputs' copies in one graph, replayed without a wait."""
+    turn, reset = prefix_loop(*LOOPS[0])
+    reset()
+    for _ in range(5):     # (a round appends to slots that the next one reads)
+        want = [turn(i) for i in range(4)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [turn(i) for i in range(4)]
+    reset()
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_shared_prefix_eager_while_another_stream_is_captured():
+    (ta, ra), (tb, rb) = prefix_loop(*LOOPS[0]), prefix_loop(*LOOPS[1])
+    ra(), rb()
+    want_a, want_b = ta(0), tb(0)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream(DEV)
+    got_b = []
+    with torch.cuda.graph(graph, capture_error_mode="relaxed"):
+        got_a = ta(0)
+        with torch.cuda.stream(side):
+            got_b.append(tb(0))
+        again = ta(0)
+    torch.cuda.synchronize()
+    assert torch.equal(got_b[0], want_b)
+    ra()
+    for _ in range(2):
+        graph.replay()
+    assert torch.equal(tb(0), want_b)                # eager after the capture
+    torch.cuda.synchronize()
+    assert torch.equal(got_a, want_a) and torch.equal(again, want_a)
+    assert pa.device_error() == 0
+
+
+def test_shared_prefix_on_one_stream_does_not_wait_for_another():
+    (ta, ra), (tb, rb) = prefix_loop(*LOOPS[0]), prefix_loop(*LOOPS[1])
+    ra(), rb()
+    want_a, want_b = ta(0), tb(0)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)
+    done = torch.cuda.Event()
+    with torch.cuda.stream(sa):
+        torch.cuda._sleep(int(4e8))                  # some 0.2 s
+        got_a = ta(0)
+        done.record()
+    with torch.cuda.stream(sb):
+        got_b = tb(0)
+    sb.synchronize()
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(got_a, want_a) and torch.equal(got_b, want_b)
+
+
+def test_shared_prefix_from_several_threads():
+    import threading
+
+    loops = [prefix_loop(*LOOPS[i % 2]) for i in range(4)]
+    want = []
+    for turn, reset in loops:
+        reset()
+        want.append([turn(i) for i in range(8)])
+    torch.cuda.synchronize()
+    got = [None] * len(loops)
+
+    def work(x):
+        with torch.cuda.stream(torch.cuda.Stream(DEV)):
+            loops[x][1]()
+            got[x] = [loops[x][0](i) for i in range(8)]
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(x,)) for x in range(len(loops))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert pa.device_error() == 0
