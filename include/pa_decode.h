@@ -326,8 +326,9 @@ pa_status pa_rope_append_kv(void* q_out, void* k_cache, void* v_cache, const voi
  * beside each other, the second on a stream of the library's own that starts
  * from `stream` and that `stream` waits for before the third (under capture: a
  * branch of the caller's graph).  max_prefix_len and
- * max_context_len bound the lengths, as in pa_decode_splitkv; the workspace
- * must hold pa_workspace_size_shared_prefix(...) bytes (device, 16-byte
+ * max_context_len bound the lengths: whatever the plan, prefix tokens past the
+ * former's last page are left out, and a sequence's own tokens past the latter's.
+ * The workspace must hold pa_workspace_size_shared_prefix(...) bytes (device, 16-byte
  * aligned, free again once the stream has passed the call).
  */
 pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
@@ -355,7 +356,8 @@ size_t pa_workspace_size_shared_prefix(const pa_shape* shape, int32_t num_prefix
  * there on are not written.
  *   weights_in, weights_out  [batch, num_kv_heads, max_blocks_per_seq * block_size]
  *                            fp32; may be the same array, else apart
- * Weights are fp32; each is summed over the rows by one thread in a fixed order,
+ * Tokens past max_context_len's last page are left out of the attention and keep
+ * their weights.  Weights are fp32; each is summed over the rows by one thread in a fixed order,
  * so that equal calls give equal bits.  The other arguments are those
  * of pa_decode_multi with an automatic split; the workspace must hold
  * pa_workspace_size_accumulate(...) bytes.

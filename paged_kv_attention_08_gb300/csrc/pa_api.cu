@@ -353,7 +353,7 @@ struct Plan {
     bool pair = false;                  // (with tile) by the two-tile kernel
     const int32_t* prefix_tables = nullptr;  // a prefix in front: see AttnParams
     const int32_t* prefix_lens = nullptr;
-    int32_t max_prefix_blocks = 0, per_prefix = 0;
+    int32_t max_prefix_blocks = 0, per_prefix = 0, prefix_token_limit = 0;
     float* scores = nullptr;            // scores wanted: see AttnParams
     int64_t score_width = 0;
     const float* weights_in = nullptr;
@@ -879,6 +879,7 @@ pa_status launch_attention(void* out, const void* q, const void* k, const void* 
     p.prefix_lens = plan.prefix_lens;
     p.max_prefix_blocks = plan.max_prefix_blocks;
     p.per_prefix = plan.per_prefix;
+    p.prefix_token_limit = plan.prefix_token_limit;
     p.token_limit = plan.token_limit;
     p.lse = plan.lse;
     p.scores = plan.scores;
@@ -1585,7 +1586,12 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, const void* k_cache,
     PrefixPlan pp;
     st = plan_prefix(shape, &pre, q_len, max_prefix_len, max_context_len, sms, &pp);
     if (st != PA_OK) return st;
+    // Each part loses the tokens past its own announced pages, by every plan: a
+    // prefix longer than announced must not push the sequences' own tokens out.
+    pp.prefix.token_limit = pages_for(&pre, max_prefix_len) * shape->block_size;
+    pp.own.token_limit = pages_for(shape, max_context_len) * shape->block_size;
     if (pp.joined) {
+        pp.own.prefix_token_limit = pp.prefix.token_limit;
         pp.own.prefix_tables = prefix_tables;
         pp.own.prefix_lens = prefix_lens;
         pp.own.max_prefix_blocks = max_prefix_blocks;

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(256, 1)
     // A prefix in front (PRE): its pages are pages 0 .. pre_pages - 1 of the
     // sequence, the own ones follow; pre_tokens may end inside the last of them.
     const int32_t* pre_row = nullptr;
-    int pre_pages = 0, pre_tokens = 0;
+    int pre_pages = 0, pre_tokens = 0, pre_reach = 0;  // pre_reach: with those past the limit
     int ent_cur = -1, ent_next = -1, cur_chunk = 0;
     auto fetch = [&](int chunk) -> int {
         const int li = chunk * 32 + lane;
@@ -255,16 +255,19 @@ __global__ void __launch_bounds__(256, 1)
         int pre_lim0 = 0, pre_lim1 = 0;  // and those of the prefix
         if constexpr (MULTI) {
             if (EXT && p.own_lens) {
-                if (real0) lim0 = prefix_limit(T, b, qi0 + (g >> gshift), Q, p.own_q, p.own_lens);
+                const int reach = reachable_tokens(p.context_lens, b, p.max_blocks, BS);
+                if (real0)
+                    lim0 = min(T, prefix_limit(reach, b, qi0 + (g >> gshift), Q, p.own_q, p.own_lens));
                 if (real1)
-                    lim1 = prefix_limit(T, b, qi0 + ((g + 8) >> gshift), Q, p.own_q, p.own_lens);
+                    lim1 = min(T, prefix_limit(reach, b, qi0 + ((g + 8) >> gshift), Q, p.own_q,
+                                               p.own_lens));
             } else {
                 const int ctx = max(__ldg(p.context_lens + b), 0);
                 lim0 = min(T, ctx - Q + qi0 + (g >> gshift) + 1);
                 lim1 = min(T, ctx - Q + qi0 + ((g + 8) >> gshift) + 1);
                 if constexpr (PRE) {  // (all of it, but for padding: see prefix_limit)
-                    pre_lim0 = pre_tokens + min(0, ctx - Q + qi0 + (g >> gshift) + 1);
-                    pre_lim1 = pre_tokens + min(0, ctx - Q + qi0 + ((g + 8) >> gshift) + 1);
+                    pre_lim0 = min(pre_tokens, pre_reach + min(0, ctx - Q + qi0 + (g >> gshift) + 1));
+                    pre_lim1 = min(pre_tokens, pre_reach + min(0, ctx - Q + qi0 + ((g + 8) >> gshift) + 1));
                 }
             }
         }
@@ -657,12 +660,13 @@ __global__ void __launch_bounds__(256, 1)
     // (every index stays inside the table row); those past it are masked
     if (!PRE) start_fetch(b, pb, min(pb + p.part_pages, p.max_blocks));
     const int reach = reachable_tokens(p.context_lens, b, p.max_blocks, BS);
-    const int T = EXT && p.token_limit ? min(reach, p.token_limit) : reach;
+    const int T = (EXT || PRE) && p.token_limit ? min(reach, p.token_limit) : reach;
     int npages = (T + BS - 1) / BS;
     if constexpr (PRE) {
         const int x = b / p.per_prefix;
         pre_row = p.prefix_tables + (size_t)x * p.max_prefix_blocks;
-        pre_tokens = reachable_tokens(p.prefix_lens, x, p.max_prefix_blocks, BS);
+        pre_reach = reachable_tokens(p.prefix_lens, x, p.max_prefix_blocks, BS);
+        pre_tokens = min(pre_reach, p.prefix_token_limit);
         pre_pages = (pre_tokens + BS - 1) / BS;
         npages += pre_pages;
         start_fetch(b, pb, min(pb + p.part_pages, npages));

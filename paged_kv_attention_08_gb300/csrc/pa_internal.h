@@ -37,8 +37,10 @@ struct AttnParams {
     const int32_t* prefix_tables;
     const int32_t* prefix_lens;
     int32_t max_prefix_blocks, per_prefix;
+    int32_t prefix_token_limit;  // its tokens from here on are not attended to
     int32_t token_limit;      // 0, or tokens from here on are not attended to (a multiple of
-                              // block_size): what the scores and weights are sized for
+                              // block_size): those of the pages announced, which the scores
+                              // and weights are sized for
     float* scores;            // warp-level kernel: [B, Hkv, Q * group, score_width] or null: q . K
                               // of every token of a read page, -inf where masked
     int64_t score_width;

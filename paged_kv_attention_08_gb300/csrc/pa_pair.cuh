@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     grid_dependency_wait();
     grid_launch_dependents();
 
-    const int T = reachable_tokens(p.context_lens, b, p.max_blocks, BS);
+    const int reach = reachable_tokens(p.context_lens, b, p.max_blocks, BS);
+    const int T = p.token_limit ? min(reach, p.token_limit) : reach;
     const int pb = part * p.part_pages, pe = min(pb + p.part_pages, (T + BS - 1) / BS);
     const int32_t* table_row = p.block_tables + (size_t)b * p.max_blocks;
     if (pe <= pb) return;  // no page of the sequence: the join reads nothing of such a partition
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // tokens below lim: the row's causal limit, the table's reach, the partition's end
         const int lim =
             u >= U ? 0
-                   : min(tend, p.own_lens ? prefix_limit(T, b, u >> gshift, Q, p.own_q, p.own_lens)
+                   : min(tend, p.own_lens ? prefix_limit(reach, b, u >> gshift, Q, p.own_q, p.own_lens)
                                           : ctx - Q + (u >> gshift) + 1);
         float m = NEG_INF, l = 0.f;
         unsigned bits_next = __ballot_sync(kFullMask, page_of(0) >= 0);

@@ -759,8 +759,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // tokens t < lim: the row's causal limit, the table's reach, the segment's end
             const int lim =
                 u >= U ? 0
-                       : min(tend, EXT && p.own_lens ? prefix_limit(g.T, g.b, u >> gshift, Q, p.own_q, p.own_lens)
-                                              : ctx - Q + (u >> gshift) + 1);
+                       : min(tend, EXT && p.own_lens
+                                       ? prefix_limit(reachable_tokens(p.context_lens, g.b, p.max_blocks, BS),
+                                                      g.b, u >> gshift, Q, p.own_q, p.own_lens)
+                                       : ctx - Q + (u >> gshift) + 1);
             const int32_t* table_row = p.block_tables + (size_t)g.b * p.max_blocks;
             // which pages of the segment's block k hold data: bit q for page q
             // (read from the table here; the K stage's record may already
