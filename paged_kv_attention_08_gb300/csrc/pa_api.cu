@@ -1140,8 +1140,11 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
         // The two launches share the SMs.  A CTA more for the prefix shortens it
         // but costs a start and an end, and takes an SM from the sequences' own
         // pages; so the prefix is cut only until it ends well before the whole
-        // call can (lengths are not known here: the own pages count as half of
-        // max_context_len, read at 33 GB/s an SM).  Two tiles to a CTA, calls in a
+        // call can (lengths are not known here: the own pages count as half of those
+        // announced, read at 33 GB/s an SM), and in any case until a CTA takes at most
+        // three times as long as with a CTA to every slot: an announced length may be
+        // a loose bound (128 sequences announced with 131,072 own tokens each:
+        // without that, 16 CTAs of 1.5 ms).  Two tiles to a CTA, calls in a
         // row: 8 units of 8191 tokens beside 64 sequences of up to 1024 take 49.9,
         // 46.0, 48.5, 51.3 us with 5, 6, 7, 8 partitions; 16 units of 65536 beside 128
         // of up to 2048 take 287, 249, 244 us with 6, 7, 8 (alone 260, 265, 267).  With
@@ -1149,13 +1152,15 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
         // with 9, the second 255 with 4 of 32 and 279 with 3.
         const double own_us =
             own_part.p.tile ? own_part.units * own_part.parts * tile_us(own_part, own_part.parts)
-                            : (double)own_part.units * max_context_len * s->head_dim * 2.0 / 33e3;
+                            : (double)own_part.units * own_part.pages * s->block_size * s->head_dim * 2.0 / 33e3;
         const int64_t most = std::max<int64_t>(
             1, std::min<int64_t>(pre_part.slots / pre_part.units, (pre_part.pages + 3) / 4));
         int64_t parts = 1;
         for (; parts < most; ++parts) {
             const double cta = tile_us(pre_part, parts);
-            if (cta <= (pre_part.pair ? 0.94 : 0.85) * (pre_part.units * parts * cta + own_us) / sms) break;
+            if (cta <= 3.0 * tile_us(pre_part, most) &&
+                cta <= (pre_part.pair ? 0.94 : 0.85) * (pre_part.units * parts * cta + own_us) / sms)
+                break;
         }
         pre_part.parts = parts;
     }
