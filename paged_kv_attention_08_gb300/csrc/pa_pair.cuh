@@ -35,8 +35,9 @@ namespace pa {
 
 constexpr float kPairRescaleSlack = 8.0f;  // log2 units: P may reach 2^8 before a rescale
 
-// bf16's P goes in two parts of 8 bits each; fp16's in one, with the normaliser
-// summed from the weights as rounded, so that the result is a mean of V's rows.
+// bf16's P goes in two parts of 8 bits each; fp16's in one, 2^kHalfLift higher
+// (pa_internal.h), with the normaliser summed from the weights as rounded, so
+// that the result is a mean of V's rows.
 // Partials only: a prefix's and the sequences' own are joined by another launch.
 template <int D, int BS, typename KV>
 __global__ void __launch_bounds__(kTileThreads, 1)
@@ -52,6 +53,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr uint32_t O_COL = 0, S_COL = 2 * D;  // tensor memory: O of tile t at t D, S at S_COL + t BN
     static_assert(S_COL + 2 * BN <= 512, "tensor memory");
     constexpr float NEG_INF = -INFINITY;
+    constexpr float kLift = kSplitP ? 0.f : kHalfLift;  // m: the row maximum less this
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -345,12 +347,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                 for (int c = 0; c < BH; c += 2) mx = fmax3(mx, sc[c], sc[c + 1]);
                 const float ms = mx * qscale;
-                const bool need = ms > m + kPairRescaleSlack;
+                const bool need = ms > m + (kPairRescaleSlack + kLift);
                 float alpha = 1.f;
                 if (need) {
-                    alpha = m == NEG_INF ? 1.f : fast_exp2(m - ms);
+                    const float base = ms - kLift;
+                    alpha = m == NEG_INF ? 1.f : fast_exp2(m - base);
                     l *= alpha;
-                    m = ms;
+                    m = base;
                 }
                 // (S is issued after the previous block's P V has completed: O is at rest)
                 if (__any_sync(kFullMask, need && alpha != 1.f)) {

@@ -74,6 +74,7 @@ constexpr float kTileRescaleSlack = 8.0f;  // log2 units: P may reach 2^8 before
 // form of the inner loop the prefill chunk 3 %.
 //   kPlain     attention alone
 //   kExtended  row statistics (p.lse), a shared prefix (p.own_lens), a limit of the tokens
+//              (fp16's P then stands 2^kHalfLift higher: see pa_internal.h)
 //   kExact     kExtended, and fp16's normaliser sums the weights as they are, not
 //              as rounded for the P V MMA: the tokens' accumulated weights are
 //              formed from it
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr float NEG_INF = -INFINITY;
     constexpr bool EXT = MODE != kPlain;
     constexpr bool kBF = std::is_same<KV, __nv_bfloat16>::value;
+    constexpr float kLift = EXT && !kBF ? kHalfLift : 0.f;  // m: the row maximum less this
     // P enters the P V MMA as 16-bit values.  bf16 keeps 8 significant bits,
     // so P is split into a high and a low part (two MMAs, ~16 bits); fp16
     // keeps 11, a relative rounding of at most 2^-11 per weight, and is used
@@ -817,12 +819,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         if (!exchange(xmax + (nx & 1) * 256, mx, mo)) break;
                         ms = fmaxf(mx, mo) * qscale;
                     }
-                    const bool need = ms > m + kTileRescaleSlack;
+                    const bool need = ms > m + (kTileRescaleSlack + kLift);
                     float alpha = 1.f;
                     if (need) {
-                        alpha = (m == NEG_INF) ? 1.f : fast_exp2(m - ms);
+                        const float base = ms - kLift;
+                        alpha = (m == NEG_INF) ? 1.f : fast_exp2(m - base);
                         l *= alpha;
-                        m = ms;
+                        m = base;
                     }
                     // O holds earlier blocks' sums only if this row had attended a token;
                     // each warpgroup rescales its own O (kHalfO) or its half of the
