@@ -282,7 +282,9 @@ typedef struct pa_rope {
  * apart: an image's patches share a time, and eviction moves tokens to lower
  * slots.  A token at a negative position (padding) or past the table, or whose
  * table entry is masked, is turned into q_out and writes nothing to the cache.
- *   q, q_out          [batch, q_len, num_heads, head_dim]     kv_dtype (q_out may be q)
+ *   q, q_out          [batch, q_len, num_heads, head_dim]     kv_dtype (q_out may be q,
+ *                     with its stride; else none of its rows meets one of q, k_new,
+ *                     v_new or the caches: PA_ERR_INVALID_ARG where they do)
  *   k_new, v_new      [batch, q_len, num_kv_heads, head_dim]  kv_dtype
  *   rotary_positions  [num_axes, batch, q_len]  int32, any value
  *   phases            [rotary_dim / 2]  int64: f_j / (2 pi) * 2^64, modulo 2^64

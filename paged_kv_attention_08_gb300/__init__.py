@@ -493,8 +493,8 @@ def _token_stride(t, name, shape):
 
 def rope_append_kv(q_out, k_cache, v_cache, q, k_new, v_new, rotary_positions, phases, axes,
                    block_tables, context_lens, interleaved: bool = False, stream=None):
-    """Turn the new tokens' queries into ``q_out`` (may be ``q``) and write
-    their turned keys and their values into the paged cache.
+    """Turn the new tokens' queries into ``q_out`` (``q`` itself, or memory of
+    its own) and write their turned keys and their values into the paged cache.
 
     q, q_out [B, Q, H, D]; k_new, v_new [B, Q, Hkv, D] (views of one fused
     projection are fine); rotary_positions int32 [axes, B, Q]; phases from

@@ -15,6 +15,21 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// Do rows of two arrays of `tokens` 16-bit rows share a byte?  Rows of one stride
+// meet if they do modulo the stride (slices of one fused buffer do not); arrays
+// of different strides are taken to where they share a range.
+bool rows_meet(const void* a, int64_t a_row, int64_t a_stride, const void* b, int64_t b_row,
+               int64_t b_stride, int64_t tokens) {
+    const size_t na = ((size_t)(tokens - 1) * a_stride + a_row) * 2;
+    const size_t nb = ((size_t)(tokens - 1) * b_stride + b_row) * 2;
+    if (!overlap(a, na, b, nb)) return false;
+    if (a_stride != b_stride || tokens == 1) return true;
+    const int64_t stride = a_stride * 2;
+    const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(b));
+    const int64_t at = ((apart % stride) + stride) % stride;  // a's rows begin here in b's stride
+    return at < b_row * 2 || at + a_row * 2 > stride;
+}
+
 }  // namespace
 
 extern "C" {
@@ -53,6 +68,16 @@ pa_status pa_rope_append_kv(void* q_out, void* k_cache, void* v_cache, const voi
         !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(phases, 8) ||
         !aligned(rotary_positions, 4) || !aligned(axes, 4) || !aligned(block_tables, 4) ||
         !aligned(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    // items of q_out are written while others of the inputs are still to be read
+    const size_t cache_bytes =
+        (size_t)shape->num_blocks * shape->block_size * (size_t)kv_row * 2;
+    const size_t out_bytes = ((size_t)(tokens - 1) * rope->q_out_stride + q_row) * 2;
+    if ((q_out != q && rows_meet(q_out, q_row, rope->q_out_stride, q, q_row, rope->q_stride, tokens)) ||
+        rows_meet(q_out, q_row, rope->q_out_stride, k_new, kv_row, rope->k_stride, tokens) ||
+        rows_meet(q_out, q_row, rope->q_out_stride, v_new, kv_row, rope->v_stride, tokens) ||
+        overlap(q_out, out_bytes, k_cache, cache_bytes) ||
+        overlap(q_out, out_bytes, v_cache, cache_bytes))
         return PA_ERR_INVALID_ARG;
     int sms = 0;
     st = device_state(&sms, nullptr);
