@@ -393,11 +393,15 @@ size_t pa_workspace_size_accumulate(const pa_shape* shape, int32_t q_len, int32_
  *                     former positions, ascending, -1 from new_lens[b] on
  * new_block_tables (and new_weights) may be block_tables (and weights)
  * themselves: the tokens then move down within their own pages, which no
- * other sequence may share.  Otherwise the new pages must not be among any
- * sequence's old ones, which stay as they were.  A kept token whose new entry
+ * other sequence may share.  Otherwise an entry of new_block_tables is the
+ * block of the same entry of block_tables (a copy of the table, or of its first
+ * columns: the tokens move down there too, more slowly), or a block that is not
+ * among any sequence's old ones; old blocks that are not among the new ones stay
+ * as they were.  A kept token whose new entry
  * is masked is not stored.  new_weights, new_lens and kept lie apart from each
  * other and from the inputs.  budget >= sink + recent, and
- * new_max_blocks_per_seq * block_size >= budget.  The num_heads and out_dtype
+ * new_max_blocks_per_seq * block_size >= budget; both tables reach at most 2^30
+ * tokens (PA_ERR_UNSUPPORTED).  The num_heads and out_dtype
  * of the shape are checked and not used.
  */
 pa_status pa_evict_kv(void* k_cache, void* v_cache, const float* weights,

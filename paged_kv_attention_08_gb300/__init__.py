@@ -673,7 +673,8 @@ def evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_ta
     accumulated ``weights`` ([B, Hkv, max_blocks * block_size] fp32, ties to
     the lowest index), moved in their order to the front of
     ``new_block_tables``' pages.  Passing ``block_tables`` / ``weights``
-    themselves as the new ones works in place; other tables must hold other
+    themselves as the new ones works in place (and so, more slowly, does a copy
+    of ``block_tables`` or of its first columns); other tables must hold other
     pages than any sequence's old ones.  ``kept`` (int32 [B, Hkv,
     budget]) receives the kept tokens' former positions, ``new_lens`` (int32
     [B]) the new lengths."""

@@ -30,6 +30,9 @@ constexpr int kMaxCached = 38 * 1024; // tokens whose keys fit in a CTA's shared
 // Keys of tokens that the selection does not weigh.
 constexpr uint32_t kKeyAlways = 0xffffffffu;  // kept whatever the weight
 constexpr uint32_t kKeyAbsent = 0u;           // of a masked page: never kept
+// In a kept token's position, between the selection and the copy: the new table
+// names a page of the old one at its own place.
+constexpr int32_t kMarked = INT32_MIN;
 
 // Integers that order as the weights do: NaN below every number, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -108,6 +111,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     // those that share the threshold's first digit
     __shared__ uint32_t shares[kMaxSelCluster][5];
     __shared__ uint32_t counted[2];
+    __shared__ int32_t mark;  // kMarked or 0
     const int tid = threadIdx.x, lane = tid & 31;
     const int C = (int)p.cluster, rank = (int)blockIdx.x % C;
     const int kvh = (int)blockIdx.x / C, b = blockIdx.y;
@@ -115,6 +119,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     for (int i = tid; i < kBins; i += kSelThreads) reinterpret_cast<uint4*>(hist)[i] = zeros;
     reinterpret_cast<uint4*>(sums)[tid] = zeros;
     if (tid < 2) counted[tid] = 0;
+    if (tid == 0) mark = 0;
     // (the others' adds may come from here on: every CTA waits for this before its first)
     if (C > 1) cluster_arrive_release();
     else __syncthreads();
@@ -125,6 +130,16 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     const float* w = p.weights + ((size_t)b * p.num_kv_heads + kvh) * p.max_blocks * p.block_size;
     int32_t* kept = p.kept + ((size_t)b * p.num_kv_heads + kvh) * p.budget;
     const int32_t* row = p.block_tables + (size_t)b * p.max_blocks;
+    // does the new table name a page of the old one at its own place (a copy of it)?
+    bool same = false;
+    if (!p.in_place) {
+        const int32_t* new_row = p.new_block_tables + (size_t)b * p.new_max_blocks;
+        const int pages = min((p.budget + p.block_size - 1) / p.block_size, p.max_blocks);
+        for (int i = tid; i < pages; i += kSelThreads) {
+            const int e = __ldg(new_row + i);
+            same |= e >= 0 && e == __ldg(row + i);
+        }
+    }
     const int npages = (T + p.block_size - 1) / p.block_size;
     const int bshift = __ffs(p.block_size) - 1;
     const int recent = T - p.recent;
@@ -179,6 +194,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         }
     };
     if (C > 1) cluster_wait_acquire();  // (also a barrier of the CTA: hist is zero)
+    if (same) mark = kMarked;
     for (int base = tid; base < nq; base += kSelThreads * 8) {
         float4 x[8];
         bool ok[8];
@@ -407,6 +423,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         left -= eq;
     }
     uint32_t j = begin + sure;  // plus the kept ones of the equal tokens before
+    const int32_t marks = mark;
     for (int i = i0; i < i1; i += 8) {
         uint32_t s = s0, e = e0;
         if (i > i0) masks(i, s, e);
@@ -414,10 +431,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
         for (uint32_t any = s | e; any; any &= any - 1) {
             const int u = __ffs(any) - 1;
             if ((s >> u) & 1u) {
-                kept[j + min(equal, left)] = t + u;
+                kept[j + min(equal, left)] = (t + u) | marks;
                 ++j;
             } else {
-                if (equal < left) kept[j + equal] = t + u;
+                if (equal < left) kept[j + equal] = (t + u) | marks;
                 ++equal;
             }
         }
@@ -443,6 +460,12 @@ constexpr int kCopyRows = 64;  // tokens of one kv head per CTA
 
 // One CTA per (64 tokens of the new row, kv head, sequence): 32 KB of keys and
 // values, eight 16-byte vectors of a thread on their way at a time.
+//
+// Where the selection found an entry that stands at the same place in both
+// tables (kept tokens carry kMarked), row j may be written over old token j,
+// which another CTA may have to read.  Then the first CTA moves all of the kv
+// head's rows in order: they come from old tokens kept[j] >= j, so that no row
+// comes from where an earlier one went.  The others only take the marks off.
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictParams p) {
     __shared__ long long src[kCopyRows], dst[kCopyRows];
     const int tid = threadIdx.x;
@@ -452,43 +475,61 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
     grid_launch_dependents();
     const size_t unit = (size_t)b * p.num_kv_heads + kvh;
     const int vecs = p.head_dim / 8;
-    if (tid < kCopyRows) {
-        const int j = j0 + tid;
-        const int t = j < p.budget ? p.kept[unit * p.budget + j] : -1;
+    const int32_t* old_row = p.block_tables + (size_t)b * p.max_blocks;
+    const int32_t* new_row = p.new_block_tables + (size_t)b * p.new_max_blocks;
+    // (volatile: a CTA that moves all rows reads entries while theirs take the marks off)
+    volatile int32_t* kept = p.kept + unit * p.budget;
+    // the old token that row j is, and where both of them lie (-1: nowhere)
+    auto place = [&](int j, bool& marked) {
+        int t = j < p.budget ? kept[j] : -1;
+        marked = t < -1;
+        if (marked) t &= ~kMarked;
         long long s = -1, d = -1;
         if (t >= 0) {
-            s = slot_of(p.block_tables + (size_t)b * p.max_blocks, t, p.block_size, p.max_blocks,
-                        p.num_blocks);
-            d = slot_of(p.new_block_tables + (size_t)b * p.new_max_blocks, j, p.block_size,
-                        p.new_max_blocks, p.num_blocks);
+            s = slot_of(old_row, t, p.block_size, p.max_blocks, p.num_blocks);
+            d = slot_of(new_row, j, p.block_size, p.new_max_blocks, p.num_blocks);
         }
         src[tid] = s;
         dst[tid] = d;
+        return t;
+    };
+    bool marked = false;
+    if (tid < kCopyRows) {
+        const int j = j0 + tid, t = place(j, marked);
+        if (marked) kept[j] = t;
         const size_t width = (size_t)p.max_blocks * p.block_size;
         const size_t new_width = (size_t)p.new_max_blocks * p.block_size;
         if ((size_t)j < new_width)
             p.new_weights[unit * new_width + j] = t >= 0 ? p.weights[unit * width + t] : 0.f;
     }
-    __syncthreads();
+    const bool in_order = __syncthreads_or(marked);
+    if (in_order && blockIdx.x > 0) return;
     const long long row = (long long)p.num_kv_heads * vecs;
     // eight vectors of a thread in flight at a time
     const int vshift = __ffs(vecs) - 1;  // (8, 16 or 32 vectors a head)
-    for (int i0 = tid; i0 < kCopyRows * 2 * vecs; i0 += kCopyThreads * 8) {
-        uint4 v[8];
+    for (int next = kCopyRows;; next += kCopyRows) {
+        for (int i0 = tid; i0 < kCopyRows * 2 * vecs; i0 += kCopyThreads * 8) {
+            uint4 v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int i = i0 + k * kCopyThreads, r = i >> (vshift + 1), c = i & (2 * vecs - 1);
-            if (r >= kCopyRows || src[r] < 0 || dst[r] < 0) continue;
-            const uint4* cache = static_cast<const uint4*>(c < vecs ? p.k_cache : p.v_cache);
-            v[k] = cache[src[r] * row + kvh * vecs + (c & (vecs - 1))];
-        }
+            for (int k = 0; k < 8; ++k) {
+                const int i = i0 + k * kCopyThreads, r = i >> (vshift + 1), c = i & (2 * vecs - 1);
+                if (r >= kCopyRows || src[r] < 0 || dst[r] < 0) continue;
+                const uint4* cache = static_cast<const uint4*>(c < vecs ? p.k_cache : p.v_cache);
+                v[k] = cache[src[r] * row + kvh * vecs + (c & (vecs - 1))];
+            }
+            if (in_order) __syncthreads();  // (as many turns in every thread)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int i = i0 + k * kCopyThreads, r = i >> (vshift + 1), c = i & (2 * vecs - 1);
-            if (r >= kCopyRows || src[r] < 0 || dst[r] < 0) continue;
-            uint4* cache = static_cast<uint4*>(c < vecs ? p.k_cache : p.v_cache);
-            cache[dst[r] * row + kvh * vecs + (c & (vecs - 1))] = v[k];
+            for (int k = 0; k < 8; ++k) {
+                const int i = i0 + k * kCopyThreads, r = i >> (vshift + 1), c = i & (2 * vecs - 1);
+                if (r >= kCopyRows || src[r] < 0 || dst[r] < 0) continue;
+                uint4* cache = static_cast<uint4*>(c < vecs ? p.k_cache : p.v_cache);
+                cache[dst[r] * row + kvh * vecs + (c & (vecs - 1))] = v[k];
+            }
         }
+        if (!in_order || next >= p.budget) return;
+        __syncthreads();  // these rows' places have been used
+        if (tid < kCopyRows) (void)place(next + tid, marked);  // (its own CTA takes a mark off)
+        __syncthreads();
     }
 }
 
@@ -608,6 +649,7 @@ __global__ void __launch_bounds__(kPackThreads, 1) evict_pack_kernel(const Evict
 }  // namespace
 
 cudaError_t launch_evict(EvictParams p, bool in_place, bool pdl, cudaStream_t stream) {
+    p.in_place = in_place ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

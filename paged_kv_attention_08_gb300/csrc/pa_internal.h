@@ -157,6 +157,7 @@ struct EvictParams {
     int32_t batch, num_kv_heads, head_dim, block_size, max_blocks, new_max_blocks;
     int32_t budget, sink, recent;
     int32_t cluster;          // CTAs that select one row together
+    int32_t in_place;         // the packing kernel moves the tokens, not the copying one
 };
 
 // Largest batch the balanced split handles (its per-sequence page counts live
