@@ -411,6 +411,14 @@ def _stream_on(dev: int, stream) -> int:
 _KV_CODE = {torch.float16: F16, torch.bfloat16: BF16}
 
 
+def _i32(x, name) -> int:
+    """A whole number of any kind (numpy's, a tensor's) as the C ABI's int32."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} {x} does not fit in 32 bits")
+    return x
+
+
 def _attention_shape(out, q, k_cache, v_cache, block_tables, context_lens):
     """Checks what ``_check_args`` checks; pa_shape and q_len of a one-token
     ([B, H, D]) or several-token ([B, Q, H, D]) query."""
@@ -586,7 +594,8 @@ def workspace_size_shared_prefix(q, k_cache, prefix_tables, block_tables, out_dt
     P, mpb = _check_prefixes(prefix_tables, shape.batch)
     with torch.cuda.device(dev):
         return int(_load().pa_workspace_size_shared_prefix(
-            shape, P, mpb, q_len, int(max_prefix_len), int(max_context_len)))
+            shape, P, mpb, q_len, _i32(max_prefix_len, "max_prefix_len"),
+            _i32(max_context_len, "max_context_len")))
 
 
 def decode_shared_prefix(out, q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables,
@@ -605,6 +614,9 @@ def decode_shared_prefix(out, q, k_cache, v_cache, prefix_tables, prefix_lens, b
         raise ValueError("prefix_lens must be [prefixes]")
     if prefix_lens.dtype != torch.int32:
         raise TypeError("prefix_lens must be int32")
+    scale = float(scale)
+    max_prefix_len = _i32(max_prefix_len, "max_prefix_len")
+    max_context_len = _i32(max_context_len, "max_context_len")
     dev = _device_of(k_cache)
     _same_device(dev, (out, q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables,
                        context_lens))
@@ -629,7 +641,8 @@ def workspace_size_accumulate(q, k_cache, block_tables, out_dtype, max_context_l
     """Bytes of workspace that ``decode_accumulate`` takes, on the tensors' device."""
     shape, q_len, dev = _sizing_shape(q, k_cache, block_tables, out_dtype)
     with torch.cuda.device(dev):
-        return int(_load().pa_workspace_size_accumulate(shape, q_len, int(max_context_len)))
+        return int(_load().pa_workspace_size_accumulate(
+            shape, q_len, _i32(max_context_len, "max_context_len")))
 
 
 def decode_accumulate(out, new_weights, q, k_cache, v_cache, block_tables, context_lens,
@@ -647,6 +660,7 @@ def decode_accumulate(out, new_weights, q, k_cache, v_cache, block_tables, conte
         raise ValueError(f"weights and new_weights must be {want}")
     if weights.dtype != torch.float32 or new_weights.dtype != torch.float32:
         raise TypeError("weights and new_weights must be float32")
+    scale, max_context_len = float(scale), _i32(max_context_len, "max_context_len")
     dev = _device_of(k_cache)
     _same_device(dev, (out, q, k_cache, v_cache, block_tables, context_lens, weights, new_weights))
     if dev != torch.cuda.current_device():
@@ -705,6 +719,7 @@ def evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_ta
     if block_tables.dtype != i32 or context_lens.dtype != i32 or new_block_tables.dtype != i32 or \
             new_lens.dtype != i32 or kept.dtype != i32:
         raise TypeError("block tables, lengths and kept must be int32")
+    sink, recent = _i32(sink, "sink"), _i32(recent, "recent")
     dev = _device_of(k_cache)
     _same_device(dev, (k_cache, v_cache, weights, block_tables, context_lens, new_block_tables,
                        new_weights, new_lens, kept))
