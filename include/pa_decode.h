@@ -359,7 +359,8 @@ size_t pa_workspace_size_shared_prefix(const pa_shape* shape, int32_t num_prefix
  *   weights_in, weights_out  [batch, num_kv_heads, max_blocks_per_seq * block_size]
  *                            fp32; may be the same array, else apart
  * Tokens past max_context_len's last page are left out of the attention and keep
- * their weights.  Weights are fp32; each is summed over the rows by one thread in a fixed order,
+ * their weights; the tables reach at most 2^30 tokens (PA_ERR_UNSUPPORTED).
+ * Weights are fp32; each is summed over the rows by one thread in a fixed order,
  * so that equal calls give equal bits.  The other arguments are those
  * of pa_decode_multi with an automatic split; the workspace must hold
  * pa_workspace_size_accumulate(...) bytes.

@@ -1676,6 +1676,8 @@ pa_status pa_decode_accumulate(void* out, float* weights_out, const float* weigh
     if (st != PA_OK) return st;
     if (q_len < 1 || !scale_ok(scale) || max_context_len < 0) return PA_ERR_INVALID_ARG;
     if ((int64_t)q_len * shape->num_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    // the loops over a row of weights stay inside 31 bits, a CTA's step past its end included
+    if ((int64_t)shape->max_blocks_per_seq * shape->block_size > (1 << 30)) return PA_ERR_UNSUPPORTED;
     if (shape->batch == 0) return PA_OK;
     st = check_ptrs(out, q, k_cache, v_cache, block_tables, context_lens);
     if (st != PA_OK) return st;

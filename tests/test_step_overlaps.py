@@ -1,4 +1,4 @@
-"""Outputs of pa.rope_append_kv that lie over its inputs: refused at the C ABI
+"""Outputs of pa.rope_append_kv that lie over its inputs, and rows of weights too long: refused at the C ABI
 (CPU: every call is built to fail its checks) and in the binding; slices of one
 buffer that do not meet are taken."""
 import ctypes
@@ -52,6 +52,15 @@ def test_rope_refuses_queries_in_the_caches(lib):
     cache = 32 * 16 * KV_ROW * 2
     for at in (KC, KC + cache - 16, VC + 4096, VC - 2 * ROW * TOKENS + 16):
         assert call(lib, at) == 1
+
+
+def test_accumulate_refuses_rows_of_weights_past_30_bits(lib):
+    def at(blocks):
+        s = pa._Shape(1, 8, 2, 64, 16, blocks, 32, pa.F16, pa.F32)
+        return lib.pa_decode_accumulate(Q, K, V, Q, KC, VC, REST, REST, ctypes.byref(s), 1, 0.1, 64, None, 0,
+                                        None)
+
+    assert at((1 << 26) + 1) == 2 and at((1 << 27) - 1) == 2
 
 
 @pytest.mark.gpu
