@@ -258,7 +258,7 @@ bool take_lane(cudaStream_t cs, Lane* lane) {
         }
     }
     (void)cudaThreadExchangeStreamCaptureMode(&mode);
-    if (!found) (void)cudaGetLastError();
+    (void)cudaGetLastError();  // (a lane still busy is no error of this call)
     return found;
 }
 
