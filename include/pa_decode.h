@@ -36,7 +36,11 @@
  *   - a sequence with no attended token gets an all-zero output row.
  *
  * Arithmetic: scores, the online softmax (running max m and normaliser l) and
- * the value accumulation are fp32; K/V/q are fp16 or bf16.  `scale` must be
+ * the value accumulation are fp32; K/V/q are fp16 or bf16.  On the way into the
+ * product with V a weight is held in two 16-bit parts, on the tile kernel (below)
+ * fp16's in one, rounded to 11 bits.  fp16 weights under 2^-25 of the row's
+ * largest count as 0 there, in pa_decode_shared_prefix and pa_decode_accumulate
+ * those under 2^-32.  `scale` must be
  * finite and > 0 (PA_ERR_INVALID_ARG otherwise).
  *
  * Calls.  All entry points validate on the host and either launch work on

@@ -81,6 +81,7 @@ enum SegOut { kOutFinal = 0, kOutPartial = 1, kOutCluster = 2, kOutRecord = 3 };
 // PRE: a shared prefix (p.prefix_tables) in front of each sequence's own pages,
 // read by each of its sequences: one launch where little is to be read (in the
 // EXT instantiations it cost 128 sequences behind 65,536 tokens 4 %).
+// In both, fp16's P stands 2^kHalfLift higher (pa_internal.h).
 template <int D, int BS, typename KV, bool MULTI, bool EXT = false, bool PRE = false>
 __global__ void __launch_bounds__(256, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -89,6 +90,8 @@ __global__ void __launch_bounds__(256, 1)
     constexpr int DS = C::DS, DW = C::DW, KSTEPS = C::KSTEPS, NT = C::NT, PKS = C::PKS;
     constexpr int ONT = C::ONT, DBLK = C::DBLK;
     constexpr float NEG_INF = -INFINITY;
+    // m: the row maximum less this
+    constexpr float kLift = (EXT || PRE) && std::is_same<KV, __half>::value ? kHalfLift : 0.f;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -365,11 +368,11 @@ __global__ void __launch_bounds__(256, 1)
                 mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 2));
                 const float ms0 = mx0 * qscale, ms1 = mx1 * qscale;
-                const bool need = (real0 && ms0 > m0 + kRescaleSlack) ||
-                                  (real1 && ms1 > m1 + kRescaleSlack);
+                const bool need = (real0 && ms0 > m0 + (kRescaleSlack + kLift)) ||
+                                  (real1 && ms1 > m1 + (kRescaleSlack + kLift));
                 if (__any_sync(kFullMask, need)) {
-                    const float n0 = real0 ? fmaxf(m0, ms0) : m0;
-                    const float n1 = real1 ? fmaxf(m1, ms1) : m1;
+                    const float n0 = real0 ? fmaxf(m0, ms0 - kLift) : m0;
+                    const float n1 = real1 ? fmaxf(m1, ms1 - kLift) : m1;
                     const float a0 = (n0 == m0) ? 1.f : fast_exp2(m0 - n0);
                     const float a1 = (n1 == m1) ? 1.f : fast_exp2(m1 - n1);
                     m0 = n0;

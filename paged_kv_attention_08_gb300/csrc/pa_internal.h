@@ -323,13 +323,14 @@ __host__ __device__ constexpr uint32_t tile_tmem_cols(int D) {
     return (uint32_t)D + kTileSBufs * tile_block_tokens(D) <= 256u ? 256u : 512u;
 }
 
-// fp16 weights in one part: P = 2^(s - m) with m the row's maximum less kHalfLift, so
-// that P is 2^7 at the maximum and, before a rescale, at most 2^15 (fp16 ends at
-// 2^16).  With P = 1 there, tokens 14 bits below the largest weight fell out of
-// fp16's normal range and those 25 bits below it vanished, whose sum can be the
-// whole output: behind a token of no value 26 bits above them, two thirds of it and
-// more.  Now those begin 21 and 32 bits down: 64K tokens that vanish are 2^-16 of
-// the row, under the weights' own rounding (2^-12).
+// fp16 weights, in one part or two: P = 2^(s - m) with m the row's maximum less
+// kHalfLift, so that P is 2^7 at the maximum and, before a rescale, at most 2^15
+// (fp16 ends at 2^16).  With P = 1 there, tokens 14 bits below the largest weight
+// fell out of fp16's normal range and those 25 bits below it vanished, whose sum
+// can be the whole output: behind tokens of no value 26 bits above the rest,
+// outputs were up to 38 times their bound off.  Now those begin 21 and 32 bits
+// down: 64K tokens that vanish are 2^-16 of the row, under the weights' own
+// rounding in one part (2^-12).
 constexpr float kHalfLift = 7.0f;
 
 // Two-tile kernel (pa_pair.cuh): 256 rows to a CTA, KV blocks of 128 tokens, up

@@ -1,5 +1,5 @@
-"""GPU tests of fp16 attention weights far below the row's largest, through the
-kernels that hold the weights in fp16 for the product with V: tokens of no
+"""GPU tests of fp16 attention weights far below the row's largest, which the
+kernels hold in fp16 (in one part or two) for the product with V: tokens of no
 value (a sink) that outweigh the others by 20 to 26 bits, so that the output
 is made of weights near the end of fp16's range."""
 import math
@@ -63,6 +63,11 @@ def checked(got, q, groups, scale, rel):
     (9, 2, 16, 1, 256, 32, 1500, 30, 1 << 20),
     (3, 40, 8, 2, 128, 16, 300, 900, 1 << 20),     # the own rows on the tile kernel
     (2, 80, 16, 4, 64, 16, 300, 900, 1 << 20),     # or two tiles to a CTA (wide own tables)
+    (4, 1, 32, 8, 128, 16, 1500, 40, 1500),        # the warp-level kernel: one launch
+    (3, 3, 8, 2, 64, 32, 700, 90, 700),
+    (2, 1, 8, 1, 256, 16, 900, 30, 900),
+    (3, 1, 8, 2, 128, 16, 900, 500, 1 << 20),      # launches of their own
+    (2, 2, 4, 4, 64, 16, 900, 500, 1 << 20),
 ])
 def test_shared_prefix(n, Q, H, Hkv, D, bs, plen, own, announced, bits):
     dtype, scale = torch.float16, D ** -0.5
@@ -81,7 +86,7 @@ def test_shared_prefix(n, Q, H, Hkv, D, bs, plen, own, announced, bits):
                      for c in (kc, vc)]
             seen = torch.arange(plen + lens[b]) < ends[b].repeat_interleave(H // Hkv)[:, None]
             groups[-1].append((torch.cat(parts[0]), torch.cat(parts[1]), seen))
-    wide = torch.full((1, announced // bs), -1, dtype=torch.int32)
+    wide = torch.full((1, (announced + bs - 1) // bs), -1, dtype=torch.int32)
     wide[:, :ptable.shape[1]] = ptable
     max_own = max(lens)
     if Q == 80:
@@ -105,6 +110,10 @@ def test_shared_prefix(n, Q, H, Hkv, D, bs, plen, own, announced, bits):
     (40, 10, 8, 2, 128, 16, [100 + 10 * b for b in range(40)]),    # one pass
     (1, 1, 16, 1, 256, 32, [3000]),                                # a compact tile
     (1, 20, 8, 1, 256, 16, [2500]),
+    (1, 1, 32, 8, 128, 16, [1500]),                                # the warp-level kernel
+    (3, 3, 8, 2, 64, 32, [900, 40, 300]),
+    (70, 1, 8, 2, 64, 16, [200 + b for b in range(70)]),
+    (1, 1, 8, 2, 128, 16, [20000]),
 ])
 def test_accumulate(B, Q, H, Hkv, D, bs, lens, bits):
     dtype, scale = torch.float16, D ** -0.5
