@@ -1015,8 +1015,9 @@ pa_status launch_tile(void* out, const void* q, const void* k, const void* v, co
 // Whether a tile plan's rows go two tiles to a CTA (pa_pair.cuh): units of more
 // than one tile that give every SM a few blocks.  With fewer, half as many CTAs
 // for the same rows cost more than their faster blocks save (256 rows of 8 kv
-// heads: prefixes of 4096 tokens, 1.7 blocks an SM, 33.5 us against 30.6 with a
-// tile to a CTA; of 16,384 tokens, 6.7 blocks, 50.3 against 56.1).
+// heads, us against a tile to a CTA: prefixes of 4096 tokens, 1.7 blocks an SM, 36.5
+// and 33.6; of 8192, 3.4 blocks, 43.2 and 39.0 alone, but 50.6 and 55.6 beside 64
+// sequences of up to 1024 own tokens; of 16,384, 6.7 blocks, 51.4 and 54.5).
 bool use_pair(const pa_shape* s, const Plan& p, int64_t rows, int pages, int sms) {
     if (!p.tile || p.balanced || s->head_dim > 128 || rows <= kTileRows) return false;
     const int64_t units = (int64_t)s->batch * s->num_kv_heads * ((rows + 2 * kTileRows - 1) / (2 * kTileRows));
@@ -1064,11 +1065,12 @@ pa_status check_prefix(const pa_shape* s, int32_t num_prefixes, int32_t max_pref
 
 // Bytes of keys and values up to which every sequence of a shared-prefix call
 // reads the prefix itself, in one launch instead of three (8 kv heads of 128, own
-// 64 tokens, us, one launch against three: 4 sequences behind 992 tokens, 16 MB, 8.9 and
-// 14.7; 8 behind 2000, 64 MB, 14.6 and 23.4; 64 behind 256, 80 MB, 19.5 and 22.9; 16
-// behind 2000, 129 MB, 22.0 and 24.8; 128 behind 192, 160 MB, 37.0 and 35.2; 4 behind
-// 16,000, 251 MB, 36.2 and 25.5).
-constexpr int64_t kJoinedBytes = 96ll << 20;
+// 64 tokens, us of calls in a row and of a graph of them, one launch against three:
+// 4 sequences behind 992 tokens, 16 MB, 11.9 (8.2) and 21.4 (14.2); 8 behind 2000, 64 MB,
+// 15.9 (14.1) and 26.7 (23.1); 64 behind 400, 116 MB, 24.6 (23.2) and 28.9 (23.9); 128
+// behind 192, 128 MB, 31.8 (30.2) and 34.6 (30.0); 32 behind 2048 with 8 heads of 64, 132
+// MB, 28.2 (26.6) and 26.4 (22.5); 4 behind 16,000, 251 MB, 38.9 (37.1) and 28.4 (23.6)).
+constexpr int64_t kJoinedBytes = 128ll << 20;
 
 pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
                       int32_t max_prefix_len, int32_t max_context_len, int sms, PrefixPlan* pp) {
@@ -1128,7 +1130,7 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
     };
     if (own_part.p.tile) {
         // few blocks are not worth another CTA's start and end (64 units of 300
-        // tokens at head_dim 256: 41.4 us for the call with one partition, 46.0 with two)
+        // tokens at head_dim 256: 46.0 us for the call with one partition, 49.3 with two)
         own_part.parts = std::max<int64_t>(
             1, std::min<int64_t>(own_part.slots / own_part.units, own_part.pages / (8 * block_pages)));
     } else if (own_part.units > own_part.slots) {
@@ -1145,11 +1147,12 @@ pa_status plan_prefix(const pa_shape* s, const pa_shape* pre, int32_t q_len,
         // three times as long as with a CTA to every slot: an announced length may be
         // a loose bound (128 sequences announced with 131,072 own tokens each:
         // without that, 16 CTAs of 1.5 ms).  Two tiles to a CTA, calls in a
-        // row: 8 units of 8191 tokens beside 64 sequences of up to 1024 take 49.9,
-        // 46.0, 48.5, 51.3 us with 5, 6, 7, 8 partitions; 16 units of 65536 beside 128
-        // of up to 2048 take 287, 249, 244 us with 6, 7, 8 (alone 260, 265, 267).  With
-        // one tile to a CTA the first took 50.0 us with 4 partitions of 16 units and 57.5
-        // with 9, the second 255 with 4 of 32 and 279 with 3.
+        // row: 8 units of 8191 tokens beside 64 sequences of up to 1024 take 55.2,
+        // 50.6, 52.9, 53.9 us with 5, 6, 7, 8 partitions; 16 units of 65536 beside 128
+        // of up to 2048 take 244, 242, 243, 246 us with 6, 7, 8, 9.  With one tile to a
+        // CTA the first takes 55.6 us with 4 partitions of 16 units and 59.5 with 9, the
+        // second 256 with 4 of 32 and 264 with 3; 32 units of 4100 at head_dim 256 take
+        // 61.0, 47.9, 46.1 us with 2, 3, 4.
         const double own_us =
             own_part.p.tile ? own_part.units * own_part.parts * tile_us(own_part, own_part.parts)
                             : (double)own_part.units * own_part.pages * s->block_size * s->head_dim * 2.0 / 33e3;

@@ -20,8 +20,8 @@
 // Bound: no one unit.  A block of two tiles takes 5300 cycles, of which the MMAs
 // (bf16: 48 of 64 cycles) are 58 % and the exponentials (16 a cycle) 39 %; the
 // rest is a tile's own chain.  512 rows of 8 kv heads of 128 on a prefix of 65,536
-// (152 SMs, with the join): bf16 180 us, 765 TFLOP/s, fp16 145 us, 946 (a tile to a CTA:
-// 203 and 156).  Also measured, bf16: P in two pieces 192; both tiles in step 186;
+// (152 SMs, with the join): bf16 183 us, 752 TFLOP/s, fp16 146 us, 940 (a tile to a CTA:
+// 197 and 154).  Also measured, bf16: P in two pieces 192; both tiles in step 186;
 // each waiting for the other's first piece 240; one issuer for both, taking
 // whichever is ready, 251; two threads to a row 190.
 #pragma once

@@ -17,7 +17,7 @@ DEV = "cuda:0"
     (4, 3, 8, 2, 900, 70, 200, 20, False),
     (60, 1, 32, 8, 120, 40, 30, 20, False),        # one launch, one pass
     (2, 5, 4, 2, 300, 300, 512, 100, False),
-    (128, 1, 16, 8, 900, 70, 200, 20, True),       # launches of their own, warp-level
+    (160, 1, 16, 8, 900, 70, 200, 20, True),       # launches of their own, warp-level
     (5, 5, 8, 2, 900, 400, 200, 100, True),        # the tile kernel
     (140, 1, 32, 8, 3000, 90, 2500, 33, True),     # two tiles to a CTA
 ])
