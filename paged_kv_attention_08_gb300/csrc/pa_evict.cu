@@ -14,7 +14,8 @@
 //
 // Bound: memory (the weights are read, each kept row is read and written).
 // Four sequences of 65,000 to 131,072 tokens, 8 kv heads of 128, cut to 8192 each:
-// 79 us to other pages (selection 26, copy 47 at 5.7 TB/s), 142 us in place.
+// 81 us to other pages (selection 27, copy 48 at 5.6 TB/s), 144 us in place, 0.6 ms
+// with a copy of the table.
 #include "pa_device.cuh"
 
 namespace pa {
@@ -96,7 +97,7 @@ __device__ __forceinline__ int quad_word(int q) { return q * 4 + (q >> 3) * 4; }
 //
 // What bounds it: the latency of its steps (a cluster barrier 1 to 2 us with
 // the skew of its CTAs), not the 17 MB that 32 rows of 128K weights are.  The
-// 32 rows of up to 131,072 tokens take 26 us; one CTA to a row, reading the row
+// 32 rows of up to 131,072 tokens take 27 us; one CTA to a row, reading the row
 // from global memory in four passes of 8 bits, took 460 us, and a cluster
 // whose CTAs read each other's whole bins 37 us.
 template <bool CACHED>
