@@ -288,7 +288,8 @@ typedef struct pa_rope {
  * table entry is masked, is turned into q_out and writes nothing to the cache.
  *   q, q_out          [batch, q_len, num_heads, head_dim]     kv_dtype (q_out may be q,
  *                     with its stride; else none of its rows meets one of q, k_new,
- *                     v_new or the caches: PA_ERR_INVALID_ARG where they do)
+ *                     v_new or the caches: PA_ERR_INVALID_ARG where they do, or
+ *                     where arrays of different strides share a range)
  *   k_new, v_new      [batch, q_len, num_kv_heads, head_dim]  kv_dtype
  *   rotary_positions  [num_axes, batch, q_len]  int32, any value
  *   phases            [rotary_dim / 2]  int64: f_j / (2 pi) * 2^64, modulo 2^64

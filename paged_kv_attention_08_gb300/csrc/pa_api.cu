@@ -212,6 +212,32 @@ bool capture_of(cudaStream_t s, bool* active, unsigned long long* id) {
     return st != cudaStreamCaptureStatusInvalidated;
 }
 
+void keep_lane(int dev, const Lane& lane) {
+    try {
+        std::lock_guard<std::mutex> lock(g_lane_mutex);
+        g_lanes[dev].push_back(lane);
+    } catch (...) {  // no memory for the list: the lane is not used again
+    }
+}
+
+// A kept lane that fits a call on `cs`, under capture `id` or not.
+bool find_lane(int dev, cudaStream_t cs, bool active, unsigned long long id, Lane* lane) {
+    std::lock_guard<std::mutex> lock(g_lane_mutex);
+    std::vector<Lane>& kept = g_lanes[dev];
+    for (size_t i = kept.size(); i-- > 0;) {
+        bool lane_active = false;
+        unsigned long long lane_id = 0;
+        if (!capture_of(kept[i].stream, &lane_active, &lane_id)) continue;
+        if (lane_active ? !(active && lane_id == id && kept[i].served == cs)
+                        : kept[i].served != cs && cudaStreamQuery(kept[i].stream) != cudaSuccess)
+            continue;
+        *lane = kept[i];
+        kept.erase(kept.begin() + (long)i);
+        return true;
+    }
+    return false;
+}
+
 // A lane of the current device forked from `cs`; false: none, nothing was done.
 bool take_lane(cudaStream_t cs, Lane* lane) {
     // (a query or creation must not touch a capture that another thread has under way)
@@ -222,21 +248,7 @@ bool take_lane(cudaStream_t cs, Lane* lane) {
     unsigned long long id = 0;
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices &&
         capture_of(cs, &active, &id)) {
-        {
-            std::lock_guard<std::mutex> lock(g_lane_mutex);
-            std::vector<Lane>& free = g_lanes[dev];
-            for (size_t i = free.size(); i-- > 0 && !found;) {
-                bool lane_active = false;
-                unsigned long long lane_id = 0;
-                if (!capture_of(free[i].stream, &lane_active, &lane_id)) continue;
-                if (lane_active ? !(active && lane_id == id && free[i].served == cs)
-                                : free[i].served != cs && cudaStreamQuery(free[i].stream) != cudaSuccess)
-                    continue;
-                *lane = free[i];
-                free.erase(free.begin() + (long)i);
-                found = true;
-            }
-        }
+        found = find_lane(dev, cs, active, id, lane);
         if (!found) {
             *lane = Lane();
             found = cudaStreamCreateWithFlags(&lane->stream, cudaStreamNonBlocking) == cudaSuccess &&
@@ -252,10 +264,7 @@ bool take_lane(cudaStream_t cs, Lane* lane) {
         lane->served = cs;
         found = cudaEventRecord(lane->fork, cs) == cudaSuccess &&
                 cudaStreamWaitEvent(lane->stream, lane->fork, 0) == cudaSuccess;
-        if (!found) {
-            std::lock_guard<std::mutex> lock(g_lane_mutex);
-            g_lanes[dev].push_back(*lane);
-        }
+        if (!found) keep_lane(dev, *lane);
     }
     (void)cudaThreadExchangeStreamCaptureMode(&mode);
     (void)cudaGetLastError();  // (a lane still busy is no error of this call)
@@ -267,10 +276,7 @@ bool join_lane(cudaStream_t cs, const Lane& lane) {
     const bool ok = cudaEventRecord(lane.join, lane.stream) == cudaSuccess &&
                     cudaStreamWaitEvent(cs, lane.join, 0) == cudaSuccess;
     int dev = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) {
-        std::lock_guard<std::mutex> lock(g_lane_mutex);
-        g_lanes[dev].push_back(lane);
-    }
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) keep_lane(dev, lane);
     return ok;
 }
 

@@ -10,8 +10,9 @@ namespace pa {
 
 // One thread per four neighbouring tokens of a kv head.  Bound: memory, 4 bytes
 // per (row, token) and 8 per token: 4 rows of 1M (token, kv head) pairs, 25 MB, in
-// 10.7 us cold, 14.0 with the combine of 1024 rows in the same launch.  The scores are stored in fp32, as they were formed.  (Reading
-// the keys again instead took 79 us there, and 135 us for 2M pairs.)
+// 10.7 us cold, 14.0 with the combine of 1024 rows in the same launch.  The scores
+// are stored in fp32, as they were formed.  (Reading the keys again instead took 79
+// us there, and 135 us for 2M pairs.)
 constexpr int kSThreads = 256;
 // Tokens that a CTA of kSThreads threads takes.
 constexpr int kSTokens = kSThreads * 4;

@@ -1,6 +1,6 @@
-"""Outputs of pa.rope_append_kv that lie over its inputs, and rows of weights too long: refused at the C ABI
-(CPU: every call is built to fail its checks) and in the binding; slices of one
-buffer that do not meet are taken."""
+"""Outputs of pa.rope_append_kv that lie over its inputs, and rows of weights that
+are too long: refused at the C ABI (CPU: every call is built to fail its checks) and
+in the binding; slices of one buffer that do not meet are taken."""
 import ctypes
 
 import pytest
