@@ -411,10 +411,14 @@ def _stream_on(dev: int, stream) -> int:
 _KV_CODE = {torch.float16: F16, torch.bfloat16: BF16}
 
 
+_2_31 = 1 << 31
+
+
 def _i32(x, name) -> int:
-    """A whole number of any kind (numpy's, a tensor's) as the C ABI's int32."""
+    """A whole number of any kind (numpy's, a tensor's) as the C ABI's int32.
+    (The calls of a step test for a plain one themselves.)"""
     x = int(x)
-    if not -0x80000000 <= x <= 0x7fffffff:
+    if not -_2_31 <= x < _2_31:
         raise ValueError(f"{name} {x} does not fit in 32 bits")
     return x
 
@@ -614,9 +618,12 @@ def decode_shared_prefix(out, q, k_cache, v_cache, prefix_tables, prefix_lens, b
         raise ValueError("prefix_lens must be [prefixes]")
     if prefix_lens.dtype != torch.int32:
         raise TypeError("prefix_lens must be int32")
-    scale = float(scale)
-    max_prefix_len = _i32(max_prefix_len, "max_prefix_len")
-    max_context_len = _i32(max_context_len, "max_context_len")
+    if type(max_prefix_len) is not int or not -_2_31 <= max_prefix_len < _2_31:
+        max_prefix_len = _i32(max_prefix_len, "max_prefix_len")
+    if type(max_context_len) is not int or not -_2_31 <= max_context_len < _2_31:
+        max_context_len = _i32(max_context_len, "max_context_len")
+    if type(scale) is not float:
+        scale = float(scale)
     dev = _device_of(k_cache)
     _same_device(dev, (out, q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables,
                        context_lens))
@@ -660,7 +667,10 @@ def decode_accumulate(out, new_weights, q, k_cache, v_cache, block_tables, conte
         raise ValueError(f"weights and new_weights must be {want}")
     if weights.dtype != torch.float32 or new_weights.dtype != torch.float32:
         raise TypeError("weights and new_weights must be float32")
-    scale, max_context_len = float(scale), _i32(max_context_len, "max_context_len")
+    if type(max_context_len) is not int or not -_2_31 <= max_context_len < _2_31:
+        max_context_len = _i32(max_context_len, "max_context_len")
+    if type(scale) is not float:
+        scale = float(scale)
     dev = _device_of(k_cache)
     _same_device(dev, (out, q, k_cache, v_cache, block_tables, context_lens, weights, new_weights))
     if dev != torch.cuda.current_device():
@@ -719,7 +729,10 @@ def evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_ta
     if block_tables.dtype != i32 or context_lens.dtype != i32 or new_block_tables.dtype != i32 or \
             new_lens.dtype != i32 or kept.dtype != i32:
         raise TypeError("block tables, lengths and kept must be int32")
-    sink, recent = _i32(sink, "sink"), _i32(recent, "recent")
+    if type(sink) is not int or not -_2_31 <= sink < _2_31:
+        sink = _i32(sink, "sink")
+    if type(recent) is not int or not -_2_31 <= recent < _2_31:
+        recent = _i32(recent, "recent")
     dev = _device_of(k_cache)
     _same_device(dev, (k_cache, v_cache, weights, block_tables, context_lens, new_block_tables,
                        new_weights, new_lens, kept))
