@@ -417,6 +417,137 @@ pa_status pa_evict_kv(void* k_cache, void* v_cache, const float* weights,
                       int32_t budget, int32_t sink, int32_t recent, void* stream);
 
 /*
+ * The 8-bit cache: keys and values as e4m3 floats with an fp32 scale for each
+ * page and kv head, half the bytes of the 16-bit cache.
+ *   k_cache, v_cache    [num_blocks, block_size, num_kv_heads, head_dim]  e4m3 codes (1 byte)
+ *   k_scales, v_scales  [num_blocks, num_kv_heads]  fp32
+ * A cached key is k_scales[block][kvh] * code, and a value likewise.
+ *
+ * pa_rope_append_kv8 is pa_rope_append_kv into that cache: queries and keys turn
+ * in the same way, and the turned keys and the values (in fp32, rounded once)
+ * become codes.  For each page that the call's tokens fall into, and each kv
+ * head, with amax the largest finite magnitude among the call's tokens of the
+ * page,
+ *   s_new = the smallest power of two with amax <= 448 s_new, in [2^-60, 2^60],
+ *   s     = s_new where the page's slot 0 is among the call's tokens,
+ *           else max(s_old, s_new), s_old the scale that the page has;
+ * codes are x / s rounded to nearest even; where s > s_old the page's slots before the
+ * call's tokens are rounded anew, as code * s_old / s (for powers of two
+ * exact but below 2^-6).  Slots behind the call's tokens stay as they are.
+ * Infinities and magnitudes past 448 * 2^60 become NaN, NaN stays NaN.  A page
+ * that takes tokens belongs to one sequence of the call.
+ * shape->kv_dtype is the dtype of q, q_out, k_new and v_new; the other
+ * arguments, the strides of `rope` and what q_out may lie over are as for
+ * pa_rope_append_kv, and q_out lies apart from the scales too.
+ */
+pa_status pa_rope_append_kv8(void* q_out, void* k_cache, void* v_cache, float* k_scales,
+                             float* v_scales, const void* q, const void* k_new, const void* v_new,
+                             const int32_t* rotary_positions, const int64_t* phases,
+                             const int32_t* axes, const int32_t* block_tables,
+                             const int32_t* context_lens, const pa_shape* shape, int32_t q_len,
+                             const pa_rope* rope, void* stream);
+
+/*
+ * pa_decode_multi (q_len = 1: pa_decode_splitkv) over the 8-bit cache, with the
+ * same masking and an automatic split.  Codes are widened exactly; the scores,
+ * the softmax and the sums are fp32, and the weights that meet the values are
+ * held in two fp16 parts.  Scales are finite and positive, whoever wrote them;
+ * v_scales outside [2^-60, 2^60] count as the nearer limit.  Scales of pages
+ * that hold no attended token are not used.  shape->kv_dtype is
+ * the dtype of q, shape->out_dtype fp32 or that.  Tokens past
+ * max_context_len's last page are left out whatever the plan.  out lies apart from the
+ * other arguments (PA_ERR_INVALID_ARG).  The workspace must hold
+ * pa_workspace_size_kv8(...) bytes (device, 16-byte aligned, free again once
+ * the stream has passed the call).
+ */
+pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                        const int32_t* context_lens, const pa_shape* shape, int32_t q_len,
+                        float scale, int32_t max_context_len, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of pa_decode_kv8 on the current device (0 where it needs none,
+ * for invalid arguments or without a device; SIZE_MAX when no size_t holds it). */
+size_t pa_workspace_size_kv8(const pa_shape* shape, int32_t q_len, int32_t max_context_len);
+
+/*
+ * The latent cache: one vector a token for all heads, whose first latent_dim
+ * elements are both the key's first part and the value, followed by the key's
+ * positional part of rope_dim elements.
+ *   cache  [num_blocks, block_size, latent_dim + rope_dim]  dtype
+ * latent_dim in {128, 256, 512}, rope_dim 64, block_size in {16, 32, 64}, any
+ * num_heads up to 65535.
+ */
+typedef struct pa_latent_shape {
+    int32_t batch;              /* B >= 0 (B = 0 launches nothing) */
+    int32_t num_heads;          /* H >= 1 */
+    int32_t latent_dim;
+    int32_t rope_dim;
+    int32_t block_size;
+    int32_t max_blocks_per_seq; /* columns of block_tables */
+    int64_t num_blocks;         /* < 2^31 */
+    int32_t dtype;              /* PA_F16 or PA_BF16: q, out, cache, new vectors, norm weight */
+    int32_t reserved;           /* 0 */
+} pa_latent_shape;
+
+/* Norm and rotary embedding of pa_rope_append_latent.  Strides in elements,
+ * multiples of 8: between the tokens of the flattened [batch * q_len] order and
+ * between the heads of a token (>= rope_dim; a token's stride spans its heads). */
+typedef struct pa_latent_rope {
+    int32_t interleaved;  /* 0: pair j is elements (j, j + 32); 1: (2j, 2j + 1) */
+    float eps;            /* >= 0, finite */
+    int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    int64_t new_stride;   /* >= latent_dim + rope_dim */
+} pa_latent_rope;
+
+/*
+ * Append to the latent cache.  The latent part x of each new token becomes
+ *   y = x / sqrt(mean(x^2) + eps) * norm_weight
+ * (fp32, rounded once; norm_weight NULL: x as it is), its positional part and
+ * that of every query head turn by the angle rotary_positions[b][i] * f_j per
+ * pair, as in pa_rope_append_kv; the token's vector goes to cache position
+ * context_lens[b] - q_len + i of sequence b (tokens without a slot store nothing)
+ * and the turned queries to q_out.
+ *   q, q_out          [batch, q_len, num_heads, rope_dim]   views with strides; q_out may be q
+ *                     (same strides); else their rows lie apart from each other, from
+ *                     latent_new's and from the cache: PA_ERR_INVALID_ARG where rows
+ *                     meet, or where arrays of different token strides share a range
+ *   latent_new        [batch, q_len, latent_dim + rope_dim]
+ *   norm_weight       [latent_dim]
+ *   rotary_positions  [batch, q_len]  int32, any value
+ *   phases            [rope_dim / 2]  int64, as for pa_rope_append_kv
+ */
+pa_status pa_rope_append_latent(void* q_out, void* cache, const void* q, const void* latent_new,
+                                const void* norm_weight, const int32_t* rotary_positions,
+                                const int64_t* phases, const int32_t* block_tables,
+                                const int32_t* context_lens, const pa_latent_shape* shape,
+                                int32_t q_len, const pa_latent_rope* rope, void* stream);
+
+/*
+ * Attention over the latent cache (the absorbed form: the up-projections of
+ * keys and values are applied to the query before and to the output after):
+ *   out[b, i, h, :] = sum_t softmax_t(scale * q[b, i, h, :] . c_t) * c_t[: latent_dim]
+ * over the tokens t <= context_lens[b] - q_len + i that the table reaches,
+ * with the masking of pa_decode_multi.
+ *   q    [batch, q_len, num_heads, latent_dim + rope_dim]
+ *   out  [batch, q_len, num_heads, latent_dim], apart from the other arguments
+ * Scores, softmax and sums are fp32; the weights that meet the values are
+ * rounded to the cache's dtype, and the normaliser sums the rounded ones.
+ * Tokens past max_context_len's last page are left out.  The workspace must
+ * hold pa_workspace_size_latent(...) bytes.
+ */
+pa_status pa_decode_latent(void* out, const void* q, const void* cache,
+                           const int32_t* block_tables, const int32_t* context_lens,
+                           const pa_latent_shape* shape, int32_t q_len, float scale,
+                           int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Workspace bytes of pa_decode_latent on the current device (0 where it needs
+ * none, for invalid arguments or without a device; SIZE_MAX when no size_t holds it). */
+size_t pa_workspace_size_latent(const pa_latent_shape* shape, int32_t q_len,
+                                int32_t max_context_len);
+
+/*
  * Test export of the page walk (MiniVLLM docs "Decoding Benchmark", "Block
  * table lookup mechanics"): out_phys[b][j] (device, int32, [batch,
  * max_blocks_per_seq]) = the physical block the decode kernels read for

@@ -26,6 +26,16 @@ or a call is rejected, an exception is raised.
     workspace_size_accumulate(q, k_cache, block_tables, out_dtype, max_context_len)
     evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_tables,
              new_weights, new_lens, kept, sink=0, recent=0)
+    rope_append_kv8(q_out, k_cache, v_cache, k_scales, v_scales, q, k_new, v_new,
+                    rotary_positions, phases, axes, block_tables, context_lens, interleaved=False)
+    decode_kv8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale,
+               max_context_len, workspace=None)
+    workspace_size_kv8(q, k_cache, block_tables, out_dtype, max_context_len)
+    rope_append_latent(q_out, cache, q, latent_new, norm_weight, rotary_positions, phases,
+                       block_tables, context_lens, eps=1e-6, interleaved=False)
+    decode_latent(out, q, cache, block_tables, context_lens, scale, max_context_len,
+                  workspace=None)
+    workspace_size_latent(q, cache, latent_dim, block_tables, max_context_len)
     workspace_size(q, k_cache, block_tables, out_dtype, max_context_len, partition_tokens=0)
     workspace_size_multi(q, k_cache, block_tables, out_dtype, max_context_len, partition_tokens=0)
     plan_info(q, k_cache, block_tables, max_context_len, partition_tokens=0)
@@ -49,7 +59,8 @@ import torch
 __all__ = ["PaError", "decode", "decode_splitkv", "decode_splitkv_noalloc", "decode_multi",
            "append_kv", "rope_phases", "rope_append_kv", "decode_shared_prefix",
            "workspace_size_shared_prefix", "decode_accumulate", "workspace_size_accumulate",
-           "evict_kv", "workspace_size", "workspace_size_multi", "plan_info", "choose_partition_tokens",
+           "evict_kv", "rope_append_kv8", "decode_kv8", "workspace_size_kv8",
+           "rope_append_latent", "decode_latent", "workspace_size_latent", "workspace_size", "workspace_size_multi", "plan_info", "choose_partition_tokens",
            "resolve_blocks", "selftest_wait_timeout", "device_error", "library_path", "F16",
            "BF16", "F32", "PARTITION_BALANCED", "set_switch", "get_switch", "SWITCH_MULTI_KERNEL",
            "SWITCH_TILE_COMPACT_Q", "KERNEL_AUTO", "KERNEL_MMA", "KERNEL_TILE"]
@@ -88,6 +99,21 @@ class _Rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class _LatentShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class _LatentRope(ctypes.Structure):
+    _fields_ = [("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("q_out_token_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+                ("new_stride", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -137,6 +163,19 @@ def _load():
             lib.pa_workspace_size_accumulate.restype = sz
             lib.pa_evict_kv.argtypes = [P] * 9 + [S, i32, i32, i32, i32, P]
             lib.pa_evict_kv.restype = ctypes.c_int
+            lib.pa_rope_append_kv8.argtypes = [P] * 13 + [S, i32, ctypes.POINTER(_Rope), P]
+            lib.pa_rope_append_kv8.restype = ctypes.c_int
+            lib.pa_decode_kv8.argtypes = [P] * 8 + [S, i32, f32, i32, P, sz, P]
+            lib.pa_decode_kv8.restype = ctypes.c_int
+            lib.pa_workspace_size_kv8.argtypes = [S, i32, i32]
+            lib.pa_workspace_size_kv8.restype = sz
+            LS = ctypes.POINTER(_LatentShape)
+            lib.pa_rope_append_latent.argtypes = [P] * 9 + [LS, i32, ctypes.POINTER(_LatentRope), P]
+            lib.pa_rope_append_latent.restype = ctypes.c_int
+            lib.pa_decode_latent.argtypes = [P] * 5 + [LS, i32, f32, i32, P, sz, P]
+            lib.pa_decode_latent.restype = ctypes.c_int
+            lib.pa_workspace_size_latent.argtypes = [LS, i32, i32]
+            lib.pa_workspace_size_latent.restype = sz
             lib.pa_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P]
             lib.pa_selftest_wait_timeout.restype = ctypes.c_int
             lib.pa_device_error.argtypes = [ctypes.POINTER(i32), P]
@@ -747,6 +786,327 @@ def evict_kv(k_cache, v_cache, weights, block_tables, context_lens, new_block_ta
         _Shape(B, Hkv, Hkv, D, bs, mb, NB, _KV_CODE[dt], F32), new_mb, kts[2], sink, recent,
         _stream_on(dev, stream)), "pa_evict_kv")
     return new_lens
+
+
+# ---- the 8-bit cache and the latent cache ----
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _check_kv8(k_cache, v_cache, k_scales, v_scales):
+    """Shapes and dtypes of an 8-bit cache; returns its (NB, bs, Hkv, D)."""
+    ks = k_cache.shape
+    if len(ks) != 4 or v_cache.shape != ks:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
+                         "num_kv_heads, head_dim]")
+    if k_cache.dtype != _E4M3 or v_cache.dtype != _E4M3:
+        raise TypeError("an 8-bit cache must be float8_e4m3fn")
+    if k_scales.shape != (ks[0], ks[2]) or v_scales.shape != (ks[0], ks[2]):
+        raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
+    if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32:
+        raise TypeError("k_scales and v_scales must be float32")
+    return ks
+
+
+def rope_append_kv8(q_out, k_cache, v_cache, k_scales, v_scales, q, k_new, v_new,
+                    rotary_positions, phases, axes, block_tables, context_lens,
+                    interleaved: bool = False, stream=None):
+    """``rope_append_kv`` into an 8-bit cache: k_cache and v_cache are
+    float8_e4m3fn [num_blocks, block_size, Hkv, D], k_scales and v_scales float32
+    [num_blocks, Hkv].  A page's scale is a power of two; where a larger value
+    arrives it rises, and the page's older tokens with it.  The other arguments
+    are those of ``rope_append_kv``."""
+    if q.dim() == 3:
+        if q_out.dim() != 3 or k_new.dim() != 3 or v_new.dim() != 3 or rotary_positions.dim() != 2:
+            raise ValueError("q, q_out, k_new, v_new and rotary_positions must all leave out "
+                             "the query-token dimension, or none")
+        rope_append_kv8(q_out.unsqueeze(1), k_cache, v_cache, k_scales, v_scales, q.unsqueeze(1),
+                        k_new.unsqueeze(1), v_new.unsqueeze(1), rotary_positions.unsqueeze(2),
+                        phases, axes, block_tables, context_lens, interleaved, stream)
+        return q_out
+    qs, bts, rs = q.shape, block_tables.shape, rotary_positions.shape
+    if len(qs) != 4:
+        raise ValueError("q must be [batch, q_len, num_heads, head_dim]")
+    NB, bs, Hkv, cache_d = _check_kv8(k_cache, v_cache, k_scales, v_scales)
+    dt = q.dtype
+    if q_out.dtype != dt or k_new.dtype != dt or v_new.dtype != dt:
+        raise TypeError("queries and new keys/values must have one dtype")
+    if dt not in _KV_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    B, Q, H, D = qs
+    if cache_d != D:
+        raise ValueError(f"q's head_dim {D} differs from the cache's {cache_d}")
+    if Q < 1:
+        raise ValueError("q_len must be at least 1")
+    if len(rs) != 3 or rs[1] != B or rs[2] != Q:
+        raise ValueError("rotary_positions must be [axes, batch, q_len]")
+    pairs = phases.numel()
+    if rotary_positions.dtype != torch.int32 or axes.dtype != torch.int32:
+        raise TypeError("rotary_positions and axes must be int32")
+    if phases.dtype != torch.int64:
+        raise TypeError("phases must be the int64 table of rope_phases")
+    if phases.dim() != 1 or axes.shape != (pairs,):
+        raise ValueError("phases and axes must hold one value per rotary pair")
+    if len(bts) != 2 or bts[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq], context_lens [batch]")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    rope = _Rope(2 * pairs, rs[0], 1 if interleaved else 0, 0,
+                 _token_stride(q, "q", qs), _token_stride(q_out, "q_out", qs),
+                 _token_stride(k_new, "k_new", (B, Q, Hkv, D)),
+                 _token_stride(v_new, "v_new", (B, Q, Hkv, D)))
+    dev = _device_of(k_cache)
+    _same_device(dev, (k_cache, v_cache, k_scales, v_scales, rotary_positions, phases, axes,
+                       block_tables, context_lens))
+    _same_device(dev, (q, q_out, k_new, v_new), contiguous=False)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rope_append_kv8(q_out, k_cache, v_cache, k_scales, v_scales, q, k_new, v_new,
+                                   rotary_positions, phases, axes, block_tables, context_lens,
+                                   interleaved, stream)
+    _check((_lib or _load()).pa_rope_append_kv8(
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+        v_scales.data_ptr(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        rotary_positions.data_ptr(), phases.data_ptr(), axes.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), _Shape(B, H, Hkv, D, bs, bts[1], NB, _KV_CODE[dt], F32), Q, rope,
+        _stream_on(dev, stream)), "pa_rope_append_kv8")
+    return q_out
+
+
+def _kv8_shape(q, k_cache, block_tables, out_dtype):
+    """pa_shape and q_len of a one-token ([B, H, D]) or several-token ([B, Q, H, D])
+    query over an 8-bit cache."""
+    qs, ks, bts, dt = q.shape, k_cache.shape, block_tables.shape, q.dtype
+    if len(qs) == 3:
+        B, H, D = qs
+        Q = 1
+    elif len(qs) == 4:
+        B, Q, H, D = qs
+        if Q < 1:
+            raise ValueError("q_len must be at least 1")
+    else:
+        raise ValueError("q must be [batch, num_heads, head_dim] or "
+                         "[batch, q_len, num_heads, head_dim]")
+    if dt not in _KV_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    if out_dtype != dt and out_dtype != torch.float32:
+        raise TypeError("out must be float32 or q's dtype")
+    if len(ks) != 4:
+        raise ValueError("k_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
+    if D != ks[3]:
+        raise ValueError(f"q's head_dim {D} differs from the cache's {ks[3]}")
+    if len(bts) != 2 or bts[0] != B:
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq]")
+    code = _KV_CODE[dt]
+    return _Shape(B, H, ks[2], D, ks[1], bts[1], ks[0], code, code if out_dtype == dt else F32), Q
+
+
+def workspace_size_kv8(q, k_cache, block_tables, out_dtype, max_context_len: int) -> int:
+    """Bytes of workspace that ``decode_kv8`` takes, on the tensors' device."""
+    shape, q_len = _kv8_shape(q, k_cache, block_tables, out_dtype)
+    with torch.cuda.device(_device_of(k_cache)):
+        return int(_load().pa_workspace_size_kv8(shape, q_len,
+                                                 _i32(max_context_len, "max_context_len")))
+
+
+def decode_kv8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+               scale: float, max_context_len: int, workspace=None, stream=None):
+    """``decode_splitkv`` (q, out [B, H, D]) or ``decode_multi`` ([B, Q, H, D]) over
+    an 8-bit cache: k_cache and v_cache float8_e4m3fn [num_blocks, block_size, Hkv,
+    D], k_scales and v_scales float32 [num_blocks, Hkv].  ``workspace``: a CUDA
+    byte tensor of ``workspace_size_kv8(...)`` bytes, else one is taken from
+    torch's allocator."""
+    _check_kv8(k_cache, v_cache, k_scales, v_scales)
+    shape, q_len = _kv8_shape(q, k_cache, block_tables, out.dtype)
+    if out.shape != q.shape:
+        raise ValueError(f"out {tuple(out.shape)} must be shaped like q {tuple(q.shape)}")
+    if context_lens.shape != (shape.batch,):
+        raise ValueError("context_lens must be [batch]")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if type(max_context_len) is not int or not -_2_31 <= max_context_len < _2_31:
+        max_context_len = _i32(max_context_len, "max_context_len")
+    if type(scale) is not float:
+        scale = float(scale)
+    dev = _device_of(k_cache)
+    _same_device(dev, (out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens))
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return decode_kv8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                              context_lens, scale, max_context_len, workspace, stream)
+    lib = _lib or _load()
+    need = 0 if workspace is not None else lib.pa_workspace_size_kv8(shape, q_len, max_context_len)
+    ws, ws_bytes = _workspace_for(workspace, need, dev, stream)
+    _check(lib.pa_decode_kv8(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+        v_scales.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), shape, q_len, scale,
+        max_context_len, ws.data_ptr(), ws_bytes, _stream_on(dev, stream)), "pa_decode_kv8")
+    return out
+
+
+def _head_strides(t, name, shape):
+    """Elements between the tokens, and between the heads of a token, of a [batch,
+    q_len, heads, width] view whose tokens lie evenly apart."""
+    if t.shape != shape:
+        raise ValueError(f"{name} {tuple(t.shape)} must be {tuple(shape)}")
+    batch, q_len, heads, width = shape
+    sb, sq, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if heads == 1:
+        sh = width
+    if q_len == 1:
+        return (sb if batch > 1 else heads * sh), sh
+    if batch > 1 and sb != q_len * sq:
+        raise ValueError(f"{name}'s tokens must lie evenly apart")
+    return sq, sh
+
+
+def rope_append_latent(q_out, cache, q, latent_new, norm_weight, rotary_positions, phases,
+                       block_tables, context_lens, eps: float = 1e-6, interleaved: bool = False,
+                       stream=None):
+    """Write the new tokens' vectors into the latent cache ([num_blocks,
+    block_size, latent_dim + 64]): the latent part normalised by its root mean
+    square times ``norm_weight`` (None: as it is), the positional part turned; and
+    turn the positional part of every head's query into ``q_out``.
+
+    q, q_out [B, Q, H, 64], views of wider rows are fine (``q_out`` may be
+    ``query[..., latent_dim:]`` of the query that ``decode_latent`` takes);
+    latent_new [B, Q, latent_dim + 64] (a view of a projection is fine);
+    rotary_positions int32 [B, Q]; phases from ``rope_phases``, 32 of them.
+    context_lens counts the Q new tokens.  For one token per sequence the
+    tensors may leave out their Q dimension."""
+    if q.dim() == 3:
+        if q_out.dim() != 3 or latent_new.dim() != 2 or rotary_positions.dim() != 1:
+            raise ValueError("q, q_out, latent_new and rotary_positions must all leave out "
+                             "the query-token dimension, or none")
+        rope_append_latent(q_out.unsqueeze(1), cache, q.unsqueeze(1), latent_new.unsqueeze(1),
+                           norm_weight, rotary_positions.unsqueeze(1), phases, block_tables,
+                           context_lens, eps, interleaved, stream)
+        return q_out
+    qs, cs, bts = q.shape, cache.shape, block_tables.shape
+    if len(qs) != 4:
+        raise ValueError("q must be [batch, q_len, num_heads, rope_dim]")
+    if len(cs) != 3:
+        raise ValueError("cache must be [num_blocks, block_size, latent_dim + rope_dim]")
+    dt = cache.dtype
+    if q.dtype != dt or q_out.dtype != dt or latent_new.dtype != dt:
+        raise TypeError("queries, new vectors and the cache must have one dtype")
+    if dt not in _KV_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    B, Q, H, P = qs
+    NB, bs, W = cs
+    if Q < 1:
+        raise ValueError("q_len must be at least 1")
+    if latent_new.dim() != 3 or rotary_positions.shape != (B, Q):
+        raise ValueError("latent_new must be [batch, q_len, latent_dim + rope_dim], "
+                         "rotary_positions [batch, q_len]")
+    if norm_weight is not None:
+        if norm_weight.dtype != dt:
+            raise TypeError("norm_weight must have the cache's dtype")
+        if norm_weight.shape != (W - P,):
+            raise ValueError("norm_weight must be [latent_dim]")
+    if phases.dtype != torch.int64 or rotary_positions.dtype != torch.int32:
+        raise TypeError("phases must be the int64 table of rope_phases, rotary_positions int32")
+    if phases.shape != (P // 2,):
+        raise ValueError("phases must hold one value per rotary pair")
+    if len(bts) != 2 or bts[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq], context_lens [batch]")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    rope = _LatentRope(1 if interleaved else 0, float(eps), *_head_strides(q, "q", qs),
+                       *_head_strides(q_out, "q_out", qs),
+                       _head_strides(latent_new.unsqueeze(2), "latent_new", (B, Q, 1, W))[0])
+    dev = _device_of(cache)
+    _same_device(dev, (cache, rotary_positions, phases, block_tables, context_lens))
+    _same_device(dev, (q, q_out, latent_new), contiguous=False)
+    if norm_weight is not None:
+        _same_device(dev, (norm_weight,))
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rope_append_latent(q_out, cache, q, latent_new, norm_weight, rotary_positions,
+                                      phases, block_tables, context_lens, eps, interleaved, stream)
+    _check((_lib or _load()).pa_rope_append_latent(
+        q_out.data_ptr(), cache.data_ptr(), q.data_ptr(), latent_new.data_ptr(),
+        None if norm_weight is None else norm_weight.data_ptr(), rotary_positions.data_ptr(),
+        phases.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+        _LatentShape(B, H, W - P, P, bs, bts[1], NB, _KV_CODE[dt], 0), Q, rope,
+        _stream_on(dev, stream)), "pa_rope_append_latent")
+    return q_out
+
+
+def _latent_shape(q, cache, latent_dim, block_tables):
+    """pa_latent_shape and q_len of a one-token ([B, H, W]) or several-token
+    ([B, Q, H, W]) query over a latent cache."""
+    qs, cs, bts, dt = q.shape, cache.shape, block_tables.shape, cache.dtype
+    if len(qs) == 3:
+        B, H, W = qs
+        Q = 1
+    elif len(qs) == 4:
+        B, Q, H, W = qs
+        if Q < 1:
+            raise ValueError("q_len must be at least 1")
+    else:
+        raise ValueError("q must be [batch, num_heads, latent_dim + rope_dim] or "
+                         "[batch, q_len, num_heads, latent_dim + rope_dim]")
+    if len(cs) != 3 or cs[2] != W:
+        raise ValueError(f"cache must be [num_blocks, block_size, {W}], as wide as q")
+    if q.dtype != dt:
+        raise TypeError("q must have the cache's dtype")
+    if dt not in _KV_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    if len(bts) != 2 or bts[0] != B:
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq]")
+    if not 0 < latent_dim < W:
+        raise ValueError("latent_dim must be smaller than the cache's rows")
+    return _LatentShape(B, H, latent_dim, W - latent_dim, cs[1], bts[1], cs[0], _KV_CODE[dt], 0), Q
+
+
+def workspace_size_latent(q, cache, latent_dim: int, block_tables, max_context_len: int) -> int:
+    """Bytes of workspace that ``decode_latent`` takes, on the tensors' device."""
+    shape, q_len = _latent_shape(q, cache, _i32(latent_dim, "latent_dim"), block_tables)
+    with torch.cuda.device(_device_of(cache)):
+        return int(_load().pa_workspace_size_latent(shape, q_len,
+                                                    _i32(max_context_len, "max_context_len")))
+
+
+def decode_latent(out, q, cache, block_tables, context_lens, scale: float, max_context_len: int,
+                  workspace=None, stream=None):
+    """Attention over a latent cache in its absorbed form: every head's key of a
+    token is the token's whole vector, its value the first ``out.shape[-1]``
+    elements.  q [B, H, W] or [B, Q, H, W], out the same with latent_dim in place
+    of W; cache [num_blocks, block_size, W]; causal over the Q query tokens, which
+    context_lens counts.  ``workspace``: a CUDA byte tensor of
+    ``workspace_size_latent(...)`` bytes, else one is taken from torch's allocator."""
+    if out.dim() != q.dim() or out.shape[:-1] != q.shape[:-1]:
+        raise ValueError(f"out {tuple(out.shape)} must be shaped like q {tuple(q.shape)} but for "
+                         "the last dimension")
+    shape, q_len = _latent_shape(q, cache, out.shape[-1], block_tables)
+    if out.dtype != q.dtype:
+        raise TypeError("out must have q's dtype")
+    if context_lens.shape != (shape.batch,):
+        raise ValueError("context_lens must be [batch]")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if type(max_context_len) is not int or not -_2_31 <= max_context_len < _2_31:
+        max_context_len = _i32(max_context_len, "max_context_len")
+    if type(scale) is not float:
+        scale = float(scale)
+    dev = _device_of(cache)
+    _same_device(dev, (out, q, cache, block_tables, context_lens))
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return decode_latent(out, q, cache, block_tables, context_lens, scale, max_context_len,
+                                 workspace, stream)
+    lib = _lib or _load()
+    need = 0 if workspace is not None else lib.pa_workspace_size_latent(shape, q_len,
+                                                                        max_context_len)
+    ws, ws_bytes = _workspace_for(workspace, need, dev, stream)
+    _check(lib.pa_decode_latent(
+        out.data_ptr(), q.data_ptr(), cache.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), shape, q_len, scale, max_context_len, ws.data_ptr(), ws_bytes,
+        _stream_on(dev, stream)), "pa_decode_latent")
+    return out
 
 
 def resolve_blocks(out_phys, block_tables, context_lens, block_size: int, num_blocks: int,

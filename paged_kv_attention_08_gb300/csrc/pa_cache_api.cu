@@ -1,0 +1,373 @@
+// Host side of the 8-bit cache (pa_rope_append_kv8, pa_decode_kv8) and of the
+// latent cache (pa_rope_append_latent, pa_decode_latent).
+#include <cmath>
+#include <cstring>
+
+#include "pa_internal.h"
+
+using namespace pa;
+
+namespace {
+
+struct Span {
+    const void* p;
+    size_t n;
+};
+
+bool overlap(Span a, Span b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.n && b.n && x < y + b.n && y < x + a.n;
+}
+
+// One array of `tokens` rows of 16-bit elements, `stride` apart.
+struct Rows {
+    const void* p;
+    int64_t row, stride;
+    Span span(int64_t tokens) const { return {p, ((size_t)(tokens - 1) * stride + row) * 2}; }
+};
+
+// Do rows of two arrays share a byte?  Rows of one stride meet if they do
+// modulo the stride (slices of one fused buffer do not); arrays of different
+// strides are taken to where they share a range.
+bool rows_meet(const Rows& a, const Rows& b, int64_t tokens) {
+    if (!overlap(a.span(tokens), b.span(tokens))) return false;
+    if (a.stride != b.stride || tokens == 1) return true;
+    const int64_t stride = a.stride * 2;
+    const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(a.p) - reinterpret_cast<uintptr_t>(b.p));
+    const int64_t at = ((apart % stride) + stride) % stride;  // a's rows begin here in b's stride
+    return at < b.row * 2 || at + a.row * 2 > stride;
+}
+
+bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.f; }
+
+pa_status check_latent(const pa_latent_shape* s) {
+    if (!s) return PA_ERR_INVALID_ARG;
+    if (s->batch < 0 || s->num_heads <= 0 || s->latent_dim <= 0 || s->rope_dim <= 0 ||
+        s->block_size <= 0 || s->max_blocks_per_seq <= 0 || s->num_blocks <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (s->dtype != PA_F16 && s->dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (s->latent_dim != 128 && s->latent_dim != 256 && s->latent_dim != 512) return PA_ERR_UNSUPPORTED;
+    if (s->rope_dim != 64) return PA_ERR_UNSUPPORTED;
+    if (s->block_size != 16 && s->block_size != 32 && s->block_size != 64) return PA_ERR_UNSUPPORTED;
+    if (s->batch > 65535 || s->num_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (s->num_blocks >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)s->max_blocks_per_seq * s->block_size > (1 << 30)) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+// Tokens of the pages that max_context_len announces, inside the table's reach.
+int announced_tokens(int32_t max_context_len, int block_size, int max_blocks) {
+    const int64_t t = max_context_len < 1 ? 1 : max_context_len;
+    const int64_t pages = (t + block_size - 1) / block_size;
+    return (int)((pages < max_blocks ? pages : max_blocks) * block_size);
+}
+
+pa_status done(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
+
+pa_status check_kv8(const pa_shape* s, int32_t q_len) {
+    const pa_status st = check_shape(s);
+    if (st != PA_OK) return st;
+    if (q_len < 1) return PA_ERR_INVALID_ARG;
+    // rows of a sequence, and tokens of a table, inside 31 bits
+    if ((int64_t)q_len * s->num_heads > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)s->max_blocks_per_seq * s->block_size > (1 << 30)) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_rope_append_kv8(void* q_out, void* k_cache, void* v_cache, float* k_scales,
+                             float* v_scales, const void* q, const void* k_new, const void* v_new,
+                             const int32_t* rotary_positions, const int64_t* phases,
+                             const int32_t* axes, const int32_t* block_tables,
+                             const int32_t* context_lens, const pa_shape* shape, int32_t q_len,
+                             const pa_rope* rope, void* stream) {
+    pa_status st = check_shape(shape);
+    if (st != PA_OK) return st;
+    if (!rope || q_len < 1 || rope->num_axes < 1 || rope->rotary_dim < 0 ||
+        rope->rotary_dim > shape->head_dim || (rope->interleaved != 0 && rope->interleaved != 1))
+        return PA_ERR_INVALID_ARG;
+    if (rope->rotary_dim == 0 || rope->rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    const int64_t q_row = (int64_t)shape->num_heads * shape->head_dim;
+    const int64_t kv_row = (int64_t)shape->num_kv_heads * shape->head_dim;
+    if (rope->q_stride < q_row || rope->q_out_stride < q_row || rope->k_stride < kv_row ||
+        rope->v_stride < kv_row)
+        return PA_ERR_INVALID_ARG;
+    if (rope->q_stride % 8 || rope->q_out_stride % 8 || rope->k_stride % 8 || rope->v_stride % 8)
+        return PA_ERR_UNSUPPORTED;
+    // query items of a page's tokens, and the tokens of a call, in 31 bits
+    const int64_t tokens = (int64_t)shape->batch * q_len;
+    if (q_row / 16 > (1 << 25) || tokens > (1ll << 31) - 1 || q_len > (1 << 30)) return PA_ERR_UNSUPPORTED;
+    if (shape->batch == 0) return PA_OK;
+    if (!q_out || !k_cache || !v_cache || !k_scales || !v_scales || !q || !k_new || !v_new ||
+        !rotary_positions || !phases || !axes || !block_tables || !context_lens)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 16) ||
+        !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(phases, 8) ||
+        !aligned(rotary_positions, 4) || !aligned(axes, 4) || !aligned(block_tables, 4) ||
+        !aligned(context_lens, 4) || !aligned(k_scales, 4) || !aligned(v_scales, 4))
+        return PA_ERR_INVALID_ARG;
+    if (q_out == q && rope->q_out_stride != rope->q_stride) return PA_ERR_INVALID_ARG;
+    // what one CTA writes others may still be to read: every output apart from
+    // the others and from the inputs
+    const Rows qo{q_out, q_row, rope->q_out_stride}, qi{q, q_row, rope->q_stride},
+        kn{k_new, kv_row, rope->k_stride}, vn{v_new, kv_row, rope->v_stride};
+    if ((q_out != q && rows_meet(qo, qi, tokens)) || rows_meet(qo, kn, tokens) || rows_meet(qo, vn, tokens))
+        return PA_ERR_INVALID_ARG;
+    const size_t cache = (size_t)shape->num_blocks * shape->block_size * (size_t)kv_row;
+    const size_t scales = (size_t)shape->num_blocks * shape->num_kv_heads * 4;
+    const size_t pairs = (size_t)rope->rotary_dim / 2;
+    const Span outs[5] = {qo.span(tokens), {k_cache, cache}, {v_cache, cache}, {k_scales, scales},
+                          {v_scales, scales}};
+    const Span ins[8] = {{rotary_positions, (size_t)tokens * rope->num_axes * 4},
+                         {phases, pairs * 8},
+                         {axes, pairs * 4},
+                         {block_tables, (size_t)shape->batch * shape->max_blocks_per_seq * 4},
+                         {context_lens, (size_t)shape->batch * 4},
+                         qi.span(tokens),
+                         kn.span(tokens),
+                         vn.span(tokens)};
+    for (int o = 0; o < 5; ++o) {
+        for (int i = 0; i < (o == 0 ? 5 : 8); ++i)  // (q_out's rows against q, k_new and v_new: above)
+            if (overlap(outs[o], ins[i])) return PA_ERR_INVALID_ARG;
+        for (int i = 0; i < o; ++i)
+            if (overlap(outs[o], outs[i])) return PA_ERR_INVALID_ARG;
+    }
+    st = device_state(nullptr, nullptr);
+    if (st != PA_OK) return st;
+    Append8Params p;
+    std::memset(&p, 0, sizeof p);
+    p.q_out = q_out;
+    p.k_cache = static_cast<uint8_t*>(k_cache);
+    p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.q = q;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.positions = rotary_positions;
+    p.phases = phases;
+    p.axes = axes;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.num_blocks = shape->num_blocks;
+    p.q_stride = rope->q_stride;
+    p.k_stride = rope->k_stride;
+    p.v_stride = rope->v_stride;
+    p.q_out_stride = rope->q_out_stride;
+    p.batch = shape->batch;
+    p.q_len = q_len;
+    p.num_heads = shape->num_heads;
+    p.num_kv_heads = shape->num_kv_heads;
+    p.head_dim = shape->head_dim;
+    p.block_size = shape->block_size;
+    p.max_blocks = shape->max_blocks_per_seq;
+    p.rotary_dim = rope->rotary_dim;
+    p.num_axes = rope->num_axes;
+    p.interleaved = rope->interleaved;
+    return done(launch_append8(p, shape->kv_dtype == PA_BF16, use_pdl(),
+                               static_cast<cudaStream_t>(stream)));
+}
+
+size_t pa_workspace_size_kv8(const pa_shape* shape, int32_t q_len, int32_t max_context_len) {
+    (void)max_context_len;
+    if (check_kv8(shape, q_len) != PA_OK) return 0;
+    return 0;
+}
+
+pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                        const int32_t* context_lens, const pa_shape* shape, int32_t q_len,
+                        float scale, int32_t max_context_len, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    pa_status st = check_kv8(shape, q_len);
+    if (st != PA_OK) return st;
+    if (max_context_len < 0 || !scale_ok(scale)) return PA_ERR_INVALID_ARG;
+    if (shape->batch == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !context_lens)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_tables, 4) ||
+        !aligned(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    const size_t values = (size_t)shape->batch * q_len * shape->num_heads * shape->head_dim;
+    const size_t cache = (size_t)shape->num_blocks * shape->block_size * shape->num_kv_heads *
+                         shape->head_dim;
+    const size_t scales = (size_t)shape->num_blocks * shape->num_kv_heads * 4;
+    const Span o{out, values * (shape->out_dtype == PA_F32 ? 4 : 2)};
+    const Span ins[7] = {{q, values * 2},
+                         {k_cache, cache},
+                         {v_cache, cache},
+                         {k_scales, scales},
+                         {v_scales, scales},
+                         {block_tables, (size_t)shape->batch * shape->max_blocks_per_seq * 4},
+                         {context_lens, (size_t)shape->batch * 4}};
+    for (const Span& i : ins)
+        if (overlap(o, i)) return PA_ERR_INVALID_ARG;
+    (void)workspace;
+    (void)workspace_bytes;
+    st = device_state(nullptr, nullptr);
+    if (st != PA_OK) return st;
+    Kv8Params p;
+    std::memset(&p, 0, sizeof p);
+    p.q = q;
+    p.out = out;
+    p.k_cache = static_cast<const uint8_t*>(k_cache);
+    p.v_cache = static_cast<const uint8_t*>(v_cache);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.num_blocks = shape->num_blocks;
+    p.qscale = scale * 1.4426950408889634f;  // log2(e)
+    p.batch = shape->batch;
+    p.q_len = q_len;
+    p.num_heads = shape->num_heads;
+    p.num_kv_heads = shape->num_kv_heads;
+    p.group = shape->num_heads / shape->num_kv_heads;
+    p.head_dim = shape->head_dim;
+    p.block_size = shape->block_size;
+    p.max_blocks = shape->max_blocks_per_seq;
+    p.token_limit = announced_tokens(max_context_len, shape->block_size, shape->max_blocks_per_seq);
+    p.out_dtype = shape->out_dtype;
+    return done(launch_kv8_attention(p, shape->kv_dtype == PA_BF16, use_pdl(),
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_rope_append_latent(void* q_out, void* cache, const void* q, const void* latent_new,
+                                const void* norm_weight, const int32_t* rotary_positions,
+                                const int64_t* phases, const int32_t* block_tables,
+                                const int32_t* context_lens, const pa_latent_shape* shape,
+                                int32_t q_len, const pa_latent_rope* rope, void* stream) {
+    pa_status st = check_latent(shape);
+    if (st != PA_OK) return st;
+    if (!rope || q_len < 1 || (rope->interleaved != 0 && rope->interleaved != 1) ||
+        !std::isfinite(rope->eps) || rope->eps < 0.f)
+        return PA_ERR_INVALID_ARG;
+    const int W = shape->latent_dim + shape->rope_dim;
+    if (rope->q_head_stride < shape->rope_dim || rope->q_out_head_stride < shape->rope_dim ||
+        rope->new_stride < W || rope->q_head_stride > (1 << 30) || rope->q_out_head_stride > (1 << 30))
+        return PA_ERR_INVALID_ARG;
+    const int64_t q_row = (shape->num_heads - 1) * rope->q_head_stride + shape->rope_dim;
+    const int64_t out_row = (shape->num_heads - 1) * rope->q_out_head_stride + shape->rope_dim;
+    if (rope->q_token_stride < q_row || rope->q_out_token_stride < out_row) return PA_ERR_INVALID_ARG;
+    if (rope->q_token_stride % 8 || rope->q_head_stride % 8 || rope->q_out_token_stride % 8 ||
+        rope->q_out_head_stride % 8 || rope->new_stride % 8)
+        return PA_ERR_UNSUPPORTED;
+    const int64_t tokens = (int64_t)shape->batch * q_len;
+    if (tokens > (1ll << 31) - 1) return PA_ERR_UNSUPPORTED;
+    if (shape->batch == 0) return PA_OK;
+    if (!q_out || !cache || !q || !latent_new || !rotary_positions || !phases || !block_tables ||
+        !context_lens)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(q_out, 16) || !aligned(cache, 16) || !aligned(q, 16) || !aligned(latent_new, 16) ||
+        !aligned(norm_weight, 16) || !aligned(phases, 8) || !aligned(rotary_positions, 4) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    if (q_out == q && (rope->q_out_token_stride != rope->q_token_stride ||
+                       rope->q_out_head_stride != rope->q_head_stride))
+        return PA_ERR_INVALID_ARG;
+    const Rows qo{q_out, out_row, rope->q_out_token_stride}, qi{q, q_row, rope->q_token_stride},
+        nw{latent_new, W, rope->new_stride};
+    if ((q_out != q && rows_meet(qo, qi, tokens)) || rows_meet(qo, nw, tokens)) return PA_ERR_INVALID_ARG;
+    const Span outs[2] = {qo.span(tokens),
+                          {cache, (size_t)shape->num_blocks * shape->block_size * W * 2}};
+    const Span ins[7] = {{rotary_positions, (size_t)tokens * 4},
+                         {phases, (size_t)shape->rope_dim / 2 * 8},
+                         {block_tables, (size_t)shape->batch * shape->max_blocks_per_seq * 4},
+                         {context_lens, (size_t)shape->batch * 4},
+                         {norm_weight, norm_weight ? (size_t)shape->latent_dim * 2 : 0},
+                         qi.span(tokens),
+                         nw.span(tokens)};
+    if (overlap(outs[0], outs[1])) return PA_ERR_INVALID_ARG;
+    for (int o = 0; o < 2; ++o)
+        for (int i = 0; i < (o == 0 ? 5 : 7); ++i)
+            if (overlap(outs[o], ins[i])) return PA_ERR_INVALID_ARG;
+    int sms = 0;
+    st = device_state(&sms, nullptr);
+    if (st != PA_OK) return st;
+    LatentAppendParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q_out = q_out;
+    p.cache = cache;
+    p.q = q;
+    p.latent_new = latent_new;
+    p.norm_weight = norm_weight;
+    p.positions = rotary_positions;
+    p.phases = phases;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.num_blocks = shape->num_blocks;
+    p.q_token_stride = rope->q_token_stride;
+    p.q_head_stride = rope->q_head_stride;
+    p.q_out_token_stride = rope->q_out_token_stride;
+    p.q_out_head_stride = rope->q_out_head_stride;
+    p.new_stride = rope->new_stride;
+    p.eps = rope->eps;
+    p.batch = shape->batch;
+    p.q_len = q_len;
+    p.num_heads = shape->num_heads;
+    p.latent_dim = shape->latent_dim;
+    p.block_size = shape->block_size;
+    p.max_blocks = shape->max_blocks_per_seq;
+    p.interleaved = rope->interleaved;
+    return done(launch_append_latent(p, shape->dtype == PA_BF16, sms, use_pdl(),
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t pa_workspace_size_latent(const pa_latent_shape* shape, int32_t q_len, int32_t max_context_len) {
+    (void)max_context_len;
+    if (check_latent(shape) != PA_OK || q_len < 1) return 0;
+    return 0;
+}
+
+pa_status pa_decode_latent(void* out, const void* q, const void* cache,
+                           const int32_t* block_tables, const int32_t* context_lens,
+                           const pa_latent_shape* shape, int32_t q_len, float scale,
+                           int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    pa_status st = check_latent(shape);
+    if (st != PA_OK) return st;
+    if (q_len < 1 || max_context_len < 0 || !scale_ok(scale)) return PA_ERR_INVALID_ARG;
+    if ((int64_t)q_len * shape->num_heads > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    if (shape->batch == 0) return PA_OK;
+    if (!out || !q || !cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(cache, 16) || !aligned(block_tables, 4) ||
+        !aligned(context_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    const size_t rows = (size_t)shape->batch * q_len * shape->num_heads;
+    const size_t W = (size_t)shape->latent_dim + shape->rope_dim;
+    const Span o{out, rows * shape->latent_dim * 2};
+    const Span ins[4] = {{q, rows * W * 2},
+                         {cache, (size_t)shape->num_blocks * shape->block_size * W * 2},
+                         {block_tables, (size_t)shape->batch * shape->max_blocks_per_seq * 4},
+                         {context_lens, (size_t)shape->batch * 4}};
+    for (const Span& i : ins)
+        if (overlap(o, i)) return PA_ERR_INVALID_ARG;
+    (void)workspace;
+    (void)workspace_bytes;
+    st = device_state(nullptr, nullptr);
+    if (st != PA_OK) return st;
+    LatentParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = q;
+    p.out = out;
+    p.cache = cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.num_blocks = shape->num_blocks;
+    p.qscale = scale * 1.4426950408889634f;  // log2(e)
+    p.batch = shape->batch;
+    p.q_len = q_len;
+    p.num_heads = shape->num_heads;
+    p.latent_dim = shape->latent_dim;
+    p.block_size = shape->block_size;
+    p.max_blocks = shape->max_blocks_per_seq;
+    p.token_limit = announced_tokens(max_context_len, shape->block_size, shape->max_blocks_per_seq);
+    return done(launch_latent_attention(p, shape->dtype == PA_BF16, use_pdl(),
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -142,6 +142,73 @@ struct RopeParams {
     uint32_t per_token_inverse;  // 2^32 / items of a token, rounded up
 };
 
+// Rotary positions and the append to the 8-bit cache.
+struct Append8Params {
+    void* q_out;              // [tokens, H, D]
+    uint8_t* k_cache;         // [num_blocks, block_size, Hkv, D] e4m3
+    uint8_t* v_cache;
+    float* k_scales;          // [num_blocks, Hkv]
+    float* v_scales;
+    const void* q;
+    const void* k_new;
+    const void* v_new;
+    const int32_t* positions; // [num_axes, tokens]
+    const int64_t* phases;
+    const int32_t* axes;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int64_t num_blocks, q_stride, k_stride, v_stride, q_out_stride;
+    int32_t batch, q_len, num_heads, num_kv_heads, head_dim, block_size, max_blocks;
+    int32_t rotary_dim, num_axes, interleaved;
+};
+
+// Attention over the 8-bit cache.
+struct Kv8Params {
+    const void* q;            // [B, Q, H, D]
+    void* out;
+    const uint8_t* k_cache;   // [num_blocks, block_size, Hkv, D] e4m3
+    const uint8_t* v_cache;
+    const float* k_scales;    // [num_blocks, Hkv]
+    const float* v_scales;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int64_t num_blocks;
+    float qscale;             // scale * log2(e)
+    int32_t batch, q_len, num_heads, num_kv_heads, group, head_dim, block_size, max_blocks;
+    int32_t token_limit;      // tokens from here on are not attended to
+    int32_t out_dtype;
+};
+
+// Append to the latent cache (strides in elements).
+struct LatentAppendParams {
+    void* q_out;              // [tokens, H, 64]
+    void* cache;              // [num_blocks, block_size, latent_dim + 64]
+    const void* q;            // [tokens, H, 64]
+    const void* latent_new;   // [tokens, latent_dim + 64]
+    const void* norm_weight;  // [latent_dim], or null: the latent part is stored as it is
+    const int32_t* positions; // [tokens]
+    const int64_t* phases;    // [32]
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int64_t num_blocks, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, new_stride;
+    float eps;
+    int32_t batch, q_len, num_heads, latent_dim, block_size, max_blocks, interleaved;
+    int32_t span;             // tokens of a CTA
+};
+
+// Attention over the latent cache.
+struct LatentParams {
+    const void* q;            // [B, Q, H, latent_dim + 64]
+    void* out;                // [B, Q, H, latent_dim]
+    const void* cache;        // [num_blocks, block_size, latent_dim + 64]
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int64_t num_blocks;
+    float qscale;             // scale * log2(e)
+    int32_t batch, q_len, num_heads, latent_dim, block_size, max_blocks;
+    int32_t token_limit;      // tokens from here on are not attended to
+};
+
 // Eviction by accumulated weight.
 struct EvictParams {
     void* k_cache;
@@ -468,6 +535,11 @@ cudaError_t launch_append(void* k_cache, void* v_cache, const void* k_new, const
                           int32_t row_bytes, bool pdl, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams& p, bool bf16, int num_sms, bool pdl,
                                cudaStream_t stream);
+cudaError_t launch_append8(const Append8Params& p, bool bf16, bool pdl, cudaStream_t stream);
+cudaError_t launch_kv8_attention(const Kv8Params& p, bool bf16, bool pdl, cudaStream_t stream);
+cudaError_t launch_append_latent(LatentAppendParams p, bool bf16, int num_sms, bool pdl,
+                                 cudaStream_t stream);
+cudaError_t launch_latent_attention(const LatentParams& p, bool bf16, bool pdl, cudaStream_t stream);
 cudaError_t launch_evict(EvictParams p, bool in_place, bool pdl, cudaStream_t stream);
 cudaError_t launch_wait_timeout(int32_t* err, uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t launch_resolve(int32_t* out_phys, const int32_t* block_tables,
