@@ -31,7 +31,6 @@ namespace pa {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;  // 2 s per wait
 std::atomic<int> g_sm_count[kMaxDevices];
 std::atomic<int32_t*> g_err_word[kMaxDevices];
 
@@ -779,8 +778,8 @@ pa_status encode_maps(const pa_shape* s, const void* k, const void* v, CUtensorM
     return PA_OK;
 }
 
-pa_status encode_maps_uncached(const pa_shape* s, const void* k, const void* v, CUtensorMap* mk,
-                               CUtensorMap* mv) {
+// The driver's encoder, looked up once.
+bool find_encode() {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -789,7 +788,12 @@ pa_status encode_maps_uncached(const pa_shape* s, const void* k, const void* v, 
             q == cudaDriverEntryPointSuccess)
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
-    if (!g_encode) return PA_ERR_CUDA;
+    return g_encode != nullptr;
+}
+
+pa_status encode_maps_uncached(const pa_shape* s, const void* k, const void* v, CUtensorMap* mk,
+                               CUtensorMap* mv) {
+    if (!find_encode()) return PA_ERR_CUDA;
     const cuuint64_t e = elem_size(s->kv_dtype);
     // dims innermost first: head_dim, kv head, slot in block, block
     const cuuint64_t dims[4] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->num_kv_heads,
@@ -1316,6 +1320,26 @@ pa_status run_multi(void* out, const void* q, const void* k_cache, const void* v
 }
 
 }  // namespace
+
+pa_status encode_tiled(CUtensorMap* map, CUtensorMapDataType type, uint32_t rank, const void* base,
+                       const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                       CUtensorMapSwizzle swizzle) {
+    if (!find_encode()) return PA_ERR_CUDA;
+    const cuuint32_t ones[5] = {1u, 1u, 1u, 1u, 1u};
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5];
+    for (uint32_t i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return g_encode(map, type, rank, const_cast<void*>(base), d, st, bx, ones,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
 }  // namespace pa
 
 using namespace pa;

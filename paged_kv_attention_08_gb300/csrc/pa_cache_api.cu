@@ -1,5 +1,6 @@
 // Host side of the 8-bit cache (pa_rope_append_kv8, pa_decode_kv8) and of the
 // latent cache (pa_rope_append_latent, pa_decode_latent).
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -72,6 +73,60 @@ pa_status check_kv8(const pa_shape* s, int32_t q_len) {
     if ((int64_t)q_len * s->num_heads > (1 << 24)) return PA_ERR_UNSUPPORTED;
     if ((int64_t)s->max_blocks_per_seq * s->block_size > (1 << 30)) return PA_ERR_UNSUPPORTED;
     return PA_OK;
+}
+
+// How a call is split: partitions of part_pages pages for each (sequence, kv
+// head, chunk of query tokens), joined in a cluster or through the workspace.
+struct Split {
+    int part_pages, parts;
+    bool cluster;
+    int chunk, chunks;  // query tokens of a CTA, and how many CTAs that makes
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Workspace: acc [rows][parts][width] fp32, then (m, l); SIZE_MAX where no size_t holds it.
+size_t partial_bytes(const Split& sp, size_t rows, int width, size_t* ml_at) {
+    if (sp.parts <= 1 || sp.cluster) return 0;
+    size_t acc = 0, ml = 0;
+    if (__builtin_mul_overflow(rows, (size_t)sp.parts, &rows) ||
+        __builtin_mul_overflow(rows, (size_t)width * 4, &acc) || __builtin_mul_overflow(rows, (size_t)8, &ml) ||
+        acc > SIZE_MAX - 255 - ml)
+        return SIZE_MAX;
+    const size_t at = (acc + 255) / 256 * 256;
+    if (ml_at) *ml_at = at;
+    return at + ml;
+}
+
+// With units = (sequence, kv head, chunk) and `slots` CTAs resident at once: one
+// wave of equal partitions where the units leave room for several, in a cluster
+// (up to 8, no second launch) where that gives about as many; else, with more
+// units than slots, partitions of about 1024 tokens, so that long and ragged
+// sequences even out over the waves.
+Split split_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
+    Split sp;
+    const int per = 16 / (s->num_heads / s->num_kv_heads);
+    sp.chunk = q_len < per ? q_len : per;
+    sp.chunks = (q_len + sp.chunk - 1) / sp.chunk;
+    const int64_t pages = announced_tokens(max_context_len, s->block_size, s->max_blocks_per_seq) / s->block_size;
+    const int64_t units = (int64_t)s->batch * s->num_kv_heads * sp.chunks;
+    const int64_t slots = (int64_t)sms * (s->head_dim == 256 ? 2 : 3);
+    const int64_t fill = slots / units;
+    int64_t parts = 1;
+    sp.cluster = false;
+    if (fill >= 2) {
+        const int64_t in_cluster = std::min<int64_t>({8, fill, ceil_div(pages, 4)});
+        const int64_t apart = std::min(fill, ceil_div(pages, 16));
+        sp.cluster = in_cluster * 4 >= apart * 3;
+        parts = sp.cluster ? in_cluster : apart;
+    } else if (fill < 1) {
+        parts = ceil_div(pages * s->block_size, 1024);
+    }
+    parts = std::min<int64_t>(parts, kMaxJoinParts);
+    sp.part_pages = (int)ceil_div(pages, parts);
+    sp.parts = (int)ceil_div(pages, sp.part_pages);
+    if (sp.parts == 1) sp.cluster = false;
+    return sp;
 }
 
 }  // namespace
@@ -172,9 +227,12 @@ pa_status pa_rope_append_kv8(void* q_out, void* k_cache, void* v_cache, float* k
 }
 
 size_t pa_workspace_size_kv8(const pa_shape* shape, int32_t q_len, int32_t max_context_len) {
-    (void)max_context_len;
-    if (check_kv8(shape, q_len) != PA_OK) return 0;
-    return 0;
+    int sms = 0;
+    if (check_kv8(shape, q_len) != PA_OK || max_context_len < 0 || shape->batch == 0 ||
+        device_state(&sms, nullptr) != PA_OK)
+        return 0;
+    const Split sp = split_kv8(shape, q_len, max_context_len, sms);
+    return partial_bytes(sp, (size_t)shape->batch * q_len * shape->num_heads, shape->head_dim, nullptr);
 }
 
 pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -192,12 +250,12 @@ pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const voi
         !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_tables, 4) ||
         !aligned(context_lens, 4))
         return PA_ERR_INVALID_ARG;
-    const size_t values = (size_t)shape->batch * q_len * shape->num_heads * shape->head_dim;
-    const size_t cache = (size_t)shape->num_blocks * shape->block_size * shape->num_kv_heads *
-                         shape->head_dim;
-    const size_t scales = (size_t)shape->num_blocks * shape->num_kv_heads * 4;
-    const Span o{out, values * (shape->out_dtype == PA_F32 ? 4 : 2)};
-    const Span ins[7] = {{q, values * 2},
+    const int D = shape->head_dim, Hkv = shape->num_kv_heads, BS = shape->block_size;
+    const size_t rows = (size_t)shape->batch * q_len * shape->num_heads;
+    const size_t cache = (size_t)shape->num_blocks * BS * Hkv * D;
+    const size_t scales = (size_t)shape->num_blocks * Hkv * 4;
+    const Span o{out, rows * D * (shape->out_dtype == PA_F32 ? 4 : 2)};
+    const Span ins[7] = {{q, rows * D * 2},
                          {k_cache, cache},
                          {v_cache, cache},
                          {k_scales, scales},
@@ -206,34 +264,81 @@ pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const voi
                          {context_lens, (size_t)shape->batch * 4}};
     for (const Span& i : ins)
         if (overlap(o, i)) return PA_ERR_INVALID_ARG;
-    (void)workspace;
-    (void)workspace_bytes;
-    st = device_state(nullptr, nullptr);
+    int sms = 0;
+    int32_t* err = nullptr;
+    st = device_state(&sms, &err);
     if (st != PA_OK) return st;
-    Kv8Params p;
-    std::memset(&p, 0, sizeof p);
+    const Split sp = split_kv8(shape, q_len, max_context_len, sms);
+    size_t ml_at = 0;
+    const size_t need = partial_bytes(sp, rows, D, &ml_at);
+    if (need) {
+        if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return PA_ERR_WORKSPACE;
+        const Span w{workspace, need};
+        if (overlap(w, o)) return PA_ERR_INVALID_ARG;
+        for (const Span& i : ins)
+            if (overlap(w, i)) return PA_ERR_INVALID_ARG;
+    }
+    const int64_t grid_y = (int64_t)Hkv * sp.chunks;
+    if (grid_y > 65535) return PA_ERR_UNSUPPORTED;
+    Kv8Launch L;
+    std::memset(&L, 0, sizeof L);
+    // one kv head's rows of a page (a column block of at most 128 bytes), swizzled for the lanes' loads
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)Hkv, (uint64_t)BS, (uint64_t)shape->num_blocks};
+    const uint64_t strides[3] = {(uint64_t)D, (uint64_t)D * Hkv, (uint64_t)D * Hkv * BS};
+    const uint32_t box[4] = {D < 128 ? (uint32_t)D : 128u, 1u, (uint32_t)BS, 1u};
+    const CUtensorMapSwizzle swizzle = D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    st = encode_tiled(&L.tmap_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, k_cache, dims, strides, box, swizzle);
+    if (st == PA_OK)
+        st = encode_tiled(&L.tmap_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, v_cache, dims, strides, box, swizzle);
+    if (st != PA_OK) return st;
+    Kv8Params& p = L.p;
     p.q = q;
     p.out = out;
-    p.k_cache = static_cast<const uint8_t*>(k_cache);
-    p.v_cache = static_cast<const uint8_t*>(v_cache);
     p.k_scales = k_scales;
     p.v_scales = v_scales;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
+    p.part_acc = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_at);
+    p.err = err;
+    p.timeout_ns = kDefaultTimeoutNs;
     p.num_blocks = shape->num_blocks;
     p.qscale = scale * 1.4426950408889634f;  // log2(e)
-    p.batch = shape->batch;
     p.q_len = q_len;
     p.num_heads = shape->num_heads;
-    p.num_kv_heads = shape->num_kv_heads;
-    p.group = shape->num_heads / shape->num_kv_heads;
-    p.head_dim = shape->head_dim;
-    p.block_size = shape->block_size;
+    p.num_kv_heads = Hkv;
+    p.group = shape->num_heads / Hkv;
     p.max_blocks = shape->max_blocks_per_seq;
-    p.token_limit = announced_tokens(max_context_len, shape->block_size, shape->max_blocks_per_seq);
+    p.q_chunk = sp.chunk;
+    p.token_limit = announced_tokens(max_context_len, BS, shape->max_blocks_per_seq);
+    p.part_pages = sp.part_pages;
+    p.num_parts = sp.parts;
+    p.cluster = sp.cluster ? sp.parts : 1;
     p.out_dtype = shape->out_dtype;
-    return done(launch_kv8_attention(p, shape->kv_dtype == PA_BF16, use_pdl(),
-                                     static_cast<cudaStream_t>(stream)));
+    L.block_size = BS;
+    L.bf16 = shape->kv_dtype == PA_BF16;
+    L.pdl = use_pdl();
+    L.grid = dim3((unsigned)sp.parts, (unsigned)grid_y, (unsigned)shape->batch);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = D == 64 ? launch_kv8_d64(L, cs) : D == 128 ? launch_kv8_d128(L, cs)
+                                                                     : launch_kv8_d256(L, cs);
+    if (e != cudaSuccess || !need) return done(e);
+    JoinParams j;
+    std::memset(&j, 0, sizeof j);
+    j.out = out;
+    j.part_acc = p.part_acc;
+    j.part_ml = p.part_ml;
+    j.context_lens = context_lens;
+    j.width = D;
+    j.group = p.group;
+    j.unit_rows = q_len * p.group;
+    j.max_blocks = p.max_blocks;
+    j.block_size = BS;
+    j.token_limit = p.token_limit;
+    j.part_pages = sp.part_pages;
+    j.num_parts = sp.parts;
+    j.out_dtype = shape->out_dtype;
+    return done(launch_join(j, shape->batch, Hkv, L.pdl, cs));
 }
 
 pa_status pa_rope_append_latent(void* q_out, void* cache, const void* q, const void* latent_new,

@@ -166,18 +166,42 @@ struct Append8Params {
 struct Kv8Params {
     const void* q;            // [B, Q, H, D]
     void* out;
-    const uint8_t* k_cache;   // [num_blocks, block_size, Hkv, D] e4m3
-    const uint8_t* v_cache;
     const float* k_scales;    // [num_blocks, Hkv]
     const float* v_scales;
     const int32_t* block_tables;
     const int32_t* context_lens;
+    float* part_acc;          // [B, Hkv, P, Q * group, D] (partitions that the join kernel reads)
+    float* part_ml;           // [B, Hkv, P, Q * group, 2]
+    int32_t* err;             // device error word, bound on every wait
+    uint64_t timeout_ns;
     int64_t num_blocks;
     float qscale;             // scale * log2(e)
-    int32_t batch, q_len, num_heads, num_kv_heads, group, head_dim, block_size, max_blocks;
+    int32_t q_len, num_heads, num_kv_heads, group, max_blocks;
+    int32_t q_chunk;          // query tokens of a CTA (q_chunk * group <= 16)
     int32_t token_limit;      // tokens from here on are not attended to
+    int32_t part_pages, num_parts;
+    int32_t cluster;          // > 1: the num_parts partitions are a cluster and join there
     int32_t out_dtype;
 };
+
+struct Kv8Launch {
+    Kv8Params p;
+    CUtensorMap tmap_k, tmap_v;
+    int block_size;
+    bool bf16, pdl;
+    dim3 grid;
+};
+
+// Joining the partitions of an attention (8-bit or latent cache).
+struct JoinParams {
+    void* out;                // [B, Q, Hkv * group, width]
+    const float* part_acc;    // [B, Hkv, P, Q * group, width]
+    const float* part_ml;
+    const int32_t* context_lens;
+    int32_t width, group, unit_rows, max_blocks, block_size;
+    int32_t token_limit, part_pages, num_parts, out_dtype;
+};
+constexpr int kMaxJoinParts = 8192;
 
 // Append to the latent cache (strides in elements).
 struct LatentAppendParams {
@@ -536,7 +560,10 @@ cudaError_t launch_append(void* k_cache, void* v_cache, const void* k_new, const
 cudaError_t launch_rope_append(const RopeParams& p, bool bf16, int num_sms, bool pdl,
                                cudaStream_t stream);
 cudaError_t launch_append8(const Append8Params& p, bool bf16, bool pdl, cudaStream_t stream);
-cudaError_t launch_kv8_attention(const Kv8Params& p, bool bf16, bool pdl, cudaStream_t stream);
+cudaError_t launch_kv8_d64(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_kv8_d128(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_kv8_d256(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_join(const JoinParams& p, int batch, int num_kv_heads, bool pdl, cudaStream_t stream);
 cudaError_t launch_append_latent(LatentAppendParams p, bool bf16, int num_sms, bool pdl,
                                  cudaStream_t stream);
 cudaError_t launch_latent_attention(const LatentParams& p, bool bf16, bool pdl, cudaStream_t stream);
@@ -550,6 +577,12 @@ cudaError_t launch_resolve(int32_t* out_phys, const int32_t* block_tables,
 pa_status check_shape(const pa_shape* s);
 // SM count and error-word address of the current device (cached; either may be null).
 pa_status device_state(int* sms, int32_t** err);
+// A tiled tensor map (cuTensorMapEncodeTiled) with strides of 1.
+pa_status encode_tiled(CUtensorMap* map, CUtensorMapDataType type, uint32_t rank, const void* base,
+                       const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                       CUtensorMapSwizzle swizzle);
+// The bound on every wait of a copy pipeline.
+constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;  // 2 s per wait
 // Whether launches carry the programmatic stream serialization attribute.
 bool use_pdl();
 inline bool aligned(const void* ptr, size_t a) { return reinterpret_cast<uintptr_t>(ptr) % a == 0; }
