@@ -56,6 +56,17 @@ pa_status check_latent(const pa_latent_shape* s) {
     return PA_OK;
 }
 
+pa_status check_latent_call(const pa_latent_shape* s, int32_t q_len) {
+    const pa_status st = check_latent(s);
+    if (st != PA_OK) return st;
+    if (q_len < 1) return PA_ERR_INVALID_ARG;
+    // rows of a sequence, and row tiles of a call, inside 31 bits
+    const int64_t rows = (int64_t)q_len * s->num_heads;
+    if (rows > (1 << 24) || rows * s->batch > (1ll << 31) - 1 || s->batch * ((rows + 15) / 16) > 65535 * 64ll)
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
 // Tokens of the pages that max_context_len announces, inside the table's reach.
 int announced_tokens(int32_t max_context_len, int block_size, int max_blocks) {
     const int64_t t = max_context_len < 1 ? 1 : max_context_len;
@@ -127,6 +138,43 @@ Split split_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int s
     sp.parts = (int)ceil_div(pages, sp.part_pages);
     if (sp.parts == 1) sp.cluster = false;
     return sp;
+}
+
+// How a call over the latent cache runs: row tiles of 16, 32 or 64, the CTAs in
+// groups that walk the same tokens; equal runs of tiles over one CTA an SM,
+// whatever the lengths, where the batch is small enough for each CTA to look
+// all lengths through (2048: 2 us), else one group to a (sequence, row group).
+struct LatentPlan {
+    int row_tile, row_tiles, row_groups, group_size;
+    bool balanced;
+    int64_t ctas;
+    size_t ml_at, desc_at, bytes;  // workspace; bytes 0: no sequence can be cut
+};
+constexpr int kMaxLatentBalanced = 2048;
+
+LatentPlan plan_latent(const pa_latent_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
+    LatentPlan pl;
+    const int64_t rows = (int64_t)q_len * s->num_heads;
+    pl.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    pl.row_tiles = (int)ceil_div(rows, pl.row_tile);
+    pl.row_groups = (int)ceil_div(pl.row_tiles, 8);
+    pl.group_size = (int)ceil_div(pl.row_tiles, pl.row_groups);
+    pl.balanced = s->batch <= kMaxLatentBalanced;
+    int64_t groups = (int64_t)s->batch * pl.row_groups;
+    if (pl.balanced) {
+        const int64_t tiles = ceil_div(announced_tokens(max_context_len, s->block_size, s->max_blocks_per_seq), 64);
+        groups = std::max<int64_t>(std::min<int64_t>(sms / pl.group_size, groups * tiles), 1);
+    }
+    pl.ctas = groups * pl.group_size;
+    pl.ml_at = pl.desc_at = pl.bytes = 0;
+    if (pl.balanced && groups > 1) {
+        auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+        const size_t records = (size_t)pl.ctas * 2 * pl.row_tile;
+        pl.ml_at = up(records * s->latent_dim * 4);
+        pl.desc_at = up(pl.ml_at + records * 8);
+        pl.bytes = pl.desc_at + (size_t)s->batch * pl.row_tiles * sizeof(LatentDesc);
+    }
+    return pl;
 }
 
 }  // namespace
@@ -423,9 +471,11 @@ pa_status pa_rope_append_latent(void* q_out, void* cache, const void* q, const v
 }
 
 size_t pa_workspace_size_latent(const pa_latent_shape* shape, int32_t q_len, int32_t max_context_len) {
-    (void)max_context_len;
-    if (check_latent(shape) != PA_OK || q_len < 1) return 0;
-    return 0;
+    int sms = 0;
+    if (check_latent_call(shape, q_len) != PA_OK || max_context_len < 0 || shape->batch == 0 ||
+        device_state(&sms, nullptr) != PA_OK)
+        return 0;
+    return plan_latent(shape, q_len, max_context_len, sms).bytes;
 }
 
 pa_status pa_decode_latent(void* out, const void* q, const void* cache,
@@ -433,10 +483,9 @@ pa_status pa_decode_latent(void* out, const void* q, const void* cache,
                            const pa_latent_shape* shape, int32_t q_len, float scale,
                            int32_t max_context_len, void* workspace, size_t workspace_bytes,
                            void* stream) {
-    pa_status st = check_latent(shape);
+    pa_status st = check_latent_call(shape, q_len);
     if (st != PA_OK) return st;
-    if (q_len < 1 || max_context_len < 0 || !scale_ok(scale)) return PA_ERR_INVALID_ARG;
-    if ((int64_t)q_len * shape->num_heads > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    if (max_context_len < 0 || !scale_ok(scale)) return PA_ERR_INVALID_ARG;
     if (shape->batch == 0) return PA_OK;
     if (!out || !q || !cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(cache, 16) || !aligned(block_tables, 4) ||
@@ -451,28 +500,65 @@ pa_status pa_decode_latent(void* out, const void* q, const void* cache,
                          {context_lens, (size_t)shape->batch * 4}};
     for (const Span& i : ins)
         if (overlap(o, i)) return PA_ERR_INVALID_ARG;
-    (void)workspace;
-    (void)workspace_bytes;
-    st = device_state(nullptr, nullptr);
+    int sms = 0;
+    int32_t* err = nullptr;
+    st = device_state(&sms, &err);
     if (st != PA_OK) return st;
-    LatentParams p;
-    std::memset(&p, 0, sizeof p);
+    const LatentPlan pl = plan_latent(shape, q_len, max_context_len, sms);
+    if (pl.bytes) {
+        if (!workspace || !aligned(workspace, 16) || workspace_bytes < pl.bytes) return PA_ERR_WORKSPACE;
+        const Span w{workspace, pl.bytes};
+        if (overlap(w, o)) return PA_ERR_INVALID_ARG;
+        for (const Span& i : ins)
+            if (overlap(w, i)) return PA_ERR_INVALID_ARG;
+    }
+    LatentLaunch L;
+    std::memset(&L, 0, sizeof L);
+    const CUtensorMapDataType type = shape->dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    // 64 elements (128 bytes) of a page's rows, and of a row tile's queries
+    const uint64_t cd[4] = {W, (uint64_t)shape->block_size, (uint64_t)shape->num_blocks, 1};
+    const uint64_t cs[3] = {W * 2, W * 2 * shape->block_size, W * 2 * shape->block_size * (uint64_t)shape->num_blocks};
+    const uint32_t cb[4] = {64, (uint32_t)shape->block_size, 1, 1};
+    st = encode_tiled(&L.tmap_c, type, 4, cache, cd, cs, cb, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != PA_OK) return st;
+    const uint64_t qd[2] = {W, rows}, qs[1] = {W * 2};
+    const uint32_t qb[2] = {64, (uint32_t)pl.row_tile};
+    st = encode_tiled(&L.tmap_q, type, 2, q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != PA_OK) return st;
+    LatentParams& p = L.p;
+    char* ws = static_cast<char*>(workspace);
     p.q = q;
     p.out = out;
-    p.cache = cache;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
+    p.part_acc = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + pl.ml_at);
+    p.part_desc = reinterpret_cast<LatentDesc*>(ws + pl.desc_at);
+    p.err = err;
+    p.timeout_ns = kDefaultTimeoutNs;
     p.num_blocks = shape->num_blocks;
     p.qscale = scale * 1.4426950408889634f;  // log2(e)
     p.batch = shape->batch;
     p.q_len = q_len;
     p.num_heads = shape->num_heads;
-    p.latent_dim = shape->latent_dim;
     p.block_size = shape->block_size;
     p.max_blocks = shape->max_blocks_per_seq;
     p.token_limit = announced_tokens(max_context_len, shape->block_size, shape->max_blocks_per_seq);
-    return done(launch_latent_attention(p, shape->dtype == PA_BF16, use_pdl(),
-                                        static_cast<cudaStream_t>(stream)));
+    p.row_tiles = pl.row_tiles;
+    p.group_size = pl.group_size;
+    p.row_groups = pl.row_groups;
+    p.balanced = pl.bytes ? 1 : 0;
+    L.row_tile = pl.row_tile;
+    L.ctas = (int)pl.ctas;
+    L.sms = sms;
+    L.bf16 = shape->dtype == PA_BF16;
+    L.pdl = use_pdl();
+    L.join = pl.bytes != 0;
+    cudaStream_t stm = static_cast<cudaStream_t>(stream);
+    return done(shape->latent_dim == 128   ? launch_latent_r128(L, stm)
+                : shape->latent_dim == 256 ? launch_latent_r256(L, stm)
+                                           : launch_latent_r512(L, stm));
 }
 
 }  // extern "C"

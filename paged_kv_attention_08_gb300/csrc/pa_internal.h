@@ -220,17 +220,40 @@ struct LatentAppendParams {
     int32_t span;             // tokens of a CTA
 };
 
+// Where the pieces of a (sequence, row tile) lie: in the records of CTA groups
+// first_group .. last_group that have tiles (record 0, in the first group
+// first_record), CTA `member` of each.
+struct LatentDesc {
+    int32_t first_group, last_group, first_record, member;
+    int64_t total;            // tiles of the call's flat order
+};
+
 // Attention over the latent cache.
 struct LatentParams {
     const void* q;            // [B, Q, H, latent_dim + 64]
     void* out;                // [B, Q, H, latent_dim]
-    const void* cache;        // [num_blocks, block_size, latent_dim + 64]
     const int32_t* block_tables;
     const int32_t* context_lens;
+    float* part_acc;          // [CTAs][2 records][row tile][latent_dim]
+    float* part_ml;           // [CTAs][2][row tile][2]
+    LatentDesc* part_desc;    // [B][row tiles]
+    int32_t* err;             // device error word, bound on every wait
+    uint64_t timeout_ns;
     int64_t num_blocks;
     float qscale;             // scale * log2(e)
-    int32_t batch, q_len, num_heads, latent_dim, block_size, max_blocks;
+    int32_t batch, q_len, num_heads, block_size, max_blocks;
     int32_t token_limit;      // tokens from here on are not attended to
+    int32_t row_tiles;        // of a sequence
+    int32_t group_size;       // adjacent CTAs that walk the same tokens, a row tile each
+    int32_t row_groups;       // groups of row tiles of a sequence
+    int32_t balanced;         // 1: equal runs of tiles; 0: a CTA group to a (sequence, row group)
+};
+
+struct LatentLaunch {
+    LatentParams p;
+    CUtensorMap tmap_c, tmap_q;
+    int row_tile, ctas, sms;
+    bool bf16, pdl, join;
 };
 
 // Eviction by accumulated weight.
@@ -566,7 +589,9 @@ cudaError_t launch_kv8_d256(const Kv8Launch& L, cudaStream_t stream);
 cudaError_t launch_join(const JoinParams& p, int batch, int num_kv_heads, bool pdl, cudaStream_t stream);
 cudaError_t launch_append_latent(LatentAppendParams p, bool bf16, int num_sms, bool pdl,
                                  cudaStream_t stream);
-cudaError_t launch_latent_attention(const LatentParams& p, bool bf16, bool pdl, cudaStream_t stream);
+cudaError_t launch_latent_r128(const LatentLaunch& L, cudaStream_t stream);
+cudaError_t launch_latent_r256(const LatentLaunch& L, cudaStream_t stream);
+cudaError_t launch_latent_r512(const LatentLaunch& L, cudaStream_t stream);
 cudaError_t launch_evict(EvictParams p, bool in_place, bool pdl, cudaStream_t stream);
 cudaError_t launch_wait_timeout(int32_t* err, uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t launch_resolve(int32_t* out_phys, const int32_t* block_tables,

@@ -1,0 +1,742 @@
+// Attention over the latent cache on the Blackwell tensor cores (tcgen05).
+//
+// The mathematics: with c_t the vector of token t (latent part of R elements,
+// positional part of 64) and q_r a query row (query token, head),
+//     out_r = sum_t 2^(s_rt - m_r) c_t[:R] / sum_t 2^(s_rt - m_r),  s_rt = scale log2(e) q_r . c_t.
+// All heads share the tokens, so that one read of a token serves every row.
+//
+// Both products are formed transposed, tokens and value elements in the MMAs' M
+// and query rows in their N:
+//     S^T [64 tokens x N] = C [64 x (R + 64)] Q^T,      M = 64
+//     O^T [R x N]        += C[:, :R]^T [R x 64] P^T,    M = 128, R / 128 of them
+// so that the tile of tokens that TMA has put into shared memory is the A
+// operand of both (K-major for the first, M-major for the second), 16, 32 or
+// 64 rows cost what they are instead of a tile of 128, and O^T of 64 rows takes
+// 256 columns of tensor memory where O would take all 512 (R = 512).
+//
+// A CTA (one to an SM) takes a run of the flattened (sequence, group of row tiles,
+// 64-token tile) order, the same number of tiles as every other CTA whatever the
+// lengths: a run is a few segments of one sequence each.  A segment that is a
+// sequence whole writes its output; of one that is cut the pieces' (m, l, O) go to
+// the workspace and join_latent_kernel joins them.  The CTAs of a group (adjacent
+// blocks) walk the same tokens for different row tiles, the second reader from L2.
+// Roles:
+//   warp 0      copies: Q of a segment, and the tiles in rings of slots: pairs of
+//               64-element column blocks (16 KB) and the positional block (8 KB);
+//               a slot is loaded again as soon as its own MMAs are done
+//   warp 1      issues S^T of a tile as its slots land, a tile ahead
+//   warp 2      issues O^T += C^T P^T as P lands in shared memory
+//   warp 3      owns tensor memory
+//   warps 4-7   softmax: a thread has two tokens and N / 4 rows; P^T to shared
+//               memory, rescales of O^T, the output
+// The running maxima move only where a score is 2^8 above them: a tile then costs
+// one vote of the warpgroup, no reduction over tokens.  The normalisers are
+// summed a thread's tokens at a time and joined at the segment's end.
+#pragma once
+
+#include <type_traits>
+
+#include "pa_device.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+
+constexpr int kLatentTile = 64;      // tokens of a tile
+constexpr int kLatentThreads = 256;
+constexpr int kLatentP = 64;         // positional elements
+
+template <int R, int N>
+struct LatentCfg {
+    static constexpr int MB = R / 128;                         // value blocks of a tile
+    static constexpr uint32_t Q_BYTES = N * (R + kLatentP) * 2u;
+    static constexpr int PBUF = (R == 512 && N == 64) ? 1 : 2;  // P^T buffers
+    static constexpr uint32_t P_BYTES = kLatentTile * 128u;
+    static constexpr uint32_t PAIR = 2u * kLatentTile * 128u, ROPE = kLatentTile * 128u;
+    static constexpr uint32_t BUDGET = 229376u;                // leaves 2 KB for barriers and statistics
+    // as many tiles' worth of slots as fit, whole pairs
+    static constexpr uint32_t TILE = MB * PAIR + ROPE;
+    static constexpr uint32_t FREE = BUDGET - Q_BYTES - PBUF * P_BYTES;
+    static constexpr int NR = FREE / TILE > 6 ? 6 : FREE / TILE;                 // positional slots
+    static constexpr int NP_RAW = (FREE - NR * ROPE) / PAIR;
+    static constexpr int NP = NP_RAW > 12 ? 12 : NP_RAW;       // pair slots
+    static constexpr uint32_t P_OFF = Q_BYTES;
+    static constexpr uint32_t ROPE_OFF = P_OFF + PBUF * P_BYTES;
+    static constexpr uint32_t PAIR_OFF = ROPE_OFF + NR * ROPE;
+    static constexpr uint32_t STAT_OFF = PAIR_OFF + NP * PAIR;  // wmax [4][N], fac [N], lim [N]
+    static constexpr uint32_t LIVE_OFF = STAT_OFF + 6 * N * 4;  // [16] 64-bit masks
+    static constexpr uint32_t BAR_OFF = LIVE_OFF + 16 * 8;
+    static constexpr int BARS = 2 * NP + 2 * NR + 15;
+    static constexpr uint32_t MISC_OFF = BAR_OFF + BARS * 8;    // tmem address, abort flag, run
+    static constexpr uint32_t SMEM = MISC_OFF + 64 + kSmemAlignSlack;
+    static_assert(SMEM <= 227u * 1024u, "shared memory");
+    static_assert(NP >= 2 * MB && NR >= 2, "two tiles in flight");
+    static constexpr uint32_t COLS_RAW = (2 + MB) * N;
+    static constexpr uint32_t COLS = COLS_RAW <= 64 ? 64 : COLS_RAW <= 128 ? 128 : COLS_RAW <= 256 ? 256 : 512;
+};
+
+namespace tc {
+
+// Lanes base .. base + 15 of the warp's quarter, 8 J consecutive columns: register
+// 4 j + 2 h + e of lane l holds lane base + l / 4 + 8 h, column 8 j + 2 (l % 4) + e.
+template <int J>
+__device__ __forceinline__ void ld_16x256b(uint32_t taddr, float* r);
+template <>
+__device__ __forceinline__ void ld_16x256b<2>(uint32_t taddr, float* r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+                   "=f"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+template <>
+__device__ __forceinline__ void ld_16x256b<4>(uint32_t taddr, float* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+          "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void ld_16x256b<8>(uint32_t taddr, float* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+          "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]),
+          "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]),
+          "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+}  // namespace tc
+
+// 2-D tiled TMA load; completion is signalled on `bar` as transaction bytes.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// The softmax warpgroup's barrier (1), and whether any of its threads votes yes.
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool vote) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((uint32_t)vote) : "memory");
+    return r != 0;
+}
+
+// Tiles of a sequence: those of its attended tokens, one (with none) for an
+// empty one, whose output is zeros.
+__device__ __forceinline__ int latent_reach(const LatentParams& p, int b) {
+    return min(min(max(__ldg(p.context_lens + b), 0), p.max_blocks * p.block_size), p.token_limit);
+}
+__device__ __forceinline__ int latent_tiles(const LatentParams& p, int b) {
+    return max((latent_reach(p, b) + kLatentTile - 1) / kLatentTile, 1);
+}
+
+// One CTA's part of the work: tiles [k0, k1) of row tile rt of sequence b, of n.
+struct LatentSeg {
+    int b, rt, k0, k1, n;
+    long long first;  // flat position of the (sequence, row tile group)'s tile 0
+};
+
+template <int R, int N, typename T>
+__global__ void __launch_bounds__(kLatentThreads, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_q,
+                  const LatentParams p) {
+    using C = LatentCfg<R, N>;
+    constexpr int MB = C::MB, NP = C::NP, NR = C::NR, PBUF = C::PBUF;
+    constexpr float NEG_INF = -INFINITY;
+    constexpr bool kBF = std::is_same<T, __nv_bfloat16>::value;
+    constexpr float kSlack = 8.f, kLift = kBF ? 0.f : kHalfLift;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + (kSmemAlignSlack - 1)) & ~uintptr_t(kSmemAlignSlack - 1));
+    const uint32_t sbase = smem_u32(smem);
+    float* wmax = reinterpret_cast<float*>(smem + C::STAT_OFF);  // [4][N]
+    float* fac = wmax + 4 * N;                                   // [N]
+    int32_t* lim = reinterpret_cast<int32_t*>(fac + N);          // [N]
+    uint64_t* live = reinterpret_cast<uint64_t*>(smem + C::LIVE_OFF);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+    uint64_t *pair_full = bar, *pair_free = pair_full + NP, *rope_full = pair_free + NP,
+             *rope_free = rope_full + NR, *s_full = rope_free + NR, *s_free = s_full + 2,
+             *p_full = s_free + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *q_free = q_full + 1,
+             *o_free = q_free + 1, *final_s = o_free + 1, *final_o = final_s + 1,
+             *live_full = final_o + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+    // start, end, flat position of the first sequence's tiles, total
+    long long* run = reinterpret_cast<long long*>(smem + C::MISC_OFF + 8);
+    int32_t* run_b = reinterpret_cast<int32_t*>(run + 4);  // the first sequence
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int BS = p.block_size, rows = p.q_len * p.num_heads;
+    const int member = (int)blockIdx.x % p.group_size, group = (int)blockIdx.x / p.group_size;
+
+    if (tid == 0) {
+        for (int i = 0; i < NP; ++i) mbar_init(smem_u32(pair_full + i), 1), mbar_init(smem_u32(pair_free + i), 1);
+        for (int i = 0; i < NR; ++i) mbar_init(smem_u32(rope_full + i), 1), mbar_init(smem_u32(rope_free + i), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(s_full + i), 1);
+            mbar_init(smem_u32(s_free + i), 128);
+            mbar_init(smem_u32(p_full + i), 128);
+            mbar_init(smem_u32(pv_done + i), 1);
+            mbar_init(smem_u32(live_full + i), 1);
+        }
+        mbar_init(smem_u32(q_full), 1);
+        mbar_init(smem_u32(q_free), 1);
+        mbar_init(smem_u32(o_free), 128);
+        mbar_init(smem_u32(final_s), 1);
+        mbar_init(smem_u32(final_o), 1);
+        *abort_flag = 0;
+        mbar_init_fence();
+        prefetch_tensormap(&tmap_c);
+        prefetch_tensormap(&tmap_q);
+    }
+    if (warp == 3) {
+        tc::tmem_alloc(smem_u32(tmem_slot), C::COLS);
+        tc::tmem_relinquish();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- the CTA's run [start, end) of the flat order (sequence, group of row
+    // tiles, tile), where it begins ----
+    if (warp == 0) {
+        if (p.balanced) {
+            long long w = 0;
+            for (int b = lane; b < p.batch; b += 32) w += latent_tiles(p, b);
+#pragma unroll
+            for (int m = 16; m >= 1; m >>= 1) w += __shfl_xor_sync(kFullMask, w, m);
+            w *= p.row_groups;
+            const long long groups = gridDim.x / p.group_size;
+            const long long start = group * w / groups, end = (group + 1) * w / groups;
+            int b = 0;
+            long long base = 0;
+            while (start < end) {
+                const int bb = b + lane;
+                const long long v = bb < p.batch ? (long long)latent_tiles(p, bb) * p.row_groups : 0;
+                long long incl = v;
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const long long o = __shfl_up_sync(kFullMask, incl, m);
+                    if (lane >= m) incl += o;
+                }
+                const unsigned hit = __ballot_sync(kFullMask, bb < p.batch && base + incl > start);
+                if (hit) {
+                    const int k = __ffs(hit) - 1;
+                    base += __shfl_sync(kFullMask, incl - v, k);
+                    b += k;
+                    break;
+                }
+                base += __shfl_sync(kFullMask, incl, 31);
+                b += 32;
+            }
+            if (lane == 0) run[0] = start, run[1] = end, run[2] = base, run[3] = w, *run_b = b;
+        } else if (lane == 0) {
+            // one (sequence, row tile group) to a CTA group, whole
+            const int b = group / p.row_groups, x = group % p.row_groups;
+            const int n = latent_tiles(p, b);
+            run[0] = (long long)x * n, run[1] = (long long)(x + 1) * n, run[2] = 0, *run_b = b;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const long long run_start = run[0], run_end = run[1];
+
+    // f(segment, its number): the run's segments of this CTA's row tiles in order,
+    // until f returns false.  Every role walks them alike.
+    auto for_segments = [&](auto&& f) {
+        int b = *run_b, s = 0;
+        long long base = run[2];
+        for (long long at = run_start; at < run_end;) {
+            const int n = latent_tiles(p, b);
+            const int x = (int)((at - base) / n), k0 = (int)((at - base) % n);
+            const int k1 = (int)min((long long)n, k0 + (run_end - at));
+            LatentSeg g{b, x * p.group_size + member, k0, k1, n, base + (long long)x * n};
+            at += k1 - k0;
+            if (at - base >= (long long)n * p.row_groups) base += (long long)n * p.row_groups, ++b;
+            if (g.rt * N >= rows) continue;  // (a group's row tiles past the last)
+            if (!f(g, s++)) return;
+        }
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool ok = mbar_wait_bounded(smem_u32(bar), parity, p.timeout_ns);
+        if (!ok) {
+            record_error(p.err, PA_ERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        return ok;
+    };
+    constexpr int kType = kBF ? 1 : 0;
+
+    if (warp == 0) {
+        // ================= copies =================
+        const int PG = kLatentTile / BS;  // pages of a tile
+        int tile = 0, pairs = 0, segs = 0;
+        for_segments([&](const LatentSeg& g, int s) {
+            const int32_t* row = p.block_tables + (size_t)g.b * p.max_blocks;
+            const int npages = (latent_reach(p, g.b) + BS - 1) / BS;
+            // lane l < PG: the entry of page l of the tile, one tile ahead
+            auto fetch = [&](int k) -> int {
+                return lane < PG ? page_phys(row, k * PG + lane, npages, p.num_blocks) : -1;
+            };
+            int next = fetch(g.k0);
+            if (s > 0 && !__all_sync(kFullMask, wait(q_free, (s - 1) & 1))) return false;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(smem_u32(q_full), C::Q_BYTES);
+                for (int c = 0; c < (R + kLatentP) / 64; ++c)
+                    tma_load_2d(sbase + c * N * 128, &tmap_q, c * 64, g.b * rows + g.rt * N, smem_u32(q_full));
+            }
+            segs = s + 1;
+            const uint64_t policy = p.group_size > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+            for (int k = g.k0; k < g.k1 && !*abort_flag; ++k, ++tile) {
+                const int phys = next;
+                if (k + 1 < g.k1) next = fetch(k + 1);
+                const unsigned on = __ballot_sync(kFullMask, phys >= 0);
+                // one slot: `blocks` column blocks from element `col` on
+                auto load = [&](uint64_t* full, uint32_t dst, int col, int blocks) {
+                    if (lane == 0) {
+                        if (on) mbar_arrive_expect_tx(smem_u32(full), (uint32_t)__popc(on) * BS * 128u * blocks);
+                        else mbar_arrive(smem_u32(full));
+                    }
+                    __syncwarp();
+                    if (phys >= 0)
+                        for (int c = 0; c < blocks; ++c)
+                            tma_load_4d(dst + c * C::ROPE + lane * BS * 128, &tmap_c, col + c * 64, 0, phys, 0,
+                                        smem_u32(full), policy);
+                };
+                const int rs = tile % NR;
+                if (tile >= NR && !__all_sync(kFullMask, wait(rope_free + rs, (tile / NR - 1) & 1))) return false;
+                if (lane == 0) {
+                    // the tile's tokens that a page holds
+                    uint64_t m = 0;
+                    for (int l = 0; l < PG; ++l)
+                        if (on >> l & 1) m |= (BS == 64 ? ~0ull : (1ull << BS) - 1) << (l * BS);
+                    live[tile & 15] = m;
+                }
+                load(rope_full + rs, sbase + C::ROPE_OFF + rs * C::ROPE, R, 1);
+                for (int m = 0; m < MB; ++m, ++pairs) {
+                    const int ps = pairs % NP;
+                    if (pairs >= NP && !__all_sync(kFullMask, wait(pair_free + ps, (pairs / NP - 1) & 1)))
+                        return false;
+                    load(pair_full + ps, sbase + C::PAIR_OFF + ps * C::PAIR, m * 128, 2);
+                }
+            }
+            return !*abort_flag;
+        });
+        if (*abort_flag && lane == 0) {
+            // copies in flight land before the CTA ends
+            for (int k = max(0, pairs - NP); k < pairs; ++k)
+                (void)mbar_wait_bounded(smem_u32(pair_full + k % NP), (k / NP) & 1, p.timeout_ns);
+            for (int k = max(0, tile - NR); k <= tile; ++k)
+                (void)mbar_wait_bounded(smem_u32(rope_full + k % NR), (k / NR) & 1, p.timeout_ns);
+            if (segs) (void)mbar_wait_bounded(smem_u32(q_full), (segs - 1) & 1, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= S^T = C Q^T =================
+        if (lane == 0) {
+            constexpr uint32_t idesc = tc::idesc_f16(kType, false, 64, N);
+            int tile = 0, pairs = 0;
+            for_segments([&](const LatentSeg& g, int s) {
+                if (!wait(q_full, s & 1)) return false;
+                for (int k = g.k0; k < g.k1 && !*abort_flag; ++k, ++tile) {
+                    if (tile >= 2 && !wait(s_free + (tile & 1), (tile / 2 - 1) & 1)) return false;
+                    const int rs = tile % NR;
+                    if (!wait(rope_full + rs, (tile / NR) & 1)) return false;
+                    mbar_arrive(smem_u32(live_full + (tile & 1)));  // hands the tile's mask on
+                    tc::fence_after_sync();
+                    const uint32_t d = tmem + (tile & 1) * N;
+                    auto block = [&](uint32_t a, int c, bool accumulate) {  // 64 elements
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_ss(d, tc::smem_desc(a + kk * 32, 16, 1024, tc::kSwizzle128B),
+                                       tc::smem_desc(sbase + c * N * 128 + kk * 32, 16, 1024, tc::kSwizzle128B),
+                                       idesc, accumulate || kk > 0);
+                    };
+                    block(sbase + C::ROPE_OFF + rs * C::ROPE, R / 64, false);
+                    for (int m = 0; m < MB; ++m, ++pairs) {
+                        const int ps = pairs % NP;
+                        if (!wait(pair_full + ps, (pairs / NP) & 1)) return false;
+                        tc::fence_after_sync();
+                        const uint32_t a = sbase + C::PAIR_OFF + ps * C::PAIR;
+                        block(a, 2 * m, true);
+                        block(a + C::ROPE, 2 * m + 1, true);
+                    }
+                    tc::commit(smem_u32(rope_free + rs));
+                    tc::commit(smem_u32(s_full + (tile & 1)));
+                }
+                tc::commit(smem_u32(q_free));
+                return !*abort_flag;
+            });
+            tc::commit(smem_u32(final_s));
+            (void)mbar_wait_bounded(smem_u32(final_s), 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ================= O^T += C^T P^T =================
+        if (lane == 0) {
+            // A and B both M- / N-major: elements and rows contiguous, tokens the rows of 128 bytes
+            constexpr uint32_t idesc = tc::idesc_f16(kType, true, 128, N) | (1u << 15);
+            int tile = 0, pairs = 0;
+            for_segments([&](const LatentSeg& g, int s) {
+                if (s > 0 && !wait(o_free, (s - 1) & 1)) return false;  // the last output is read
+                for (int k = g.k0; k < g.k1 && !*abort_flag; ++k, ++tile) {
+                    const int pb = tile % PBUF;
+                    if (!wait(p_full + pb, (tile / PBUF) & 1)) return false;
+                    tc::fence_after_sync();
+                    const uint32_t pt = sbase + C::P_OFF + pb * C::P_BYTES;
+                    for (int m = 0; m < MB; ++m, ++pairs) {
+                        const int ps = pairs % NP;
+                        const uint32_t a = sbase + C::PAIR_OFF + ps * C::PAIR;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)  // 16 tokens
+                            tc::mma_ss(tmem + (2 + m) * N,
+                                       tc::smem_desc(a + kk * 2048, C::ROPE, 1024, tc::kSwizzle128B),
+                                       tc::smem_desc(pt + kk * 2048, C::P_BYTES, 1024, tc::kSwizzle128B), idesc,
+                                       k > g.k0 || kk > 0);
+                        tc::commit(smem_u32(pair_free + ps));
+                    }
+                    tc::commit(smem_u32(pv_done + (tile & 1)));
+                }
+                return !*abort_flag;
+            });
+            tc::commit(smem_u32(final_o));
+            (void)mbar_wait_bounded(smem_u32(final_o), 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ================= softmax =================
+        constexpr int J = N / 8;              // groups of 8 rows; a thread has two rows of each
+        const int w = warp - 4, quarter = w << 21;   // lanes 32 w on: tokens 16 w on in lanes 32 w .. + 15
+        const int tg = lane >> 2, tq = lane & 3;
+        int tile = 0, pairs = 0;
+        for_segments([&](const LatentSeg& g, int s) {
+            const int ctx = max(__ldg(p.context_lens + g.b), 0), reach = latent_reach(p, g.b);
+            const int r0 = g.rt * N;
+            softmax_sync();  // the last segment's statistics are read
+            for (int c = w * 32 + lane; c < N; c += 128)
+                lim[c] = r0 + c < rows ? min(reach, ctx - p.q_len + (r0 + c) / p.num_heads + 1) : reach;
+            const int least = min(reach, ctx - p.q_len + r0 / p.num_heads + 1);
+            float ref[2 * J], sum[2 * J];     // reference exponents and normalisers of the thread's rows
+#pragma unroll
+            for (int i = 0; i < 2 * J; ++i) ref[i] = NEG_INF, sum[i] = 0.f;
+            for (int k = g.k0; k < g.k1; ++k, ++tile, pairs += MB) {
+                const int t0 = k * kLatentTile;
+                wait(s_full + (tile & 1), (tile / 2) & 1);
+                wait(live_full + (tile & 1), (tile / 2) & 1);
+                tc::fence_after_sync();
+                uint64_t valid = live[tile & 15];
+                if (reach - t0 < kLatentTile) valid &= reach > t0 ? (1ull << (reach - t0)) - 1 : 0ull;
+                float x[4 * J];
+                tc::ld_16x256b<J>(tmem + quarter + (tile & 1) * N, x);
+                tc::wait_ld();
+                tc::fence_before_sync();
+                mbar_arrive(smem_u32(s_free + (tile & 1)));
+                const bool masked = valid != ~0ull || least < t0 + kLatentTile;
+#pragma unroll
+                for (int i = 0; i < 4 * J; ++i) x[i] *= p.qscale;
+                if (masked) {
+                    if (k == g.k0) softmax_sync();  // lim
+#pragma unroll
+                    for (int i = 0; i < 4 * J; ++i) {
+                        const int t = w * 16 + tg + (i & 2) * 4, c = (i >> 2) * 8 + tq * 2 + (i & 1);
+                        if (!(valid >> t & 1) || t0 + t >= lim[c]) x[i] = NEG_INF;
+                    }
+                }
+                float above = NEG_INF;
+#pragma unroll
+                for (int i = 0; i < 4 * J; ++i) above = fmaxf(above, x[i] - ref[(i >> 2) * 2 + (i & 1)]);
+                // (an abort anywhere brings all of the warpgroup to the second vote)
+                if (softmax_any(above > kSlack + kLift || *abort_flag)) {
+                    if (softmax_any(*abort_flag)) return false;
+                    // some row's maximum has risen: the tile's maxima, new references
+#pragma unroll
+                    for (int i = 0; i < 2 * J; ++i) {
+                        float v = fmaxf(x[(i >> 1) * 4 + (i & 1)], x[(i >> 1) * 4 + 2 + (i & 1)]);
+                        v = fmaxf(v, __shfl_xor_sync(kFullMask, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(kFullMask, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(kFullMask, v, 16));
+                        if (tg == 0) wmax[w * N + (i >> 1) * 8 + tq * 2 + (i & 1)] = v;
+                    }
+                    softmax_sync();
+#pragma unroll
+                    for (int i = 0; i < 2 * J; ++i) {
+                        const int c = (i >> 1) * 8 + tq * 2 + (i & 1);
+                        const float v = fmaxf(fmaxf(wmax[c], wmax[N + c]), fmaxf(wmax[2 * N + c], wmax[3 * N + c]));
+                        const float to = fmaxf(ref[i], v - kLift);
+                        const float f = to == ref[i] ? 1.f : fast_exp2(ref[i] - to);
+                        if (w == 0 && tg == 0) fac[c] = f;
+                        ref[i] = to;
+                        sum[i] *= f;
+                    }
+                    if (k > g.k0) wait(pv_done + ((tile - 1) & 1), ((tile - 1) / 2) & 1);
+                    softmax_sync();
+                    if (k > g.k0) {
+                        // O^T (elements in lanes, rows in columns) on the new references
+                        tc::fence_after_sync();
+                        for (int c0 = 0; c0 < MB * N; c0 += 16) {
+                            uint32_t o[16];
+                            tc::ld_32x32b_x16(tmem + quarter + 2 * N + c0, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[c0 % N + i]);
+                            tc::st_32x32b_x16(tmem + quarter + 2 * N + c0, o);
+                        }
+                        tc::wait_st();
+                    }
+                }
+                // ---- weights, rounded to the cache's type as they meet the values ----
+                uint32_t pk[2 * J];
+#pragma unroll
+                for (int i = 0; i < 2 * J; ++i) {
+                    // i: group j = i / 2, token tg or tg + 8; two neighbouring rows
+                    const int a = (i >> 1) * 4 + (i & 1) * 2, r = (i >> 1) * 2;
+                    float e0 = fast_exp2(x[a] - ref[r]), e1 = fast_exp2(x[a + 1] - ref[r + 1]);
+                    if (masked) {  // (rows without a token so far: -inf less -inf)
+                        if (x[a] == NEG_INF) e0 = 0.f;
+                        if (x[a + 1] == NEG_INF) e1 = 0.f;
+                    }
+                    pk[i] = Mma<T>::pack(e0, e1);
+                    Mma<T>::unpack(pk[i], e0, e1);
+                    sum[r] += e0;
+                    sum[r + 1] += e1;
+                }
+                // the buffer's last reader, O^T of PBUF tiles ago, is done
+                if (tile >= PBUF) wait(pv_done + ((tile - PBUF) & 1), ((tile - PBUF) / 2) & 1);
+                const uint32_t pt = sbase + C::P_OFF + (tile % PBUF) * C::P_BYTES;
+#pragma unroll
+                for (int i = 0; i < 2 * J; ++i) {
+                    const int t = w * 16 + tg + (i & 1) * 8;
+                    const uint32_t at = pt + t * 128 + (((i >> 1) ^ (t & 7)) << 4) + tq * 4;
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pk[i]) : "memory");
+                }
+                if (valid != ~0ull) {
+                    // tokens without a page, or past the context: their rows must be
+                    // finite for the product with weights of 0
+                    for (int i = w * 32 + lane; i < kLatentTile * 8 * 2 * MB; i += 128) {
+                        const int t = (i >> 3) % kLatentTile, blk = (i >> 3) / kLatentTile;
+                        if (!(valid >> t & 1))
+                            *reinterpret_cast<uint4*>(smem + C::PAIR_OFF + ((pairs + blk / 2) % NP) * C::PAIR +
+                                                      (blk & 1) * C::ROPE + t * 128 + (i & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc::fence_before_sync();
+                mbar_arrive(smem_u32(p_full + tile % PBUF));
+            }
+            // ---- the segment's output ----
+            softmax_sync();
+#pragma unroll
+            for (int i = 0; i < 2 * J; ++i) {
+                float v = sum[i];
+                v += __shfl_xor_sync(kFullMask, v, 4);
+                v += __shfl_xor_sync(kFullMask, v, 8);
+                v += __shfl_xor_sync(kFullMask, v, 16);
+                const int c = (i >> 1) * 8 + tq * 2 + (i & 1);
+                if (tg == 0) wmax[w * N + c] = v;
+                if (w == 0 && tg == 0) fac[c] = ref[i];
+            }
+            wait(pv_done + ((tile - 1) & 1), ((tile - 1) / 2) & 1);
+            if (softmax_any(*abort_flag)) return false;
+            tc::fence_after_sync();
+            const bool whole = g.k0 == 0 && g.k1 == g.n;
+            const size_t rec = ((size_t)blockIdx.x * 2 + (g.first + g.k0 == run_start ? 0 : 1)) * N;
+            const int count = min(N, rows - r0);
+            for (int c0 = 0; c0 < MB * N; c0 += 16) {
+                uint32_t o[16];
+                tc::ld_32x32b_x16(tmem + quarter + 2 * N + c0, o);
+                tc::wait_ld();
+                const int d = c0 / N * 128 + w * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int c = c0 % N + i;
+                    if (c >= count) continue;
+                    const float v = __uint_as_float(o[i]);
+                    if (whole) {
+                        const float l = (wmax[c] + wmax[N + c]) + (wmax[2 * N + c] + wmax[3 * N + c]);
+                        store_out(p.out, ((size_t)g.b * rows + r0 + c) * R + d, l == 0.f ? 0.f : v / l,
+                                  kBF ? PA_BF16 : PA_F16);
+                    } else {
+                        p.part_acc[(rec + c) * R + d] = v;
+                    }
+                }
+            }
+            if (!whole)
+                for (int c = w * 32 + lane; c < count; c += 128)
+                    *reinterpret_cast<float2*>(p.part_ml + (rec + c) * 2) = make_float2(
+                        fac[c], (wmax[c] + wmax[N + c]) + (wmax[2 * N + c] + wmax[3 * N + c]));
+            tc::fence_before_sync();
+            mbar_arrive(smem_u32(o_free));
+            return true;
+        });
+    }
+    // ---- where the join finds the pieces of a (sequence, row tile): said by the
+    // CTA that has its first tile ----
+    if (p.balanced && warp == 3 && lane == 0) {
+        const long long groups = gridDim.x / p.group_size, total = run[3];
+        for_segments([&](const LatentSeg& g, int) {
+            if (g.k0 == 0) {
+                // group x has the tiles from floor(x total / groups) on
+                LatentDesc d;
+                d.first_group = group;
+                d.last_group = (int)(((g.first + g.n) * groups - 1) / total);
+                d.first_record = g.first == run_start ? 0 : 1;
+                d.member = member;
+                d.total = total;
+                p.part_desc[(size_t)g.b * p.row_tiles + g.rt] = d;
+            }
+            return true;
+        });
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 3) tc::tmem_dealloc(tmem, C::COLS);
+}
+
+// Joins the pieces of cut (sequence, row tile)s: row r of the unit, its pieces
+// (m, l, O) in the groups' records.  A CTA takes `rows_per` rows of a unit, R / 4
+// threads hold four elements each of a row and the CTA's groups of them share the
+// pieces.
+constexpr int kLatentJoinThreads = 512;
+
+template <int R, int N, typename T>
+__global__ void __launch_bounds__(kLatentJoinThreads)
+    join_latent_kernel(const LatentParams p, int rows_per, int groups) {
+    constexpr int LANES = R / 4, SHARES = kLatentJoinThreads / LANES;
+    extern __shared__ float stat[];               // [pieces] weights
+    __shared__ float4 sums[SHARES][LANES];
+    __shared__ float red[2][kLatentJoinThreads / 32];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const LatentDesc d = p.part_desc[blockIdx.x];
+    if (d.first_group == d.last_group) return;    // whole: written already
+    const int b = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
+    const int rows = p.q_len * p.num_heads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int pieces = d.last_group - d.first_group + 1;
+    // record of piece x, or -1: a group without tiles
+    auto record = [&](int x) -> long long {
+        const long long g = d.first_group + x;
+        if (g * d.total / groups == (g + 1) * d.total / groups) return -1;
+        return (g * p.group_size + d.member) * 2 + (x == 0 ? d.first_record : 0);
+    };
+    const int c0 = blockIdx.y * rows_per;
+    for (int c = c0; c < min(c0 + rows_per, min(N, rows - rt * N)); ++c) {
+        float m = -INFINITY, l = 0.f;
+        for (int x = tid; x < pieces; x += kLatentJoinThreads) {
+            const long long r = record(x);
+            const float v = r < 0 ? -INFINITY : p.part_ml[(r * N + c) * 2];
+            stat[x] = v;
+            m = fmaxf(m, v);
+        }
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, k));
+        if (lane == 0) red[0][warp] = m;
+        __syncthreads();
+        float M = red[0][0];
+#pragma unroll
+        for (int k = 1; k < kLatentJoinThreads / 32; ++k) M = fmaxf(M, red[0][k]);
+        for (int x = tid; x < pieces; x += kLatentJoinThreads) {
+            const long long r = record(x);
+            const float w = stat[x] == -INFINITY ? 0.f : fast_exp2(stat[x] - M);
+            stat[x] = w;
+            if (r >= 0) l = fmaf(w, p.part_ml[(r * N + c) * 2 + 1], l);
+        }
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(kFullMask, l, k);
+        if (lane == 0) red[1][warp] = l;
+        __syncthreads();
+        float L = red[1][0];
+#pragma unroll
+        for (int k = 1; k < kLatentJoinThreads / 32; ++k) L += red[1][k];
+        const int col = tid % LANES, share = tid / LANES;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int x = share; x < pieces; x += SHARES) {
+            const long long r = record(x);
+            if (r < 0) continue;
+            const float w = stat[x];
+            const float4 v = *reinterpret_cast<const float4*>(p.part_acc + (r * N + c) * R + col * 4);
+            a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y);
+            a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
+        }
+        sums[share][col] = a;
+        __syncthreads();
+        if (share == 0) {
+#pragma unroll
+            for (int x = 1; x < SHARES; ++x) {
+                const float4 v = sums[x][col];
+                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+            }
+            const float f = L == 0.f ? 0.f : 1.f / L;
+            T* at = static_cast<T*>(p.out) + ((size_t)b * rows + rt * N + c) * R + col * 4;
+            *reinterpret_cast<uint2*>(at) =
+                make_uint2(Mma<T>::pack(a.x * f, a.y * f), Mma<T>::pack(a.z * f, a.w * f));
+        }
+        __syncthreads();  // sums, stat and red are used again
+    }
+}
+
+template <int R, int N, typename T>
+cudaError_t launch_latent_inst(const LatentLaunch& L, cudaStream_t stream) {
+    static AttrFlags raised;
+    auto kern = latent_kernel<R, N, T>;
+    cudaError_t e = raise_smem_limit_once(kern, raised);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)L.ctas);
+    cfg.blockDim = dim3(kLatentThreads);
+    cfg.dynamicSmemBytes = LatentCfg<R, N>::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.pdl ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kern, L.tmap_c, L.tmap_q, L.p);
+    if (e != cudaSuccess || !L.join) return e;
+    const int units = L.p.batch * L.p.row_tiles, groups = L.ctas / L.p.group_size;
+    // about four CTAs an SM, where the rows suffice
+    int rows_per = (int)(((long long)N * units + 4 * L.sms - 1) / (4 * L.sms));
+    rows_per = rows_per < 1 ? 1 : rows_per > N ? N : rows_per;
+    cfg.gridDim = dim3((unsigned)units, (unsigned)((N + rows_per - 1) / rows_per));
+    cfg.blockDim = dim3(kLatentJoinThreads);
+    cfg.dynamicSmemBytes = (size_t)groups * 4;
+    return cudaLaunchKernelEx(&cfg, join_latent_kernel<R, N, T>, L.p, rows_per, groups);
+}
+
+template <int R>
+cudaError_t launch_latent_for_r(const LatentLaunch& L, cudaStream_t stream) {
+    switch (L.row_tile) {
+        case 16:
+            return L.bf16 ? launch_latent_inst<R, 16, __nv_bfloat16>(L, stream)
+                          : launch_latent_inst<R, 16, __half>(L, stream);
+        case 32:
+            return L.bf16 ? launch_latent_inst<R, 32, __nv_bfloat16>(L, stream)
+                          : launch_latent_inst<R, 32, __half>(L, stream);
+        default:
+            return L.bf16 ? launch_latent_inst<R, 64, __nv_bfloat16>(L, stream)
+                          : launch_latent_inst<R, 64, __half>(L, stream);
+    }
+}
+
+}  // namespace pa
