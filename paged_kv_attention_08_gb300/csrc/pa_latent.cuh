@@ -76,6 +76,25 @@ struct LatentCfg {
 
 namespace tc {
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r));
+    return r != 0;
+}
+
+// mma_ss with the descriptors as words.
+__device__ __forceinline__ void mma_parts(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                          uint32_t b_hi, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
 // Lanes base .. base + 15 of the warp's quarter, 8 J consecutive columns: register
 // 4 j + 2 h + e of lane l holds lane base + l / 4 + 8 h, column 8 j + 2 (l % 4) + e.
 template <int J>
@@ -275,15 +294,22 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             if (!f(g, s++)) return;
         }
     };
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool ok = mbar_wait_bounded(smem_u32(bar), parity, p.timeout_ns);
+    auto wait_at = [&](uint32_t at, uint32_t parity) -> bool {
+        const bool ok = mbar_wait_bounded(at, parity, p.timeout_ns);
         if (!ok) {
             record_error(p.err, PA_ERR_TIMEOUT);
             *abort_flag = 1;
         }
         return ok;
     };
+    auto wait = [&](uint64_t* b, uint32_t parity) -> bool { return wait_at(smem_u32(b), parity); };
+    // a value that is the same in every lane, in a uniform register
+    auto uniform = [](uint32_t x) -> uint32_t { return __shfl_sync(kFullMask, x, 0); };
     constexpr int kType = kBF ? 1 : 0;
+    // high words of the operands' descriptors (8-row groups 1024 bytes apart, version 1,
+    // 128-byte swizzle); a low word is the address / 16 and, M- / N-major, the distance
+    // of the 64-element blocks above it
+    constexpr uint32_t kDesc = (1024u >> 4) | (1u << 14) | ((uint32_t)tc::kSwizzle128B << 29);
 
     if (warp == 0) {
         // ================= copies =================
@@ -351,72 +377,106 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ================= S^T = C Q^T =================
-        if (lane == 0) {
-            constexpr uint32_t idesc = tc::idesc_f16(kType, false, 64, N);
-            int tile = 0, pairs = 0;
-            for_segments([&](const LatentSeg& g, int s) {
-                if (!wait(q_full, s & 1)) return false;
-                for (int k = g.k0; k < g.k1 && !*abort_flag; ++k, ++tile) {
-                    if (tile >= 2 && !wait(s_free + (tile & 1), (tile / 2 - 1) & 1)) return false;
-                    const int rs = tile % NR;
-                    if (!wait(rope_full + rs, (tile / NR) & 1)) return false;
-                    mbar_arrive(smem_u32(live_full + (tile & 1)));  // hands the tile's mask on
-                    tc::fence_after_sync();
-                    const uint32_t d = tmem + (tile & 1) * N;
-                    auto block = [&](uint32_t a, int c, bool accumulate) {  // 64 elements
+        // (the whole warp walks, so that descriptors stay in uniform registers;
+        // one lane issues: with one lane walking, an MMA took 94 cycles to issue)
+        constexpr uint32_t idesc = tc::idesc_f16(kType, false, 64, N);
+        const uint32_t qbase = uniform(sbase >> 4);
+        const bool one = tc::elect_one();
+        int tile = 0, pairs = 0;
+        for_segments([&](const LatentSeg& g, int s) {
+            if (!__all_sync(kFullMask, wait(q_full, s & 1))) return false;
+            for (int k = g.k0; k < g.k1; ++k, ++tile) {
+                // operand addresses / 16 and barriers, the same in every lane
+                const int rs = tile % NR;
+                const uint32_t rope = uniform((sbase + C::ROPE_OFF + rs * C::ROPE) >> 4);
+                uint32_t at[MB], full[MB];
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_ss(d, tc::smem_desc(a + kk * 32, 16, 1024, tc::kSwizzle128B),
-                                       tc::smem_desc(sbase + c * N * 128 + kk * 32, 16, 1024, tc::kSwizzle128B),
-                                       idesc, accumulate || kk > 0);
-                    };
-                    block(sbase + C::ROPE_OFF + rs * C::ROPE, R / 64, false);
-                    for (int m = 0; m < MB; ++m, ++pairs) {
-                        const int ps = pairs % NP;
-                        if (!wait(pair_full + ps, (pairs / NP) & 1)) return false;
-                        tc::fence_after_sync();
-                        const uint32_t a = sbase + C::PAIR_OFF + ps * C::PAIR;
-                        block(a, 2 * m, true);
-                        block(a + C::ROPE, 2 * m + 1, true);
+                for (int m = 0; m < MB; ++m) {
+                    const int ps = (pairs + m) % NP;
+                    at[m] = uniform((sbase + C::PAIR_OFF + ps * C::PAIR) >> 4);
+                    full[m] = uniform(smem_u32(pair_full + ps));
+                }
+                const uint32_t d = uniform(tmem + (tile & 1) * N);
+                bool ok = !*abort_flag && (tile < 2 || wait(s_free + (tile & 1), (tile / 2 - 1) & 1)) &&
+                          wait(rope_full + rs, (tile / NR) & 1);
+                if (!__all_sync(kFullMask, ok)) return false;
+                tc::fence_after_sync();
+                auto block = [&](uint32_t a, int c, bool first) {  // 64 elements
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_parts(d, a + kk * 2 + (1u << 16), kDesc, qbase + c * N * 8 + kk * 2 + (1u << 16),
+                                      kDesc, idesc, !(first && kk == 0));
+                };
+                if (one) {
+                    block(rope, R / 64, true);
+                    mbar_arrive(smem_u32(live_full + (tile & 1)));  // hands the tile's mask on
+                }
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    if (!__all_sync(kFullMask, wait_at(full[m], ((pairs + m) / NP) & 1))) return false;
+                    tc::fence_after_sync();
+                    if (one) {
+                        block(at[m], 2 * m, false);
+                        block(at[m] + (C::ROPE >> 4), 2 * m + 1, false);
                     }
+                }
+                pairs += MB;
+                if (one) {
                     tc::commit(smem_u32(rope_free + rs));
                     tc::commit(smem_u32(s_full + (tile & 1)));
                 }
-                tc::commit(smem_u32(q_free));
-                return !*abort_flag;
-            });
+                __syncwarp();
+            }
+            if (one) tc::commit(smem_u32(q_free));
+            __syncwarp();
+            return true;
+        });
+        if (one) {
             tc::commit(smem_u32(final_s));
             (void)mbar_wait_bounded(smem_u32(final_s), 0, p.timeout_ns);
         }
         __syncwarp();
     } else if (warp == 2) {
         // ================= O^T += C^T P^T =================
-        if (lane == 0) {
-            // A and B both M- / N-major: elements and rows contiguous, tokens the rows of 128 bytes
-            constexpr uint32_t idesc = tc::idesc_f16(kType, true, 128, N) | (1u << 15);
-            int tile = 0, pairs = 0;
-            for_segments([&](const LatentSeg& g, int s) {
-                if (s > 0 && !wait(o_free, (s - 1) & 1)) return false;  // the last output is read
-                for (int k = g.k0; k < g.k1 && !*abort_flag; ++k, ++tile) {
-                    const int pb = tile % PBUF;
-                    if (!wait(p_full + pb, (tile / PBUF) & 1)) return false;
-                    tc::fence_after_sync();
-                    const uint32_t pt = sbase + C::P_OFF + pb * C::P_BYTES;
-                    for (int m = 0; m < MB; ++m, ++pairs) {
-                        const int ps = pairs % NP;
-                        const uint32_t a = sbase + C::PAIR_OFF + ps * C::PAIR;
+        // A and B both M- / N-major: elements and rows contiguous, tokens the rows of 128 bytes
+        constexpr uint32_t idesc = tc::idesc_f16(kType, true, 128, N) | (1u << 15);
+        const uint32_t otmem = uniform(tmem + 2 * N);
+        const bool one = tc::elect_one();
+        int tile = 0, pairs = 0;
+        for_segments([&](const LatentSeg& g, int s) {
+            // the last segment's output is read
+            if (s > 0 && !__all_sync(kFullMask, wait(o_free, (s - 1) & 1))) return false;
+            for (int k = g.k0; k < g.k1; ++k, ++tile) {
+                const int pb = tile % PBUF;
+                const uint32_t pt = uniform((sbase + C::P_OFF + pb * C::P_BYTES) >> 4);
+                uint32_t at[MB], freed[MB];
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    const int ps = (pairs + m) % NP;
+                    at[m] = uniform((sbase + C::PAIR_OFF + ps * C::PAIR) >> 4);
+                    freed[m] = uniform(smem_u32(pair_free + ps));
+                }
+                pairs += MB;
+                if (!__all_sync(kFullMask, !*abort_flag && wait(p_full + pb, (tile / PBUF) & 1))) return false;
+                tc::fence_after_sync();
+                const bool first = k == g.k0;
+                if (one) {
+#pragma unroll
+                    for (int m = 0; m < MB; ++m) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)  // 16 tokens
-                            tc::mma_ss(tmem + (2 + m) * N,
-                                       tc::smem_desc(a + kk * 2048, C::ROPE, 1024, tc::kSwizzle128B),
-                                       tc::smem_desc(pt + kk * 2048, C::P_BYTES, 1024, tc::kSwizzle128B), idesc,
-                                       k > g.k0 || kk > 0);
-                        tc::commit(smem_u32(pair_free + ps));
+                            tc::mma_parts(otmem + m * N, at[m] + kk * 128 + (C::ROPE >> 4 << 16), kDesc,
+                                          pt + kk * 128 + (C::P_BYTES >> 4 << 16), kDesc, idesc,
+                                          !(first && kk == 0));
+                        tc::commit(freed[m]);
                     }
-                    tc::commit(smem_u32(pv_done + (tile & 1)));
                 }
-                return !*abort_flag;
-            });
+                if (one) tc::commit(smem_u32(pv_done + (tile & 1)));
+                __syncwarp();
+            }
+            return true;
+        });
+        if (one) {
             tc::commit(smem_u32(final_o));
             (void)mbar_wait_bounded(smem_u32(final_o), 0, p.timeout_ns);
         }
@@ -612,88 +672,102 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     if (warp == 3) tc::tmem_dealloc(tmem, C::COLS);
 }
 
-// Joins the pieces of cut (sequence, row tile)s: row r of the unit, its pieces
-// (m, l, O) in the groups' records.  A CTA takes `rows_per` rows of a unit, R / 4
-// threads hold four elements each of a row and the CTA's groups of them share the
-// pieces.
-constexpr int kLatentJoinThreads = 512;
+// Joins the pieces of cut (sequence, row tile)s: with each piece's (m, l, O),
+// out = sum 2^(m - M) O / sum 2^(m - M) l.  `warps` warps of a CTA take a row, a
+// lane R / 32 of its columns: one where many units keep the GPU busy (a piece or
+// two each), eight that share the pieces where a few long sequences lie in up to
+// a piece an SM.  Bound by the latency of its steps (descriptor, statistics,
+// sums); rows one after the other in a CTA took 72 us for 8192 rows of two pieces.
+constexpr int kLatentJoinThreads = 256;
 
 template <int R, int N, typename T>
 __global__ void __launch_bounds__(kLatentJoinThreads)
-    join_latent_kernel(const LatentParams p, int rows_per, int groups) {
-    constexpr int LANES = R / 4, SHARES = kLatentJoinThreads / LANES;
-    extern __shared__ float stat[];               // [pieces] weights
-    __shared__ float4 sums[SHARES][LANES];
-    __shared__ float red[2][kLatentJoinThreads / 32];
+    join_latent_kernel(const LatentParams p, int warps, int groups) {
+    constexpr int V = R / 128;  // vectors of four columns of a lane, 128 columns apart
+    __shared__ float4 sums[kLatentJoinThreads / 32][R / 4];
+    __shared__ float2 stat[kLatentJoinThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
+    const int rows = p.q_len * p.num_heads;
+    const int share = warp % warps, c = blockIdx.y * (kLatentJoinThreads / 32 / warps) + warp / warps;
     grid_dependency_wait();
     grid_launch_dependents();
     const LatentDesc d = p.part_desc[blockIdx.x];
-    if (d.first_group == d.last_group) return;    // whole: written already
-    const int b = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
-    const int rows = p.q_len * p.num_heads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (d.first_group == d.last_group) return;  // whole: written already
     const int pieces = d.last_group - d.first_group + 1;
-    // record of piece x, or -1: a group without tiles
-    auto record = [&](int x) -> long long {
+    const bool on = c < min(N, rows - rt * N);
+    float M = -INFINITY, L = 0.f;
+    float4 a[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // pieces share, share + warps, ..., 32 at a time: their statistics a lane each
+    for (int x0 = share; on && x0 < pieces; x0 += 32 * warps) {
+        const int x = x0 + lane * warps;
         const long long g = d.first_group + x;
-        if (g * d.total / groups == (g + 1) * d.total / groups) return -1;
-        return (g * p.group_size + d.member) * 2 + (x == 0 ? d.first_record : 0);
-    };
-    const int c0 = blockIdx.y * rows_per;
-    for (int c = c0; c < min(c0 + rows_per, min(N, rows - rt * N)); ++c) {
-        float m = -INFINITY, l = 0.f;
-        for (int x = tid; x < pieces; x += kLatentJoinThreads) {
-            const long long r = record(x);
-            const float v = r < 0 ? -INFINITY : p.part_ml[(r * N + c) * 2];
-            stat[x] = v;
-            m = fmaxf(m, v);
-        }
+        // (a group without tiles has no record)
+        const bool has = x < pieces && g * d.total / groups != (g + 1) * d.total / groups;
+        const long long rec = ((g * p.group_size + d.member) * 2 + (x == 0 ? d.first_record : 0)) * N + c;
+        const float2 ml = has ? *reinterpret_cast<const float2*>(p.part_ml + rec * 2)
+                              : make_float2(-INFINITY, 0.f);
+        float m = fmaxf(M, ml.x);
 #pragma unroll
         for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, k));
-        if (lane == 0) red[0][warp] = m;
-        __syncthreads();
-        float M = red[0][0];
-#pragma unroll
-        for (int k = 1; k < kLatentJoinThreads / 32; ++k) M = fmaxf(M, red[0][k]);
-        for (int x = tid; x < pieces; x += kLatentJoinThreads) {
-            const long long r = record(x);
-            const float w = stat[x] == -INFINITY ? 0.f : fast_exp2(stat[x] - M);
-            stat[x] = w;
-            if (r >= 0) l = fmaf(w, p.part_ml[(r * N + c) * 2 + 1], l);
-        }
+        const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - m);
+        float l = w * ml.y;  // (0 * NaN: a row of NaN stays one)
 #pragma unroll
         for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(kFullMask, l, k);
-        if (lane == 0) red[1][warp] = l;
-        __syncthreads();
-        float L = red[1][0];
+        L = L * f + l;
+        M = m;
 #pragma unroll
-        for (int k = 1; k < kLatentJoinThreads / 32; ++k) L += red[1][k];
-        const int col = tid % LANES, share = tid / LANES;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int v = 0; v < V; ++v) a[v].x *= f, a[v].y *= f, a[v].z *= f, a[v].w *= f;
+        const unsigned there = __ballot_sync(kFullMask, has);
+        const int n = 32 - __clz(there);
 #pragma unroll 4
-        for (int x = share; x < pieces; x += SHARES) {
-            const long long r = record(x);
-            if (r < 0) continue;
-            const float w = stat[x];
-            const float4 v = *reinterpret_cast<const float4*>(p.part_acc + (r * N + c) * R + col * 4);
-            a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y);
-            a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
-        }
-        sums[share][col] = a;
-        __syncthreads();
-        if (share == 0) {
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(kFullMask, w, i);
+            const long long ri = __shfl_sync(kFullMask, rec, i);
+            if (!(there >> i & 1)) continue;
+            const float4* src = reinterpret_cast<const float4*>(p.part_acc + ri * R) + lane;
 #pragma unroll
-            for (int x = 1; x < SHARES; ++x) {
-                const float4 v = sums[x][col];
-                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+            for (int v = 0; v < V; ++v) {
+                const float4 y = src[v * 32];
+                a[v].x = fmaf(wi, y.x, a[v].x), a[v].y = fmaf(wi, y.y, a[v].y);
+                a[v].z = fmaf(wi, y.z, a[v].z), a[v].w = fmaf(wi, y.w, a[v].w);
             }
-            const float f = L == 0.f ? 0.f : 1.f / L;
-            T* at = static_cast<T*>(p.out) + ((size_t)b * rows + rt * N + c) * R + col * 4;
-            *reinterpret_cast<uint2*>(at) =
-                make_uint2(Mma<T>::pack(a.x * f, a.y * f), Mma<T>::pack(a.z * f, a.w * f));
         }
-        __syncthreads();  // sums, stat and red are used again
     }
+    if (warps > 1) {
+        if (lane == 0) stat[warp] = make_float2(M, L);
+#pragma unroll
+        for (int v = 0; v < V; ++v) sums[warp][v * 32 + lane] = a[v];
+        __syncthreads();
+        if (share != 0) return;
+        float m = M;
+        for (int k = 1; k < warps; ++k) m = fmaxf(m, stat[warp + k].x);
+        float f = M == -INFINITY ? 0.f : fast_exp2(M - m);
+        L *= f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v].x *= f, a[v].y *= f, a[v].z *= f, a[v].w *= f;
+        for (int k = 1; k < warps; ++k) {
+            const float2 ml = stat[warp + k];
+            f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+            L = fmaf(f, ml.y, L);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float4 y = sums[warp + k][v * 32 + lane];
+                a[v].x = fmaf(f, y.x, a[v].x), a[v].y = fmaf(f, y.y, a[v].y);
+                a[v].z = fmaf(f, y.z, a[v].z), a[v].w = fmaf(f, y.w, a[v].w);
+            }
+        }
+    }
+    if (!on) return;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    T* at = static_cast<T*>(p.out) + ((size_t)b * rows + rt * N + c) * R + lane * 4;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        *reinterpret_cast<uint2*>(at + v * 128) =
+            make_uint2(Mma<T>::pack(a[v].x * inv, a[v].y * inv), Mma<T>::pack(a[v].z * inv, a[v].w * inv));
 }
 
 template <int R, int N, typename T>
@@ -715,13 +789,12 @@ cudaError_t launch_latent_inst(const LatentLaunch& L, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, kern, L.tmap_c, L.tmap_q, L.p);
     if (e != cudaSuccess || !L.join) return e;
     const int units = L.p.batch * L.p.row_tiles, groups = L.ctas / L.p.group_size;
-    // about four CTAs an SM, where the rows suffice
-    int rows_per = (int)(((long long)N * units + 4 * L.sms - 1) / (4 * L.sms));
-    rows_per = rows_per < 1 ? 1 : rows_per > N ? N : rows_per;
-    cfg.gridDim = dim3((unsigned)units, (unsigned)((N + rows_per - 1) / rows_per));
+    const int warps = units * 4 < groups ? 8 : 1;  // five pieces and more to a unit
+    const int rows = kLatentJoinThreads / 32 / warps;
+    cfg.gridDim = dim3((unsigned)units, (unsigned)((N + rows - 1) / rows));
     cfg.blockDim = dim3(kLatentJoinThreads);
-    cfg.dynamicSmemBytes = (size_t)groups * 4;
-    return cudaLaunchKernelEx(&cfg, join_latent_kernel<R, N, T>, L.p, rows_per, groups);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_latent_kernel<R, N, T>, L.p, warps, groups);
 }
 
 template <int R>
