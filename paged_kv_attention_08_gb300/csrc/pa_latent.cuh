@@ -27,8 +27,8 @@
 //   warp 1      issues S^T of a tile as its slots land, a tile ahead
 //   warp 2      issues O^T += C^T P^T as P lands in shared memory
 //   warp 3      owns tensor memory
-//   warps 4-7   softmax: a thread has two tokens and N / 4 rows; P^T to shared
-//               memory, rescales of O^T, the output
+//   warps 4-11  softmax, a warpgroup to half of the rows: a thread has two tokens and
+//               N / 8 rows; P^T to shared memory, rescales of O^T, the output
 // The running maxima move only where a score is 2^8 above them: a tile then costs
 // one vote of the warpgroup, no reduction over tokens.  The normalisers are
 // summed a thread's tokens at a time and joined at the segment's end.
@@ -42,7 +42,7 @@
 namespace pa {
 
 constexpr int kLatentTile = 64;      // tokens of a tile
-constexpr int kLatentThreads = 256;
+constexpr int kLatentThreads = 384;
 constexpr int kLatentP = 64;         // positional elements
 
 template <int R, int N>
@@ -100,6 +100,13 @@ __device__ __forceinline__ void mma_parts(uint32_t d_tmem, uint32_t a_lo, uint32
 template <int J>
 __device__ __forceinline__ void ld_16x256b(uint32_t taddr, float* r);
 template <>
+__device__ __forceinline__ void ld_16x256b<1>(uint32_t taddr, float* r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+}
+template <>
 __device__ __forceinline__ void ld_16x256b<2>(uint32_t taddr, float* r) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
@@ -118,22 +125,23 @@ __device__ __forceinline__ void ld_16x256b<4>(uint32_t taddr, float* r) {
         : "r"(taddr)
         : "memory");
 }
-template <>
-__device__ __forceinline__ void ld_16x256b<8>(uint32_t taddr, float* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-        "%30, %31}, [%32];"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
-          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
-          "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]),
-          "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]),
-          "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-        : "r"(taddr)
-        : "memory");
+__device__ __forceinline__ void ld_32x32b_x8(uint32_t taddr, float (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+                   "=f"(r[7])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 }  // namespace tc
+
+// Brings a box to L2 ahead of its load.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
 
 // 2-D tiled TMA load; completion is signalled on `bar` as transaction bytes.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
@@ -145,15 +153,39 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// The softmax warpgroup's barrier (1), and whether any of its threads votes yes.
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool vote) {
+// A softmax warpgroup's barrier (id 1 or 2), and whether any of its threads votes yes.
+__device__ __forceinline__ void group_sync(int id) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool group_any(int id, bool vote) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"((uint32_t)vote) : "memory");
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((uint32_t)vote), "r"(id) : "memory");
     return r != 0;
+}
+
+// Eight rows' values of the lane's element (f: their factors) become eight
+// consecutive elements of row `lane % 8`, packed: three exchanges among eight lanes.
+template <typename T>
+__device__ __forceinline__ uint4 transpose8(const float (&v)[8], int lane) {
+    uint32_t a[4], b[2][2];
+    const bool o1 = lane & 1, o2 = lane & 2, o4 = lane & 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // rows 2 i + (lane & 1), elements lane & ~1 and the next
+        const float got = __shfl_xor_sync(kFullMask, o1 ? v[2 * i] : v[2 * i + 1], 1);
+        a[i] = o1 ? Mma<T>::pack(got, v[2 * i + 1]) : Mma<T>::pack(v[2 * i], got);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // rows 4 i + (lane & 3), four elements
+        const uint32_t got = __shfl_xor_sync(kFullMask, o2 ? a[2 * i] : a[2 * i + 1], 2);
+        b[i][0] = o2 ? got : a[2 * i];
+        b[i][1] = o2 ? a[2 * i + 1] : got;
+    }
+    const uint32_t g0 = __shfl_xor_sync(kFullMask, o4 ? b[0][0] : b[1][0], 4);
+    const uint32_t g1 = __shfl_xor_sync(kFullMask, o4 ? b[0][1] : b[1][1], 4);
+    return o4 ? make_uint4(g0, g1, b[1][0], b[1][1]) : make_uint4(b[0][0], b[0][1], g0, g1);
 }
 
 // Tiles of a sequence: those of its attended tokens, one (with none) for an
@@ -210,14 +242,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         for (int i = 0; i < NR; ++i) mbar_init(smem_u32(rope_full + i), 1), mbar_init(smem_u32(rope_free + i), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(s_full + i), 1);
-            mbar_init(smem_u32(s_free + i), 128);
-            mbar_init(smem_u32(p_full + i), 128);
+            mbar_init(smem_u32(s_free + i), 8);  // a lane of each softmax warp
+            mbar_init(smem_u32(p_full + i), 8);
             mbar_init(smem_u32(pv_done + i), 1);
             mbar_init(smem_u32(live_full + i), 1);
         }
         mbar_init(smem_u32(q_full), 1);
         mbar_init(smem_u32(q_free), 1);
-        mbar_init(smem_u32(o_free), 128);
+        mbar_init(smem_u32(o_free), 8);
         mbar_init(smem_u32(final_s), 1);
         mbar_init(smem_u32(final_o), 1);
         *abort_flag = 0;
@@ -322,7 +354,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             auto fetch = [&](int k) -> int {
                 return lane < PG ? page_phys(row, k * PG + lane, npages, p.num_blocks) : -1;
             };
-            int next = fetch(g.k0);
+            int next = fetch(g.k0), ahead = fetch(g.k0 + 1);
             if (s > 0 && !__all_sync(kFullMask, wait(q_free, (s - 1) & 1))) return false;
             if (lane == 0) {
                 mbar_arrive_expect_tx(smem_u32(q_full), C::Q_BYTES);
@@ -333,7 +365,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             const uint64_t policy = p.group_size > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
             for (int k = g.k0; k < g.k1 && !*abort_flag; ++k, ++tile) {
                 const int phys = next;
-                if (k + 1 < g.k1) next = fetch(k + 1);
+                next = ahead;
+                if (k + 2 < g.k1) ahead = fetch(k + 2);
+                // the next tile to L2: its slots are free late, a load from there is short
+                if (member == 0 && k + 1 < g.k1 && next >= 0)
+                    for (int c = 0; c < R + kLatentP; c += 64) tma_prefetch_4d(&tmap_c, c, 0, next, 0);
                 const unsigned on = __ballot_sync(kFullMask, phys >= 0);
                 // one slot: `blocks` column blocks from element `col` on
                 auto load = [&](uint64_t* full, uint32_t dst, int col, int blocks) {
@@ -483,18 +519,19 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         __syncwarp();
     } else if (warp >= 4) {
         // ================= softmax =================
-        constexpr int J = N / 8;              // groups of 8 rows; a thread has two rows of each
-        const int w = warp - 4, quarter = w << 21;   // lanes 32 w on: tokens 16 w on in lanes 32 w .. + 15
-        const int tg = lane >> 2, tq = lane & 3;
+        constexpr int NC = N / 2, J = NC / 8;  // rows of a warpgroup, in groups of 8: a thread has two of each
+        const int wg = (warp - 4) >> 2, w = warp & 3, id = 1 + wg;
+        const int quarter = w << 21;           // lanes 32 w on; tokens 16 w on in lanes 32 w .. + 15
+        const int tg = lane >> 2, tq = lane & 3, cb = wg * NC;
         int tile = 0, pairs = 0;
         for_segments([&](const LatentSeg& g, int s) {
             const int ctx = max(__ldg(p.context_lens + g.b), 0), reach = latent_reach(p, g.b);
             const int r0 = g.rt * N;
-            softmax_sync();  // the last segment's statistics are read
-            for (int c = w * 32 + lane; c < N; c += 128)
+            group_sync(id);  // the last segment's statistics are read
+            for (int c = cb + w * 32 + lane; c < cb + NC; c += 128)
                 lim[c] = r0 + c < rows ? min(reach, ctx - p.q_len + (r0 + c) / p.num_heads + 1) : reach;
             const int least = min(reach, ctx - p.q_len + r0 / p.num_heads + 1);
-            float ref[2 * J], sum[2 * J];     // reference exponents and normalisers of the thread's rows
+            float ref[2 * J], sum[2 * J];      // reference exponents and normalisers of the thread's rows
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) ref[i] = NEG_INF, sum[i] = 0.f;
             for (int k = g.k0; k < g.k1; ++k, ++tile, pairs += MB) {
@@ -502,21 +539,23 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 wait(s_full + (tile & 1), (tile / 2) & 1);
                 wait(live_full + (tile & 1), (tile / 2) & 1);
                 tc::fence_after_sync();
-                uint64_t valid = live[tile & 15];
-                if (reach - t0 < kLatentTile) valid &= reach > t0 ? (1ull << (reach - t0)) - 1 : 0ull;
                 float x[4 * J];
-                tc::ld_16x256b<J>(tmem + quarter + (tile & 1) * N, x);
+                tc::ld_16x256b<J>(tmem + quarter + (tile & 1) * N + cb, x);
+                uint64_t valid = live[tile & 15];
+                const bool aborted = *abort_flag;
+                if (reach - t0 < kLatentTile) valid &= reach > t0 ? (1ull << (reach - t0)) - 1 : 0ull;
+                const bool masked = valid != ~0ull || least < t0 + kLatentTile;
                 tc::wait_ld();
                 tc::fence_before_sync();
-                mbar_arrive(smem_u32(s_free + (tile & 1)));
-                const bool masked = valid != ~0ull || least < t0 + kLatentTile;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(s_free + (tile & 1)));
 #pragma unroll
                 for (int i = 0; i < 4 * J; ++i) x[i] *= p.qscale;
                 if (masked) {
-                    if (k == g.k0) softmax_sync();  // lim
+                    if (k == g.k0) group_sync(id);  // lim
 #pragma unroll
                     for (int i = 0; i < 4 * J; ++i) {
-                        const int t = w * 16 + tg + (i & 2) * 4, c = (i >> 2) * 8 + tq * 2 + (i & 1);
+                        const int t = w * 16 + tg + (i & 2) * 4, c = cb + (i >> 2) * 8 + tq * 2 + (i & 1);
                         if (!(valid >> t & 1) || t0 + t >= lim[c]) x[i] = NEG_INF;
                     }
                 }
@@ -524,8 +563,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4 * J; ++i) above = fmaxf(above, x[i] - ref[(i >> 2) * 2 + (i & 1)]);
                 // (an abort anywhere brings all of the warpgroup to the second vote)
-                if (softmax_any(above > kSlack + kLift || *abort_flag)) {
-                    if (softmax_any(*abort_flag)) return false;
+                if (group_any(id, above > kSlack + kLift || aborted)) {
+                    if (group_any(id, *abort_flag)) return false;
                     // some row's maximum has risen: the tile's maxima, new references
 #pragma unroll
                     for (int i = 0; i < 2 * J; ++i) {
@@ -533,12 +572,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                         v = fmaxf(v, __shfl_xor_sync(kFullMask, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(kFullMask, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(kFullMask, v, 16));
-                        if (tg == 0) wmax[w * N + (i >> 1) * 8 + tq * 2 + (i & 1)] = v;
+                        if (tg == 0) wmax[w * N + cb + (i >> 1) * 8 + tq * 2 + (i & 1)] = v;
                     }
-                    softmax_sync();
+                    group_sync(id);
 #pragma unroll
                     for (int i = 0; i < 2 * J; ++i) {
-                        const int c = (i >> 1) * 8 + tq * 2 + (i & 1);
+                        const int c = cb + (i >> 1) * 8 + tq * 2 + (i & 1);
                         const float v = fmaxf(fmaxf(wmax[c], wmax[N + c]), fmaxf(wmax[2 * N + c], wmax[3 * N + c]));
                         const float to = fmaxf(ref[i], v - kLift);
                         const float f = to == ref[i] ? 1.f : fast_exp2(ref[i] - to);
@@ -547,18 +586,19 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                         sum[i] *= f;
                     }
                     if (k > g.k0) wait(pv_done + ((tile - 1) & 1), ((tile - 1) / 2) & 1);
-                    softmax_sync();
+                    group_sync(id);
                     if (k > g.k0) {
                         // O^T (elements in lanes, rows in columns) on the new references
                         tc::fence_after_sync();
-                        for (int c0 = 0; c0 < MB * N; c0 += 16) {
-                            uint32_t o[16];
-                            tc::ld_32x32b_x16(tmem + quarter + 2 * N + c0, o);
+                        for (int c0 = 0; c0 < MB * NC; c0 += 8) {
+                            const uint32_t at = tmem + quarter + (2 + c0 / NC) * N + cb + c0 % NC;
+                            float o[8];
+                            tc::ld_32x32b_x8(at, o);
                             tc::wait_ld();
+                            uint32_t u[8];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[c0 % N + i]);
-                            tc::st_32x32b_x16(tmem + quarter + 2 * N + c0, o);
+                            for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(o[i] * fac[cb + c0 % NC + i]);
+                            tc::st_32x32b_x8(at, u);
                         }
                         tc::wait_st();
                     }
@@ -567,7 +607,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 uint32_t pk[2 * J];
 #pragma unroll
                 for (int i = 0; i < 2 * J; ++i) {
-                    // i: group j = i / 2, token tg or tg + 8; two neighbouring rows
+                    // i: group i / 2, token tg or tg + 8; two neighbouring rows
                     const int a = (i >> 1) * 4 + (i & 1) * 2, r = (i >> 1) * 2;
                     float e0 = fast_exp2(x[a] - ref[r]), e1 = fast_exp2(x[a + 1] - ref[r + 1]);
                     if (masked) {  // (rows without a token so far: -inf less -inf)
@@ -585,13 +625,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 2 * J; ++i) {
                     const int t = w * 16 + tg + (i & 1) * 8;
-                    const uint32_t at = pt + t * 128 + (((i >> 1) ^ (t & 7)) << 4) + tq * 4;
+                    const uint32_t at = pt + t * 128 + ((((cb >> 3) + (i >> 1)) ^ (t & 7)) << 4) + tq * 4;
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pk[i]) : "memory");
                 }
                 if (valid != ~0ull) {
                     // tokens without a page, or past the context: their rows must be
                     // finite for the product with weights of 0
-                    for (int i = w * 32 + lane; i < kLatentTile * 8 * 2 * MB; i += 128) {
+                    for (int i = tid - 128; i < kLatentTile * 8 * 2 * MB; i += 256) {
                         const int t = (i >> 3) % kLatentTile, blk = (i >> 3) / kLatentTile;
                         if (!(valid >> t & 1))
                             *reinterpret_cast<uint4*>(smem + C::PAIR_OFF + ((pairs + blk / 2) % NP) * C::PAIR +
@@ -601,51 +641,60 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 }
                 fence_proxy_async_smem();
                 tc::fence_before_sync();
-                mbar_arrive(smem_u32(p_full + tile % PBUF));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(p_full + tile % PBUF));
             }
             // ---- the segment's output ----
-            softmax_sync();
+            group_sync(id);
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
                 float v = sum[i];
                 v += __shfl_xor_sync(kFullMask, v, 4);
                 v += __shfl_xor_sync(kFullMask, v, 8);
                 v += __shfl_xor_sync(kFullMask, v, 16);
-                const int c = (i >> 1) * 8 + tq * 2 + (i & 1);
+                const int c = cb + (i >> 1) * 8 + tq * 2 + (i & 1);
                 if (tg == 0) wmax[w * N + c] = v;
                 if (w == 0 && tg == 0) fac[c] = ref[i];
             }
             wait(pv_done + ((tile - 1) & 1), ((tile - 1) / 2) & 1);
-            if (softmax_any(*abort_flag)) return false;
+            if (group_any(id, *abort_flag)) return false;
             tc::fence_after_sync();
             const bool whole = g.k0 == 0 && g.k1 == g.n;
-            const size_t rec = ((size_t)blockIdx.x * 2 + (g.first + g.k0 == run_start ? 0 : 1)) * N;
+            const size_t rec = (size_t)blockIdx.x * 2 + (g.first + g.k0 == run_start ? 0 : 1);
             const int count = min(N, rows - r0);
-            for (int c0 = 0; c0 < MB * N; c0 += 16) {
-                uint32_t o[16];
-                tc::ld_32x32b_x16(tmem + quarter + 2 * N + c0, o);
-                tc::wait_ld();
-                const int d = c0 / N * 128 + w * 32 + lane;
+            auto total = [&](int c) { return (wmax[c] + wmax[N + c]) + (wmax[2 * N + c] + wmax[3 * N + c]); };
+            if (!whole)
+                for (int c = cb + w * 32 + lane; c < cb + NC; c += 128)
+                    *reinterpret_cast<float2*>(p.part_ml + (rec * N + c) * 2) = make_float2(fac[c], total(c));
+            group_sync(id);
+            for (int c = cb + w * 32 + lane; c < cb + NC; c += 128) {
+                const float l = total(c);
+                fac[c] = l == 0.f ? 0.f : 1.f / l;
+            }
+            group_sync(id);
+            for (int m = 0; m < MB; ++m) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int c = c0 % N + i;
-                    if (c >= count) continue;
-                    const float v = __uint_as_float(o[i]);
+                for (int c0 = 0; c0 < NC; c0 += 8) {
+                    float o[8];
+                    tc::ld_32x32b_x8(tmem + quarter + (2 + m) * N + cb + c0, o);
+                    tc::wait_ld();
+                    const int d = m * 128 + w * 32 + lane, c = cb + c0;
                     if (whole) {
-                        const float l = (wmax[c] + wmax[N + c]) + (wmax[2 * N + c] + wmax[3 * N + c]);
-                        store_out(p.out, ((size_t)g.b * rows + r0 + c) * R + d, l == 0.f ? 0.f : v / l,
-                                  kBF ? PA_BF16 : PA_F16);
-                    } else {
-                        p.part_acc[(rec + c) * R + d] = v;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] *= fac[c + i];
+                        const uint4 v = transpose8<T>(o, lane);
+                        const int r = c + (lane & 7);
+                        if (r < count)
+                            *reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
+                                                      ((size_t)g.b * rows + r0 + r) * R + (d & ~7)) = v;
+                    } else {  // [element][row]: whole sectors a lane
+                        st_global_v8(p.part_acc + (rec * R + d) * N + c, o);
                     }
                 }
             }
-            if (!whole)
-                for (int c = w * 32 + lane; c < count; c += 128)
-                    *reinterpret_cast<float2*>(p.part_ml + (rec + c) * 2) = make_float2(
-                        fac[c], (wmax[c] + wmax[N + c]) + (wmax[2 * N + c] + wmax[3 * N + c]));
             tc::fence_before_sync();
-            mbar_arrive(smem_u32(o_free));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(o_free));
             return true;
         });
     }
@@ -673,101 +722,90 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 }
 
 // Joins the pieces of cut (sequence, row tile)s: with each piece's (m, l, O),
-// out = sum 2^(m - M) O / sum 2^(m - M) l.  `warps` warps of a CTA take a row, a
-// lane R / 32 of its columns: one where many units keep the GPU busy (a piece or
-// two each), eight that share the pieces where a few long sequences lie in up to
-// a piece an SM.  Bound by the latency of its steps (descriptor, statistics,
-// sums); rows one after the other in a CTA took 72 us for 8192 rows of two pieces.
+// out = sum 2^(m - M) O / sum 2^(m - M) l.  A thread takes a row and eight
+// elements; neighbouring threads have neighbouring rows, as a piece's records lie
+// ([element][row]).  SHARES threads share the pieces: one where many units keep
+// the GPU busy (a piece or two each), eight where a few long sequences lie in up to
+// a piece an SM.  Bound by the latency of its steps (descriptor, statistics and
+// sums): rows one after the other in a CTA took 72 us for 8192 rows of two pieces.
 constexpr int kLatentJoinThreads = 256;
 
-template <int R, int N, typename T>
-__global__ void __launch_bounds__(kLatentJoinThreads)
-    join_latent_kernel(const LatentParams p, int warps, int groups) {
-    constexpr int V = R / 128;  // vectors of four columns of a lane, 128 columns apart
-    __shared__ float4 sums[kLatentJoinThreads / 32][R / 4];
-    __shared__ float2 stat[kLatentJoinThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
-    const int rows = p.q_len * p.num_heads;
-    const int share = warp % warps, c = blockIdx.y * (kLatentJoinThreads / 32 / warps) + warp / warps;
+template <int R, int N, typename T, int SHARES>
+__global__ void __launch_bounds__(kLatentJoinThreads) join_latent_kernel(const LatentParams p, int groups) {
+    constexpr int PER = kLatentJoinThreads / SHARES, AHEAD = 4;
+    __shared__ float sums[SHARES > 1 ? SHARES : 1][10][PER];
     grid_dependency_wait();
     grid_launch_dependents();
     const LatentDesc d = p.part_desc[blockIdx.x];
     if (d.first_group == d.last_group) return;  // whole: written already
+    const int b = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
+    const int rows = p.q_len * p.num_heads;
+    const int share = threadIdx.x / PER, at = blockIdx.y * PER + threadIdx.x % PER;
+    const int c = at % N, e0 = at / N * 8;      // (R / 8 * N is a multiple of PER)
     const int pieces = d.last_group - d.first_group + 1;
-    const bool on = c < min(N, rows - rt * N);
-    float M = -INFINITY, L = 0.f;
-    float4 a[V];
+    float M = -INFINITY, L = 0.f, a[8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    // pieces share, share + warps, ..., 32 at a time: their statistics a lane each
-    for (int x0 = share; on && x0 < pieces; x0 += 32 * warps) {
-        const int x = x0 + lane * warps;
-        const long long g = d.first_group + x;
-        // (a group without tiles has no record)
-        const bool has = x < pieces && g * d.total / groups != (g + 1) * d.total / groups;
-        const long long rec = ((g * p.group_size + d.member) * 2 + (x == 0 ? d.first_record : 0)) * N + c;
-        const float2 ml = has ? *reinterpret_cast<const float2*>(p.part_ml + rec * 2)
-                              : make_float2(-INFINITY, 0.f);
-        float m = fmaxf(M, ml.x);
+    for (int i = 0; i < 8; ++i) a[i] = 0.f;
+    for (int x0 = share; x0 < pieces; x0 += SHARES * AHEAD) {
+        float2 ml[AHEAD];
+        float y[AHEAD][8];
 #pragma unroll
-        for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, k));
-        const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-        const float f = M == -INFINITY ? 0.f : fast_exp2(M - m);
-        float l = w * ml.y;  // (0 * NaN: a row of NaN stays one)
+        for (int k = 0; k < AHEAD; ++k) {
+            const int x = x0 + k * SHARES;
+            const long long g = d.first_group + x;
+            ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(kFullMask, l, k);
-        L = L * f + l;
-        M = m;
+            for (int i = 0; i < 8; ++i) y[k][i] = 0.f;
+            // (a group without tiles has no record)
+            if (x < pieces && g * d.total / groups != (g + 1) * d.total / groups) {
+                const long long rec = (g * p.group_size + d.member) * 2 + (x == 0 ? d.first_record : 0);
+                ml[k] = *reinterpret_cast<const float2*>(p.part_ml + (rec * N + c) * 2);
 #pragma unroll
-        for (int v = 0; v < V; ++v) a[v].x *= f, a[v].y *= f, a[v].z *= f, a[v].w *= f;
-        const unsigned there = __ballot_sync(kFullMask, has);
-        const int n = 32 - __clz(there);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(kFullMask, w, i);
-            const long long ri = __shfl_sync(kFullMask, rec, i);
-            if (!(there >> i & 1)) continue;
-            const float4* src = reinterpret_cast<const float4*>(p.part_acc + ri * R) + lane;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float4 y = src[v * 32];
-                a[v].x = fmaf(wi, y.x, a[v].x), a[v].y = fmaf(wi, y.y, a[v].y);
-                a[v].z = fmaf(wi, y.z, a[v].z), a[v].w = fmaf(wi, y.w, a[v].w);
+                for (int i = 0; i < 8; ++i) y[k][i] = p.part_acc[(rec * R + e0 + i) * N + c];
             }
         }
-    }
-    if (warps > 1) {
-        if (lane == 0) stat[warp] = make_float2(M, L);
-#pragma unroll
-        for (int v = 0; v < V; ++v) sums[warp][v * 32 + lane] = a[v];
-        __syncthreads();
-        if (share != 0) return;
         float m = M;
-        for (int k = 1; k < warps; ++k) m = fmaxf(m, stat[warp + k].x);
-        float f = M == -INFINITY ? 0.f : fast_exp2(M - m);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) m = fmaxf(m, ml[k].x);
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - m);
+        M = m;
         L *= f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) a[v].x *= f, a[v].y *= f, a[v].z *= f, a[v].w *= f;
-        for (int k = 1; k < warps; ++k) {
-            const float2 ml = stat[warp + k];
-            f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-            L = fmaf(f, ml.y, L);
+        for (int i = 0; i < 8; ++i) a[i] *= f;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float4 y = sums[warp + k][v * 32 + lane];
-                a[v].x = fmaf(f, y.x, a[v].x), a[v].y = fmaf(f, y.y, a[v].y);
-                a[v].z = fmaf(f, y.z, a[v].z), a[v].w = fmaf(f, y.w, a[v].w);
-            }
+        for (int k = 0; k < AHEAD; ++k) {
+            const float w = ml[k].x == -INFINITY ? 0.f : fast_exp2(ml[k].x - m);
+            L = fmaf(w, ml[k].y, L);            // (0 * NaN: a row of NaN stays one)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = fmaf(w, y[k][i], a[i]);
         }
     }
-    if (!on) return;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    T* at = static_cast<T*>(p.out) + ((size_t)b * rows + rt * N + c) * R + lane * 4;
+    if constexpr (SHARES > 1) {
+        const int t = threadIdx.x % PER;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        *reinterpret_cast<uint2*>(at + v * 128) =
-            make_uint2(Mma<T>::pack(a[v].x * inv, a[v].y * inv), Mma<T>::pack(a[v].z * inv, a[v].w * inv));
+        for (int i = 0; i < 8; ++i) sums[share][i][t] = a[i];
+        sums[share][8][t] = M;
+        sums[share][9][t] = L;
+        __syncthreads();
+        if (share != 0) return;
+#pragma unroll
+        for (int k = 1; k < SHARES; ++k) M = fmaxf(M, sums[k][8][t]);
+        L = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < SHARES; ++k) {
+            const float m = sums[k][8][t], w = m == -INFINITY ? 0.f : fast_exp2(m - M);
+            L = fmaf(w, sums[k][9][t], L);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = fmaf(w, sums[k][i][t], a[i]);
+        }
+    }
+    if (rt * N + c >= rows) return;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + ((size_t)b * rows + rt * N + c) * R + e0) =
+        make_uint4(Mma<T>::pack(a[0] * inv, a[1] * inv), Mma<T>::pack(a[2] * inv, a[3] * inv),
+                   Mma<T>::pack(a[4] * inv, a[5] * inv), Mma<T>::pack(a[6] * inv, a[7] * inv));
 }
 
 template <int R, int N, typename T>
@@ -789,12 +827,13 @@ cudaError_t launch_latent_inst(const LatentLaunch& L, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, kern, L.tmap_c, L.tmap_q, L.p);
     if (e != cudaSuccess || !L.join) return e;
     const int units = L.p.batch * L.p.row_tiles, groups = L.ctas / L.p.group_size;
-    const int warps = units * 4 < groups ? 8 : 1;  // five pieces and more to a unit
-    const int rows = kLatentJoinThreads / 32 / warps;
-    cfg.gridDim = dim3((unsigned)units, (unsigned)((N + rows - 1) / rows));
+    const bool shared = units * 4 < groups;  // five pieces and more to a unit
+    const int per = kLatentJoinThreads / (shared ? 8 : 1);
+    cfg.gridDim = dim3((unsigned)units, (unsigned)((R / 8 * N + per - 1) / per));
     cfg.blockDim = dim3(kLatentJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join_latent_kernel<R, N, T>, L.p, warps, groups);
+    return shared ? cudaLaunchKernelEx(&cfg, join_latent_kernel<R, N, T, 8>, L.p, groups)
+                  : cudaLaunchKernelEx(&cfg, join_latent_kernel<R, N, T, 1>, L.p, groups);
 }
 
 template <int R>
