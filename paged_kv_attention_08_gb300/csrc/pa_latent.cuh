@@ -135,6 +135,16 @@ __device__ __forceinline__ void ld_32x32b_x8(uint32_t taddr, float (&r)[8]) {
 
 }  // namespace tc
 
+// Has phase `parity` of an mbarrier completed?  (Looks once, does not wait.)
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // Brings a box to L2 ahead of its load.
 __device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
     asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
@@ -326,15 +336,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             if (!f(g, s++)) return;
         }
     };
-    auto wait_at = [&](uint32_t at, uint32_t parity) -> bool {
-        const bool ok = mbar_wait_bounded(at, parity, p.timeout_ns);
+    auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+        const bool ok = mbar_wait_bounded(smem_u32(b), parity, p.timeout_ns);
         if (!ok) {
             record_error(p.err, PA_ERR_TIMEOUT);
             *abort_flag = 1;
         }
         return ok;
     };
-    auto wait = [&](uint64_t* b, uint32_t parity) -> bool { return wait_at(smem_u32(b), parity); };
     // a value that is the same in every lane, in a uniform register
     auto uniform = [](uint32_t x) -> uint32_t { return __shfl_sync(kFullMask, x, 0); };
     constexpr int kType = kBF ? 1 : 0;
@@ -417,26 +426,51 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         // one lane issues: with one lane walking, an MMA took 94 cycles to issue)
         constexpr uint32_t idesc = tc::idesc_f16(kType, false, 64, N);
         const uint32_t qbase = uniform(sbase >> 4);
+        const int watch = lane < 2 + MB ? lane : 0;
         const bool one = tc::elect_one();
         int tile = 0, pairs = 0;
         for_segments([&](const LatentSeg& g, int s) {
             if (!__all_sync(kFullMask, wait(q_full, s & 1))) return false;
             for (int k = g.k0; k < g.k1; ++k, ++tile) {
-                // operand addresses / 16 and barriers, the same in every lane
+                // operand addresses / 16, the same in every lane
                 const int rs = tile % NR;
                 const uint32_t rope = uniform((sbase + C::ROPE_OFF + rs * C::ROPE) >> 4);
-                uint32_t at[MB], full[MB];
+                uint32_t at[MB];
 #pragma unroll
-                for (int m = 0; m < MB; ++m) {
-                    const int ps = (pairs + m) % NP;
-                    at[m] = uniform((sbase + C::PAIR_OFF + ps * C::PAIR) >> 4);
-                    full[m] = uniform(smem_u32(pair_full + ps));
-                }
+                for (int m = 0; m < MB; ++m)
+                    at[m] = uniform((sbase + C::PAIR_OFF + (pairs + m) % NP * C::PAIR) >> 4);
                 const uint32_t d = uniform(tmem + (tile & 1) * N);
-                bool ok = !*abort_flag && (tile < 2 || wait(s_free + (tile & 1), (tile / 2 - 1) & 1)) &&
-                          wait(rope_full + rs, (tile / NR) & 1);
-                if (!__all_sync(kFullMask, ok)) return false;
-                tc::fence_after_sync();
+                // lane 0 watches the score buffer, lane 1 the positional slot, lane 2 + m
+                // pair m: a tile whose slots have all landed costs one look
+                const int mine = (pairs + watch - 2) % NP;
+                const uint32_t bar_at = smem_u32(watch == 0   ? s_free + (tile & 1)
+                                                 : watch == 1 ? rope_full + rs
+                                                              : pair_full + mine);
+                const uint32_t parity = watch == 0   ? (tile / 2 - 1) & 1
+                                        : watch == 1 ? (tile / NR) & 1
+                                                     : ((pairs + watch - 2) / NP) & 1;
+                uint32_t ready = 0;
+                auto need = [&](uint32_t bits) -> bool {
+                    if ((ready & bits) == bits) return true;
+                    uint64_t start = 0;
+                    for (uint32_t it = 1;; ++it) {
+                        ready = __ballot_sync(kFullMask, (watch == 0 && tile < 2) || mbar_test_wait(bar_at, parity));
+                        if ((ready & bits) == bits) break;
+                        if ((it & 255u) == 0) {
+                            const uint64_t now = global_timer_ns();
+                            if (!start) start = now;
+                            if (__any_sync(kFullMask, *abort_flag || now - start > p.timeout_ns)) {
+                                record_error(p.err, PA_ERR_TIMEOUT);
+                                *abort_flag = 1;
+                                return false;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    tc::fence_after_sync();
+                    return true;
+                };
+                if (!need(3)) return false;
                 auto block = [&](uint32_t a, int c, bool first) {  // 64 elements
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
@@ -449,8 +483,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 }
 #pragma unroll
                 for (int m = 0; m < MB; ++m) {
-                    if (!__all_sync(kFullMask, wait_at(full[m], ((pairs + m) / NP) & 1))) return false;
-                    tc::fence_after_sync();
+                    if (!need(4u << m)) return false;
                     if (one) {
                         block(at[m], 2 * m, false);
                         block(at[m] + (C::ROPE >> 4), 2 * m + 1, false);
