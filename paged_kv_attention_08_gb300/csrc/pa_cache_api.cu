@@ -92,7 +92,24 @@ struct Split {
     int part_pages, parts;
     bool cluster;
     int chunk, chunks;  // query tokens of a CTA, and how many CTAs that makes
+    int kind;           // index of the kernel in kKv8
 };
+
+// The kernels by head_dim and rows of a CTA.
+struct Kv8Kernel {
+    int head_dim, rows;
+    cudaError_t (*launch)(const Kv8Launch&, cudaStream_t);
+    int (*ctas)();
+};
+const Kv8Kernel kKv8[] = {{64, 8, launch_kv8_d64_n1, kv8_ctas_d64_n1},
+                          {64, 16, launch_kv8_d64_n2, kv8_ctas_d64_n2},
+                          {64, 32, launch_kv8_d64_n4, kv8_ctas_d64_n4},
+                          {128, 8, launch_kv8_d128_n1, kv8_ctas_d128_n1},
+                          {128, 16, launch_kv8_d128_n2, kv8_ctas_d128_n2},
+                          {128, 32, launch_kv8_d128_n4, kv8_ctas_d128_n4},
+                          {256, 8, launch_kv8_d256_n1, kv8_ctas_d256_n1},
+                          {256, 16, launch_kv8_d256_n2, kv8_ctas_d256_n2}};
+constexpr int kKv8Count = sizeof kKv8 / sizeof kKv8[0];
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -116,12 +133,19 @@ size_t partial_bytes(const Split& sp, size_t rows, int width, size_t* ml_at) {
 // sequences even out over the waves.
 Split split_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
     Split sp;
-    const int per = 16 / (s->num_heads / s->num_kv_heads);
+    // the smallest row tile that holds a sequence's rows, or the largest there is
+    const int group = s->num_heads / s->num_kv_heads;
+    sp.kind = -1;
+    for (int i = 0; i < kKv8Count; ++i)
+        if (kKv8[i].head_dim == s->head_dim &&
+            (sp.kind < 0 || (int64_t)q_len * group > kKv8[sp.kind].rows))
+            sp.kind = i;
+    const int per = kKv8[sp.kind].rows / group;
     sp.chunk = q_len < per ? q_len : per;
     sp.chunks = (q_len + sp.chunk - 1) / sp.chunk;
     const int64_t pages = announced_tokens(max_context_len, s->block_size, s->max_blocks_per_seq) / s->block_size;
     const int64_t units = (int64_t)s->batch * s->num_kv_heads * sp.chunks;
-    const int64_t slots = (int64_t)sms * (s->head_dim == 256 ? 2 : 3);
+    const int64_t slots = (int64_t)sms * kKv8[sp.kind].ctas();
     const int64_t fill = slots / units;
     int64_t parts = 1;
     sp.cluster = false;
@@ -134,7 +158,9 @@ Split split_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int s
         parts = ceil_div(pages * s->block_size, 1024);
     }
     parts = std::min<int64_t>(parts, kMaxJoinParts);
-    sp.part_pages = (int)ceil_div(pages, parts);
+    // whole steps of the kernel: 32 tokens
+    const int step = 32 / s->block_size;
+    sp.part_pages = (int)(ceil_div(ceil_div(pages, parts), step) * step);
     sp.parts = (int)ceil_div(pages, sp.part_pages);
     if (sp.parts == 1) sp.cluster = false;
     return sp;
@@ -364,12 +390,11 @@ pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const voi
     p.cluster = sp.cluster ? sp.parts : 1;
     p.out_dtype = shape->out_dtype;
     L.block_size = BS;
-    L.bf16 = shape->kv_dtype == PA_BF16;
     L.pdl = use_pdl();
+    p.bf16 = shape->kv_dtype == PA_BF16;
     L.grid = dim3((unsigned)sp.parts, (unsigned)grid_y, (unsigned)shape->batch);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = D == 64 ? launch_kv8_d64(L, cs) : D == 128 ? launch_kv8_d128(L, cs)
-                                                                     : launch_kv8_d256(L, cs);
+    const cudaError_t e = kKv8[sp.kind].launch(L, cs);
     if (e != cudaSuccess || !need) return done(e);
     JoinParams j;
     std::memset(&j, 0, sizeof j);

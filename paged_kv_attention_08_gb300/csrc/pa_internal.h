@@ -177,7 +177,8 @@ struct Kv8Params {
     int64_t num_blocks;
     float qscale;             // scale * log2(e)
     int32_t q_len, num_heads, num_kv_heads, group, max_blocks;
-    int32_t q_chunk;          // query tokens of a CTA (q_chunk * group <= 16)
+    int32_t q_chunk;          // query tokens of a CTA (q_chunk * group fills its 8-row tiles)
+    int32_t bf16;             // q's type
     int32_t token_limit;      // tokens from here on are not attended to
     int32_t part_pages, num_parts;
     int32_t cluster;          // > 1: the num_parts partitions are a cluster and join there
@@ -188,7 +189,7 @@ struct Kv8Launch {
     Kv8Params p;
     CUtensorMap tmap_k, tmap_v;
     int block_size;
-    bool bf16, pdl;
+    bool pdl;
     dim3 grid;
 };
 
@@ -583,9 +584,24 @@ cudaError_t launch_append(void* k_cache, void* v_cache, const void* k_new, const
 cudaError_t launch_rope_append(const RopeParams& p, bool bf16, int num_sms, bool pdl,
                                cudaStream_t stream);
 cudaError_t launch_append8(const Append8Params& p, bool bf16, bool pdl, cudaStream_t stream);
-cudaError_t launch_kv8_d64(const Kv8Launch& L, cudaStream_t stream);
-cudaError_t launch_kv8_d128(const Kv8Launch& L, cudaStream_t stream);
-cudaError_t launch_kv8_d256(const Kv8Launch& L, cudaStream_t stream);
+// Attention over the 8-bit cache, by head_dim and 8-row tiles of a CTA, and the
+// CTAs of it that an SM holds.
+cudaError_t launch_kv8_d64_n1(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_kv8_d64_n2(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_kv8_d64_n4(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_kv8_d128_n1(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_kv8_d128_n2(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_kv8_d128_n4(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_kv8_d256_n1(const Kv8Launch& L, cudaStream_t stream);
+cudaError_t launch_kv8_d256_n2(const Kv8Launch& L, cudaStream_t stream);
+int kv8_ctas_d64_n1();
+int kv8_ctas_d64_n2();
+int kv8_ctas_d64_n4();
+int kv8_ctas_d128_n1();
+int kv8_ctas_d128_n2();
+int kv8_ctas_d128_n4();
+int kv8_ctas_d256_n1();
+int kv8_ctas_d256_n2();
 cudaError_t launch_join(const JoinParams& p, int batch, int num_kv_heads, bool pdl, cudaStream_t stream);
 cudaError_t launch_append_latent(LatentAppendParams p, bool bf16, int num_sms, bool pdl,
                                  cudaStream_t stream);

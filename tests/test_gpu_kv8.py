@@ -201,9 +201,14 @@ def check(c, scale=None, want_lens=None, **kw):
     want = cref.attention(c["q"], k, v, c["table"], lens, scale)
     tokens = max(1, int((c["table"] >= 0).sum(1).max())) * k.shape[1]
     held = c["table"][(c["table"] >= 0) & (c["table"] < len(k))].long()
-    # weights in two fp16 parts: 2^-22 of each, and under 2^-16 whatever the lift
-    ref.close_out(run(c, scale, **kw), want,
-                  cref.attention_slack(c["q"], k[held], v[held], scale, tokens, 2.0 ** -16))
+    got = run(c, scale, **kw)
+    ref.close_out(got, want, cref.attention_slack(c["q"], k[held], v[held], scale, tokens, weights(got.dtype)))
+
+
+def weights(out_dtype):
+    """Rounding of a weight on the way to the values: fp32 outputs in two fp16
+    parts (2^-22, and under 2^-16 whatever the lift), 16-bit ones once to fp16."""
+    return 2.0 ** -16 if out_dtype == torch.float32 else 2.0 ** -11
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
@@ -272,7 +277,8 @@ def test_masked_pages_and_nan_in_unread_places(Q):
     scale = 128 ** -0.5
     k, v = cref.values8(clean["k_cache"], clean["k_scales"]), cref.values8(clean["v_cache"], clean["v_scales"])
     want = cref.attention(c["q"], k, v, c["table"], c["lens"], scale)
-    ref.close_out(run(c, scale), want, cref.attention_slack(c["q"], k, v, scale, 160, 2.0 ** -16))
+    ref.close_out(run(c, scale), want,
+                  cref.attention_slack(c["q"], k, v, scale, 160, weights(torch.bfloat16)))
 
 
 def test_lengths_past_the_table_and_past_the_announced():
@@ -361,7 +367,8 @@ def test_graph_replay_follows_lengths_and_tables():
     torch.cuda.synchronize()
     k, v = cref.values8(c["k_cache"], c["k_scales"]), cref.values8(c["v_cache"], c["v_scales"])
     want = cref.attention(c["q"], k, v, c["table"], c["lens"], 128 ** -0.5)
-    ref.close_out(out.cpu(), want, cref.attention_slack(c["q"], k, v, 128 ** -0.5, 3000, 2.0 ** -16))
+    ref.close_out(out.cpu(), want, cref.attention_slack(
+        c["q"], k, v, 128 ** -0.5, 3000, weights(torch.bfloat16)))
 
 
 def test_equal_calls_give_equal_bits():
@@ -379,4 +386,4 @@ def test_one_sequences_nan_stays_its_own():
     got = run(c, 0.1)
     assert torch.isnan(got[1]).all()
     ref.close_out(got[0::2], want[0::2], cref.attention_slack(
-        torch.nan_to_num(c["q"]), k, v, 0.1, 208, 2.0 ** -16))
+        torch.nan_to_num(c["q"]), k, v, 0.1, 208, weights(torch.bfloat16)))
