@@ -851,10 +851,10 @@ def rope_append_kv8(q_out, k_cache, v_cache, k_scales, v_scales, q, k_new, v_new
         raise ValueError("block_tables must be [batch, max_blocks_per_seq], context_lens [batch]")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise TypeError("block_tables and context_lens must be int32")
+    kv = (B, Q, Hkv, D)
     rope = _Rope(2 * pairs, rs[0], 1 if interleaved else 0, 0,
                  _token_stride(q, "q", qs), _token_stride(q_out, "q_out", qs),
-                 _token_stride(k_new, "k_new", (B, Q, Hkv, D)),
-                 _token_stride(v_new, "v_new", (B, Q, Hkv, D)))
+                 _token_stride(k_new, "k_new", kv), _token_stride(v_new, "v_new", kv))
     dev = _device_of(k_cache)
     _same_device(dev, (k_cache, v_cache, k_scales, v_scales, rotary_positions, phases, axes,
                        block_tables, context_lens))
@@ -944,12 +944,9 @@ def decode_kv8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, conte
     return out
 
 
-def _head_strides(t, name, shape):
+def _head_strides(t, name, batch, q_len, heads, width):
     """Elements between the tokens, and between the heads of a token, of a [batch,
     q_len, heads, width] view whose tokens lie evenly apart."""
-    if t.shape != shape:
-        raise ValueError(f"{name} {tuple(t.shape)} must be {tuple(shape)}")
-    batch, q_len, heads, width = shape
     sb, sq, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
@@ -985,8 +982,8 @@ def rope_append_latent(q_out, cache, q, latent_new, norm_weight, rotary_position
                            context_lens, eps, interleaved, stream)
         return q_out
     qs, cs, bts = q.shape, cache.shape, block_tables.shape
-    if len(qs) != 4:
-        raise ValueError("q must be [batch, q_len, num_heads, rope_dim]")
+    if len(qs) != 4 or q_out.shape != qs:
+        raise ValueError("q and q_out must be [batch, q_len, num_heads, rope_dim]")
     if len(cs) != 3:
         raise ValueError("cache must be [num_blocks, block_size, latent_dim + rope_dim]")
     dt = cache.dtype
@@ -998,39 +995,47 @@ def rope_append_latent(q_out, cache, q, latent_new, norm_weight, rotary_position
     NB, bs, W = cs
     if Q < 1:
         raise ValueError("q_len must be at least 1")
-    if latent_new.dim() != 3 or rotary_positions.shape != (B, Q):
+    if latent_new.shape != (B, Q, W) or rotary_positions.shape != (B, Q):
         raise ValueError("latent_new must be [batch, q_len, latent_dim + rope_dim], "
                          "rotary_positions [batch, q_len]")
+    weight = None
     if norm_weight is not None:
         if norm_weight.dtype != dt:
             raise TypeError("norm_weight must have the cache's dtype")
         if norm_weight.shape != (W - P,):
             raise ValueError("norm_weight must be [latent_dim]")
-    if phases.dtype != torch.int64 or rotary_positions.dtype != torch.int32:
+        weight = norm_weight.data_ptr()
+    i32 = torch.int32
+    if phases.dtype != torch.int64 or rotary_positions.dtype != i32:
         raise TypeError("phases must be the int64 table of rope_phases, rotary_positions int32")
     if phases.shape != (P // 2,):
         raise ValueError("phases must hold one value per rotary pair")
     if len(bts) != 2 or bts[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [batch, max_blocks_per_seq], context_lens [batch]")
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    if block_tables.dtype != i32 or context_lens.dtype != i32:
         raise TypeError("block_tables and context_lens must be int32")
-    rope = _LatentRope(1 if interleaved else 0, float(eps), *_head_strides(q, "q", qs),
-                       *_head_strides(q_out, "q_out", qs),
-                       _head_strides(latent_new.unsqueeze(2), "latent_new", (B, Q, 1, W))[0])
+    qt, qh = _head_strides(q, "q", B, Q, H, P)
+    ot, oh = _head_strides(q_out, "q_out", B, Q, H, P)
+    nb, nt, nd = latent_new.stride()
+    if nd != 1 or (Q > 1 and B > 1 and nb != Q * nt):
+        raise ValueError("latent_new's rows must be contiguous, its tokens evenly apart")
+    if Q == 1:
+        nt = nb if B > 1 else W
     dev = _device_of(cache)
     _same_device(dev, (cache, rotary_positions, phases, block_tables, context_lens))
     _same_device(dev, (q, q_out, latent_new), contiguous=False)
-    if norm_weight is not None:
+    if weight is not None:
         _same_device(dev, (norm_weight,))
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return rope_append_latent(q_out, cache, q, latent_new, norm_weight, rotary_positions,
                                       phases, block_tables, context_lens, eps, interleaved, stream)
     _check((_lib or _load()).pa_rope_append_latent(
-        q_out.data_ptr(), cache.data_ptr(), q.data_ptr(), latent_new.data_ptr(),
-        None if norm_weight is None else norm_weight.data_ptr(), rotary_positions.data_ptr(),
-        phases.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-        _LatentShape(B, H, W - P, P, bs, bts[1], NB, _KV_CODE[dt], 0), Q, rope,
+        q_out.data_ptr(), cache.data_ptr(), q.data_ptr(), latent_new.data_ptr(), weight,
+        rotary_positions.data_ptr(), phases.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), _LatentShape(B, H, W - P, P, bs, bts[1], NB, _KV_CODE[dt], 0), Q,
+        _LatentRope(1 if interleaved else 0, eps if type(eps) is float else float(eps), qt, qh, ot, oh,
+                    nt),
         _stream_on(dev, stream)), "pa_rope_append_latent")
     return q_out
 

@@ -23,7 +23,7 @@ SOURCES = ["pa_api.cu", "pa_step_api.cu", "pa_combine.cu", "pa_rope.cu", "pa_evi
            "pa_cache_api.cu", "pa_kv8_append.cu", "pa_kv8_attn_d64_n1.cu", "pa_kv8_attn_d64_n2.cu",
            "pa_kv8_attn_d64_n4.cu", "pa_kv8_attn_d128_n1.cu", "pa_kv8_attn_d128_n2.cu",
            "pa_kv8_attn_d128_n4.cu", "pa_kv8_attn_d256_n1.cu", "pa_kv8_attn_d256_n2.cu",
-           "pa_join.cu", "pa_latent_append.cu", "pa_latent_r128.cu",
+           "pa_latent_append.cu", "pa_latent_r128.cu",
            "pa_latent_r256.cu", "pa_latent_r512.cu", "pa_weights.cu", "pa_weights_tile.cu",
            "pa_attn_d64.cu", "pa_attn_d128.cu", "pa_attn_d256.cu",
            "pa_attn_d64_multi.cu", "pa_attn_d128_multi.cu", "pa_attn_d256_multi.cu",

@@ -80,19 +80,23 @@ pa_status check_kv8(const pa_shape* s, int32_t q_len) {
     const pa_status st = check_shape(s);
     if (st != PA_OK) return st;
     if (q_len < 1) return PA_ERR_INVALID_ARG;
-    // rows of a sequence, and tokens of a table, inside 31 bits
+    // rows of a sequence, units of a call and tokens of a table inside 31 bits
     if ((int64_t)q_len * s->num_heads > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)s->batch * s->num_heads * q_len > (1ll << 31) - 1) return PA_ERR_UNSUPPORTED;
     if ((int64_t)s->max_blocks_per_seq * s->block_size > (1 << 30)) return PA_ERR_UNSUPPORTED;
     return PA_OK;
 }
 
-// How a call is split: partitions of part_pages pages for each (sequence, kv
-// head, chunk of query tokens), joined in a cluster or through the workspace.
-struct Split {
-    int part_pages, parts;
-    bool cluster;
-    int chunk, chunks;  // query tokens of a CTA, and how many CTAs that makes
-    int kind;           // index of the kernel in kKv8
+// How a call over the 8-bit cache runs.
+struct Kv8Plan {
+    int kind;             // index of the kernel in kKv8
+    int chunk, chunks;    // query tokens of a CTA, and how many CTAs that makes
+    int64_t units;        // (sequence, kv head, chunk)
+    int group_size, unit_groups;
+    bool balanced;
+    int cluster, part_steps;
+    int64_t ctas;
+    size_t ml_at, desc_at, bytes;  // workspace
 };
 
 // The kernels by head_dim and rows of a CTA.
@@ -112,58 +116,60 @@ const Kv8Kernel kKv8[] = {{64, 8, launch_kv8_d64_n1, kv8_ctas_d64_n1},
 constexpr int kKv8Count = sizeof kKv8 / sizeof kKv8[0];
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Workspace: acc [rows][parts][width] fp32, then (m, l); SIZE_MAX where no size_t holds it.
-size_t partial_bytes(const Split& sp, size_t rows, int width, size_t* ml_at) {
-    if (sp.parts <= 1 || sp.cluster) return 0;
-    size_t acc = 0, ml = 0;
-    if (__builtin_mul_overflow(rows, (size_t)sp.parts, &rows) ||
-        __builtin_mul_overflow(rows, (size_t)width * 4, &acc) || __builtin_mul_overflow(rows, (size_t)8, &ml) ||
-        acc > SIZE_MAX - 255 - ml)
-        return SIZE_MAX;
-    const size_t at = (acc + 255) / 256 * 256;
-    if (ml_at) *ml_at = at;
-    return at + ml;
-}
+// Largest batch whose lengths every CTA looks through for its run (2 us).
+constexpr int kMaxBalancedLens = 2048;
 
-// With units = (sequence, kv head, chunk) and `slots` CTAs resident at once: one
-// wave of equal partitions where the units leave room for several, in a cluster
-// (up to 8, no second launch) where that gives about as many; else, with more
-// units than slots, partitions of about 1024 tokens, so that long and ragged
-// sequences even out over the waves.
-Split split_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
-    Split sp;
+// Short calls of few units: clusters of up to 8 CTAs, up to 16 steps to a CTA
+// and no second launch (8 sequences of 700 tokens, 8 kv heads: 7.8 us against 9.9
+// in runs that a second launch joins; 16 sequences of 1 .. 16,384 tokens in
+// clusters of 3 took 89 us).  Else equal runs of steps over the CTAs
+// that the GPU holds (64 sequences of 1 .. 4096 tokens: a unit to a CTA took 75 us,
+// runs 60 with the join: DRAM at 82 %).  With more than 3 units for each of them,
+// where the waves even out by themselves (128 sequences of 1 .. 2048: 61 us against
+// 68 in runs), of short contexts (32 sequences of 300: 8 against 16), or with more
+// lengths than a CTA looks through, a unit to a CTA.
+Kv8Plan plan_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
+    Kv8Plan pl;
     // the smallest row tile that holds a sequence's rows, or the largest there is
     const int group = s->num_heads / s->num_kv_heads;
-    sp.kind = -1;
+    pl.kind = -1;
     for (int i = 0; i < kKv8Count; ++i)
         if (kKv8[i].head_dim == s->head_dim &&
-            (sp.kind < 0 || (int64_t)q_len * group > kKv8[sp.kind].rows))
-            sp.kind = i;
-    const int per = kKv8[sp.kind].rows / group;
-    sp.chunk = q_len < per ? q_len : per;
-    sp.chunks = (q_len + sp.chunk - 1) / sp.chunk;
-    const int64_t pages = announced_tokens(max_context_len, s->block_size, s->max_blocks_per_seq) / s->block_size;
-    const int64_t units = (int64_t)s->batch * s->num_kv_heads * sp.chunks;
-    const int64_t slots = (int64_t)sms * kKv8[sp.kind].ctas();
-    const int64_t fill = slots / units;
-    int64_t parts = 1;
-    sp.cluster = false;
-    if (fill >= 2) {
-        const int64_t in_cluster = std::min<int64_t>({8, fill, ceil_div(pages, 4)});
-        const int64_t apart = std::min(fill, ceil_div(pages, 16));
-        sp.cluster = in_cluster * 4 >= apart * 3;
-        parts = sp.cluster ? in_cluster : apart;
-    } else if (fill < 1) {
-        parts = ceil_div(pages * s->block_size, 1024);
+            (pl.kind < 0 || (int64_t)q_len * group > kKv8[pl.kind].rows))
+            pl.kind = i;
+    const int per = kKv8[pl.kind].rows / group;
+    pl.chunk = q_len < per ? q_len : per;
+    pl.chunks = (q_len + pl.chunk - 1) / pl.chunk;
+    const int64_t steps = ceil_div(announced_tokens(max_context_len, s->block_size, s->max_blocks_per_seq), 32);
+    pl.units = (int64_t)s->batch * s->num_kv_heads * pl.chunks;
+    const int64_t slots = (int64_t)sms * kKv8[pl.kind].ctas();
+    const int64_t fill = slots / pl.units;
+    pl.balanced = false;
+    pl.cluster = 1;
+    // (a power of two: clusters of 7 that fill the GPU took 12.8 us where 4 took 7.8)
+    int64_t in_cluster = 8;
+    while (in_cluster > 1 && in_cluster > std::min(fill, ceil_div(steps, 2))) in_cluster /= 2;
+    if (in_cluster >= 2 && ceil_div(steps, in_cluster) <= 16) pl.cluster = (int)in_cluster;
+    if (pl.cluster == 1 && steps > 16)
+        pl.balanced = pl.units <= 3 * slots && s->batch <= kMaxBalancedLens;
+    pl.part_steps = (int)ceil_div(steps, pl.cluster);
+    const int64_t per_seq = (int64_t)s->num_kv_heads * pl.chunks;
+    pl.unit_groups = (int)ceil_div(per_seq, 32);
+    pl.group_size = (int)ceil_div(per_seq, pl.unit_groups);
+    pl.ctas = pl.units * pl.cluster;
+    if (pl.balanced)
+        pl.ctas = std::max<int64_t>(std::min(slots / pl.group_size, (int64_t)s->batch * pl.unit_groups * steps), 1) *
+                  pl.group_size;
+    pl.ml_at = pl.desc_at = pl.bytes = 0;
+    if (pl.balanced) {
+        const size_t rows = (size_t)pl.ctas * 2 * kKv8[pl.kind].rows;
+        pl.ml_at = up256(rows * s->head_dim * 4);
+        pl.desc_at = up256(pl.ml_at + rows * 8);
+        pl.bytes = pl.desc_at + (size_t)pl.units * sizeof(PieceDesc);
     }
-    parts = std::min<int64_t>(parts, kMaxJoinParts);
-    // whole steps of the kernel: 32 tokens
-    const int step = 32 / s->block_size;
-    sp.part_pages = (int)(ceil_div(ceil_div(pages, parts), step) * step);
-    sp.parts = (int)ceil_div(pages, sp.part_pages);
-    if (sp.parts == 1) sp.cluster = false;
-    return sp;
+    return pl;
 }
 
 // How a call over the latent cache runs: row tiles of 16, 32 or 64, the CTAs in
@@ -176,7 +182,6 @@ struct LatentPlan {
     int64_t ctas;
     size_t ml_at, desc_at, bytes;  // workspace; bytes 0: no sequence can be cut
 };
-constexpr int kMaxLatentBalanced = 2048;
 
 LatentPlan plan_latent(const pa_latent_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
     LatentPlan pl;
@@ -185,7 +190,7 @@ LatentPlan plan_latent(const pa_latent_shape* s, int32_t q_len, int32_t max_cont
     pl.row_tiles = (int)ceil_div(rows, pl.row_tile);
     pl.row_groups = (int)ceil_div(pl.row_tiles, 8);
     pl.group_size = (int)ceil_div(pl.row_tiles, pl.row_groups);
-    pl.balanced = s->batch <= kMaxLatentBalanced;
+    pl.balanced = s->batch <= kMaxBalancedLens;
     int64_t groups = (int64_t)s->batch * pl.row_groups;
     if (pl.balanced) {
         const int64_t tiles = ceil_div(announced_tokens(max_context_len, s->block_size, s->max_blocks_per_seq), 64);
@@ -194,11 +199,10 @@ LatentPlan plan_latent(const pa_latent_shape* s, int32_t q_len, int32_t max_cont
     pl.ctas = groups * pl.group_size;
     pl.ml_at = pl.desc_at = pl.bytes = 0;
     if (pl.balanced && groups > 1) {
-        auto up = [](size_t x) { return (x + 255) / 256 * 256; };
         const size_t records = (size_t)pl.ctas * 2 * pl.row_tile;
-        pl.ml_at = up(records * s->latent_dim * 4);
-        pl.desc_at = up(pl.ml_at + records * 8);
-        pl.bytes = pl.desc_at + (size_t)s->batch * pl.row_tiles * sizeof(LatentDesc);
+        pl.ml_at = up256(records * s->latent_dim * 4);
+        pl.desc_at = up256(pl.ml_at + records * 8);
+        pl.bytes = pl.desc_at + (size_t)s->batch * pl.row_tiles * sizeof(PieceDesc);
     }
     return pl;
 }
@@ -305,8 +309,7 @@ size_t pa_workspace_size_kv8(const pa_shape* shape, int32_t q_len, int32_t max_c
     if (check_kv8(shape, q_len) != PA_OK || max_context_len < 0 || shape->batch == 0 ||
         device_state(&sms, nullptr) != PA_OK)
         return 0;
-    const Split sp = split_kv8(shape, q_len, max_context_len, sms);
-    return partial_bytes(sp, (size_t)shape->batch * q_len * shape->num_heads, shape->head_dim, nullptr);
+    return plan_kv8(shape, q_len, max_context_len, sms).bytes;
 }
 
 pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -342,18 +345,14 @@ pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const voi
     int32_t* err = nullptr;
     st = device_state(&sms, &err);
     if (st != PA_OK) return st;
-    const Split sp = split_kv8(shape, q_len, max_context_len, sms);
-    size_t ml_at = 0;
-    const size_t need = partial_bytes(sp, rows, D, &ml_at);
-    if (need) {
-        if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return PA_ERR_WORKSPACE;
-        const Span w{workspace, need};
+    const Kv8Plan pl = plan_kv8(shape, q_len, max_context_len, sms);
+    if (pl.bytes) {
+        if (!workspace || !aligned(workspace, 16) || workspace_bytes < pl.bytes) return PA_ERR_WORKSPACE;
+        const Span w{workspace, pl.bytes};
         if (overlap(w, o)) return PA_ERR_INVALID_ARG;
         for (const Span& i : ins)
             if (overlap(w, i)) return PA_ERR_INVALID_ARG;
     }
-    const int64_t grid_y = (int64_t)Hkv * sp.chunks;
-    if (grid_y > 65535) return PA_ERR_UNSUPPORTED;
     Kv8Launch L;
     std::memset(&L, 0, sizeof L);
     // one kv head's rows of a page (a column block of at most 128 bytes), swizzled for the lanes' loads
@@ -372,46 +371,35 @@ pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const voi
     p.v_scales = v_scales;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
-    p.part_acc = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_at);
+    char* ws = static_cast<char*>(workspace);
+    p.part_acc = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + pl.ml_at);
+    p.part_desc = reinterpret_cast<PieceDesc*>(ws + pl.desc_at);
     p.err = err;
     p.timeout_ns = kDefaultTimeoutNs;
     p.num_blocks = shape->num_blocks;
     p.qscale = scale * 1.4426950408889634f;  // log2(e)
+    p.batch = shape->batch;
     p.q_len = q_len;
     p.num_heads = shape->num_heads;
     p.num_kv_heads = Hkv;
     p.group = shape->num_heads / Hkv;
     p.max_blocks = shape->max_blocks_per_seq;
-    p.q_chunk = sp.chunk;
+    p.q_chunk = pl.chunk;
+    p.chunks = pl.chunks;
+    p.group_size = pl.group_size;
+    p.unit_groups = pl.unit_groups;
+    p.bf16 = shape->kv_dtype == PA_BF16;
     p.token_limit = announced_tokens(max_context_len, BS, shape->max_blocks_per_seq);
-    p.part_pages = sp.part_pages;
-    p.num_parts = sp.parts;
-    p.cluster = sp.cluster ? sp.parts : 1;
+    p.balanced = pl.balanced ? 1 : 0;
+    p.cluster = pl.cluster;
+    p.part_steps = pl.part_steps;
     p.out_dtype = shape->out_dtype;
     L.block_size = BS;
+    L.units = (int)pl.units;
     L.pdl = use_pdl();
-    p.bf16 = shape->kv_dtype == PA_BF16;
-    L.grid = dim3((unsigned)sp.parts, (unsigned)grid_y, (unsigned)shape->batch);
-    cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = kKv8[sp.kind].launch(L, cs);
-    if (e != cudaSuccess || !need) return done(e);
-    JoinParams j;
-    std::memset(&j, 0, sizeof j);
-    j.out = out;
-    j.part_acc = p.part_acc;
-    j.part_ml = p.part_ml;
-    j.context_lens = context_lens;
-    j.width = D;
-    j.group = p.group;
-    j.unit_rows = q_len * p.group;
-    j.max_blocks = p.max_blocks;
-    j.block_size = BS;
-    j.token_limit = p.token_limit;
-    j.part_pages = sp.part_pages;
-    j.num_parts = sp.parts;
-    j.out_dtype = shape->out_dtype;
-    return done(launch_join(j, shape->batch, Hkv, L.pdl, cs));
+    L.grid = dim3((unsigned)pl.ctas);
+    return done(kKv8[pl.kind].launch(L, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_rope_append_latent(void* q_out, void* cache, const void* q, const void* latent_new,
@@ -559,7 +547,7 @@ pa_status pa_decode_latent(void* out, const void* q, const void* cache,
     p.context_lens = context_lens;
     p.part_acc = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float*>(ws + pl.ml_at);
-    p.part_desc = reinterpret_cast<LatentDesc*>(ws + pl.desc_at);
+    p.part_desc = reinterpret_cast<PieceDesc*>(ws + pl.desc_at);
     p.err = err;
     p.timeout_ns = kDefaultTimeoutNs;
     p.num_blocks = shape->num_blocks;

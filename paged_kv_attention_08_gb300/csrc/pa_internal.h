@@ -162,6 +162,14 @@ struct Append8Params {
     int32_t rotary_dim, num_axes, interleaved;
 };
 
+// Where the pieces of a unit lie that an attention over the 8-bit or the latent
+// cache has cut: in the records of CTA groups first_group .. last_group that have
+// work (record 0, in the first group first_record), CTA `member` of each.
+struct PieceDesc {
+    int32_t first_group, last_group, first_record, member;
+    int64_t total;            // steps, or tiles, of the call's flat order
+};
+
 // Attention over the 8-bit cache.
 struct Kv8Params {
     const void* q;            // [B, Q, H, D]
@@ -170,39 +178,33 @@ struct Kv8Params {
     const float* v_scales;
     const int32_t* block_tables;
     const int32_t* context_lens;
-    float* part_acc;          // [B, Hkv, P, Q * group, D] (partitions that the join kernel reads)
-    float* part_ml;           // [B, Hkv, P, Q * group, 2]
+    float* part_acc;          // [CTAs][2 records][rows of a CTA][D]
+    float* part_ml;           // [CTAs][2][rows of a CTA][2]
+    PieceDesc* part_desc;       // [units]
     int32_t* err;             // device error word, bound on every wait
     uint64_t timeout_ns;
     int64_t num_blocks;
     float qscale;             // scale * log2(e)
-    int32_t q_len, num_heads, num_kv_heads, group, max_blocks;
+    int32_t batch, q_len, num_heads, num_kv_heads, group, max_blocks;
     int32_t q_chunk;          // query tokens of a CTA (q_chunk * group fills its 8-row tiles)
+    int32_t chunks;           // of a sequence's query tokens
+    int32_t group_size;       // adjacent CTAs that walk the same tokens, a unit each
+    int32_t unit_groups;      // groups of units of a sequence
     int32_t bf16;             // q's type
     int32_t token_limit;      // tokens from here on are not attended to
-    int32_t part_pages, num_parts;
-    int32_t cluster;          // > 1: the num_parts partitions are a cluster and join there
+    int32_t balanced;         // 1: equal runs of steps; else a unit to a CTA, or to a cluster
+    int32_t cluster;          // CTAs of a unit, part_steps steps each
+    int32_t part_steps;
     int32_t out_dtype;
 };
 
 struct Kv8Launch {
     Kv8Params p;
     CUtensorMap tmap_k, tmap_v;
-    int block_size;
+    int block_size, units;
     bool pdl;
     dim3 grid;
 };
-
-// Joining the partitions of an attention (8-bit or latent cache).
-struct JoinParams {
-    void* out;                // [B, Q, Hkv * group, width]
-    const float* part_acc;    // [B, Hkv, P, Q * group, width]
-    const float* part_ml;
-    const int32_t* context_lens;
-    int32_t width, group, unit_rows, max_blocks, block_size;
-    int32_t token_limit, part_pages, num_parts, out_dtype;
-};
-constexpr int kMaxJoinParts = 8192;
 
 // Append to the latent cache (strides in elements).
 struct LatentAppendParams {
@@ -221,14 +223,6 @@ struct LatentAppendParams {
     int32_t span;             // tokens of a CTA
 };
 
-// Where the pieces of a (sequence, row tile) lie: in the records of CTA groups
-// first_group .. last_group that have tiles (record 0, in the first group
-// first_record), CTA `member` of each.
-struct LatentDesc {
-    int32_t first_group, last_group, first_record, member;
-    int64_t total;            // tiles of the call's flat order
-};
-
 // Attention over the latent cache.
 struct LatentParams {
     const void* q;            // [B, Q, H, latent_dim + 64]
@@ -237,7 +231,7 @@ struct LatentParams {
     const int32_t* context_lens;
     float* part_acc;          // [CTAs][2 records][row tile][latent_dim]
     float* part_ml;           // [CTAs][2][row tile][2]
-    LatentDesc* part_desc;    // [B][row tiles]
+    PieceDesc* part_desc;    // [B][row tiles]
     int32_t* err;             // device error word, bound on every wait
     uint64_t timeout_ns;
     int64_t num_blocks;
@@ -602,7 +596,6 @@ int kv8_ctas_d128_n2();
 int kv8_ctas_d128_n4();
 int kv8_ctas_d256_n1();
 int kv8_ctas_d256_n2();
-cudaError_t launch_join(const JoinParams& p, int batch, int num_kv_heads, bool pdl, cudaStream_t stream);
 cudaError_t launch_append_latent(LatentAppendParams p, bool bf16, int num_sms, bool pdl,
                                  cudaStream_t stream);
 cudaError_t launch_latent_r128(const LatentLaunch& L, cudaStream_t stream);

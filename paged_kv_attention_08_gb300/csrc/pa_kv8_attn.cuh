@@ -1,5 +1,12 @@
-// Attention over the 8-bit cache: one CTA per (sequence, kv head and chunk of up
-// to 32 query rows, partition of the sequence's pages).
+// Attention over the 8-bit cache.  A unit is a (sequence, kv head, chunk of up to
+// 32 query rows).  The CTAs work in groups, adjacent blocks that walk the same
+// tokens for different units of a sequence (a page's kv heads lie side by side:
+// read at different times, 128 bytes each, they cost 166 us where read together
+// they cost 94).  A group takes an equal run of the flattened (sequence, group of
+// units, 32-token step) order whatever the lengths, a few segments each (the
+// pieces of a unit that is cut are joined by kv8_join_kernel); or a CTA takes a
+// unit whole, or, of few and short units, a partition that a cluster of up to 8
+// joins.
 //
 // The mathematics: with codes k8, v8 and the page's scales sk, sv,
 //     s_t = scale * sk (q . k8_t),      out = sum_t 2^(s_t) sv v8_t / sum_t 2^(s_t)
@@ -47,8 +54,9 @@ struct Kv8Cfg {
     static constexpr uint32_t PAGE = BS * D;        // bytes of a page's keys of one head
     static constexpr uint32_t TILE = STEP * D;      // and of a step's
     static constexpr bool QSMEM = KSTEPS * NR > 16; // queries' fragments in shared memory, not registers
-    static constexpr int REGS = (D / 16) * NR * 4 + (QSMEM ? 0 : KSTEPS * NR * 2) + 8 * NR;  // those that stay
-    static constexpr int CTAS = REGS > 120 ? 2 : REGS > 60 ? 3 : 4;                          // per SM
+    // CTAs of an SM: two hold the queries, sums and weights in registers; at head_dim
+    // 64 three do (three at 128: the same time, with spills)
+    static constexpr int CTAS = D == 64 && NR < 4 ? 3 : 2;
     // stages of a ring: as a CTA's share of shared memory allows
     static constexpr int NS_RAW = (int)((224u / CTAS - 4u) * 1024u / (NW * 2 * TILE));
     static constexpr int NS = NS_RAW > 4 ? 4 : NS_RAW < 1 ? 1 : NS_RAW;
@@ -57,7 +65,8 @@ struct Kv8Cfg {
     // the join of the warps, and of a cluster, in the rings' place
     static constexpr uint32_t JOIN = 4u * (NW * R * D + 2 * NW * R + R * D + 2 * R);
     static constexpr uint32_t BAR_OFF = RING > JOIN ? RING : JOIN;
-    static constexpr uint32_t Q_OFF = BAR_OFF + (8 + 4) * NW * NS + 16 - (12 * NW * NS) % 16;
+    static constexpr uint32_t RUN_OFF = BAR_OFF + (8 + 4) * NW * NS + 16 - (12 * NW * NS) % 16;
+    static constexpr uint32_t Q_OFF = RUN_OFF + 48;
     static constexpr uint32_t SMEM = Q_OFF + (QSMEM ? KSTEPS * NR * 256u : 0u) + kSmemAlignSlack;
     static_assert(SMEM * CTAS <= 227u * 1024u - CTAS * 1024u, "shared memory");
 };
@@ -109,9 +118,11 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tig = lane & 3;
     const int G = p.group, Hkv = p.num_kv_heads, Q = p.q_len;
-    const int part = blockIdx.x, b = blockIdx.z;
-    const int kvh = (int)blockIdx.y % Hkv, qi0 = (int)blockIdx.y / Hkv * p.q_chunk;
-    const int R = min(p.q_chunk, Q - qi0) * G;
+    const int gshift = __ffs(G) - 1;  // the group is a power of two
+    // start, end, flat position of the present sequence's steps, total, present
+    // position; the present sequence
+    long long* run = reinterpret_cast<long long*>(smem + C::RUN_OFF);
+    int32_t* run_b = reinterpret_cast<int32_t*>(run + 5);
 
     if (tid == 0) {
         for (int i = 0; i < NW * NS; ++i) mbar_init(smem_u32(full + i), 1);
@@ -122,24 +133,65 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
     grid_dependency_wait();
     grid_launch_dependents();
 
+    const int per_seq = Hkv * p.chunks;  // units of a sequence
+    auto steps_of = [&](int b) -> int {
+        const int t = min(min(max(__ldg(p.context_lens + b), 0), p.max_blocks * BS), p.token_limit);
+        return max((t + STEP - 1) / STEP, 1);  // (an empty sequence writes its zeros)
+    };
+    if (p.balanced && warp == 0) {
+        // the CTA's run: [start, end) of all steps, and the sequence that it begins in
+        long long w = 0;
+        for (int b = lane; b < p.batch; b += 32) w += steps_of(b);
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) w += __shfl_xor_sync(kFullMask, w, k);
+        w *= p.unit_groups;
+        const long long groups = gridDim.x / p.group_size, group = blockIdx.x / p.group_size;
+        const long long start = group * w / groups, end = (group + 1) * w / groups;
+        int b = 0;
+        long long base = 0;
+        while (start < end) {
+            const int bb = b + lane;
+            const long long v = bb < p.batch ? (long long)steps_of(bb) * p.unit_groups : 0;
+            long long incl = v;
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+                const long long o = __shfl_up_sync(kFullMask, incl, k);
+                if (lane >= k) incl += o;
+            }
+            const unsigned hit = __ballot_sync(kFullMask, bb < p.batch && base + incl > start);
+            if (hit) {
+                const int k = __ffs(hit) - 1;
+                base += __shfl_sync(kFullMask, incl - v, k);
+                b += k;
+                break;
+            }
+            base += __shfl_sync(kFullMask, incl, 31);
+            b += 32;
+        }
+        if (lane == 0) run[0] = run[4] = start, run[1] = end, run[2] = base, run[3] = w, *run_b = b;
+    }
+    __syncthreads();  // barriers initialised, the run known
+
+    bool aborted = false;
+    int done = 0;  // steps of the warp's ring so far
+
+    // Steps [k0, k1) of unit (b, kvh, chunk); `record`: where a piece's (m, l, acc)
+    // go, -1 for a whole unit's output, -2 for a cluster's.
+    auto segment = [&](int b, int kvh, int chunk, int k0, int k1, long long record) {
+    const int qi0 = chunk * p.q_chunk;
+    const int R = min(p.q_chunk, Q - qi0) * G;
     const int ctx = max(__ldg(p.context_lens + b), 0);
     const int reach = min(min(ctx, p.max_blocks * BS), p.token_limit);  // tokens of the call
-    const int pb = part * p.part_pages;
-    const int pe = min(pb + p.part_pages, (reach + BS - 1) / BS);
+    const int pb = k0 * PP, pe = min(k1 * PP, (reach + BS - 1) / BS);
     auto row_off = [&](int r) -> size_t {
-        return (((size_t)b * Q + qi0 + r / G) * p.num_heads + kvh * G + r % G) * D;
+        return (((size_t)b * Q + qi0 + (r >> gshift)) * p.num_heads + kvh * G + (r & (G - 1))) * D;
     };
-    if (pb >= pe && p.cluster <= 1) {
-        if (p.num_parts <= 1)
-            for (int i = tid; i < R * D; i += 128) store_out(p.out, row_off(i / D) + i % D, 0.f, p.out_dtype);
-        return;  // (the join does not read partitions past the context)
-    }
 
     // ---- the warp's steps of PP pages: number warp, warp + NW, ... of the
-    // partition's; it keeps 32 table entries ahead, one a lane, and the scales of
+    // segment's; it keeps 32 table entries ahead, one a lane, and the scales of
     // the pages that it consumes ----
     constexpr int WINDOW = 32 / PP;  // steps whose entries the lanes hold
-    const int steps = (pe - pb + PP - 1) / PP;
+    const int steps = pe > pb ? (pe - pb + PP - 1) / PP : 0;
     const int n_s = steps > warp ? (steps - warp + NW - 1) / NW : 0;
     const int32_t* table = p.block_tables + (size_t)b * p.max_blocks;
     auto fetch = [&](int chunk) -> int {
@@ -153,7 +205,6 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
         sv_ahead = e >= 0 ? __ldg(p.v_scales + (size_t)e * Hkv + kvh) : 1.f;
     };
     int ent = fetch(0), ent_next = fetch(1);
-    __syncthreads();  // barriers initialised
     // Whole warp: entries of its step i, and (one lane) the copies.
     auto issue = [&](int i) {
         if (i > 0 && i % WINDOW == 0) {
@@ -169,11 +220,12 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             on |= (e[u] >= 0 ? 1u : 0u) << u;
         }
         if (lane == 0) {
-            const int sidx = warp * NS + i % NS;
+            const int sidx = warp * NS + (done + i) % NS;
             const uint32_t bar = smem_u32(full + sidx);
             on_of[sidx] = (int32_t)on;
             if (on) {
-                const uint64_t policy = l2_policy_evict_first();
+                // (several chunks of rows read the same pages)
+                const uint64_t policy = p.chunks > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
                 mbar_arrive_expect_tx(bar, 2 * C::PAGE * __popc(on));
 #pragma unroll
                 for (int u = 0; u < PP; ++u) {
@@ -191,6 +243,7 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             }
         }
     };
+    fence_proxy_async_smem();  // the last segment's join used the rings
     for (int i = 0; i < min(n_s, NS); ++i) issue(i);
     fetch_scales(ent);
 
@@ -198,7 +251,6 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
     // each tile, scaled by a power of two ----
     uint2 qf[C::QSMEM ? 1 : KSTEPS][C::QSMEM ? 1 : NR];
     float qk[NR][2];  // of rows 2 tig, + 1: scale * log2(e), and the row's power of two taken out again
-    int lim[NR][2];   // tokens that the row attends to: its query token's causal limit
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
         const bool real = j * 8 + g < R;  // (other rows: zeros, their results are not used)
@@ -240,14 +292,13 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = j * 8 + tig * 2 + e;
-            qk[j][e] = __shfl_sync(kFullMask, back, (tig * 2 + e) * 4);
-            lim[j][e] = r < R ? min(reach, ctx - Q + qi0 + r / G + 1) : reach;
-        }
+        for (int e = 0; e < 2; ++e) qk[j][e] = __shfl_sync(kFullMask, back, (tig * 2 + e) * 4);
     }
     if constexpr (C::QSMEM) __syncthreads();
-    const int lim_least = min(reach, ctx - Q + qi0 + 1);  // the first row's
+    // Tokens that a row attends to: its query token's causal limit; the first row's
+    // is the least.  (Rows past R see all: their results are not used.)
+    const int lim_first = ctx - Q + qi0 + 1, lim_least = min(reach, lim_first);
+    auto lim = [&](int r) { return min(reach, lim_first + (r >> gshift)); };
 
     float m[NR][2], l[NR][2], acc[MT][NR][4];
 #pragma unroll
@@ -260,12 +311,12 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
         for (int j = 0; j < NR; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
 
     float sk = 0.f, sv = 1.f;
-    bool aborted = false;
     int issued = min(n_s, NS);
     for (int i = 0; i < n_s; ++i) {
         if (i % WINDOW == 0) sk = sk_ahead, sv = sv_ahead;
-        const int sidx = warp * NS + i % NS;
-        if (!__all_sync(kFullMask, mbar_wait_bounded(smem_u32(full + sidx), (i / NS) & 1, p.timeout_ns))) {
+        const int sidx = warp * NS + (done + i) % NS;
+        if (!__all_sync(kFullMask,
+                        mbar_wait_bounded(smem_u32(full + sidx), ((done + i) / NS) & 1, p.timeout_ns))) {
             if (lane == 0) record_error(p.err, PA_ERR_TIMEOUT);
             aborted = true;
         }
@@ -341,7 +392,7 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
                         x = fmaf(x, qk[j][c & 1] * page_sk[u], lv[u]);
                         if (masked) {
                             const int at = t * 16 + (c >> 1) * 8 + g;
-                            if (first + at >= lim[j][c & 1] || !held(at)) x = NEG_INF;
+                            if (first + at >= lim(j * 8 + tig * 2 + (c & 1)) || !held(at)) x = NEG_INF;
                         }
                         above = fmaxf(above, x - m[j][c & 1]);
                     }
@@ -439,10 +490,12 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             // copies in flight land before the stages are used again
             if (lane == 0)
                 for (int k = i + 1; k < issued; ++k)
-                    (void)mbar_wait_bounded(smem_u32(full + warp * NS + k % NS), (k / NS) & 1, p.timeout_ns);
+                    (void)mbar_wait_bounded(smem_u32(full + warp * NS + (done + k) % NS),
+                                            ((done + k) / NS) & 1, p.timeout_ns);
             break;
         }
     }
+    done += n_s;
 
     // ---- join the warps' results in the rings' place ----
 #pragma unroll
@@ -472,7 +525,6 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             if (g == 0) mm[warp * R + r] = m[j][e], ml[warp * R + r] = l[j][e];
         }
     __syncthreads();
-    const size_t row0 = (((size_t)b * Hkv + kvh) * p.num_parts + part) * ((size_t)Q * G) + (size_t)qi0 * G;
     for (int idx = tid; idx < R * D; idx += 128) {
         const int r = idx / D, d = idx % D;
         float M = NEG_INF;
@@ -486,22 +538,24 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             A = fmaf(f, macc[((size_t)w * R + r) * D + d], A);
             L = fmaf(f, ml[w * R + r], L);
         }
-        if (p.cluster > 1) {
+        if (record == -2) {
             cpart[idx] = A;
             if (d == 0) cpart[R * D + r] = M, cpart[R * D + R + r] = L;
-        } else if (p.num_parts > 1) {
-            p.part_acc[(row0 + r) * D + d] = A;
-            if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (row0 + r) * 2) = make_float2(M, L);
+        } else if (record >= 0) {
+            p.part_acc[(record * C::R + r) * D + d] = A;
+            if (d == 0)
+                *reinterpret_cast<float2*>(p.part_ml + (record * C::R + r) * 2) = make_float2(M, L);
         } else {
             store_out(p.out, row_off(r) + d, L == 0.f ? 0.f : A / L, p.out_dtype);
         }
     }
-    if (p.cluster > 1) {
+    if (record == -2) {
         // the cluster's partitions, through distributed shared memory: each CTA
         // finishes a share of the outputs
         cluster_sync_release_acquire();
+        const int part = (int)blockIdx.x % p.cluster;
         const uint32_t cp = smem_u32(cpart);
-        const int P = p.num_parts, share = (R * D + P - 1) / P;
+        const int P = p.cluster, share = (R * D + P - 1) / P;
         const int end = min((part + 1) * share, R * D);
         uint32_t base[kMaxClusterParts];
 #pragma unroll
@@ -531,6 +585,139 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
         }
         cluster_sync_relaxed();  // no CTA leaves while others read its shared memory
     }
+    };
+
+    // ---- the CTA's segments: those of its run, or its unit's one (the walk's state
+    // stays in shared memory: in registers it spilled) ----
+    if (p.balanced && run[0] >= run[1]) return;
+    for (;;) {
+        int b, x, k0, k1;
+        long long record = -1;
+        if (p.balanced) {
+            b = *run_b;
+            const long long base = run[2], at = run[4];
+            const int n = steps_of(b);
+            const int xg = (int)((at - base) / n), member = (int)blockIdx.x % p.group_size;
+            x = xg * p.group_size + member;
+            k0 = (int)(at - base - (long long)xg * n);
+            k1 = (int)min((long long)n, k0 + (run[1] - at));
+            if (k0 > 0 || k1 < n) record = blockIdx.x * 2ll + (at == run[0] ? 0 : 1);
+            if (k0 == 0 && tid == 0 && x < per_seq) {
+                // where the join finds the unit's pieces: group g has the steps from
+                // floor(g total / groups) on
+                const long long first = base + (long long)xg * n, groups = gridDim.x / p.group_size;
+                PieceDesc d;
+                d.first_group = (int)blockIdx.x / p.group_size;
+                d.last_group = (int)(((first + n) * groups - 1) / run[3]);
+                d.first_record = first == run[0] ? 0 : 1;
+                d.member = member;
+                d.total = run[3];
+                p.part_desc[(size_t)b * per_seq + x] = d;
+            }
+        } else {
+            const long long u = blockIdx.x / p.cluster;
+            const int part = (int)blockIdx.x % p.cluster;
+            b = (int)(u / per_seq);
+            x = (int)(u % per_seq);
+            const int n = steps_of(b);
+            k0 = min(part * p.part_steps, n);
+            k1 = p.cluster > 1 ? min(k0 + p.part_steps, n) : n;
+            if (p.cluster > 1) record = -2;
+        }
+        if (x < per_seq) segment(b, x / p.chunks, x % p.chunks, k0, k1, record);
+        if (!p.balanced) return;
+        if (__syncthreads_or(aborted)) return;  // (and the rings are free again)
+        if (tid == 0) {
+            run[4] += k1 - k0;
+            const long long whole = (long long)steps_of(b) * p.unit_groups;
+            if (run[4] - run[2] >= whole) run[2] += whole, *run_b = b + 1;
+        }
+        __syncthreads();
+        if (run[4] >= run[1]) return;
+    }
+}
+
+// Joins the pieces of cut units: with each piece's (m, l, acc),
+//     out = sum 2^(m - M) acc / sum 2^(m - M) l.
+// A thread takes four elements of a row; SHARES threads share the pieces (eight
+// where a few units lie in seven runs and more, else one).  Bound by the latency of
+// its steps: the unit's descriptor, then statistics and sums.
+constexpr int kKv8JoinThreads = 256;
+
+template <int D, int RT, int SHARES>
+__global__ void __launch_bounds__(kKv8JoinThreads) kv8_join_kernel(const Kv8Params p, int groups) {
+    constexpr int PER = kKv8JoinThreads / SHARES, LANES = D / 4, AHEAD = 4;
+    __shared__ float sums[SHARES][6][PER];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const PieceDesc d = p.part_desc[blockIdx.x];
+    if (d.first_group == d.last_group) return;  // whole: written already
+    const int u = blockIdx.x, chunk = u % p.chunks, kvh = u / p.chunks % p.num_kv_heads;
+    const int b = u / (p.chunks * p.num_kv_heads), qi0 = chunk * p.q_chunk;
+    const int R = min(p.q_chunk, p.q_len - qi0) * p.group;
+    const int share = threadIdx.x / PER, at = blockIdx.y * PER + threadIdx.x % PER;
+    const int r = at / LANES, col = at % LANES * 4;
+    const int pieces = r < R ? d.last_group - d.first_group + 1 : 0;
+    float M = -INFINITY, L = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int x0 = share; x0 < pieces; x0 += SHARES * AHEAD) {
+        float2 ml[AHEAD];
+        float4 y[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int x = x0 + k * SHARES;
+            const long long g = d.first_group + x;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            // (a group without steps has no record)
+            if (x < pieces && g * d.total / groups != (g + 1) * d.total / groups) {
+                const long long row =
+                    ((g * p.group_size + d.member) * 2 + (x == 0 ? d.first_record : 0)) * RT + r;
+                ml[k] = *reinterpret_cast<const float2*>(p.part_ml + row * 2);
+                y[k] = *reinterpret_cast<const float4*>(p.part_acc + row * D + col);
+            }
+        }
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) m = fmaxf(m, ml[k].x);
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - m);
+        M = m;
+        L *= f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] *= f;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const float w = ml[k].x == -INFINITY ? 0.f : fast_exp2(ml[k].x - m);
+            L = fmaf(w, ml[k].y, L);  // (0 * NaN: a row of NaN stays one)
+            a[0] = fmaf(w, y[k].x, a[0]), a[1] = fmaf(w, y[k].y, a[1]);
+            a[2] = fmaf(w, y[k].z, a[2]), a[3] = fmaf(w, y[k].w, a[3]);
+        }
+    }
+    if constexpr (SHARES > 1) {
+        const int t = threadIdx.x % PER;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[share][i][t] = a[i];
+        sums[share][4][t] = M;
+        sums[share][5][t] = L;
+        __syncthreads();
+        if (share != 0) return;
+#pragma unroll
+        for (int k = 1; k < SHARES; ++k) M = fmaxf(M, sums[k][4][t]);
+        L = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < SHARES; ++k) {
+            const float m = sums[k][4][t], w = m == -INFINITY ? 0.f : fast_exp2(m - M);
+            L = fmaf(w, sums[k][5][t], L);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = fmaf(w, sums[k][i][t], a[i]);
+        }
+    }
+    if (r >= R) return;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t o = (((size_t)b * p.q_len + qi0 + r / p.group) * p.num_heads + kvh * p.group + r % p.group) * D + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_out(p.out, o + i, a[i] * inv, p.out_dtype);
 }
 
 template <int D, int BS, int NR, bool HL>
@@ -562,11 +749,31 @@ cudaError_t launch_kv8_inst(const Kv8Launch& L, cudaStream_t stream) {
 }
 
 template <int D, int NR>
+cudaError_t launch_kv8_join(const Kv8Launch& L, cudaStream_t stream) {
+    const int groups = (int)L.grid.x / L.p.group_size;
+    const bool shared = (long long)L.units * 6 < L.grid.x;  // seven pieces and more to a unit
+    const int per = kKv8JoinThreads / (shared ? 8 : 1), rows = L.p.q_chunk * L.p.group;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)L.units, (unsigned)((rows * (D / 4) + per - 1) / per));
+    cfg.blockDim = dim3(kKv8JoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.pdl ? 1 : 0;
+    return shared ? cudaLaunchKernelEx(&cfg, kv8_join_kernel<D, NR * 8, 8>, L.p, groups)
+                  : cudaLaunchKernelEx(&cfg, kv8_join_kernel<D, NR * 8, 1>, L.p, groups);
+}
+
+template <int D, int NR>
 cudaError_t launch_kv8_for(const Kv8Launch& L, cudaStream_t stream) {
     const bool two = L.p.out_dtype == PA_F32;
-    if (L.block_size == 16)
-        return two ? launch_kv8_inst<D, 16, NR, true>(L, stream) : launch_kv8_inst<D, 16, NR, false>(L, stream);
-    return two ? launch_kv8_inst<D, 32, NR, true>(L, stream) : launch_kv8_inst<D, 32, NR, false>(L, stream);
+    const cudaError_t e =
+        L.block_size == 16
+            ? (two ? launch_kv8_inst<D, 16, NR, true>(L, stream) : launch_kv8_inst<D, 16, NR, false>(L, stream))
+            : (two ? launch_kv8_inst<D, 32, NR, true>(L, stream) : launch_kv8_inst<D, 32, NR, false>(L, stream));
+    return e != cudaSuccess || !L.p.balanced ? e : launch_kv8_join<D, NR>(L, stream);
 }
 
 // Resident CTAs per SM of an instantiation (pages of 16 and 32 alike).

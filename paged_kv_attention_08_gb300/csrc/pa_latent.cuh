@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         for_segments([&](const LatentSeg& g, int) {
             if (g.k0 == 0) {
                 // group x has the tiles from floor(x total / groups) on
-                LatentDesc d;
+                PieceDesc d;
                 d.first_group = group;
                 d.last_group = (int)(((g.first + g.n) * groups - 1) / total);
                 d.first_record = g.first == run_start ? 0 : 1;
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kLatentJoinThreads) join_latent_kernel(const L
     __shared__ float sums[SHARES > 1 ? SHARES : 1][10][PER];
     grid_dependency_wait();
     grid_launch_dependents();
-    const LatentDesc d = p.part_desc[blockIdx.x];
+    const PieceDesc d = p.part_desc[blockIdx.x];
     if (d.first_group == d.last_group) return;  // whole: written already
     const int b = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
     const int rows = p.q_len * p.num_heads;
@@ -860,7 +860,7 @@ cudaError_t launch_latent_inst(const LatentLaunch& L, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, kern, L.tmap_c, L.tmap_q, L.p);
     if (e != cudaSuccess || !L.join) return e;
     const int units = L.p.batch * L.p.row_tiles, groups = L.ctas / L.p.group_size;
-    const bool shared = units * 4 < groups;  // five pieces and more to a unit
+    const bool shared = (long long)units * 6 < L.ctas;  // seven pieces and more to a unit
     const int per = kLatentJoinThreads / (shared ? 8 : 1);
     cfg.gridDim = dim3((unsigned)units, (unsigned)((R / 8 * N + per - 1) / per));
     cfg.blockDim = dim3(kLatentJoinThreads);
