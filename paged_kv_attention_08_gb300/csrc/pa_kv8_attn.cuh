@@ -63,10 +63,11 @@ struct Kv8Cfg {
     static constexpr uint32_t RING = NW * NS * 2 * TILE;
     static constexpr int R = NR * 8;
     // the join of the warps, and of a cluster, in the rings' place
-    static constexpr uint32_t JOIN = 4u * (NW * R * D + 2 * NW * R + R * D + 2 * R);
+    static constexpr uint32_t JOIN = 4u * (NW * R * D + R * D + 2 * NW * R + 4 * R);
     static constexpr uint32_t BAR_OFF = RING > JOIN ? RING : JOIN;
     static constexpr uint32_t RUN_OFF = BAR_OFF + (8 + 4) * NW * NS + 16 - (12 * NW * NS) % 16;
-    static constexpr uint32_t Q_OFF = RUN_OFF + 48;
+    static constexpr uint32_t QK_OFF = RUN_OFF + 48;  // [R] the queries' factors (beside the fragments)
+    static constexpr uint32_t Q_OFF = QK_OFF + (QSMEM ? R * 4u : 0u);
     static constexpr uint32_t SMEM = Q_OFF + (QSMEM ? KSTEPS * NR * 256u : 0u) + kSmemAlignSlack;
     static_assert(SMEM * CTAS <= 227u * 1024u - CTAS * 1024u, "shared memory");
 };
@@ -92,6 +93,19 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 }
 
 
+// Four consecutive outputs v * f in the output's type.
+__device__ __forceinline__ void store4(void* out, size_t at, float4 v, float f, int out_dtype) {
+    v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+    if (out_dtype == PA_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+    else if (out_dtype == PA_F16)
+        *reinterpret_cast<uint2*>(static_cast<__half*>(out) + at) =
+            make_uint2(Mma<__half>::pack(v.x, v.y), Mma<__half>::pack(v.z, v.w));
+    else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+            make_uint2(Mma<__nv_bfloat16>::pack(v.x, v.y), Mma<__nv_bfloat16>::pack(v.z, v.w));
+}
+
 // 8 x 8 16-bit values, a row to four lanes, transposed.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t r;
@@ -114,6 +128,7 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
     int32_t* on_of = reinterpret_cast<int32_t*>(full + NW * NS);
     uint2* qs = reinterpret_cast<uint2*>(smem + C::Q_OFF);  // [KSTEPS][NR][32]
+    float* qks = reinterpret_cast<float*>(smem + C::QK_OFF);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tig = lane & 3;
@@ -243,34 +258,43 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             }
         }
     };
+    // The queries, B operand of S^T: element order of a lane's keys, row g of each
+    // tile.  (Loaded ahead of the first pages, behind which they waited 4 us.)  With
+    // the fragments in shared memory a warp takes the tiles warp, warp + NW, ...
+    constexpr int MINE = C::QSMEM ? (NR + NW - 1) / NW : NR, STRIDE = C::QSMEM ? NW : 1;
+    const int j0 = C::QSMEM ? warp : 0;
+    uint2 raw[MINE][KSTEPS];
+#pragma unroll
+    for (int y = 0; y < MINE; ++y) {
+        const int r = (j0 + y * STRIDE) * 8 + g;
+        const bool real = r < R;  // (other rows: zeros, their results are not used)
+        const char* q = static_cast<const char*>(p.q) + row_off(real ? r : 0) * 2;
+#pragma unroll
+        for (int k = 0; k < KSTEPS; ++k) {
+            const int d = k / (C::ROW / 16) * C::ROW + tig * (C::ROW / 4) + k % (C::ROW / 16) * 4;
+            raw[y][k] = real ? __ldg(reinterpret_cast<const uint2*>(q + d * 2)) : make_uint2(0, 0);
+        }
+    }
     fence_proxy_async_smem();  // the last segment's join used the rings
     for (int i = 0; i < min(n_s, NS); ++i) issue(i);
     fetch_scales(ent);
 
-    // ---- the queries, B operand of S^T: element order of a lane's keys, row g of
-    // each tile, scaled by a power of two ----
+    // each row scaled by a power of two
     uint2 qf[C::QSMEM ? 1 : KSTEPS][C::QSMEM ? 1 : NR];
     float qk[NR][2];  // of rows 2 tig, + 1: scale * log2(e), and the row's power of two taken out again
 #pragma unroll
-    for (int j = 0; j < NR; ++j) {
-        const bool real = j * 8 + g < R;  // (other rows: zeros, their results are not used)
-        const char* q = static_cast<const char*>(p.q) + row_off(real ? j * 8 + g : 0) * 2;
-        auto load = [&](int k) {
-            const int d = k / (C::ROW / 16) * C::ROW + tig * (C::ROW / 4) + k % (C::ROW / 16) * 4;
-            return real ? __ldg(reinterpret_cast<const uint2*>(q + d * 2)) : make_uint2(0, 0);
-        };
+    for (int y = 0; y < MINE; ++y) {
+        const int j = j0 + y * STRIDE;
         auto widen = [&](uint32_t x, float& lo, float& hi) {
             if (p.bf16) Mma<__nv_bfloat16>::unpack(x, lo, hi);
             else Mma<__half>::unpack(x, lo, hi);
         };
         float top = 0.f;
-        uint2 v[KSTEPS];
 #pragma unroll
         for (int k = 0; k < KSTEPS; ++k) {
-            v[k] = load(k);
             float a, c, d, e;
-            widen(v[k].x, a, c);
-            widen(v[k].y, d, e);
+            widen(raw[y][k].x, a, c);
+            widen(raw[y][k].y, d, e);
             top = fmaxf(top, fmaxf(fmaxf(fabsf(a), fabsf(c)), fmaxf(fabsf(d), fabsf(e))));
         }
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
@@ -282,19 +306,29 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
 #pragma unroll
         for (int k = 0; k < KSTEPS; ++k) {
             float a, c, d, e;
-            widen(v[k].x, a, c);
-            widen(v[k].y, d, e);
-            const uint2 y = make_uint2(Mma<__half>::pack(a * f, c * f), Mma<__half>::pack(d * f, e * f));
+            widen(raw[y][k].x, a, c);
+            widen(raw[y][k].y, d, e);
+            const uint2 v = make_uint2(Mma<__half>::pack(a * f, c * f), Mma<__half>::pack(d * f, e * f));
             if constexpr (C::QSMEM) {
-                if (warp == 0) qs[(k * NR + j) * 32 + lane] = y;
+                if (j < NR) qs[(k * NR + j) * 32 + lane] = v;
             } else {
-                qf[k][j] = y;
+                qf[k][y] = v;
             }
         }
+        if constexpr (C::QSMEM) {
+            if (j < NR && tig == 0) qks[j * 8 + g] = back;
+        } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) qk[j][e] = __shfl_sync(kFullMask, back, (tig * 2 + e) * 4);
+            for (int e = 0; e < 2; ++e) qk[y][e] = __shfl_sync(kFullMask, back, (tig * 2 + e) * 4);
+        }
     }
-    if constexpr (C::QSMEM) __syncthreads();
+    if constexpr (C::QSMEM) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) qk[j][e] = qks[j * 8 + tig * 2 + e];
+    }
     // Tokens that a row attends to: its query token's causal limit; the first row's
     // is the least.  (Rows past R see all: their results are not used.)
     const int lim_first = ctx - Q + qi0 + 1, lim_least = min(reach, lim_first);
@@ -505,9 +539,10 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
 #pragma unroll
             for (int x = 4; x <= 16; x <<= 1) l[j][e] += __shfl_xor_sync(kFullMask, l[j][e], x);
     float* macc = reinterpret_cast<float*>(smem);       // [NW][R][D]
-    float* mm = macc + NW * R * D;                      // [NW][R]
+    float* cpart = macc + NW * R * D;                   // cluster: acc [R][D], m [R], l [R]
+    float* mm = cpart + R * D + 2 * R;                  // [NW][R], then the warps' factors
     float* ml = mm + NW * R;                            // [NW][R]
-    float* cpart = ml + NW * R;                         // cluster: acc [R][D], m [R], l [R]
+    float* tot = ml + NW * R;                           // [R][2] m and l of the row
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NR; ++j)
@@ -525,28 +560,37 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             if (g == 0) mm[warp * R + r] = m[j][e], ml[warp * R + r] = l[j][e];
         }
     __syncthreads();
-    for (int idx = tid; idx < R * D; idx += 128) {
-        const int r = idx / D, d = idx % D;
-        float M = NEG_INF;
+    if (tid < R) {
+        float M = NEG_INF, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, mm[w * R + r]);
-        float A = 0.f, L = 0.f;
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, mm[w * R + tid]);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float x = mm[w * R + r];
-            const float f = x == NEG_INF ? 0.f : fast_exp2(x - M);
-            A = fmaf(f, macc[((size_t)w * R + r) * D + d], A);
-            L = fmaf(f, ml[w * R + r], L);
+            const float x = mm[w * R + tid], f = x == NEG_INF ? 0.f : fast_exp2(x - M);
+            mm[w * R + tid] = f;
+            L = fmaf(f, ml[w * R + tid], L);
+        }
+        if (record == -2) cpart[R * D + tid] = M, cpart[R * D + R + tid] = L;
+        else if (record >= 0)
+            *reinterpret_cast<float2*>(p.part_ml + (record * C::R + tid) * 2) = make_float2(M, L);
+        tot[tid] = L == 0.f ? 0.f : 1.f / L;
+    }
+    __syncthreads();
+    for (int idx = tid; idx < R * (D / 4); idx += 128) {
+        const int r = idx / (D / 4);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float4 v = reinterpret_cast<const float4*>(macc)[w * R * (D / 4) + idx];
+            const float f = mm[w * R + r];
+            a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
         }
         if (record == -2) {
-            cpart[idx] = A;
-            if (d == 0) cpart[R * D + r] = M, cpart[R * D + R + r] = L;
+            reinterpret_cast<float4*>(cpart)[idx] = a;
         } else if (record >= 0) {
-            p.part_acc[(record * C::R + r) * D + d] = A;
-            if (d == 0)
-                *reinterpret_cast<float2*>(p.part_ml + (record * C::R + r) * 2) = make_float2(M, L);
+            reinterpret_cast<float4*>(p.part_acc + record * C::R * D)[idx] = a;
         } else {
-            store_out(p.out, row_off(r) + d, L == 0.f ? 0.f : A / L, p.out_dtype);
+            store4(p.out, row_off(r) + idx % (D / 4) * 4, a, tot[r], p.out_dtype);
         }
     }
     if (record == -2) {
@@ -716,8 +760,7 @@ __global__ void __launch_bounds__(kKv8JoinThreads) kv8_join_kernel(const Kv8Para
     if (r >= R) return;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const size_t o = (((size_t)b * p.q_len + qi0 + r / p.group) * p.num_heads + kvh * p.group + r % p.group) * D + col;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) store_out(p.out, o + i, a[i] * inv, p.out_dtype);
+    store4(p.out, o, make_float4(a[0], a[1], a[2], a[3]), inv, p.out_dtype);
 }
 
 template <int D, int BS, int NR, bool HL>
