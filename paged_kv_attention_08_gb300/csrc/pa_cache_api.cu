@@ -543,6 +543,7 @@ pa_status pa_decode_latent(void* out, const void* q, const void* cache,
     char* ws = static_cast<char*>(workspace);
     p.q = q;
     p.out = out;
+    p.cache = cache;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.part_acc = reinterpret_cast<float*>(ws);

@@ -227,6 +227,7 @@ struct LatentAppendParams {
 struct LatentParams {
     const void* q;            // [B, Q, H, latent_dim + 64]
     void* out;                // [B, Q, H, latent_dim]
+    const void* cache;        // [num_blocks, block_size, latent_dim + 64]
     const int32_t* block_tables;
     const int32_t* context_lens;
     float* part_acc;          // [CTAs][2 records][row tile][latent_dim]

@@ -145,11 +145,9 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Brings a box to L2 ahead of its load.
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+// Brings `bytes` (a multiple of 16) to L2 ahead of their load.
+__device__ __forceinline__ void l2_prefetch(const void* at, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(at)), "r"(bytes)
                  : "memory");
 }
 
@@ -376,9 +374,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 const int phys = next;
                 next = ahead;
                 if (k + 2 < g.k1) ahead = fetch(k + 2);
-                // the next tile to L2: its slots are free late, a load from there is short
+                // the next tile's pages to L2, each in one piece: their slots are free
+                // late, and the loads by column block read 128 bytes a row
                 if (member == 0 && k + 1 < g.k1 && next >= 0)
-                    for (int c = 0; c < R + kLatentP; c += 64) tma_prefetch_4d(&tmap_c, c, 0, next, 0);
+                    l2_prefetch(static_cast<const T*>(p.cache) + (size_t)next * BS * (R + kLatentP),
+                                (uint32_t)BS * (R + kLatentP) * 2u);
                 const unsigned on = __ballot_sync(kFullMask, phys >= 0);
                 // one slot: `blocks` column blocks from element `col` on
                 auto load = [&](uint64_t* full, uint32_t dst, int col, int blocks) {
