@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     volatile uint32_t* abort_flag = tmem_slot + 1;
     // start, end, flat position of the first sequence's tiles, total
     long long* run = reinterpret_cast<long long*>(smem + C::MISC_OFF + 8);
-    int32_t* run_b = reinterpret_cast<int32_t*>(run + 4);  // the first sequence
+    int32_t* run_b = reinterpret_cast<int32_t*>(run + 4);  // the first sequence; 1: no run, units in turn
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int BS = p.block_size, rows = p.q_len * p.num_heads;
@@ -277,11 +277,24 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     if (warp == 0) {
         if (p.balanced) {
             long long w = 0;
-            for (int b = lane; b < p.batch; b += 32) w += latent_tiles(p, b);
+            int most = 0;
+            for (int b = lane; b < p.batch; b += 32) {
+                const int n = latent_tiles(p, b);
+                w += n;
+                most = max(most, n);
+            }
 #pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) w += __shfl_xor_sync(kFullMask, w, m);
+            for (int m = 16; m >= 1; m >>= 1) {
+                w += __shfl_xor_sync(kFullMask, w, m);
+                most = max(most, __shfl_xor_sync(kFullMask, most, m));
+            }
             w *= p.row_groups;
-            const long long groups = gridDim.x / p.group_size;
+            const long long groups = gridDim.x / p.group_size, units = (long long)p.batch * p.row_groups;
+            // Sequences of about one length, about as many as groups: each whole to a
+            // group in turn, where that is at most a cut's own cost longer (its
+            // partial results and the join, measured in tiles).
+            constexpr int kCut = N == 64 ? 12 : 4;
+            const bool in_turn = (units + groups - 1) / groups * most * groups <= w + kCut * groups;
             const long long start = group * w / groups, end = (group + 1) * w / groups;
             int b = 0;
             long long base = 0;
@@ -304,12 +317,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 base += __shfl_sync(kFullMask, incl, 31);
                 b += 32;
             }
-            if (lane == 0) run[0] = start, run[1] = end, run[2] = base, run[3] = w, *run_b = b;
+            if (lane == 0) run[0] = start, run[1] = end, run[2] = base, run[3] = w, run_b[0] = b, run_b[1] = in_turn;
         } else if (lane == 0) {
-            // one (sequence, row tile group) to a CTA group, whole
-            const int b = group / p.row_groups, x = group % p.row_groups;
-            const int n = latent_tiles(p, b);
-            run[0] = (long long)x * n, run[1] = (long long)(x + 1) * n, run[2] = 0, *run_b = b;
+            run_b[1] = 1;  // a group to each (sequence, row tile group)
         }
     }
     tc::fence_before_sync();
@@ -318,18 +328,34 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const long long run_start = run[0], run_end = run[1];
 
-    // f(segment, its number): the run's segments of this CTA's row tiles in order,
-    // until f returns false.  Every role walks them alike.
+    // f(segment, its number): the CTA's segments in order, until f returns false.
+    // Every role walks them alike.
+    const bool in_turn = run_b[1] != 0;
     auto for_segments = [&](auto&& f) {
-        int b = *run_b, s = 0;
-        long long base = run[2];
-        for (long long at = run_start; at < run_end;) {
-            const int n = latent_tiles(p, b);
-            const int x = (int)((at - base) / n), k0 = (int)((at - base) % n);
-            const int k1 = (int)min((long long)n, k0 + (run_end - at));
-            LatentSeg g{b, x * p.group_size + member, k0, k1, n, base + (long long)x * n};
-            at += k1 - k0;
-            if (at - base >= (long long)n * p.row_groups) base += (long long)n * p.row_groups, ++b;
+        const long long groups = gridDim.x / p.group_size, units = (long long)p.batch * p.row_groups;
+        int b = run_b[0], s = 0;
+        long long base = run[2], at = in_turn ? group : run_start;
+        while (at < (in_turn ? units : run_end)) {
+            LatentSeg g;
+            int x;
+            if (in_turn) {
+                g.b = (int)(at / p.row_groups);
+                x = (int)(at % p.row_groups);
+                g.n = g.k1 = latent_tiles(p, g.b);
+                g.k0 = 0;
+                g.first = 0;
+                at += groups;
+            } else {
+                g.b = b;
+                g.n = latent_tiles(p, b);
+                x = (int)((at - base) / g.n);
+                g.k0 = (int)(at - base - (long long)x * g.n);
+                g.k1 = (int)min((long long)g.n, g.k0 + (run_end - at));
+                g.first = base + (long long)x * g.n;
+                at += g.k1 - g.k0;
+                if (at - base >= (long long)g.n * p.row_groups) base += (long long)g.n * p.row_groups, ++b;
+            }
+            g.rt = x * p.group_size + member;
             if (g.rt * N >= rows) continue;  // (a group's row tiles past the last)
             if (!f(g, s++)) return;
         }
@@ -362,13 +388,18 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 return lane < PG ? page_phys(row, k * PG + lane, npages, p.num_blocks) : -1;
             };
             int next = fetch(g.k0), ahead = fetch(g.k0 + 1);
-            if (s > 0 && !__all_sync(kFullMask, wait(q_free, (s - 1) & 1))) return false;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(smem_u32(q_full), C::Q_BYTES);
-                for (int c = 0; c < (R + kLatentP) / 64; ++c)
-                    tma_load_2d(sbase + c * N * 128, &tmap_q, c * 64, g.b * rows + g.rt * N, smem_u32(q_full));
-            }
-            segs = s + 1;
+            // (a later segment's queries behind its first tile, whose slots are free earlier)
+            auto load_q = [&]() -> bool {
+                if (s > 0 && !__all_sync(kFullMask, wait(q_free, (s - 1) & 1))) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(smem_u32(q_full), C::Q_BYTES);
+                    for (int c = 0; c < (R + kLatentP) / 64; ++c)
+                        tma_load_2d(sbase + c * N * 128, &tmap_q, c * 64, g.b * rows + g.rt * N, smem_u32(q_full));
+                }
+                segs = s + 1;
+                return true;
+            };
+            if (s == 0 && !load_q()) return false;
             const uint64_t policy = p.group_size > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
             for (int k = g.k0; k < g.k1 && !*abort_flag; ++k, ++tile) {
                 const int phys = next;
@@ -408,6 +439,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                         return false;
                     load(pair_full + ps, sbase + C::PAIR_OFF + ps * C::PAIR, m * 128, 2);
                 }
+                if (s > 0 && k == g.k0 && !load_q()) return false;
             }
             return !*abort_flag;
         });
@@ -740,7 +772,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 // group x has the tiles from floor(x total / groups) on
                 PieceDesc d;
                 d.first_group = group;
-                d.last_group = (int)(((g.first + g.n) * groups - 1) / total);
+                d.last_group = in_turn ? group : (int)(((g.first + g.n) * groups - 1) / total);
                 d.first_record = g.first == run_start ? 0 : 1;
                 d.member = member;
                 d.total = total;
