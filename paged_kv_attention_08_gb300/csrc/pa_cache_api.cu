@@ -121,15 +121,14 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // Largest batch whose lengths every CTA looks through for its run (2 us).
 constexpr int kMaxBalancedLens = 2048;
 
-// Short calls of few units: clusters of up to 8 CTAs, up to 16 steps to a CTA
-// and no second launch (8 sequences of 700 tokens, 8 kv heads: 7.8 us against 9.9
-// in runs that a second launch joins; 16 sequences of 1 .. 16,384 tokens in
-// clusters of 3 took 89 us).  Else equal runs of steps over the CTAs
+// Few units, up to 32 steps to a CTA: clusters of up to 8 CTAs and no second launch
+// (8 sequences of 4 x 3000 tokens, 8 kv heads: 19.6 us against 28.5 in runs; at 64
+// steps 4 sequences of 1000 .. 16,384 took 29 us against 25).  Else equal runs of steps over the CTAs
 // that the GPU holds (64 sequences of 1 .. 4096 tokens: a unit to a CTA took 75 us,
 // runs 60 with the join: DRAM at 82 %).  With more than 3 units for each of them,
-// where the waves even out by themselves (128 sequences of 1 .. 2048: 61 us against
-// 68 in runs), of short contexts (32 sequences of 300: 8 against 16), or with more
-// lengths than a CTA looks through, a unit to a CTA.
+// where the waves even out by themselves (128 sequences of 1 .. 2048: 62 us against
+// 68 in runs), of contexts up to 48 steps (64 sequences of 100 .. 1500: 33 us against
+// 36), or with more lengths than a CTA looks through, a unit to a CTA.
 Kv8Plan plan_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
     Kv8Plan pl;
     // the smallest row tile that holds a sequence's rows, or the largest there is
@@ -151,8 +150,8 @@ Kv8Plan plan_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int 
     // (a power of two: clusters of 7 that fill the GPU took 12.8 us where 4 took 7.8)
     int64_t in_cluster = 8;
     while (in_cluster > 1 && in_cluster > std::min(fill, ceil_div(steps, 2))) in_cluster /= 2;
-    if (in_cluster >= 2 && ceil_div(steps, in_cluster) <= 16) pl.cluster = (int)in_cluster;
-    if (pl.cluster == 1 && steps > 16)
+    if (in_cluster >= 2 && ceil_div(steps, in_cluster) <= 32) pl.cluster = (int)in_cluster;
+    if (pl.cluster == 1 && steps > 48)
         pl.balanced = pl.units <= 3 * slots && s->batch <= kMaxBalancedLens;
     pl.part_steps = (int)ceil_div(steps, pl.cluster);
     const int64_t per_seq = (int64_t)s->num_kv_heads * pl.chunks;

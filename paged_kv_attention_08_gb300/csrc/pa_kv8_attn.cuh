@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
 #pragma unroll
                     for (int j = 0; j < NR; ++j) {
                         uint2 y;
-                        if constexpr (C::QSMEM) y = qs[(k * NR + j) * 32 + lane];
+                        if constexpr (C::QSMEM) y = lds64(smem_u32(smem) + C::Q_OFF + ((k * NR + j) * 32 + lane) * 8);
                         else y = qf[k][j];
                         Mma<__half>::mma(s[0][j], a[0], y.x, y.y);
                         Mma<__half>::mma(s[1][j], a[1], y.x, y.y);
