@@ -450,8 +450,11 @@ pa_status pa_rope_append_kv8(void* q_out, void* k_cache, void* v_cache, float* k
 /*
  * pa_decode_multi (q_len = 1: pa_decode_splitkv) over the 8-bit cache, with the
  * same masking and an automatic split.  Codes are widened exactly; the scores,
- * the softmax and the sums are fp32, and the weights that meet the values are
- * held in two fp16 parts.  Scales are finite and positive, whoever wrote them;
+ * the softmax and the sums are fp32; the weights that meet the values are
+ * rounded once to fp16 where out has 16 bits (the normaliser sums the rounded
+ * ones) and held in two fp16 parts where it has 32; weights under 2^-32 of the
+ * row's largest count as 0.  A NaN or infinity in a cached value or scale that one
+ * row attends to may reach its sequence's other rows.  Scales are finite and positive, whoever wrote them;
  * v_scales outside [2^-60, 2^60] count as the nearer limit.  Scales of pages
  * that hold no attended token are not used.  shape->kv_dtype is
  * the dtype of q, shape->out_dtype fp32 or that.  Tokens past
@@ -532,7 +535,9 @@ pa_status pa_rope_append_latent(void* q_out, void* cache, const void* q, const v
  *   q    [batch, q_len, num_heads, latent_dim + rope_dim]
  *   out  [batch, q_len, num_heads, latent_dim], apart from the other arguments
  * Scores, softmax and sums are fp32; the weights that meet the values are
- * rounded to the cache's dtype, and the normaliser sums the rounded ones.
+ * rounded to the cache's dtype, and the normaliser sums the rounded ones (fp16
+ * weights under 2^-32 of the row's largest count as 0).  A NaN or infinity in a
+ * cached vector that one row attends to may reach its sequence's other rows.
  * Tokens past max_context_len's last page are left out.  The workspace must
  * hold pa_workspace_size_latent(...) bytes.
  */
