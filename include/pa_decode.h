@@ -435,7 +435,7 @@ pa_status pa_evict_kv(void* k_cache, void* v_cache, const float* weights,
  * call's tokens are rounded anew, as code * s_old / s (for powers of two
  * exact but below 2^-6).  Slots behind the call's tokens stay as they are.
  * Infinities and magnitudes past 448 * 2^60 become NaN, NaN stays NaN.  A page
- * that takes tokens belongs to one sequence of the call.
+ * that takes tokens belongs to one sequence of the call, at one place of its table.
  * shape->kv_dtype is the dtype of q, q_out, k_new and v_new; the other
  * arguments, the strides of `rope` and what q_out may lie over are as for
  * pa_rope_append_kv, and q_out lies apart from the scales too.

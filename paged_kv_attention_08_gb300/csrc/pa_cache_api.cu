@@ -540,7 +540,6 @@ pa_status pa_decode_latent(void* out, const void* q, const void* cache,
     if (st != PA_OK) return st;
     LatentParams& p = L.p;
     char* ws = static_cast<char*>(workspace);
-    p.q = q;
     p.out = out;
     p.cache = cache;
     p.block_tables = block_tables;

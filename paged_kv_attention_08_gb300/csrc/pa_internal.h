@@ -225,7 +225,6 @@ struct LatentAppendParams {
 
 // Attention over the latent cache.
 struct LatentParams {
-    const void* q;            // [B, Q, H, latent_dim + 64]
     void* out;                // [B, Q, H, latent_dim]
     const void* cache;        // [num_blocks, block_size, latent_dim + 64]
     const int32_t* block_tables;

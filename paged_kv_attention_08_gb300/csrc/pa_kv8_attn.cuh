@@ -94,6 +94,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ void sts128_zero(uint32_t a) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -429,16 +432,26 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
                 for (int t = 0; t < 2; ++t) {
                     const int u = t * 16 / BS;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float& x = s[t][j][c];
-                        x = fmaf(x, qk[j][c & 1] * page_sk[u], lv[u]);
-                        if (masked) {
-                            const int at = t * 16 + (c >> 1) * 8 + g;
-                            if (first + at >= lim(j * 8 + tig * 2 + (c & 1)) || !held(at)) x = NEG_INF;
-                        }
-                        above = fmaxf(above, x - m[j][c & 1]);
-                    }
+                    for (int c = 0; c < 4; ++c)
+                        s[t][j][c] = fmaf(s[t][j][c], qk[j][c & 1] * page_sk[u], lv[u]);
                 }
+            if (masked) {
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int at = t * 16 + (c >> 1) * 8 + g;
+                            if (first + at >= lim(j * 8 + tig * 2 + (c & 1)) || !held(at)) s[t][j][c] = NEG_INF;
+                        }
+            }
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) above = fmaxf(above, s[t][j][c] - m[j][c & 1]);
             if (__any_sync(kFullMask, above > kSlack + kHalfLift)) {
 #pragma unroll
                 for (int j = 0; j < NR; ++j)
@@ -455,7 +468,22 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
                         for (int k = 0; k < MT; ++k) acc[k][j][e] *= f, acc[k][j][2 + e] *= f;
                     }
             }
-            // ---- weights: P^T, B operand of the second product ----
+            if (!whole) {
+                // slots without a token hold zeros in the second product: 0 * NaN is not 0
+                for (int i = lane; i < STEP * (D / 16); i += 32) {
+                    const int at = i / (C::ROW / 16) % STEP, blk = i / (C::ROW / 16) / STEP;
+                    if (!held(at))
+                        sts128_zero(vt + blk * STEP * C::ROW + at * C::ROW + i % (C::ROW / 16) * 16);
+                }
+                __syncwarp();
+            }
+            // ---- weights: P^T, B operand of the second product (a row without a token
+            // so far has m = -inf, and weights 2^-inf) ----
+            float mr[NR][2];
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mr[j][e] = m[j][e] == NEG_INF ? 0.f : m[j][e];
             uint32_t ph[2][NR][2], pl[HL ? 2 : 1][HL ? NR : 1][2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -464,12 +492,8 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
                 for (int j = 0; j < NR; ++j)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float e0 = fast_exp2(s[t][j][2 * h] - m[j][0]);
-                        float e1 = fast_exp2(s[t][j][2 * h + 1] - m[j][1]);
-                        if (masked) {  // (rows without a token so far: -inf less -inf)
-                            if (s[t][j][2 * h] == NEG_INF) e0 = 0.f;
-                            if (s[t][j][2 * h + 1] == NEG_INF) e1 = 0.f;
-                        }
+                        const float e0 = fast_exp2(s[t][j][2 * h] - mr[j][0]);
+                        const float e1 = fast_exp2(s[t][j][2 * h + 1] - mr[j][1]);
                         const uint32_t hi = Mma<__half>::pack(e0, e1);
                         float h0, h1;
                         Mma<__half>::unpack(hi, h0, h1);
@@ -500,9 +524,6 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
                             const uint2 x = lds64(vt + chunk8<C::ROW>(at, g >> 1) + (g & 1) * 8);
                             v[r][0] = x.x, v[r][1] = x.y;
                         }
-                        if (!whole && !held(at))  // slots without a token: 0 * NaN is not 0
-#pragma unroll
-                            for (int w = 0; w < WORDS; ++w) v[r][w] = 0;
                     }
 #pragma unroll
                     for (int w = 0; w < WORDS; ++w)
