@@ -697,9 +697,11 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             k1 = p.cluster > 1 ? min(k0 + p.part_steps, n) : n;
             if (p.cluster > 1) record = -2;
         }
-        if (x < per_seq) segment(b, x / p.chunks, x % p.chunks, k0, k1, record);
+        if (x < per_seq && !aborted) segment(b, x / p.chunks, x % p.chunks, k0, k1, record);
         if (!p.balanced) return;
-        if (__syncthreads_or(aborted)) return;  // (and the rings are free again)
+        // the rings are free again; after a timeout the walk goes on without its
+        // segments, so that the join finds every unit's descriptor
+        aborted = __syncthreads_or(aborted);
         if (tid == 0) {
             run[4] += k1 - k0;
             const long long whole = (long long)steps_of(b) * p.unit_groups;
