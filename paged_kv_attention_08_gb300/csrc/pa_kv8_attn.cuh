@@ -567,8 +567,10 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
         for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int x = 4; x <= 16; x <<= 1) l[j][e] += __shfl_xor_sync(kFullMask, l[j][e], x);
-    float* macc = reinterpret_cast<float*>(smem);       // [NW][R][D]
-    float* cpart = macc + NW * R * D;                   // cluster: acc [R][D], m [R], l [R]
+    float4* macc = reinterpret_cast<float4*>(smem);     // [NW][R][D / 4], a row's vectors permuted:
+    // eight lanes that store at once have two g and four rows of the same banks
+    auto mix = [](int r) { return C::ROW == 128 ? r >> 1 & 3 : (r >> 1 & 1) | (r & 4); };
+    float* cpart = reinterpret_cast<float*>(macc) + NW * R * D;  // cluster: acc [R][D], m [R], l [R]
     float* mm = cpart + R * D + 2 * R;                  // [NW][R], then the warps' factors
     float* ml = mm + NW * R;                            // [NW][R]
     float* tot = ml + NW * R;                           // [R][2] m and l of the row
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
 #pragma unroll
             for (int k = 0; k < MT; k += 2) {
                 const int blk = k / (PER / 2), d = blk * C::ROW + g * PER + k % (PER / 2) * 2;
-                *reinterpret_cast<float4*>(macc + ((size_t)warp * R + r) * D + d) =
+                macc[(warp * R + r) * (D / 4) + ((d / 4) ^ mix(r))] =
                     make_float4(acc[k][j][e], acc[k][j][2 + e], acc[k + 1][j][e], acc[k + 1][j][2 + e]);
             }
             if (g == 0) mm[warp * R + r] = m[j][e], ml[warp * R + r] = l[j][e];
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float4 v = reinterpret_cast<const float4*>(macc)[w * R * (D / 4) + idx];
+            const float4 v = macc[w * R * (D / 4) + (idx ^ mix(r))];
             const float f = mm[w * R + r];
             a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
         }
