@@ -630,33 +630,36 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
         cluster_sync_release_acquire();
         const int part = (int)blockIdx.x % p.cluster;
         const uint32_t cp = smem_u32(cpart);
-        const int P = p.cluster, share = (R * D + P - 1) / P;
-        const int end = min((part + 1) * share, R * D);
+        const int P = p.cluster, share = (R * (D / 4) + P - 1) / P;
+        const int end = min((part + 1) * share, R * (D / 4));
         uint32_t base[kMaxClusterParts];
 #pragma unroll
         for (int x = 0; x < kMaxClusterParts; ++x) base[x] = map_cluster_rank(cp, (uint32_t)(x < P ? x : 0));
         for (int idx = part * share + tid; idx < end; idx += 128) {
-            const int r = idx / D;
-            float m[kMaxClusterParts], l[kMaxClusterParts], a[kMaxClusterParts], M = NEG_INF;
+            const int r = idx / (D / 4);
+            float m[kMaxClusterParts], l[kMaxClusterParts], M = NEG_INF;
+            float4 a[kMaxClusterParts];
 #pragma unroll
             for (int x = 0; x < kMaxClusterParts; ++x)
                 if (x < P) {
                     m[x] = ld_cluster_f32(base[x] + 4u * (R * D + r));
                     l[x] = ld_cluster_f32(base[x] + 4u * (R * D + R + r));
-                    a[x] = ld_cluster_f32(base[x] + 4u * idx);
+                    a[x] = ld_cluster_v4f32(base[x] + 16u * idx);
                 }
 #pragma unroll
             for (int x = 0; x < kMaxClusterParts; ++x)
                 if (x < P) M = fmaxf(M, m[x]);
-            float A = 0.f, L = 0.f;
+            float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+            float L = 0.f;
 #pragma unroll
             for (int x = 0; x < kMaxClusterParts; ++x)
                 if (x < P) {  // (0 * NaN: a row of NaN stays one)
                     const float f = m[x] == NEG_INF ? 0.f : fast_exp2(m[x] - M);
-                    A = fmaf(f, a[x], A);
+                    A.x = fmaf(f, a[x].x, A.x), A.y = fmaf(f, a[x].y, A.y);
+                    A.z = fmaf(f, a[x].z, A.z), A.w = fmaf(f, a[x].w, A.w);
                     L = fmaf(f, l[x], L);
                 }
-            store_out(p.out, row_off(r) + idx % D, L == 0.f ? 0.f : A / L, p.out_dtype);
+            store4(p.out, row_off(r) + idx % (D / 4) * 4, A, L == 0.f ? 0.f : 1.f / L, p.out_dtype);
         }
         cluster_sync_relaxed();  // no CTA leaves while others read its shared memory
     }
