@@ -122,13 +122,15 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr int kMaxBalancedLens = 2048;
 
 // Few units, up to 32 steps to a CTA: clusters of up to 8 CTAs and no second launch
-// (8 sequences of 4 x 3000 tokens, 8 kv heads: 19.6 us against 28.5 in runs; at 64
-// steps 4 sequences of 1000 .. 16,384 took 29 us against 25).  Else equal runs of steps over the CTAs
-// that the GPU holds (64 sequences of 1 .. 4096 tokens: a unit to a CTA took 75 us,
-// runs 60 with the join: DRAM at 82 %).  With more than 3 units for each of them,
-// where the waves even out by themselves (128 sequences of 1 .. 2048: 62 us against
-// 68 in runs), of contexts up to 48 steps (64 sequences of 100 .. 1500: 33 us against
-// 36), or with more lengths than a CTA looks through, a unit to a CTA.
+// (8 kv heads; 8 sequences of 4 x 3000 tokens: 16.4 us against 26.4 in runs).  Up to 64
+// steps where they fill more than half of the GPU (4 sequences of 16,384 tokens 28 us
+// against 34 in runs, of 1000 .. 16,384 25.5 against 24; but one of 16,384 20 against 15).
+// Else equal runs of steps over the CTAs that the GPU holds (64 sequences of 1 .. 4096
+// tokens 56.6 us with the join, a unit to a CTA 61.6; 16 of 1 .. 16,384: 54 and 81).
+// With more than 3 units for each of them, where the waves even out by themselves (128
+// sequences of 1 .. 2048: 56 us against 60 in runs), of contexts up to 48 steps (64
+// sequences of 100 .. 1500: 29 us against 34), or with more lengths than a CTA looks
+// through, a unit to a CTA.
 Kv8Plan plan_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
     Kv8Plan pl;
     // the smallest row tile that holds a sequence's rows, or the largest there is
@@ -150,7 +152,8 @@ Kv8Plan plan_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int 
     // (a power of two: clusters of 7 that fill the GPU took 12.8 us where 4 took 7.8)
     int64_t in_cluster = 8;
     while (in_cluster > 1 && in_cluster > std::min(fill, ceil_div(steps, 2))) in_cluster /= 2;
-    if (in_cluster >= 2 && ceil_div(steps, in_cluster) <= 32) pl.cluster = (int)in_cluster;
+    const int64_t most = 2 * in_cluster * pl.units > slots ? 64 : 32;
+    if (in_cluster >= 2 && ceil_div(steps, in_cluster) <= most) pl.cluster = (int)in_cluster;
     if (pl.cluster == 1 && steps > 48)
         pl.balanced = pl.units <= 3 * slots && s->batch <= kMaxBalancedLens;
     pl.part_steps = (int)ceil_div(steps, pl.cluster);
