@@ -158,10 +158,18 @@ def run8(c, out_dtype=None, ws=None):
 
 @pytest.mark.parametrize("B,Q,H,Hkv,D,bs,T", [
     (1, 40, 32, 8, 64, 16, 600),     # 5 chunks of 8 kv heads: two groups of units a sequence
-    (3, 40, 16, 2, 64, 16, 700),     # chunks of 32 rows, cut by runs
+    (3, 40, 16, 2, 64, 16, 700),     # chunks of 32 rows, clusters
+    (5, 4, 64, 8, 64, 16, 4200),     # clusters that fill the GPU, 33 steps a CTA
     (2, 3, 16, 1, 256, 32, 1500),    # 48 rows at head_dim 256
     (2, 8, 4, 1, 128, 32, 1500),     # 32 rows at head_dim 128
     (1, 1, 8, 1, 128, 16, 20000),    # a unit over many runs
+    (1, 1, 8, 1, 64, 16, 9000),      # runs over each head_dim and row tile
+    (1, 2, 8, 1, 64, 32, 9000),
+    (2, 4, 8, 1, 64, 16, 9100),
+    (2, 2, 8, 1, 128, 32, 9000),
+    (1, 4, 8, 1, 128, 16, 9000),
+    (2, 1, 4, 1, 256, 16, 9000),
+    (1, 5, 8, 2, 256, 32, 9000),
     (130, 1, 8, 8, 64, 16, 40),      # short contexts, a unit to a CTA
 ])
 def test_plans_of_the_8_bit_attention(B, Q, H, Hkv, D, bs, T):
