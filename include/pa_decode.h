@@ -450,10 +450,12 @@ pa_status pa_rope_append_kv8(void* q_out, void* k_cache, void* v_cache, float* k
 /*
  * pa_decode_multi (q_len = 1: pa_decode_splitkv) over the 8-bit cache, with the
  * same masking and an automatic split.  Codes are widened exactly; the scores,
- * the softmax and the sums are fp32; the weights that meet the values are
- * rounded once to fp16 where out has 16 bits (the normaliser sums the rounded
- * ones) and held in two fp16 parts where it has 32; weights under 2^-32 of the
- * row's largest count as 0.  A NaN or infinity in a cached value or scale that one
+ * the softmax and the sums are fp32, the normaliser of every attended token's
+ * softmax weight as it is.  On the way into the product with the values a token
+ * counts with its softmax weight times its page's v_scale: that product is rounded
+ * once to fp16 (by at most 2^-11 of it) where out has 16 bits and held in two fp16
+ * parts where it has 32, and one under 2^-32 of the row's largest adds nothing to
+ * the output.  A NaN or infinity in a cached value or scale that one
  * row attends to may reach its sequence's other rows.  Scales are finite and positive, whoever wrote them;
  * v_scales outside [2^-60, 2^60] count as the nearer limit.  Scales of pages
  * that hold no attended token are not used.  shape->kv_dtype is

@@ -39,10 +39,14 @@
 // 8K tokens, 64 rows: 51 us, 2.1 a step of 32 tokens.
 //
 // Weights meet the values as fp16, 2^kHalfLift up (pa_internal.h): once rounded
-// (2^-12) where the output has 16 bits, the normaliser summing the rounded
-// ones; in two parts where it has 32.  The queries are brought to fp16 exactly, each
-// row scaled by a power of two to below 2^15 (elements 2^-28 and less of the
-// row's largest begin to round).
+// (by at most 2^-11 of each) where the output has 16 bits, in two parts where it
+// has 32.  One part is half of the second product; its rounding is that of an fp16
+// output, an eighth of a bf16 output's, and averages out over the tokens.  What it
+// loses whole are tokens whose w_t lies 2^-32 under the row's largest: their values
+// add nothing to an output, but their 2^(s_t) may be most of the normaliser (a page
+// of zero values has sv = 2^-60).  So l sums the weights as they are, in fp32.
+// The queries are brought to fp16 exactly, each row scaled by a power of two to
+// below 2^15 (elements 2^-28 and less of the row's largest begin to round).
 #pragma once
 
 #include "pa_kv8.cuh"
@@ -495,15 +499,16 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
                         const float e0 = fast_exp2(s[t][j][2 * h] - mr[j][0]);
                         const float e1 = fast_exp2(s[t][j][2 * h + 1] - mr[j][1]);
                         const uint32_t hi = Mma<__half>::pack(e0, e1);
-                        float h0, h1;
-                        Mma<__half>::unpack(hi, h0, h1);
                         ph[t][j][h] = movmatrix_trans(hi);
                         if constexpr (HL) {
+                            float h0, h1;
+                            Mma<__half>::unpack(hi, h0, h1);
                             pl[t][j][h] = movmatrix_trans(Mma<__half>::pack(e0 - h0, e1 - h1));
-                            h0 = e0, h1 = e1;
                         }
-                        l[j][0] = fmaf(h0, inv_sv[u], l[j][0]);
-                        l[j][1] = fmaf(h1, inv_sv[u], l[j][1]);
+                        // (not the rounded ones: a page whose values are far smaller than
+                        // another's has weights that vanish in fp16, not in the softmax)
+                        l[j][0] = fmaf(e0, inv_sv[u], l[j][0]);
+                        l[j][1] = fmaf(e1, inv_sv[u], l[j][1]);
                     }
             }
 
