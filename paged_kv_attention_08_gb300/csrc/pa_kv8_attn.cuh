@@ -45,6 +45,11 @@
 // loses whole are tokens whose w_t lies 2^-32 under the row's largest: their values
 // add nothing to an output, but their 2^(s_t) may be most of the normaliser (a page
 // of zero values has sv = 2^-60).  So l sums the weights as they are, in fp32.
+// fp32 ends as well, at 2^-126: where a page on the scale 2^60 is met, tokens of one
+// on 2^-60 lie there from 2^-6 of its weights down, however many they are.  So pages
+// more than 2^64 under the largest scale sum 2^(s_t - m) itself, which loses no token
+// above 2^-69 of the row's largest, and where a sum moves to another reference, the
+// factor 2^(m' - m) of l is applied as two halves (scale_sum), each inside fp32.
 // The queries are brought to fp16 exactly, each row scaled by a power of two to
 // below 2^15 (elements 2^-28 and less of the row's largest begin to round).
 #pragma once
@@ -119,6 +124,14 @@ __device__ __forceinline__ void store4(void* out, size_t at, float4 v, float f, 
     else
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
             make_uint2(Mma<__nv_bfloat16>::pack(v.x, v.y), Mma<__nv_bfloat16>::pack(v.z, v.w));
+}
+
+// l * 2^d (d <= 0) where 2^d itself may be below fp32's numbers and l far above one;
+// f: 2^d, or 0.
+__device__ __forceinline__ float scale_sum(float l, float d, float& f) {
+    const float h = fast_exp2(0.5f * d);
+    f = h * h;
+    return l * h * h;
 }
 
 // 8 x 8 16-bit values, a row to four lanes, transposed.
@@ -360,6 +373,7 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
         for (int j = 0; j < NR; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
 
     float sk = 0.f, sv = 1.f;
+    float lv_top = NEG_INF;  // largest log2 sv that the warp has met
     int issued = min(n_s, NS);
     for (int i = 0; i < n_s; ++i) {
         if (i % WINDOW == 0) sk = sk_ahead, sv = sv_ahead;
@@ -465,9 +479,9 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
 #pragma unroll
                         for (int x = 4; x <= 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
                         const float to = fmaxf(m[j][e], top - kHalfLift);
-                        const float f = to == m[j][e] ? 1.f : fast_exp2(m[j][e] - to);
+                        float f = 1.f;
+                        if (to != m[j][e]) l[j][e] = scale_sum(l[j][e], m[j][e] - to, f);
                         m[j][e] = to;
-                        l[j][e] *= f;
 #pragma unroll
                         for (int k = 0; k < MT; ++k) acc[k][j][e] *= f, acc[k][j][2 + e] *= f;
                     }
@@ -488,6 +502,20 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
             for (int j = 0; j < NR; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) mr[j][e] = m[j][e] == NEG_INF ? 0.f : m[j][e];
+#pragma unroll
+            for (int u = 0; u < PP; ++u) {
+                lv_top = fmaxf(lv_top, lv[u]);
+                if (lv_top - lv[u] > 64.f) {
+                    // weights times sv may lie below fp32's numbers: the sum without sv
+#pragma unroll
+                    for (int t = u * (2 / PP); t < (u + 1) * (2 / PP); ++t)
+#pragma unroll
+                        for (int j = 0; j < NR; ++j)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) l[j][c & 1] += fast_exp2(s[t][j][c] - mr[j][c & 1] - lv[u]);
+                    inv_sv[u] = 0.f;
+                }
+            }
             uint32_t ph[2][NR][2], pl[HL ? 2 : 1][HL ? NR : 1][2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -602,9 +630,10 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
         for (int w = 0; w < NW; ++w) M = fmaxf(M, mm[w * R + tid]);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float x = mm[w * R + tid], f = x == NEG_INF ? 0.f : fast_exp2(x - M);
+            const float x = mm[w * R + tid];
+            float f;
+            L += scale_sum(ml[w * R + tid], x == NEG_INF ? x : x - M, f);
             mm[w * R + tid] = f;
-            L = fmaf(f, ml[w * R + tid], L);
         }
         if (record == -2) cpart[R * D + tid] = M, cpart[R * D + R + tid] = L;
         else if (record >= 0)
@@ -659,10 +688,10 @@ __global__ void __launch_bounds__(128, Kv8Cfg<D, BS, NR>::CTAS)
 #pragma unroll
             for (int x = 0; x < kMaxClusterParts; ++x)
                 if (x < P) {  // (0 * NaN: a row of NaN stays one)
-                    const float f = m[x] == NEG_INF ? 0.f : fast_exp2(m[x] - M);
+                    float f;
+                    L += scale_sum(l[x], m[x] == NEG_INF ? NEG_INF : m[x] - M, f);
                     A.x = fmaf(f, a[x].x, A.x), A.y = fmaf(f, a[x].y, A.y);
                     A.z = fmaf(f, a[x].z, A.z), A.w = fmaf(f, a[x].w, A.w);
-                    L = fmaf(f, l[x], L);
                 }
             store4(p.out, row_off(r) + idx % (D / 4) * 4, A, L == 0.f ? 0.f : 1.f / L, p.out_dtype);
         }
@@ -764,15 +793,15 @@ __global__ void __launch_bounds__(kKv8JoinThreads) kv8_join_kernel(const Kv8Para
         float m = M;
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) m = fmaxf(m, ml[k].x);
-        const float f = M == -INFINITY ? 0.f : fast_exp2(M - m);
+        float f;
+        L = scale_sum(L, M == -INFINITY ? M : M - m, f);
         M = m;
-        L *= f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] *= f;
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            const float w = ml[k].x == -INFINITY ? 0.f : fast_exp2(ml[k].x - m);
-            L = fmaf(w, ml[k].y, L);  // (0 * NaN: a row of NaN stays one)
+            float w;  // (0 * NaN: a row of NaN stays one)
+            L += scale_sum(ml[k].y, ml[k].x == -INFINITY ? ml[k].x : ml[k].x - m, w);
             a[0] = fmaf(w, y[k].x, a[0]), a[1] = fmaf(w, y[k].y, a[1]);
             a[2] = fmaf(w, y[k].z, a[2]), a[3] = fmaf(w, y[k].w, a[3]);
         }
@@ -792,8 +821,9 @@ __global__ void __launch_bounds__(kKv8JoinThreads) kv8_join_kernel(const Kv8Para
         for (int i = 0; i < 4; ++i) a[i] = 0.f;
 #pragma unroll
         for (int k = 0; k < SHARES; ++k) {
-            const float m = sums[k][4][t], w = m == -INFINITY ? 0.f : fast_exp2(m - M);
-            L = fmaf(w, sums[k][5][t], L);
+            const float m = sums[k][4][t];
+            float w;
+            L += scale_sum(sums[k][5][t], m == -INFINITY ? m : m - M, w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[i] = fmaf(w, sums[k][i][t], a[i]);
         }

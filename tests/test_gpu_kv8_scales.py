@@ -96,7 +96,7 @@ OUTS = [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16),
     (2, 8, 2, 128, 32, [601, 64]),
     (1, 4, 1, 64, 16, [9000]),
     (1, 16, 1, 256, 16, [3001]),
-    (60, 8, 8, 64, 16, [17 * (b % 7) + 30 for b in range(60)]),
+    (30, 8, 8, 64, 16, [17 * (b % 7) + 30 for b in range(30)]),
 ])
 @pytest.mark.parametrize("exponents", [(0, -8, -16, -24, -31, -38), (-60, -60, -60, 4)])
 def test_pages_of_uneven_value_scales(exponents, B, H, Hkv, D, bs, lens, dtype, out_dtype):
@@ -105,8 +105,8 @@ def test_pages_of_uneven_value_scales(exponents, B, H, Hkv, D, bs, lens, dtype, 
 
 @pytest.mark.parametrize("dtype,out_dtype", OUTS)
 @pytest.mark.parametrize("B,H,Hkv,D,bs,T,runs", [
-    (130, 8, 8, 64, 16, 64, False),     # a unit to a CTA
-    (130, 8, 8, 64, 32, 64, False),
+    (30, 8, 8, 64, 16, 64, False),     # a unit to a CTA
+    (30, 8, 8, 64, 32, 64, False),
     (2, 4, 2, 128, 16, 320, False),     # clusters
     (2, 4, 2, 128, 32, 320, False),
     (1, 4, 1, 128, 16, 9024, True),     # runs
@@ -160,3 +160,34 @@ def test_weight_on_a_page_of_tiny_values(dtype, tiny):
                                             (torch.float16, -24), (torch.float16, 6)])
 def test_scales_far_from_one(dtype, exponent):
     check(*uneven(65, (exponent,), 1, 4, 1, 128, 16, [200], dtype), dtype)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,H,Hkv,D,bs,T,runs,drop", [
+    (30, 8, 8, 64, 16, 256, False, 8),     # a unit to a CTA: warps of tiny pages only
+    (30, 16, 8, 64, 32, 512, False, 8),
+    (2, 4, 2, 128, 16, 1024, False, 10),    # clusters
+    (1, 4, 1, 256, 32, 2048, False, 11),
+    (1, 4, 1, 128, 16, 9024, True, 13),     # runs
+    (1, 4, 1, 128, 32, 9024, True, 14),
+    (1, 4, 1, 64, 16, 9024, True, 15),      # tiny pages beside the large one: under 2^-126 of it
+])
+@pytest.mark.parametrize("at", [0, 3, -1])
+def test_scales_at_both_ends_at_once(at, B, H, Hkv, D, bs, T, runs, drop, out_dtype):
+    """One page of values on the scale 2^60, the others on 2^-60 with scores `drop`
+    binary orders lower: their values are nothing beside the large ones, their number
+    is a visible share of the normaliser.  Weights times scales lie past fp32's range."""
+    pages = T // bs
+    table = torch.randperm(B * pages, generator=torch.Generator().manual_seed(T)).view(B, pages)
+    table = table.to(torch.int32)
+    big = table[:, at].long()
+    kc, vc = (torch.zeros(B * pages, bs, Hkv, D).to(E4M3) for _ in range(2))
+    raw = torch.randint(0x58, 0x7e, vc.shape, generator=torch.Generator().manual_seed(T + 1),
+                        dtype=torch.uint8)              # 16 .. 416
+    vc.view(torch.uint8)[:] = raw
+    kc[big] = torch.ones(1).to(E4M3)
+    ks, vs = torch.ones(B * pages, Hkv), torch.full((B * pages, Hkv), 2.0 ** -60)
+    vs[big] = 2.0 ** 60
+    q = torch.ones(B, 1, H, D, dtype=torch.bfloat16)
+    check(q, kc, vc, ks, vs, table, torch.full((B,), T, dtype=torch.int32),
+          drop / (1.4426950408889634 * D), out_dtype, expect_runs=runs)
