@@ -472,7 +472,8 @@ pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const voi
                         size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of pa_decode_kv8 on the current device (0 where it needs none,
- * for invalid arguments or without a device; SIZE_MAX when no size_t holds it). */
+ * for invalid arguments or without a device): enough for every batch up to
+ * shape->batch and every announced length up to max_context_len, the rest the same. */
 size_t pa_workspace_size_kv8(const pa_shape* shape, int32_t q_len, int32_t max_context_len);
 
 /*
@@ -550,7 +551,8 @@ pa_status pa_decode_latent(void* out, const void* q, const void* cache,
                            void* stream);
 
 /* Workspace bytes of pa_decode_latent on the current device (0 where it needs
- * none, for invalid arguments or without a device; SIZE_MAX when no size_t holds it). */
+ * none, for invalid arguments or without a device): enough for every batch up to
+ * shape->batch and every announced length up to max_context_len, the rest the same. */
 size_t pa_workspace_size_latent(const pa_latent_shape* shape, int32_t q_len,
                                 int32_t max_context_len);
 

@@ -902,7 +902,8 @@ def _kv8_shape(q, k_cache, block_tables, out_dtype):
 
 
 def workspace_size_kv8(q, k_cache, block_tables, out_dtype, max_context_len: int) -> int:
-    """Bytes of workspace that ``decode_kv8`` takes, on the tensors' device."""
+    """Bytes of workspace that ``decode_kv8`` takes, on the tensors' device: enough for
+    every smaller batch and announced length too (the rest of the shapes the same)."""
     shape, q_len = _kv8_shape(q, k_cache, block_tables, out_dtype)
     with torch.cuda.device(_device_of(k_cache)):
         return int(_load().pa_workspace_size_kv8(shape, q_len,
@@ -1068,7 +1069,8 @@ def _latent_shape(q, cache, latent_dim, block_tables):
 
 
 def workspace_size_latent(q, cache, latent_dim: int, block_tables, max_context_len: int) -> int:
-    """Bytes of workspace that ``decode_latent`` takes, on the tensors' device."""
+    """Bytes of workspace that ``decode_latent`` takes, on the tensors' device: enough for
+    every smaller batch and announced length too (the rest of the shapes the same)."""
     shape, q_len = _latent_shape(q, cache, _i32(latent_dim, "latent_dim"), block_tables)
     with torch.cuda.device(_device_of(cache)):
         return int(_load().pa_workspace_size_latent(shape, q_len,

@@ -174,6 +174,25 @@ Kv8Plan plan_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int 
     return pl;
 }
 
+// Workspace that serves every batch up to this one and every context up to this
+// length.  More steps never need less; more sequences do, where a cluster or a CTA
+// takes a unit, so the largest batches of each rule of plan_kv8 are asked: units
+// up to a 16th, 8th, 4th and half of the slots, and the largest batch of runs.
+size_t kv8_bytes_up_to(const pa_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
+    const Kv8Plan pl = plan_kv8(s, q_len, max_context_len, sms);
+    const int64_t per_seq = pl.units / s->batch, slots = (int64_t)sms * kKv8[pl.kind].ctas();
+    const int64_t runs = std::min<int64_t>(3 * slots / per_seq, kMaxBalancedLens);
+    size_t bytes = pl.bytes;
+    pa_shape less = *s;
+    for (const int64_t batch : {runs, slots / (2 * per_seq), slots / (4 * per_seq), slots / (8 * per_seq),
+                                slots / (16 * per_seq)}) {
+        if (batch < 1 || batch >= s->batch) continue;
+        less.batch = (int32_t)batch;
+        bytes = std::max(bytes, plan_kv8(&less, q_len, max_context_len, sms).bytes);
+    }
+    return bytes;
+}
+
 // How a call over the latent cache runs: row tiles of 16, 32 or 64, the CTAs in
 // groups that walk the same tokens; equal runs of tiles over one CTA an SM,
 // whatever the lengths, where the batch is small enough for each CTA to look
@@ -311,7 +330,7 @@ size_t pa_workspace_size_kv8(const pa_shape* shape, int32_t q_len, int32_t max_c
     if (check_kv8(shape, q_len) != PA_OK || max_context_len < 0 || shape->batch == 0 ||
         device_state(&sms, nullptr) != PA_OK)
         return 0;
-    return plan_kv8(shape, q_len, max_context_len, sms).bytes;
+    return kv8_bytes_up_to(shape, q_len, max_context_len, sms);
 }
 
 pa_status pa_decode_kv8(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -490,7 +509,10 @@ size_t pa_workspace_size_latent(const pa_latent_shape* shape, int32_t q_len, int
     if (check_latent_call(shape, q_len) != PA_OK || max_context_len < 0 || shape->batch == 0 ||
         device_state(&sms, nullptr) != PA_OK)
         return 0;
-    return plan_latent(shape, q_len, max_context_len, sms).bytes;
+    // (of the batches up to this one the largest that takes runs needs most)
+    pa_latent_shape most = *shape;
+    most.batch = std::min(shape->batch, kMaxBalancedLens);
+    return plan_latent(&most, q_len, max_context_len, sms).bytes;
 }
 
 pa_status pa_decode_latent(void* out, const void* q, const void* cache,
