@@ -493,7 +493,7 @@ typedef struct pa_latent_shape {
     int32_t max_blocks_per_seq; /* columns of block_tables */
     int64_t num_blocks;         /* < 2^31 */
     int32_t dtype;              /* PA_F16 or PA_BF16: q, out, cache, new vectors, norm weight */
-    int32_t reserved;           /* 0 */
+    int32_t reserved;           /* 0 (else PA_ERR_INVALID_ARG) */
 } pa_latent_shape;
 
 /* Norm and rotary embedding of pa_rope_append_latent.  Strides in elements,

@@ -44,7 +44,7 @@ bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.f; }
 pa_status check_latent(const pa_latent_shape* s) {
     if (!s) return PA_ERR_INVALID_ARG;
     if (s->batch < 0 || s->num_heads <= 0 || s->latent_dim <= 0 || s->rope_dim <= 0 ||
-        s->block_size <= 0 || s->max_blocks_per_seq <= 0 || s->num_blocks <= 0)
+        s->block_size <= 0 || s->max_blocks_per_seq <= 0 || s->num_blocks <= 0 || s->reserved != 0)
         return PA_ERR_INVALID_ARG;
     if (s->dtype != PA_F16 && s->dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
     if (s->latent_dim != 128 && s->latent_dim != 256 && s->latent_dim != 512) return PA_ERR_UNSUPPORTED;
