@@ -537,9 +537,11 @@ pa_status pa_rope_append_latent(void* q_out, void* cache, const void* q, const v
  * with the masking of pa_decode_multi.
  *   q    [batch, q_len, num_heads, latent_dim + rope_dim]
  *   out  [batch, q_len, num_heads, latent_dim], apart from the other arguments
- * Scores, softmax and sums are fp32; the weights that meet the values are
- * rounded to the cache's dtype, and the normaliser sums the rounded ones (fp16
- * weights under 2^-32 of the row's largest count as 0).  A NaN or infinity in a
+ * Scores, softmax and sums are fp32.  On the way into the product with the values a
+ * weight is held in two bf16 parts, in a bf16 cache of latent_dim 512 with more than
+ * 32 rows (q_len * num_heads) in one, rounded to 8 bits, in an fp16 cache in one,
+ * rounded to 11 bits (those under 2^-32 of the row's largest count as 0); the
+ * normaliser sums weights in one part as rounded.  A NaN or infinity in a
  * cached vector that one row attends to may reach its sequence's other rows.
  * Tokens past max_context_len's last page are left out.  The workspace must
  * hold pa_workspace_size_latent(...) bytes.

@@ -9,6 +9,7 @@
 // and query rows in their N:
 //     S^T [64 tokens x N] = C [64 x (R + 64)] Q^T,      M = 64
 //     O^T [R x N]        += C[:, :R]^T [R x 64] P^T,    M = 128, R / 128 of them
+// (P^T of bf16 weights as [64 x 2N], their high and low parts side by side)
 // so that the tile of tokens that TMA has put into shared memory is the A
 // operand of both (K-major for the first, M-major for the second), 16, 32 or
 // 64 rows cost what they are instead of a tile of 128, and O^T of 64 rows takes
@@ -33,6 +34,18 @@
 // one vote of the warpgroup, no reduction over tokens.  The normalisers are
 // summed a thread's tokens at a time and joined at the segment's end.
 //
+// Weights meet the values in 16 bits, the MMA's operands having one type.  fp16's 11
+// bits (at most 2^-11 off, as an fp16 output) are held once, the normaliser summing
+// the rounded ones.  bf16's 8 bits would put 2^-8 of a weight on a bf16 output's own
+// 2^-8 (16 heads, 64 ragged sequences: 0.0013 off where the output's rounding is
+// 0.0011), so those are held in two parts, 16 bits: the low parts are N more columns
+// of the same MMAs, summed at the end.  Without and with them (4 x 65,536 tokens): 16
+// heads 63.3 and 63.4 us, 32 65.5 and 66.5; 128 heads at latent_dim 256 72.4 and
+// 73.7, at 128 57.5 and 61.5.  At latent_dim 512 with 64 rows tensor memory has no 256
+// columns more, and low parts by MMAs of their own into the same ones took 132 us
+// where one part takes 103, the error staying at 0.0017 (the output's rounding):
+// there bf16 weights are rounded once.
+//
 // Bounds (latent_dim 512; isolated MMAs: M = 64, N = 64 30 cycles, N = 16 22;
 // M = 128 44 and 36).  With 64 rows shared memory's 128 bytes a cycle: a tile's S^T
 // reads 147 KB of it and O^T 98, its load writes 72, 2480 cycles in all; a tile takes 2950.
@@ -53,12 +66,15 @@ constexpr int kLatentTile = 64;      // tokens of a tile
 constexpr int kLatentThreads = 384;
 constexpr int kLatentP = 64;         // positional elements
 
-template <int R, int N>
+template <int R, int N, bool BF>
 struct LatentCfg {
     static constexpr int MB = R / 128;                         // value blocks of a tile
+    static constexpr int PARTS = BF && (R < 512 || N < 64) ? 2 : 1;  // of a weight
+    static constexpr int ON = N * PARTS;                       // columns of P^T and of a value block of O^T
     static constexpr uint32_t Q_BYTES = N * (R + kLatentP) * 2u;
     static constexpr int PBUF = (R == 512 && N == 64) ? 1 : 2;  // P^T buffers
-    static constexpr uint32_t P_BYTES = kLatentTile * 128u;
+    static constexpr uint32_t P_BLOCK = kLatentTile * 128u;    // 64 columns
+    static constexpr uint32_t P_BYTES = (ON + 63) / 64 * P_BLOCK;
     static constexpr uint32_t PAIR = 2u * kLatentTile * 128u, ROPE = kLatentTile * 128u;
     static constexpr uint32_t BUDGET = 229376u;                // leaves 2 KB for barriers and statistics
     // as many tiles' worth of slots as fit, whole pairs
@@ -78,7 +94,7 @@ struct LatentCfg {
     static constexpr uint32_t SMEM = MISC_OFF + 64 + kSmemAlignSlack;
     static_assert(SMEM <= 227u * 1024u, "shared memory");
     static_assert(NP >= 2 * MB && NR >= 2, "two tiles in flight");
-    static constexpr uint32_t COLS_RAW = (2 + MB) * N;
+    static constexpr uint32_t COLS_RAW = 2 * N + MB * ON;
     static constexpr uint32_t COLS = COLS_RAW <= 64 ? 64 : COLS_RAW <= 128 ? 128 : COLS_RAW <= 256 ? 256 : 512;
 };
 
@@ -223,10 +239,10 @@ template <int R, int N, typename T>
 __global__ void __launch_bounds__(kLatentThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_q,
                   const LatentParams p) {
-    using C = LatentCfg<R, N>;
-    constexpr int MB = C::MB, NP = C::NP, NR = C::NR, PBUF = C::PBUF;
-    constexpr float NEG_INF = -INFINITY;
     constexpr bool kBF = std::is_same<T, __nv_bfloat16>::value;
+    using C = LatentCfg<R, N, kBF>;
+    constexpr int MB = C::MB, NP = C::NP, NR = C::NR, PBUF = C::PBUF, ON = C::ON, PARTS = C::PARTS;
+    constexpr float NEG_INF = -INFINITY;
     constexpr float kSlack = 8.f, kLift = kBF ? 0.f : kHalfLift;
 
     extern __shared__ uint8_t smem_raw[];
@@ -548,7 +564,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     } else if (warp == 2) {
         // ================= O^T += C^T P^T =================
         // A and B both M- / N-major: elements and rows contiguous, tokens the rows of 128 bytes
-        constexpr uint32_t idesc = tc::idesc_f16(kType, true, 128, N) | (1u << 15);
+        constexpr uint32_t idesc = tc::idesc_f16(kType, true, 128, ON) | (1u << 15);
         const uint32_t otmem = uniform(tmem + 2 * N);
         const bool one = tc::elect_one();
         int tile = 0, pairs = 0;
@@ -574,8 +590,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     for (int m = 0; m < MB; ++m) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)  // 16 tokens
-                            tc::mma_parts(otmem + m * N, at[m] + kk * 128 + (C::ROPE >> 4 << 16), kDesc,
-                                          pt + kk * 128 + (C::P_BYTES >> 4 << 16), kDesc, idesc,
+                            tc::mma_parts(otmem + m * ON, at[m] + kk * 128 + (C::ROPE >> 4 << 16), kDesc,
+                                          pt + kk * 128 + (C::P_BLOCK >> 4 << 16), kDesc, idesc,
                                           !(first && kk == 0));
                         tc::commit(freed[m]);
                     }
@@ -663,7 +679,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     if (k > g.k0) {
                         // O^T (elements in lanes, rows in columns) on the new references
                         tc::fence_after_sync();
-                        for (int c0 = 0; c0 < MB * NC; c0 += 8) {
+                        for (int c0 = 0; c0 < MB * PARTS * NC; c0 += 8) {
                             const uint32_t at = tmem + quarter + (2 + c0 / NC) * N + cb + c0 % NC;
                             float o[8];
                             tc::ld_32x32b_x8(at, o);
@@ -676,8 +692,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                         tc::wait_st();
                     }
                 }
-                // ---- weights, rounded to the cache's type as they meet the values ----
-                uint32_t pk[2 * J];
+                // ---- weights, in 16 bits as they meet the values: rounded once, or in two parts ----
+                uint32_t pk[2 * J], pl[PARTS == 2 ? 2 * J : 1];
 #pragma unroll
                 for (int i = 0; i < 2 * J; ++i) {
                     // i: group i / 2, token tg or tg + 8; two neighbouring rows
@@ -688,7 +704,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                         if (x[a + 1] == NEG_INF) e1 = 0.f;
                     }
                     pk[i] = Mma<T>::pack(e0, e1);
-                    Mma<T>::unpack(pk[i], e0, e1);
+                    float h0, h1;
+                    Mma<T>::unpack(pk[i], h0, h1);
+                    if constexpr (PARTS == 2) pl[i] = Mma<T>::pack(e0 - h0, e1 - h1);
+                    else e0 = h0, e1 = h1;  // (the normaliser sums the rounded ones)
                     sum[r] += e0;
                     sum[r + 1] += e1;
                 }
@@ -700,6 +719,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     const int t = w * 16 + tg + (i & 1) * 8;
                     const uint32_t at = pt + t * 128 + ((((cb >> 3) + (i >> 1)) ^ (t & 7)) << 4) + tq * 4;
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pk[i]) : "memory");
+                    if constexpr (PARTS == 2) {  // columns N on
+                        const uint32_t lo = N == 64 ? at + C::P_BLOCK
+                                                    : pt + t * 128 + (((((N + cb) >> 3) + (i >> 1)) ^ (t & 7)) << 4) + tq * 4;
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(lo), "r"(pl[i]) : "memory");
+                    }
                 }
                 if (valid != ~0ull) {
                     // tokens without a page, or past the context: their rows must be
@@ -749,8 +773,17 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
                 for (int c0 = 0; c0 < NC; c0 += 8) {
                     float o[8];
-                    tc::ld_32x32b_x8(tmem + quarter + (2 + m) * N + cb + c0, o);
-                    tc::wait_ld();
+                    const uint32_t from = tmem + quarter + 2 * N + m * ON + cb + c0;
+                    tc::ld_32x32b_x8(from, o);
+                    if constexpr (PARTS == 2) {
+                        float lo[8];
+                        tc::ld_32x32b_x8(from + N, lo);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] += lo[i];
+                    } else {
+                        tc::wait_ld();
+                    }
                     const int d = m * 128 + w * 32 + lane, c = cb + c0;
                     if (whole) {
 #pragma unroll
@@ -890,7 +923,7 @@ cudaError_t launch_latent_inst(const LatentLaunch& L, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)L.ctas);
     cfg.blockDim = dim3(kLatentThreads);
-    cfg.dynamicSmemBytes = LatentCfg<R, N>::SMEM;
+    cfg.dynamicSmemBytes = LatentCfg<R, N, std::is_same<T, __nv_bfloat16>::value>::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
