@@ -452,10 +452,9 @@ pa_status pa_rope_append_kv8(void* q_out, void* k_cache, void* v_cache, float* k
  * same masking and an automatic split.  Codes are widened exactly; the scores,
  * the softmax and the sums are fp32, the normaliser of every attended token's
  * softmax weight as it is.  On the way into the product with the values a token
- * counts with its softmax weight times its page's v_scale: that product is rounded
- * once to fp16 (by at most 2^-11 of it) where out has 16 bits and held in two fp16
- * parts where it has 32, and one under 2^-32 of the row's largest adds nothing to
- * the output.  A NaN or infinity in a cached value or scale that one
+ * counts with its softmax weight times its page's v_scale: that product is held in
+ * two fp16 parts, rounded once to fp16 (by at most 2^-11 of it) where out is bf16, and
+ * one under 2^-32 of the row's largest adds nothing to the output.  A NaN or infinity in a cached value or scale that one
  * row attends to may reach its sequence's other rows.  Scales are finite and positive, whoever wrote them;
  * v_scales outside [2^-60, 2^60] count as the nearer limit.  Scales of pages
  * that hold no attended token are not used.  shape->kv_dtype is

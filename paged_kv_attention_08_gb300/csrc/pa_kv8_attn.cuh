@@ -38,13 +38,15 @@
 // latency of a step's chain on the two warps that a scheduler holds: 16 sequences of
 // 8K tokens, 64 rows: 51 us, 2.1 a step of 32 tokens.
 //
-// Weights meet the values as fp16, 2^kHalfLift up (pa_internal.h): once rounded
-// (by at most 2^-11 of each) where the output has 16 bits, in two parts where it
-// has 32.  One part is half of the second product; its rounding is that of an fp16
-// output, an eighth of a bf16 output's, and averages out over the tokens.  What it
-// loses whole are tokens whose w_t lies 2^-32 under the row's largest: their values
-// add nothing to an output, but their 2^(s_t) may be most of the normaliser (a page
-// of zero values has sv = 2^-60).  So l sums the weights as they are, in fp32.
+// Weights meet the values as fp16, 2^kHalfLift up (pa_internal.h), in two parts; once
+// rounded (by at most 2^-11 of each) where the output is bf16, whose own rounding is
+// eight times that.  In one part it is half of the second product: 51 us against 57 for
+// 16 sequences of 8K tokens with 64 rows of 256, 56 against 57 for 64 of 1 .. 4096, no
+// difference for 4 of 131,072; an fp16 output's error would grow by a tenth (0.00020
+// to 0.00022).  Tokens whose w_t lies 2^-32 under the row's largest are lost whole:
+// their values add nothing to an output, but their 2^(s_t) may be most of the
+// normaliser (a page of zero values has sv = 2^-60).  So l sums the weights as they
+// are, in fp32.
 // fp32 ends as well, at 2^-126: where a page on the scale 2^60 is met, tokens of one
 // on 2^-60 lie there from 2^-6 of its weights down, however many they are.  So pages
 // more than 2^64 under the largest scale sum 2^(s_t - m) itself, which loses no token
@@ -882,7 +884,7 @@ cudaError_t launch_kv8_join(const Kv8Launch& L, cudaStream_t stream) {
 
 template <int D, int NR>
 cudaError_t launch_kv8_for(const Kv8Launch& L, cudaStream_t stream) {
-    const bool two = L.p.out_dtype == PA_F32;
+    const bool two = L.p.out_dtype != PA_BF16;
     const cudaError_t e =
         L.block_size == 16
             ? (two ? launch_kv8_inst<D, 16, NR, true>(L, stream) : launch_kv8_inst<D, 16, NR, false>(L, stream))
