@@ -122,14 +122,14 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr int kMaxBalancedLens = 2048;
 
 // Few units, up to 32 steps to a CTA: clusters of up to 8 CTAs and no second launch
-// (8 kv heads; 8 sequences of 4 x 3000 tokens: 16.4 us against 26.4 in runs).  Up to 64
+// (8 kv heads; 8 sequences of 4 x 3000 tokens: 17.7 us against 27.3 in runs).  Up to 64
 // steps where they fill more than half of the GPU (4 sequences of 16,384 tokens 28 us
 // against 34 in runs, of 1000 .. 16,384 25.5 against 24; but one of 16,384 20 against 15).
 // Else equal runs of steps over the CTAs that the GPU holds (64 sequences of 1 .. 4096
-// tokens 56.6 us with the join, a unit to a CTA 61.6; 16 of 1 .. 16,384: 54 and 81).
+// tokens 57 us with the join, a unit to a CTA 62; 16 of 1 .. 16,384: 55 and 130).
 // With more than 3 units for each of them, where the waves even out by themselves (128
-// sequences of 1 .. 2048: 56 us against 60 in runs), of contexts up to 48 steps (64
-// sequences of 100 .. 1500: 29 us against 34), or with more lengths than a CTA looks
+// sequences of 1 .. 2048: 57 us against 60 in runs), of contexts up to 48 steps (64
+// sequences of 100 .. 1500: 30 us against 34), or with more lengths than a CTA looks
 // through, a unit to a CTA.
 Kv8Plan plan_kv8(const pa_shape* s, int32_t q_len, int32_t max_context_len, int sms) {
     Kv8Plan pl;

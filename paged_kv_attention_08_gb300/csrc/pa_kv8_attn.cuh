@@ -31,10 +31,10 @@
 // registers that the conversion turns into the A operand; the weights change
 // sides by movmatrix.
 // Bounds: of few rows DRAM (4 sequences of 131,072 tokens, 8 kv heads of 128, 1.08
-// GB: 174 us, 6.2 TB/s; the copies alone 170), behind it the half-rate pipe of the
-// conversions and permutations (two cycles each; 34 % busy) and the MMAs (one in
-// 2 cycles an SM; 15 %); of 64 sequences of 1 .. 4096 tokens (270 MB) 56 us, 4.8
-// TB/s, 12 us of them starts, cuts and the join.  Of many rows at head_dim 256 the
+// GB: 176 us, 6.1 TB/s; the copies alone 170), behind it the half-rate pipe of the
+// conversions and permutations (two cycles each; 33 % busy) and the MMAs (one in
+// 2 cycles an SM; 21 % with weights in two parts); of 64 sequences of 1 .. 4096
+// tokens (270 MB) 57 us, 4.7 TB/s, 12 us of them starts, cuts and the join.  Of many rows at head_dim 256 the
 // latency of a step's chain on the two warps that a scheduler holds: 16 sequences of
 // 8K tokens, 64 rows: 51 us, 2.1 a step of 32 tokens.
 //

@@ -49,9 +49,9 @@
 // Bounds (latent_dim 512; isolated MMAs: M = 64, N = 64 30 cycles, N = 16 22;
 // M = 128 44 and 36).  With 64 rows shared memory's 128 bytes a cycle: a tile's S^T
 // reads 147 KB of it and O^T 98, its load writes 72, 2480 cycles in all; a tile takes 2950.
-// 4 sequences of 65,536 tokens, 128 heads (302 MB, 73 GFLOP): 103 us, 710
-// TFLOP/s; 32 of 4001 .. 4096 with two query tokens: 113 us.  With 16 rows DRAM: 64
-// sequences of 1 .. 8192 tokens, 16 heads (304 MB): 67 us, 4.5 TB/s, 5.4 between the
+// 4 sequences of 65,536 tokens, 128 heads (302 MB, 73 GFLOP): 102 us, 715
+// TFLOP/s; 32 of 4001 .. 4096 with two query tokens: 111 us.  With 16 rows DRAM: 64
+// sequences of 1 .. 8192 tokens, 16 heads (304 MB): 68 us, 4.5 TB/s, 5.4 between the
 // first tile (4 us, when all SMs start at once) and the pieces' ends (5 us with the join).
 #pragma once
 
